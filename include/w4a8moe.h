@@ -410,6 +410,95 @@ typedef struct {
 int w4a8_moe_workspace_layout(int64_t T, int64_t H, int64_t I, int64_t E, int k,
                               w4a8_moe_layout* layout /* host pointer */);
 
+/*
+ * Operators around the routed experts.
+ *
+ * What a transformer block needs next to the layer: the norms before and after
+ * it with gate and residual, dense matrix products in 16 bits (the router's
+ * gate, a shared expert), and grouped expert routing.  The conventions at the
+ * top hold, with these additions: an element type is a w4a8_dtype; a row
+ * stride ("ld") is in elements and may exceed the row's length; every pointer
+ * is aligned to its element size (16-byte alignment of pointers and row strides
+ * takes the faster loads, with the same results).
+ */
+typedef enum { W4A8_DTYPE_BF16 = 0, W4A8_DTYPE_F16 = 1, W4A8_DTYPE_F32 = 2 } w4a8_dtype;
+typedef enum { W4A8_SCORE_SOFTMAX = 0, W4A8_SCORE_SIGMOID = 1 } w4a8_score;
+typedef enum { W4A8_NORM_NONE = 0, W4A8_NORM_RMS = 1, W4A8_NORM_LAYER = 2 } w4a8_norm;
+typedef enum {
+  W4A8_ACT_NONE = 0,
+  W4A8_ACT_RELU = 1,
+  W4A8_ACT_SILU = 2,      /* z / (1 + exp(-z))                                       */
+  W4A8_ACT_GELU = 3,      /* z * Phi(z), Phi the normal distribution function        */
+  W4A8_ACT_GELU_TANH = 4  /* z/2 * (1 + tanh(sqrt(2/pi) * (z + 0.044715 * z^3)))     */
+} w4a8_act;
+
+/*
+ * (8) Grouped expert routing.  Per token, with logits l [E]:
+ *   s = softmax(l) or sigmoid(l) (score);  c = s + bias (c = s without a bias).
+ *   The E experts form n_group groups of E / n_group neighbours.  A group's
+ *   score is the sum of its group_top (1 or 2) largest c; the topk_group groups
+ *   with the largest scores are kept (equal scores: lower group first).
+ *   ids = the k experts of kept groups with the largest c in descending order
+ *   (equal c: lower id first);  w_j = s[ids_j], with renormalize != 0 divided by
+ *   (their sum + 1e-20), times scale.
+ * The bias takes part in the choice only.  A softmax without a bias is ranked
+ * by the logits (the same order, without ties made by rounding).
+ * A logit that is -inf, the lowest finite value of its type or NaN takes its
+ * expert out: s = 0, c = -inf.  When fewer than k experts are left, the places
+ * are filled with the lowest ids among the experts that are out or in groups
+ * that were not kept, with weight 0, so ids are always distinct and in [0, E).
+ *   logits [T][ld] fp32, bf16 or f16 (ld >= E)   bias fp32 [E] or NULL
+ *   topk_ids int32 [T][k]   topk_w fp32 [T][k]
+ *   1 <= E <= 1024, 1 <= n_group <= 32 dividing E, 1 <= topk_group <= n_group,
+ *   group_top <= E / n_group, 1 <= k <= min(32, topk_group * E / n_group), T >= 0.
+ */
+int moe_route_grouped_topk(const void* logits, int logits_dtype, int64_t ld, int64_t T, int64_t E, int k, int score,
+                           const float* bias, int n_group, int topk_group, int group_top, int renormalize,
+                           float scale, int32_t* topk_ids, float* topk_w, void* stream);
+
+/*
+ * (9) The norms after and before a block, fused with its gate and residual:
+ *   u = norm_post(f)
+ *   h = residual_scale * residual + branch_scale * gate * u
+ *   y = norm_pre(h)
+ * f [T][H] is the output of one block, h the residual stream behind it, y the
+ * input of the next block.  A norm (w4a8_norm) is none, rms:
+ * v / sqrt(mean(v^2) + eps) * w (+ b), or layer: (v - mean(v)) /
+ * sqrt(mean((v - mean(v))^2) + eps) * w (+ b); w = NULL is 1, b = NULL is 0.
+ * Everything between the loads and the stores is fp32; h and y are each rounded
+ * once, y from the unrounded h.
+ *   f, y [T][H] of `dtype`   residual, h [T][H] of `residual_dtype` (dtype or fp32)
+ *   residual = NULL: h = branch_scale * gate * u.  h or y may be NULL (not wanted).
+ *   gate [gate_rows][gate_cols] of `gate_dtype` (dtype or fp32) or NULL (1): gate_rows
+ *     divides T and token t uses gate row t / (T / gate_rows); gate_cols is H or 1.
+ *   w_post, b_post, w_pre, b_pre [H] of `param_dtype` (dtype or fp32), each may be NULL.
+ *   1 <= H <= 32768.  h may be the residual's and y may be f's own memory (same
+ *   row stride); no other overlap.
+ */
+int block_norm(const void* f, int64_t ldf, int dtype, const void* residual, int64_t ldr, int residual_dtype, int post,
+               const void* w_post, const void* b_post, const void* gate, int64_t ldg, int64_t gate_rows,
+               int64_t gate_cols, int gate_dtype, float branch_scale, float residual_scale, int pre,
+               const void* w_pre, const void* b_pre, int param_dtype, float eps, int64_t T, int64_t H, void* h,
+               int64_t ldh, void* y, int64_t ldy, void* stream);
+
+/*
+ * (10) Dense Linear in 16 bits with bias, activation, gating and residual in the
+ * epilogue:
+ *   z = x w^T + bias (fp32 accumulation)
+ *   out = act(z) + residual                              gated = 0
+ *   out = act(z[:, :N/2]) * z[:, N/2:] + residual        gated = 1 (w: gate rows, then the others)
+ *   x [M][K], w [N][K] bf16 or f16 (`dtype`, the same for both)
+ *   out, residual [M][N or N/2] of `out_dtype` (dtype or fp32), residual may be NULL
+ *   and may be out's own memory (same row stride)
+ *   bias [N] of `bias_dtype` (dtype or fp32) or NULL
+ *   0 <= M, N <= 2^20, 1 <= K <= 2^20.
+ * ws: dense_linear_workspace_bytes(M, N, K) bytes (0: none, then NULL will do), 16-byte aligned.
+ */
+int dense_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int dtype, const void* bias, int bias_dtype,
+                 int act, int gated, const void* residual, int64_t ldr, void* out, int64_t ldo, int out_dtype,
+                 int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes, void* stream);
+size_t dense_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
 #ifdef __cplusplus
 }
 #endif

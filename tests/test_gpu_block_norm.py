@@ -1,0 +1,171 @@
+"""The fused block norm on the GPU against its definition in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import block_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+
+
+def _np(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def _check(lib, T, H, dtype="bf16", rdtype="bf16", post="rms", pre="rms", gate=None, pdtype="f32", bias=False,
+           residual=True, branch=0.75, resid=1.25, eps=1e-6, pad=0, shift=0, seed=0, alias=False):
+    g = torch.Generator("cuda").manual_seed(seed)
+
+    def mat(n, m, dt, s=1.0):  # rows `pad` elements apart, starting `shift` elements into the memory
+        buf = torch.full((n * (m + pad) + shift + 8,), float("nan"), dtype=DT[dt], device="cuda")
+        v = buf[shift:shift + n * (m + pad)].view(n, m + pad)[:, :m]
+        v.copy_((torch.randn((n, m), device="cuda", generator=g) * s + 0.3).to(DT[dt]))
+        return v
+
+    f, r = mat(T, H, dtype), mat(T, H, rdtype, 2.0) if residual else None
+    par = {}
+    for name, kind in (("post", post), ("pre", pre)):
+        par["w_" + name] = (1 + 0.3 * torch.randn(H, device="cuda", generator=g)).to(DT[pdtype]) if kind != "none" else None
+        par["b_" + name] = (0.2 * torch.randn(H, device="cuda", generator=g)).to(DT[pdtype]) if bias and kind != "none" else None
+    gt = None if gate is None else mat(gate[0], gate[1], dtype)
+    fn, rn = _np(f), _np(r)
+    outs = dict(h=r, y=f) if alias else {}
+    h, y = lib.block_norm(f, r, post=post, pre=pre, gate=gt, branch_scale=branch, residual_scale=resid, eps=eps,
+                          residual_dtype=DT[rdtype], **par, **outs)
+    torch.cuda.synchronize()
+    assert h.dtype == DT[rdtype] and y.dtype == DT[dtype]
+    b32, r32 = float(np.float32(branch)), float(np.float32(resid))
+    (rh, bh), (ry, by) = ref.block_norm(fn, rn, post, _np(par["w_post"]), _np(par["b_post"]), _np(gt), b32, r32, pre,
+                                        _np(par["w_pre"]), _np(par["b_pre"]), float(np.float32(eps)),
+                                        T // gate[0] if gate else 1)
+    ref.check(_np(h), rh, bh, rdtype, "h")
+    ref.check(_np(y), ry, by, dtype, "y")
+
+
+@pytest.mark.parametrize("post,pre", [("rms", "rms"), ("none", "rms"), ("rms", "none"), ("layer", "layer"),
+                                      ("none", "layer"), ("layer", "none"), ("none", "none")])
+@pytest.mark.parametrize("H", [1, 7, 64, 200, 1003, 4096])
+def test_kinds_and_widths(lib, post, pre, H):
+    _check(lib, 5, H, post=post, pre=pre, bias=True, seed=H)
+
+
+@pytest.mark.parametrize("dtype,rdtype", [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f16", "f32"),
+                                          ("f32", "f32")])
+@pytest.mark.parametrize("H", [256, 1001, 7168])
+@pytest.mark.parametrize("gate", [None, "channel", "token", "full", "sample", "sample-token"])
+def test_types_and_gates(lib, dtype, rdtype, H, gate):
+    T = 12
+    shape = {None: None, "channel": (1, H), "token": (T, 1), "full": (T, H), "sample": (3, H),
+             "sample-token": (4, 1)}[gate]
+    _check(lib, T, H, dtype=dtype, rdtype=rdtype, gate=shape, post="layer", pre="rms", bias=True, seed=1)
+
+
+@pytest.mark.parametrize("H", [8192, 8200, 16384, 16392, 32768, 8191, 12345, 32767])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_long_rows(lib, H, dtype):
+    _check(lib, 3, H, dtype=dtype, rdtype=dtype, pre="layer", bias=True, seed=2)
+
+
+@pytest.mark.parametrize("T", [1, 2, 153, 700, 3001])
+@pytest.mark.parametrize("H", [96, 1536])
+def test_row_counts(lib, T, H):
+    _check(lib, T, H, gate=(T, 1), seed=3)
+
+
+@pytest.mark.parametrize("pad,shift", [(8, 0), (3, 0), (0, 1), (8, 8), (1, 5), (0, 4)])
+@pytest.mark.parametrize("H", [512, 777])
+def test_strides_and_alignment(lib, pad, shift, H):
+    _check(lib, 9, H, pad=pad, shift=shift, gate=(9, H), seed=4)
+
+
+def test_parameters_in_the_activations_type(lib):
+    _check(lib, 6, 640, pdtype="bf16", post="layer", pre="layer", bias=True)
+    _check(lib, 6, 641, dtype="f16", rdtype="f16", pdtype="f16", post="rms", pre="layer", bias=True)
+
+
+def test_in_place(lib):
+    _check(lib, 300, 1024, alias=True, seed=6)
+    _check(lib, 300, 515, alias=True, rdtype="f32", seed=6)
+
+
+def test_no_residual_and_single_outputs(lib):
+    _check(lib, 7, 384, residual=False, post="none", pre="rms")
+    f = torch.randn((7, 384), device="cuda").to(torch.bfloat16)
+    r = torch.randn((7, 384), device="cuda").to(torch.bfloat16)
+    h, y = lib.block_norm(f, r, pre="rms")
+    h1, none = lib.block_norm(f, r, pre="rms", want_y=False)
+    none2, y1 = lib.block_norm(f, r, pre="rms", want_h=False)
+    assert none is None and none2 is None
+    assert torch.equal(h, h1) and torch.equal(y, y1)
+    assert torch.equal(h, (f.float() + r.float()).to(torch.bfloat16))
+
+
+def test_zero_rows_constant_rows_and_no_rows(lib):
+    f = torch.zeros((4, 256), dtype=torch.bfloat16, device="cuda")
+    f[1] = 3.0
+    h, y = lib.block_norm(f, post="layer", pre="rms")
+    assert torch.all(h[:2] == 0) and torch.all(y == 0)  # a constant row has no deviation
+    h, y = lib.block_norm(f, post="rms", pre="none")
+    assert torch.all(h[0] == 0) and torch.all(h[1] == 1)
+    h, y = lib.block_norm(f[:0], post="rms")
+    assert h.shape == (0, 256) and y.shape == (0, 256)
+
+
+def test_large_mean_keeps_its_variance(lib):
+    # the deviations are taken from the mean before they are squared: a mean 2^11 times larger costs no digits
+    g = torch.Generator("cuda").manual_seed(7)
+    f = torch.randn((4, 2048), device="cuda", generator=g) + 2048.0
+    h, _ = lib.block_norm(f, post="layer", pre="none", eps=0.0)
+    d = f.double() - f.double().mean(1, keepdim=True)
+    want = d / d.square().mean(1, keepdim=True).sqrt()
+    # |error of the mean| <= 48 * 2^-24 * 2048 (derived as for the sums), relative to a deviation of 1
+    assert (h.double() - want).abs().max() <= 2 * 48 * 2.0 ** -24 * 2048
+
+
+def test_non_finite_rows_stay_in_their_rows(lib):
+    f = torch.ones((3, 512), dtype=torch.float16, device="cuda")
+    f[1, 100] = float("inf")
+    f[2, 5] = float("nan")
+    h, y = lib.block_norm(f, post="rms", pre="rms")
+    assert torch.isfinite(h[0]).all() and torch.isfinite(y[0]).all()
+    assert torch.isnan(h[1, 100]) and torch.isnan(y[1]).all() and torch.isnan(y[2]).all()
+
+
+def test_other_stream(lib):
+    f = torch.randn((2048, 4096), device="cuda").to(torch.bfloat16)
+    want = lib.block_norm(f, f, post="rms")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = lib.block_norm(f, f, post="rms")
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+def test_refusals(lib):
+    f = torch.zeros((6, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, device="cuda")
+    with pytest.raises(lib.W4A8Error, match="H=40000"):
+        lib.block_norm(torch.zeros((1, 40000), dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(lib.W4A8Error, match="gate_rows=4"):
+        lib.block_norm(f, gate=torch.ones((4, 1), dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(lib.W4A8Error, match="gate_cols=2"):
+        lib.block_norm(f, gate=torch.ones((6, 2), dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(lib.W4A8Error, match="none"):
+        lib.block_norm(f, post="none", w_post=w)
+    with pytest.raises(lib.W4A8Error, match="eps"):
+        lib.block_norm(f, eps=-1.0)
+    with pytest.raises(lib.W4A8Error, match="nothing to compute"):
+        lib.block_norm(f, want_h=False, want_y=False)
+    with pytest.raises(ValueError, match="post"):
+        lib.block_norm(f, post="group")
+    with pytest.raises(TypeError, match="residual"):
+        lib.block_norm(f, f.half())
+    with pytest.raises(ValueError, match="residual"):
+        lib.block_norm(f, f[:5])
+    with pytest.raises(TypeError, match="one dtype"):
+        lib.block_norm(f, post="rms", w_post=w, pre="rms", w_pre=w.to(torch.bfloat16))
+    with pytest.raises(ValueError, match="w_pre"):
+        lib.block_norm(f, w_pre=torch.ones(63, device="cuda"))

@@ -1,0 +1,164 @@
+"""dense_linear on the GPU against its definition in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import block_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+
+
+def _np(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def _mat(n, m, dt, g, pad=0, shift=0, ints=False, scale=1.0):
+    """[n, m] with rows `pad` elements apart, `shift` elements into the memory; NaN around it."""
+    buf = torch.full((n * (m + pad) + shift + 8,), float("nan"), dtype=DT[dt], device="cuda")
+    v = buf[shift:shift + n * (m + pad)].view(n, m + pad)[:, :m]
+    if ints:
+        v.copy_(torch.randint(-2, 3, (n, m), device="cuda", generator=g).to(DT[dt]))
+    else:
+        v.copy_((torch.randn((n, m), device="cuda", generator=g) * scale).to(DT[dt]))
+    return v
+
+
+def _check(lib, M, N, K, dtype="bf16", out="bf16", act="none", gated=False, bias=None, residual=False, pad=0, shift=0,
+           opad=0, seed=0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    x = _mat(M, K, dtype, g, pad, shift)
+    w = _mat(N, K, dtype, g, pad, shift, scale=1.5 / K ** 0.5)
+    b = None if bias is None else torch.randn(N, device="cuda", generator=g).to(DT[bias])
+    n_out = N // 2 if gated else N
+    r = _mat(M, n_out, out, g, opad, shift) if residual else None
+    obuf = torch.full((M, n_out + opad), 7.0, dtype=DT[out], device="cuda")
+    o = obuf[:, :n_out]
+    got = lib.dense_linear(x, w, bias=b, act=act, gated=gated, residual=r, out_dtype=DT[out], out=o)
+    torch.cuda.synchronize()
+    assert got is o and lib.device_error() == 0
+    assert torch.all(obuf[:, n_out:] == 7.0)  # nothing beside the rows
+    want, bound = ref.linear(_np(x), _np(w), _np(b), act, gated, _np(r))
+    ref.check(_np(o), want, bound, out)
+
+
+SIZES = [(1, 1, 1), (1, 256, 1024), (1, 33, 77), (3, 17, 64), (8, 128, 4096), (9, 40, 513), (16, 512, 2048),
+         (17, 16, 96), (33, 200, 1000), (64, 256, 1536), (65, 130, 320), (100, 72, 64), (128, 384, 512),
+         (129, 257, 130), (255, 64, 1024), (256, 512, 256), (300, 300, 300), (513, 1000, 200), (1025, 48, 2056)]
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+@pytest.mark.parametrize("gated", [False, True])
+def test_sizes(lib, M, N, K, gated):
+    N = 2 * N if gated else N
+    _check(lib, M, N, K, gated=gated, act="silu" if gated else "none", bias="f32", residual=True, seed=M + N)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 64, 7168), (8, 256, 520), (40, 96, 3000), (130, 272, 1056), (700, 260, 1024),
+                                   (2000, 520, 640)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_whole_numbers_are_exact(lib, M, N, K, dtype):
+    # sums of whole numbers below 2^24 have no rounding: every product is there once, at its place
+    g = torch.Generator("cuda").manual_seed(K)
+    x, w = _mat(M, K, dtype, g, ints=True), _mat(N, K, dtype, g, ints=True)
+    got = lib.dense_linear(x, w, out_dtype=torch.float32)
+    want = x.cpu().double() @ w.cpu().double().t()
+    assert torch.equal(got.cpu().double(), want)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M", [3, 50, 300])
+def test_activations(lib, act, gated, M):
+    _check(lib, M, 192, 256, act=act, gated=gated, out="f32", seed=11)
+
+
+@pytest.mark.parametrize("dtype,out,bias", [("bf16", "bf16", "bf16"), ("bf16", "f32", "f32"), ("f16", "f16", "f16"),
+                                            ("f16", "f32", "f16"), ("f16", "f16", "f32")])
+@pytest.mark.parametrize("M", [1, 20, 70, 400])
+def test_types(lib, dtype, out, bias, M):
+    _check(lib, M, 320, 384, dtype=dtype, out=out, act="gelu", bias=bias, residual=True, seed=12)
+
+
+@pytest.mark.parametrize("pad,shift,opad", [(8, 0, 8), (0, 1, 0), (3, 0, 1), (1, 8, 3), (8, 4, 4), (24, 16, 16)])
+@pytest.mark.parametrize("M", [2, 24, 90, 600])
+@pytest.mark.parametrize("K", [256, 333])
+def test_strides_and_alignment(lib, pad, shift, opad, M, K):
+    _check(lib, M, 136, K, pad=pad, shift=shift, opad=opad, bias="f32", residual=True, seed=13)
+
+
+@pytest.mark.parametrize("M", [1, 30, 77, 260, 1500])
+def test_residual_in_place_and_repeatable(lib, M):
+    g = torch.Generator("cuda").manual_seed(14)
+    x, w = _mat(M, 2048, "bf16", g), _mat(128, 2048, "bf16", g)
+    r = _mat(M, 128, "bf16", g)
+    a = lib.dense_linear(x, w, residual=r)
+    b = lib.dense_linear(x, w, residual=r)
+    assert torch.equal(a, b)  # sums are added in a fixed order
+    lib.dense_linear(x, w, residual=r, out=r)
+    assert torch.equal(a, r)
+
+
+def test_rows_do_not_mix(lib):
+    # a NaN or an infinity in one token, or one weight row, stays in its row or column
+    g = torch.Generator("cuda").manual_seed(15)
+    for M in (4, 60, 300):
+        x, w = _mat(M, 200, "bf16", g), _mat(96, 200, "bf16", g)
+        x[1, 3] = float("nan")
+        w[70, 199] = float("inf")
+        y = lib.dense_linear(x, w)
+        good = torch.ones_like(y, dtype=torch.bool)
+        good[1] = False
+        good[:, 70] = False
+        assert torch.isfinite(y[good]).all() and torch.isnan(y[1]).all() and not torch.isfinite(y[:, 70]).any()
+
+
+def test_empty(lib):
+    x, w = torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros((32, 64), dtype=torch.bfloat16, device="cuda")
+    assert lib.dense_linear(x, w).shape == (0, 32)
+    assert lib.dense_linear(w, x).shape == (32, 0)
+
+
+@pytest.mark.parametrize("M", [5, 64, 1024])
+def test_other_stream_and_graph(lib, M):
+    g = torch.Generator("cuda").manual_seed(16)
+    x, w = _mat(M, 512, "bf16", g), _mat(256, 512, "bf16", g)
+    want = lib.dense_linear(x, w)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = torch.empty_like(want)
+    with torch.cuda.stream(s):
+        lib.dense_linear(x, w, out=out)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            lib.dense_linear(x, w, out=out)
+        out.zero_()
+        graph.replay()
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(out, want)
+
+
+def test_refusals(lib):
+    x = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((32, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(TypeError, match="x must be one of"):
+        lib.dense_linear(x.float(), w.float())
+    with pytest.raises(TypeError, match="w must be one of"):
+        lib.dense_linear(x, w.half())
+    with pytest.raises(ValueError, match="64 columns"):
+        lib.dense_linear(x, w[:, :32])
+    with pytest.raises(ValueError, match="even"):
+        lib.dense_linear(x, w[:31], gated=True)
+    with pytest.raises(ValueError, match="act"):
+        lib.dense_linear(x, w, act="tanh")
+    with pytest.raises(TypeError, match="out_dtype"):
+        lib.dense_linear(x, w, out_dtype=torch.float16)
+    with pytest.raises(ValueError, match="residual"):
+        lib.dense_linear(x, w, residual=torch.zeros((4, 31), dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError, match="bias"):
+        lib.dense_linear(x, w, bias=torch.zeros(31, device="cuda"))
+    with pytest.raises(lib.W4A8Error, match="K=0"):
+        lib.dense_linear(x[:, :0], w[:, :0])
+    with pytest.raises(TypeError, match="CUDA tensor"):
+        lib.dense_linear(x.cpu(), w)

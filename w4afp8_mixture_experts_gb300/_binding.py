@@ -16,6 +16,7 @@ from .build import LIB
 
 _c_i64 = ctypes.c_int64
 _c_int = ctypes.c_int
+_c_f32 = ctypes.c_float
 _c_vp = ctypes.c_void_p
 _c_sz = ctypes.c_size_t
 
@@ -59,6 +60,14 @@ _SIGS = {
     "w4a8_moe_forward_noalloc": (_c_int, [_c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_vp,
                                           _c_vp, _c_vp, _c_vp, _c_vp, _c_vp]),
     "w4a8_moe_noalloc_scratch_bytes": (_c_sz, []),
+    "moe_route_grouped_topk": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_vp, _c_int, _c_int,
+                                        _c_int, _c_int, _c_f32, _c_vp, _c_vp, _c_vp]),
+    "block_norm": (_c_int, [_c_vp, _c_i64, _c_int, _c_vp, _c_i64, _c_int, _c_int, _c_vp, _c_vp, _c_vp, _c_i64,
+                            _c_i64, _c_i64, _c_int, _c_f32, _c_f32, _c_int, _c_vp, _c_vp, _c_int, _c_f32, _c_i64,
+                            _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp]),
+    "dense_linear": (_c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_int, _c_vp, _c_int, _c_int, _c_int, _c_vp, _c_i64,
+                              _c_vp, _c_i64, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_sz, _c_vp]),
+    "dense_linear_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64]),
 }
 
 
@@ -388,6 +397,170 @@ def w4a8_moe_forward_noalloc(x, logits, k: int, w13, w13_s, w2, w2_s, out, renor
     _check(load().w4a8_moe_forward_noalloc(_p(x), _p(logits), T, H, I, E, k, int(bool(renormalize)), _p(w13),
                                            _p(w13_s), _p(w2), _p(w2_s), _p(out), _stream()))
     return out
+
+
+# --- operators around the routed experts -----------------------------------------------------------------------
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_NORMS = {"none": 0, "rms": 1, "layer": 2}
+_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _mat(t, name, dev, shape=None, dtypes=(torch.bfloat16, torch.float16, torch.float32)):
+    """Checks a CUDA matrix whose rows are contiguous (any row stride); returns (pointer, row stride, dtype id)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions")
+    rows, cols = t.shape
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {(rows, cols)}")
+    rs, cs = t.stride()
+    if cs != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows > 1 and rs < cols:
+        raise ValueError(f"{name} has overlapping rows (row stride {rs}, {cols} columns)")
+    return t.data_ptr(), max(rs, cols, 1), _DTYPES[t.dtype]
+
+
+def _vec(t, name, dev, n, dtypes):
+    """Checks a contiguous CUDA vector of n elements (None passes); returns its pointer or None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _one_of(table, value, name):
+    got = table.get(value)
+    if got is None:
+        raise ValueError(f"{name} must be one of {sorted(table)}, got {value!r}")
+    return got
+
+
+def moe_route_grouped_topk(logits, k: int, bias=None, score: str = "sigmoid", n_group: int = 1, topk_group: int = 1,
+                           group_top: int = 1, renormalize: bool = True, scale: float = 1.0):
+    """Grouped routing.  logits [T, E] fp32, bf16 or f16 (any row stride), bias fp32 [E] or None (choice only) ->
+    (ids int32 [T, k], weights fp32 [T, k]).  A logit of -inf (or its type's lowest value, or NaN) takes its expert
+    out; see moe_route_grouped_topk in include/w4a8moe.h for the rules."""
+    dev = logits.device if isinstance(logits, torch.Tensor) else None
+    lp, ld, ldt = _mat(logits, "logits", dev)
+    T, E = logits.shape
+    bp = _vec(bias, "bias", dev, E, (torch.float32,))
+    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        _check(load().moe_route_grouped_topk(lp, ldt, ld, T, E, k, _one_of(_SCORES, score, "score"), bp, n_group,
+                                             topk_group, group_top, int(bool(renormalize)), scale, ids.data_ptr(),
+                                             w.data_ptr(), _stream(dev)))
+    return ids, w
+
+
+def block_norm(f, residual=None, *, post: str = "none", w_post=None, b_post=None, gate=None, branch_scale: float = 1.0,
+               residual_scale: float = 1.0, pre: str = "rms", w_pre=None, b_pre=None, eps: float = 1e-6,
+               residual_dtype=None, want_h: bool = True, want_y: bool = True, h=None, y=None):
+    """The norms after and before a block with its gate and residual, in one pass:
+    u = norm_post(f), h = residual_scale * residual + branch_scale * gate * u, y = norm_pre(h).
+
+    f [T, H] bf16, f16 or fp32; residual [T, H] of f's dtype or fp32 (None: none; h then has residual_dtype, by
+    default f's); gate [1 or B or T, H or 1] of f's dtype or fp32, B dividing T; w_*, b_* [H], all of f's dtype or all
+    fp32.  post and pre are "none", "rms" or "layer".  Returns (h, y); h or y may be given as outputs (h may be
+    residual and y may be f itself), and is None where want_h or want_y is false."""
+    dev = f.device if isinstance(f, torch.Tensor) else None
+    fp, ldf, fd = _mat(f, "f", dev)
+    T, H = f.shape
+    either = (f.dtype, torch.float32)
+    rp, ldr = None, 0
+    rdt = residual_dtype or f.dtype
+    if residual is not None:
+        rp, ldr, _ = _mat(residual, "residual", dev, (T, H), either)
+        if residual_dtype not in (None, residual.dtype):
+            raise ValueError(f"residual_dtype {residual_dtype} differs from the residual's {residual.dtype}")
+        rdt = residual.dtype
+    elif rdt not in either:
+        raise TypeError(f"residual_dtype must be one of {either}, got {rdt}")
+    params = [t for t in (w_post, b_post, w_pre, b_pre) if t is not None]
+    pdt = params[0].dtype if params else torch.float32
+    pts = [_vec(t, n, dev, H, either) for t, n in ((w_post, "w_post"), (b_post, "b_post"), (w_pre, "w_pre"),
+                                                   (b_pre, "b_pre"))]
+    if any(t.dtype != pdt for t in params):
+        raise TypeError("w_post, b_post, w_pre and b_pre must have one dtype")
+    gp, ldg, gr, gc, gd = None, 0, 1, 1, 2
+    if gate is not None:
+        gp, ldg, gd = _mat(gate, "gate", dev, None, either)
+        gr, gc = gate.shape
+    hp, ldh, yp, ldy = None, 0, None, 0
+    if want_h:
+        if h is None:
+            h = torch.empty((T, H), dtype=rdt, device=dev)
+        hp, ldh, _ = _mat(h, "h", dev, (T, H), (rdt,))
+    if want_y:
+        if y is None:
+            y = torch.empty((T, H), dtype=f.dtype, device=dev)
+        yp, ldy, _ = _mat(y, "y", dev, (T, H), (f.dtype,))
+    with torch.cuda.device(dev):
+        _check(load().block_norm(fp, ldf, fd, rp, ldr, _DTYPES[rdt], _one_of(_NORMS, post, "post"), pts[0], pts[1], gp,
+                                 ldg, gr, gc, gd, branch_scale, residual_scale, _one_of(_NORMS, pre, "pre"), pts[2],
+                                 pts[3], _DTYPES[pdt], eps, T, H, hp, ldh, yp, ldy, _stream(dev)))
+    return (h if want_h else None), (y if want_y else None)
+
+
+def dense_linear(x, w, bias=None, act: str = "none", gated: bool = False, residual=None, out_dtype=None, out=None,
+                 ws=None):
+    """act(x w^T + bias) + residual, or with gated act(z[:, :N/2]) * z[:, N/2:] + residual for z = x w^T + bias.
+
+    x [M, K], w [N, K] bf16 or f16 (one dtype, any row strides); bias [N] of that dtype or fp32; residual and the
+    result [M, N] ([M, N/2] when gated) of out_dtype: x's dtype (default) or fp32.  act is "none", "relu", "silu",
+    "gelu" or "gelu_tanh".  out may be given, also as the residual itself; ws is a uint8 workspace of
+    dense_linear_workspace_bytes(M, N, K) bytes for repeated calls (made here when needed)."""
+    dev = x.device if isinstance(x, torch.Tensor) else None
+    xp, ldx, xd = _mat(x, "x", dev, None, (torch.bfloat16, torch.float16))
+    wp, ldw, _ = _mat(w, "w", dev, None, (x.dtype,))
+    M, K = x.shape
+    N = w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError(f"w must have {K} columns, got {w.shape[1]}")
+    if gated and N % 2:
+        raise ValueError(f"w must have an even number of rows when gated, got {N}")
+    either = (x.dtype, torch.float32)
+    odt = out_dtype or x.dtype
+    if odt not in either:
+        raise TypeError(f"out_dtype must be one of {either}, got {odt}")
+    n_out = N // 2 if gated else N
+    bp = _vec(bias, "bias", dev, N, either)
+    rp, ldr = None, 0
+    if residual is not None:
+        rp, ldr, _ = _mat(residual, "residual", dev, (M, n_out), (odt,))
+    if out is None:
+        out = torch.empty((M, n_out), dtype=odt, device=dev)
+    op, ldo, od = _mat(out, "out", dev, (M, n_out), (odt,))
+    need = dense_linear_workspace_bytes(M, N, K)
+    if ws is None and need:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        _check(load().dense_linear(xp, ldx, wp, ldw, xd, bp, 2 if bias is None else _DTYPES[bias.dtype],
+                                   _one_of(_ACTS, act, "act"), int(bool(gated)), rp, ldr, op, ldo, od, M, N, K,
+                                   None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                                   _stream(dev)))
+    return out
+
+
+def dense_linear_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load().dense_linear_workspace_bytes(M, N, K))
 
 
 def device_error() -> int:
