@@ -492,7 +492,9 @@ int block_norm(const void* f, int64_t ldf, int dtype, const void* residual, int6
  *   and may be out's own memory (same row stride)
  *   bias [N] of `bias_dtype` (dtype or fp32) or NULL
  *   0 <= M, N <= 2^20, 1 <= K <= 2^20.
- * ws: dense_linear_workspace_bytes(M, N, K) bytes (0: none, then NULL will do), 16-byte aligned.
+ * ws: needed only where x or w is not 16-byte aligned in its pointer and row
+ * stride (copies of both with aligned rows): dense_linear_workspace_bytes(M, N,
+ * K) bytes, 16-byte aligned; otherwise, or where that is 0, NULL will do.
  */
 int dense_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int dtype, const void* bias, int bias_dtype,
                  int act, int gated, const void* residual, int64_t ldr, void* out, int64_t ldo, int out_dtype,

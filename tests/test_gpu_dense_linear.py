@@ -45,7 +45,8 @@ def _check(lib, M, N, K, dtype="bf16", out="bf16", act="none", gated=False, bias
 
 SIZES = [(1, 1, 1), (1, 256, 1024), (1, 33, 77), (3, 17, 64), (8, 128, 4096), (9, 40, 513), (16, 512, 2048),
          (17, 16, 96), (33, 200, 1000), (64, 256, 1536), (65, 130, 320), (100, 72, 64), (128, 384, 512),
-         (129, 257, 130), (255, 64, 1024), (256, 512, 256), (300, 300, 300), (513, 1000, 200), (1025, 48, 2056)]
+         (129, 257, 130), (255, 64, 1024), (256, 512, 256), (300, 300, 300), (513, 1000, 200), (1025, 48, 2056),
+         (2304, 1288, 320), (2305, 1283, 130), (4100, 700, 72), (520, 9000, 64)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -56,7 +57,7 @@ def test_sizes(lib, M, N, K, gated):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 64, 7168), (8, 256, 520), (40, 96, 3000), (130, 272, 1056), (700, 260, 1024),
-                                   (2000, 520, 640)])
+                                   (2000, 520, 640), (2300, 1544, 640), (9000, 520, 2048)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_whole_numbers_are_exact(lib, M, N, K, dtype):
     # sums of whole numbers below 2^24 have no rounding: every product is there once, at its place
@@ -69,23 +70,23 @@ def test_whole_numbers_are_exact(lib, M, N, K, dtype):
 
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("gated", [False, True])
-@pytest.mark.parametrize("M", [3, 50, 300])
-def test_activations(lib, act, gated, M):
-    _check(lib, M, 192, 256, act=act, gated=gated, out="f32", seed=11)
+@pytest.mark.parametrize("M,N", [(3, 192), (50, 192), (300, 192), (1300, 2000)])
+def test_activations(lib, act, gated, M, N):
+    _check(lib, M, N, 256, act=act, gated=gated, out="f32", seed=11)
 
 
 @pytest.mark.parametrize("dtype,out,bias", [("bf16", "bf16", "bf16"), ("bf16", "f32", "f32"), ("f16", "f16", "f16"),
                                             ("f16", "f32", "f16"), ("f16", "f16", "f32")])
-@pytest.mark.parametrize("M", [1, 20, 70, 400])
-def test_types(lib, dtype, out, bias, M):
-    _check(lib, M, 320, 384, dtype=dtype, out=out, act="gelu", bias=bias, residual=True, seed=12)
+@pytest.mark.parametrize("M,N", [(1, 320), (20, 320), (70, 320), (400, 320), (1400, 2000)])
+def test_types(lib, dtype, out, bias, M, N):
+    _check(lib, M, N, 384, dtype=dtype, out=out, act="gelu", bias=bias, residual=True, seed=12)
 
 
 @pytest.mark.parametrize("pad,shift,opad", [(8, 0, 8), (0, 1, 0), (3, 0, 1), (1, 8, 3), (8, 4, 4), (24, 16, 16)])
-@pytest.mark.parametrize("M", [2, 24, 90, 600])
+@pytest.mark.parametrize("M,N", [(2, 136), (24, 136), (90, 136), (600, 136), (1100, 2088)])
 @pytest.mark.parametrize("K", [256, 333])
-def test_strides_and_alignment(lib, pad, shift, opad, M, K):
-    _check(lib, M, 136, K, pad=pad, shift=shift, opad=opad, bias="f32", residual=True, seed=13)
+def test_strides_and_alignment(lib, pad, shift, opad, M, N, K):
+    _check(lib, M, N, K, pad=pad, shift=shift, opad=opad, bias="f32", residual=True, seed=13)
 
 
 @pytest.mark.parametrize("M", [1, 30, 77, 260, 1500])

@@ -526,7 +526,7 @@ def dense_linear(x, w, bias=None, act: str = "none", gated: bool = False, residu
     x [M, K], w [N, K] bf16 or f16 (one dtype, any row strides); bias [N] of that dtype or fp32; residual and the
     result [M, N] ([M, N/2] when gated) of out_dtype: x's dtype (default) or fp32.  act is "none", "relu", "silu",
     "gelu" or "gelu_tanh".  out may be given, also as the residual itself; ws is a uint8 workspace of
-    dense_linear_workspace_bytes(M, N, K) bytes for repeated calls (made here when needed)."""
+    dense_linear_workspace_bytes(M, N, K) bytes, used where x or w is not 16-byte aligned (made here when needed)."""
     dev = x.device if isinstance(x, torch.Tensor) else None
     xp, ldx, xd = _mat(x, "x", dev, None, (torch.bfloat16, torch.float16))
     wp, ldw, _ = _mat(w, "w", dev, None, (x.dtype,))
@@ -548,9 +548,8 @@ def dense_linear(x, w, bias=None, act: str = "none", gated: bool = False, residu
     if out is None:
         out = torch.empty((M, n_out), dtype=odt, device=dev)
     op, ldo, od = _mat(out, "out", dev, (M, n_out), (odt,))
-    need = dense_linear_workspace_bytes(M, N, K)
-    if ws is None and need:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    if ws is None and (xp | wp | 2 * ldx | 2 * ldw) % 16:  # operands without 16-byte alignment are copied there
+        ws = torch.empty(dense_linear_workspace_bytes(M, N, K), dtype=torch.uint8, device=dev)
     with torch.cuda.device(dev):
         _check(load().dense_linear(xp, ldx, wp, ldw, xd, bp, 2 if bias is None else _DTYPES[bias.dtype],
                                    _one_of(_ACTS, act, "act"), int(bool(gated)), rp, ldr, op, ldo, od, M, N, K,

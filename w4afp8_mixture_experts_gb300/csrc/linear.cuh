@@ -19,6 +19,11 @@ struct LinearParams {
   int dtype, out_dtype, bias_f32, act, gated;
 };
 
+constexpr int kStreamRows = 16;  // rows of x up to which the weights are streamed through mma.sync
+
+int launch_linear_stream(const LinearParams& p, cudaStream_t st);  // M <= kStreamRows
+int launch_linear_tc(LinearParams p, void* ws, size_t ws_bytes, cudaStream_t st);
+
 __device__ __forceinline__ float activate(float z, int act) {
   switch (act) {
     case W4A8_ACT_RELU: return fmaxf(z, 0.f);

@@ -1,0 +1,828 @@
+// dense_linear on the 5th-generation tensor cores: out = act(x W^T + bias) [* other half] + residual.
+//
+// Two kernels, both fed by TMA (128-byte swizzle, 64 k per stage) with fp32 accumulators in tensor memory:
+//
+//   pair kernel (many rows): a cluster of two CTAs computes a 256 x 256 tile with tcgen05.mma.cta_group::2 (x
+//   rows on M, 128 per CTA; W rows on N, each CTA loads half of them).  Persistent, the accumulator double
+//   buffered over the whole tensor memory, so that the epilogue of one tile runs under the products of the
+//   next.  When gated, one CTA loads 128 gate rows and the other the 128 matching rows of the other half: both
+//   CTAs then hold, for their 128 tokens, the two halves of 128 output columns side by side.
+//
+//   split kernel (few rows, or few tiles): a CTA computes a 128 x BN tile with W rows on M and tokens on N over
+//   one piece of K; the CTAs of a cluster take the pieces of one tile, push their partial products into the
+//   shared memory of the CTA that owns a token, and every owner adds its parts in rank order and finishes its
+//   tokens.  One launch, no workspace, and a result that does not depend on timing.
+//
+// Every wait is bounded: on expiry the CTA raises its abort flag and the device error word, lets its copies and
+// products in flight finish (again with a limit), frees its tensor memory and returns.
+#include "linear.cuh"
+
+namespace w4a8 {
+namespace {
+
+constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s: no legitimate wait comes close
+constexpr int kBK = 64;                         // k per stage: one 128-byte swizzled row of 16-bit values
+constexpr int kATile = 128 * kBK * 2;           // bytes of 128 rows of a stage
+constexpr int kMaxSmem = 227 * 1024;
+
+__device__ unsigned int g_linear_error;
+
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Waits for a phase of `bar`, at most kTimeoutNs; gives up early when another role of the CTA has given up.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t n = 0;; ++n) {
+    if (try_wait_cluster(bar, parity)) return true;
+    if ((n & 127u) == 127u) {
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - t0 > kTimeoutNs) {
+        *abort_flag = 1;
+        atomicOr(&g_linear_error, 1u);
+        return false;
+      }
+    }
+  }
+}
+
+// Waits for an operation in flight after an abort, whatever the abort flag; bit 2 of the error word on expiry.
+__device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
+  if (try_wait_cluster(bar, parity)) return;
+  const uint64_t t0 = globaltimer_ns();
+  while (!try_wait_cluster(bar, parity)) {
+    if (globaltimer_ns() - t0 > kTimeoutNs) {
+      atomicOr(&g_linear_error, 4u);
+      return;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t map_to_cta(uint32_t saddr, uint32_t cta) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(cta));
+  return r;
+}
+__device__ __forceinline__ void remote_arrive(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// shared-memory operand: K-major, 128-byte swizzle, 8-row groups 1024 B apart
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1u) << 16) |
+         (static_cast<uint64_t>(1024u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46) |
+         (static_cast<uint64_t>(2u) << 61);
+}
+// fp32 accumulator, both operands f16 or both bf16, K-major
+__host__ __device__ constexpr uint32_t idesc_f16(bool bf16, uint32_t m, uint32_t n) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+template <int CG>
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// arrives on `bar` of both CTAs of the pair when every product issued so far has completed
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// a box of a matrix into this CTA's shared memory, signalled on a barrier of either CTA of the pair
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* m, uint32_t bar, int32_t x, int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+
+__device__ __forceinline__ void activate_all(float (&v)[32], int act) {
+  switch (act) {  // one branch for the 32 values
+    case W4A8_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = activate(v[i], W4A8_ACT_RELU);
+      break;
+    case W4A8_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = activate(v[i], W4A8_ACT_SILU);
+      break;
+    case W4A8_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = activate(v[i], W4A8_ACT_GELU);
+      break;
+    case W4A8_ACT_GELU_TANH:
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = activate(v[i], W4A8_ACT_GELU_TANH);
+      break;
+    default: break;
+  }
+}
+
+// --- pair kernel ---------------------------------------------------------------------------------------------
+
+constexpr int kPairStages = 6;
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairThreads = 128 + kPairEpiWarps * 32;
+constexpr int kPairStageBytes = 2 * kATile;  // of one CTA: 128 rows of x, 128 rows of W
+constexpr int kStageRow = 17;                // fp32 row of a warp's 32 x 16 transposing block, padded
+constexpr int kPairOffBias = kPairStages * kPairStageBytes;
+constexpr int kPairOffStg = kPairOffBias + kPairEpiWarps * 128 * 4;
+constexpr int kPairOffBar = kPairOffStg + kPairEpiWarps * 32 * kStageRow * 4;
+constexpr int kPairSmem = kPairOffBar + (2 * kPairStages + 5) * 8 + 16 + 1024;
+static_assert(kPairSmem <= kMaxSmem, "shared memory");
+static_assert(kPairOffBar % 8 == 0, "barrier alignment");
+
+struct PairPlan {
+  int tiles_m, tiles_n, tiles, kblocks;
+  int out_cols;  // output columns of a tile: 256, or 128 when gated
+  int vec_out;   // out and residual rows take 16-byte accesses
+};
+
+// Tiles in an order that keeps the rows and columns in flight compact: bands of 8 row blocks, columns in turn.
+__device__ __forceinline__ void pair_tile(const PairPlan& pl, int i, int& tm, int& tn) {
+  constexpr int kBand = 8;
+  const int per_band = kBand * pl.tiles_n;
+  const int band = i / per_band, in = i - band * per_band;
+  const int rows = min(kBand, pl.tiles_m - band * kBand);
+  tn = in / rows;
+  tm = band * kBand + in - tn * rows;
+}
+
+// 32 output columns of this thread's row, from column n on
+__device__ __forceinline__ void store_row32(const LinearParams& p, const PairPlan& pl, float (&v)[32], int m0, int row,
+                                            int n, float* stg) {
+  if (pl.vec_out && n + 32 <= p.n_out) {
+    const int m = m0 + row;
+    if (m >= p.M) return;
+    if (p.out_dtype == W4A8_DTYPE_F32) {
+      float* o = static_cast<float*>(p.out) + m * p.ldo + n;
+      if (p.residual) {
+        const float4* r = reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + m * p.ldr + n);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 a = r[i];
+          v[4 * i] += a.x;
+          v[4 * i + 1] += a.y;
+          v[4 * i + 2] += a.z;
+          v[4 * i + 3] += a.w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        reinterpret_cast<float4*>(o)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      return;
+    }
+    uint16_t* o = static_cast<uint16_t*>(p.out) + m * p.ldo + n;
+    const uint4* r =
+        p.residual ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.residual) + m * p.ldr + n) : nullptr;
+    const bool bf16 = p.out_dtype == W4A8_DTYPE_BF16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[4];
+      if (r) {
+        const uint4 a = r[i];
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 f;
+          if (bf16) {
+            f = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+          } else {
+            f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+          }
+          v[8 * i + 2 * j] += f.x;
+          v[8 * i + 2 * j + 1] += f.y;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (bf16) {
+          w[j] = bf16x2_bits(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+        } else {
+          const __half2 h = __floats2half2_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+          w[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      reinterpret_cast<uint4*>(o)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return;
+  }
+  // rows without alignment, or a tile's last columns: 16 columns at a time through shared memory, so that the
+  // lanes of a warp touch neighbouring columns of two rows instead of 32 rows
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) stg[lane * kStageRow + i] = v[16 * h + i];
+    __syncwarp();
+    const int c = n + 16 * h + (lane & 15);
+    if (c < p.n_out) {
+#pragma unroll 4
+      for (int i = lane >> 4; i < 32; i += 2) {
+        const int m = m0 + i;
+        if (m >= p.M) break;
+        float a = stg[i * kStageRow + (lane & 15)];
+        if (p.residual) a += load_any(p.residual, m * p.ldr + c, p.out_dtype);
+        store_any(p.out, m * p.ldo + c, a, p.out_dtype);
+      }
+    }
+  }
+}
+
+template <bool GATED>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw,
+                       const LinearParams p, const PairPlan pl) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairOffBar);  // the first CTA's count for both
+  uint64_t* empty = full + kPairStages;
+  uint64_t* tfull = empty + kPairStages;  // [2] accumulator ready, in both CTAs
+  uint64_t* tempty = tfull + 2;           // [2] accumulator read by both CTAs (the first CTA's)
+  uint64_t* mdrain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  pdl_trigger();
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tx);
+    tma_prefetch_desc(&tw);
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 2 * kPairEpiWarps);
+    }
+    mbar_init(mdrain, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();
+  cluster_wait();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+
+  const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+  if (warp == 0) {
+    if (lane == 0) {  // TMA producer of this CTA's half of every stage
+      uint32_t it = 0;
+      for (int i = first; i < pl.tiles; i += stride) {
+        int tm, tn;
+        pair_tile(pl, i, tm, tn);
+        const int m = tm * 256 + rank * 128;
+        const int n = GATED ? rank * p.n_out + tn * 128 : tn * 256 + rank * 128;
+        for (int kb = 0; kb < pl.kblocks; ++kb, ++it) {
+          const int s = it % kPairStages;
+          if (!wait_bar(&empty[s], ((it / kPairStages) & 1) ^ 1, abort_flag)) goto stop;
+          uint8_t* at = smem + s * kPairStageBytes;
+          const uint32_t bar = map_to_cta(smem_u32(&full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStageBytes);
+          tma_load_pair(at, &tx, bar, kb * kBK, m);
+          tma_load_pair(at + kATile, &tw, bar, kb * kBK, n);
+        }
+      }
+    stop:
+      // the last stages' slots are released before the CTA may go (and, after an abort, their loads have landed)
+      const uint32_t n = it < kPairStages ? it : kPairStages;
+      for (uint32_t j = it - n; j < it; ++j) {
+        const uint32_t s = j % kPairStages, ph = (j / kPairStages) & 1;
+        if ((*abort_flag || !wait_bar(&empty[s], ph, abort_flag)) && rank == 0) drain_bar(&full[s], ph);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {  // the pair's products
+      const uint32_t idesc = idesc_f16(p.dtype == W4A8_DTYPE_BF16, 256, 256);
+      uint32_t it = 0;
+      int n = 0;
+      for (int i = first; i < pl.tiles; i += stride, ++n) {
+        const int buf = n & 1;
+        if (!wait_bar(&tempty[buf], ((n >> 1) & 1) ^ 1, abort_flag)) break;
+        tc_fence_after();
+        bool ok = true;
+        for (int kb = 0; kb < pl.kblocks; ++kb, ++it) {
+          const int s = it % kPairStages;
+          if (!(ok = wait_bar(&full[s], (it / kPairStages) & 1, abort_flag))) break;
+          tc_fence_after();
+          const uint32_t at = smem_u32(smem + s * kPairStageBytes);
+          const uint64_t a = operand_desc(at), b = operand_desc(at + kATile);
+#pragma unroll
+          for (int k = 0; k < kBK / 16; ++k) mma_f16<2>(tmem + buf * 256, a + 2 * k, b + 2 * k, idesc, kb > 0 || k > 0);
+          commit_pair(&empty[s]);
+        }
+        if (!ok) break;
+        commit_pair(&tfull[buf]);
+      }
+      if (*abort_flag) {
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(mdrain))
+                     : "memory");
+        drain_bar(mdrain, 0);
+      }
+    }
+  } else if (warp >= 4) {  // epilogue: warp e reads lane quarter e % 4, columns by e / 4
+    const int e = warp - 4, quarter = warp & 3, half = e >> 2;
+    float* bias = reinterpret_cast<float*>(smem + kPairOffBias) + e * 128;
+    float* stg = reinterpret_cast<float*>(smem + kPairOffStg) + e * 32 * kStageRow;
+    const uint32_t tempty0 = map_to_cta(smem_u32(tempty), 0);
+    const int bd = p.bias_f32 ? W4A8_DTYPE_F32 : p.dtype;
+    constexpr int kCols = GATED ? 64 : 128;  // output columns of this warp
+    int n = 0;
+    for (int i = first; i < pl.tiles; i += stride, ++n) {
+      int tm, tn;
+      pair_tile(pl, i, tm, tn);
+      const int buf = n & 1;
+      const int n0 = tn * pl.out_cols + half * kCols;
+      const int m0 = tm * 256 + rank * 128 + quarter * 32;
+      if (p.bias) {  // [0, 64) gate, [64, 128) other half when gated
+        __syncwarp();
+        for (int c = lane; c < 128; c += 32) {
+          const int col = n0 + (GATED ? c & 63 : c);
+          bias[c] = col < p.n_out ? load_any(p.bias, col + (GATED && c >= 64 ? p.n_out : 0), bd) : 0.f;
+        }
+        __syncwarp();
+      }
+      if (__any_sync(0xffffffffu, !wait_bar(&tfull[buf], (n >> 1) & 1, abort_flag))) break;
+      tc_fence_after();
+      const uint32_t at = tmem + buf * 256 + (static_cast<uint32_t>(quarter * 32) << 16) + half * kCols;
+#pragma unroll 1
+      for (int c = 0; c < kCols; c += 32) {
+        float v[32], u[32];
+        __syncwarp();
+        tmem_ld32(at + c, reinterpret_cast<uint32_t*>(v));
+        if (GATED) tmem_ld32(at + 128 + c, reinterpret_cast<uint32_t*>(u));
+        tmem_wait_ld_pin<32>(reinterpret_cast<uint32_t*>(v));
+        if (GATED) tmem_wait_ld_pin<32>(reinterpret_cast<uint32_t*>(u));
+        if (c + 32 == kCols) {  // every value is in registers: the accumulator is free
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) remote_arrive(tempty0 + buf * 8);
+        }
+        if (n0 + c >= p.n_out) continue;
+        if (p.bias) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 b = *reinterpret_cast<const float4*>(bias + c + 4 * j);
+            v[4 * j] += b.x;
+            v[4 * j + 1] += b.y;
+            v[4 * j + 2] += b.z;
+            v[4 * j + 3] += b.w;
+          }
+        }
+        activate_all(v, p.act);
+        if (GATED) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] *= p.bias ? u[j] + bias[64 + c + j] : u[j];
+        }
+        store_row32(p, pl, v, m0, lane, n0 + c, stg);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_arrive();  // no CTA leaves while the other may still signal it or read its operands
+  cluster_wait();
+  if (warp == 2) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+// --- split kernel --------------------------------------------------------------------------------------------
+
+constexpr int kSplitThreads = 256;
+
+template <int BN>
+struct SplitCfg {
+  static constexpr int kStageBytes = kATile + BN * kBK * 2;
+  static constexpr int kStages = BN == 128 ? 4 : BN == 64 ? 6 : 7;
+  static constexpr int kOffRed = kStages * kStageBytes;       // [source CTA][token of mine][128 W rows] fp32
+  static constexpr int kOffBar = kOffRed + BN * 128 * 4;
+  static constexpr int kSmem = kOffBar + (2 * kStages + 2) * 8 + 16 + 1024;
+  static constexpr uint32_t kTmemCols = BN;
+  static_assert(kSmem <= kMaxSmem, "shared memory");
+};
+
+template <int BN, bool GATED>
+__global__ void __launch_bounds__(kSplitThreads, 1)
+    linear_split_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw,
+                        const LinearParams p, int splits, int kblocks, int vec_out) {
+  using C = SplitCfg<BN>;
+  constexpr int kOutCols = GATED ? 64 : 128;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* done = empty + C::kStages;
+  uint64_t* mdrain = done + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = splits > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int n0 = (blockIdx.x / splits) * kOutCols, m0 = blockIdx.y * BN;
+  pdl_trigger();
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tx);
+    tma_prefetch_desc(&tw);
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(done, 1);
+    mbar_init(mdrain, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (splits > 1) cluster_arrive();  // matched before the first remote store
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+
+  const int kb0 = static_cast<int>(static_cast<int64_t>(rank) * kblocks / splits);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * kblocks / splits);
+  int issued = 0;  // stages whose loads this thread has issued
+  if (warp == 0 && lane == 0) {
+    int& it = issued;
+    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+      const int s = it % C::kStages;
+      if (!wait_bar(&empty[s], ((it / C::kStages) & 1) ^ 1, abort_flag)) break;
+      uint8_t* at = smem + s * C::kStageBytes;
+      mbar_arrive_expect_tx(&full[s], C::kStageBytes);
+      if (GATED) {
+        tma_load_2d(at, &tw, &full[s], kb * kBK, n0);
+        tma_load_2d(at + kATile / 2, &tw, &full[s], kb * kBK, p.n_out + n0);
+      } else {
+        tma_load_2d(at, &tw, &full[s], kb * kBK, n0);
+      }
+      tma_load_2d(at + kATile, &tx, &full[s], kb * kBK, m0);
+    }
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_f16(p.dtype == W4A8_DTYPE_BF16, 128, BN);
+    int it = 0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+      const int s = it % C::kStages;
+      if (!(ok = wait_bar(&full[s], (it / C::kStages) & 1, abort_flag))) break;
+      tc_fence_after();
+      const uint32_t at = smem_u32(smem + s * C::kStageBytes);
+      const uint64_t a = operand_desc(at), b = operand_desc(at + kATile);
+#pragma unroll
+      for (int k = 0; k < kBK / 16; ++k) mma_f16<1>(tmem, a + 2 * k, b + 2 * k, idesc, it > 0 || k > 0);
+      mma_commit(&empty[s]);
+    }
+    if (ok) {
+      mma_commit(done);
+    } else {
+      mma_commit(mdrain);
+      drain_bar(mdrain, 0);
+    }
+  }
+  __syncwarp();
+  const bool ok = !__any_sync(0xffffffffu, !wait_bar(done, 0, abort_flag));
+  if (!ok)
+    for (int j = issued < C::kStages ? 0 : issued - C::kStages; j < issued; ++j)
+      drain_bar(&full[j % C::kStages], (j / C::kStages) & 1);
+  __syncwarp();
+  tc_fence_after();
+  if (splits > 1) cluster_wait();
+  // this CTA's partial products to the owners of their tokens: warp w reads lane quarter w % 4 (W rows), half
+  // w / 4 of the tokens
+  const int own = BN / splits;  // tokens of an owner
+  const int quarter = warp & 3, f = quarter * 32 + lane;
+  if (ok) {
+    constexpr int kCols = BN / 2;
+    constexpr int kStep = kCols < 32 ? kCols : 32;
+    const uint32_t red = smem_u32(smem + C::kOffRed);
+#pragma unroll 1
+    for (int c = (warp >> 2) * kCols; c < (warp >> 2) * kCols + kCols; c += kStep) {
+      float v[kStep];
+      if constexpr (kStep == 32)
+        tmem_ld32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c, reinterpret_cast<uint32_t*>(v));
+      else
+        tmem_ld16(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c, reinterpret_cast<uint32_t*>(v));
+      tmem_wait_ld_pin<kStep>(reinterpret_cast<uint32_t*>(v));
+#pragma unroll
+      for (int j = 0; j < kStep; ++j) {
+        const int q = (c + j) / own, tok = (c + j) - q * own;
+        const uint32_t to = red + ((rank * own + tok) * 128 + f) * 4;
+        if (splits > 1)
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_to_cta(to, q)), "f"(v[j]) : "memory");
+        else
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(v[j]) : "memory");
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (splits > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+  if (!ok) return;
+  // 8 output columns of one of this CTA's tokens per thread and turn
+  const float* red = reinterpret_cast<const float*>(smem + C::kOffRed);
+  const int bd = p.bias_f32 ? W4A8_DTYPE_F32 : p.dtype;
+  for (int i = threadIdx.x; i < own * (kOutCols / 8); i += kSplitThreads) {
+    const int tok = i / (kOutCols / 8), col = i % (kOutCols / 8) * 8;
+    const int m = m0 + rank * own + tok, n = n0 + col;
+    if (m >= p.M || n >= p.n_out) continue;
+    float v[8], u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.f;
+    for (int s = 0; s < splits; ++s) {
+      const float* src = red + (s * own + tok) * 128 + col;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] += src[j];
+        if (GATED) u[j] += src[64 + j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool in = n + j < p.n_out;
+      if (p.bias && in) v[j] += load_any(p.bias, n + j, bd);
+      v[j] = activate(v[j], p.act);
+      if (GATED) v[j] *= p.bias && in ? u[j] + load_any(p.bias, p.n_out + n + j, bd) : u[j];
+    }
+    if (vec_out && n + 8 <= p.n_out) {
+      if (p.out_dtype == W4A8_DTYPE_F32) {
+        float* o = static_cast<float*>(p.out) + m * p.ldo + n;
+        if (p.residual) {
+          const float* r = static_cast<const float*>(p.residual) + m * p.ldr + n;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] += r[j];
+        }
+        reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        if (p.residual) {
+          const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.residual) + m * p.ldr + n);
+          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 r = p.out_dtype == W4A8_DTYPE_BF16
+                                 ? make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u))
+                                 : __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+            v[2 * j] += r.x;
+            v[2 * j + 1] += r.y;
+          }
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (p.out_dtype == W4A8_DTYPE_BF16) {
+            w[j] = bf16x2_bits(v[2 * j], v[2 * j + 1]);
+          } else {
+            const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + m * p.ldo + n) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (n + j >= p.n_out) break;
+        if (p.residual) v[j] += load_any(p.residual, m * p.ldr + n + j, p.out_dtype);
+        store_any(p.out, m * p.ldo + n + j, v[j], p.out_dtype);
+      }
+    }
+  }
+}
+
+// --- operands without 16-byte alignment ------------------------------------------------------------------------
+
+// Rows of x and w to 16-byte-aligned rows of the workspace (zeros past K), 8 elements per thread.
+__global__ void __launch_bounds__(256) linear_repack_kernel(const uint16_t* x, int64_t ldx, int64_t items_x, uint16_t* px,
+                                                            const uint16_t* w, int64_t ldw, int64_t items, uint16_t* pw,
+                                                            int K, int k8) {
+  pdl_trigger();
+  pdl_wait();
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < items; i += gridDim.x * 256ll) {
+    const bool is_x = i < items_x;
+    const int64_t j = is_x ? i : i - items_x;
+    const int64_t row = j / k8;
+    const int k = static_cast<int>(j - row * k8) * 8;
+    const uint16_t* src = (is_x ? x + row * ldx : w + row * ldw) + k;
+    uint32_t v[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t lo = k + 2 * c < K ? src[2 * c] : 0, hi = k + 2 * c + 1 < K ? src[2 * c + 1] : 0;
+      v[c] = lo | (hi << 16);
+    }
+    reinterpret_cast<uint4*>(is_x ? px : pw)[j] = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// --- host side -----------------------------------------------------------------------------------------------
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static EncodeFn fn = [] {
+    void* q = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      q = nullptr;
+    return reinterpret_cast<EncodeFn>(q);
+  }();
+  return fn;
+}
+
+// rows x K 16-bit matrix, boxes of box_rows x 64 k (zeros outside), 128-byte swizzle
+int row_map(CUtensorMap* m, const void* base, int dtype, int64_t rows, int64_t K, int64_t ld, int box_rows,
+            const char* name) {
+  EncodeFn fn = encode_fn();
+  if (!fn) return set_error(W4A8_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {kBK, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r =
+      fn(m, dtype == W4A8_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return set_error(W4A8_ERR_INVALID_ARG, "tensor map for %s rejected (CUresult %d)", name, static_cast<int>(r));
+  return W4A8_OK;
+}
+
+int read_linear_error() {
+  unsigned int v = 0;
+  cudaMemcpyFromSymbol(&v, g_linear_error, sizeof(v));
+  const unsigned int zero = 0;
+  cudaMemcpyToSymbol(g_linear_error, &zero, sizeof(zero));
+  return static_cast<int>(v);
+}
+
+struct Registrar {
+  Registrar() { register_device_error_reader(&read_linear_error); }
+} registrar;
+
+bool vec_rows(const LinearParams& p) {
+  const int64_t size = static_cast<int64_t>(dtype_size(p.out_dtype));
+  return aligned16(p.out) && p.ldo * size % 16 == 0 &&
+         (!p.residual || (aligned16(p.residual) && p.ldr * size % 16 == 0));
+}
+
+template <class... KArgs, class... Args>
+int launch_cluster(const char* what, void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, int cluster,
+                   cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  lc.gridDim = grid;
+  lc.blockDim = dim3(threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = st;
+  lc.attrs = attr;
+  lc.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&lc, kern, static_cast<KArgs>(args)...);
+  if (e != cudaSuccess) return set_error(W4A8_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  return check_launch(what);
+}
+
+template <bool GATED>
+int launch_pair(const LinearParams& p, cudaStream_t st) {
+  static DeviceOnce attrs;
+  auto kern = linear_pair_kernel<GATED>;
+  if (int rc = attrs.run([&] {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem) != cudaSuccess)
+          return check_launch("cudaFuncSetAttribute(linear_pair)");
+        return static_cast<int>(W4A8_OK);
+      }))
+    return rc;
+  CUtensorMap tx, tw;
+  int rc;
+  if ((rc = row_map(&tx, p.x, p.dtype, p.M, p.K, p.ldx, 128, "x"))) return rc;
+  if ((rc = row_map(&tw, p.w, p.dtype, p.N, p.K, p.ldw, 128, "w"))) return rc;
+  PairPlan pl;
+  pl.out_cols = GATED ? 128 : 256;
+  pl.tiles_m = static_cast<int>(ceil_div(p.M, 256));
+  pl.tiles_n = static_cast<int>(ceil_div(p.n_out, pl.out_cols));
+  const int64_t tiles = static_cast<int64_t>(pl.tiles_m) * pl.tiles_n;
+  pl.tiles = static_cast<int>(tiles);
+  pl.kblocks = static_cast<int>(ceil_div(p.K, kBK));
+  pl.vec_out = vec_rows(p);
+  const int64_t pairs = tiles < num_sms() / 2 ? tiles : num_sms() / 2;
+  return launch_cluster("linear_pair_kernel", kern, dim3(static_cast<unsigned>(2 * pairs)), kPairThreads, kPairSmem, 1,
+                        st, tx, tw, p, pl);
+}
+
+template <int BN, bool GATED>
+int launch_split(const LinearParams& p, int splits, cudaStream_t st) {
+  using C = SplitCfg<BN>;
+  static DeviceOnce attrs;
+  auto kern = linear_split_kernel<BN, GATED>;
+  if (int rc = attrs.run([&] {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+          return check_launch("cudaFuncSetAttribute(linear_split)");
+        return static_cast<int>(W4A8_OK);
+      }))
+    return rc;
+  CUtensorMap tx, tw;
+  int rc;
+  if ((rc = row_map(&tx, p.x, p.dtype, p.M, p.K, p.ldx, BN, "x"))) return rc;
+  if ((rc = row_map(&tw, p.w, p.dtype, p.N, p.K, p.ldw, GATED ? 64 : 128, "w"))) return rc;
+  const int64_t nb = ceil_div(p.n_out, GATED ? 64 : 128), mb = ceil_div(p.M, BN);
+  return launch_cluster("linear_split_kernel", kern, dim3(static_cast<unsigned>(nb * splits), static_cast<unsigned>(mb)),
+                        kSplitThreads, C::kSmem, splits, st, tx, tw, p, splits, static_cast<int>(ceil_div(p.K, kBK)),
+                        static_cast<int>(vec_rows(p)));
+}
+
+template <int BN>
+int launch_split_bn(const LinearParams& p, int splits, cudaStream_t st) {
+  return p.gated ? launch_split<BN, true>(p, splits, st) : launch_split<BN, false>(p, splits, st);
+}
+
+}  // namespace
+
+int launch_linear_tc(LinearParams p, void* ws, size_t ws_bytes, cudaStream_t st) {
+  if (!(aligned16(p.x) && aligned16(p.w) && p.ldx % 8 == 0 && p.ldw % 8 == 0)) {
+    const int64_t k8 = ceil_div(p.K, 8);
+    const size_t need = static_cast<size_t>(p.M + static_cast<int64_t>(p.N)) * k8 * 16;
+    W4A8_REQUIRE(ws && ws_bytes >= need && aligned16(ws),
+                 "x and w without 16-byte alignment need %zu bytes of 16-byte aligned workspace", need);
+    uint16_t* px = static_cast<uint16_t*>(ws);
+    uint16_t* pw = px + p.M * k8 * 8;
+    const int64_t items = (p.M + static_cast<int64_t>(p.N)) * k8;
+    const int64_t blocks = ceil_div(items, 256);
+    if (int rc = launch_pdl("linear_repack_kernel", linear_repack_kernel,
+                            dim3(static_cast<unsigned>(blocks < 32 * num_sms() ? blocks : 32 * num_sms())), dim3(256), 0,
+                            st, static_cast<const uint16_t*>(p.x), p.ldx, p.M * k8, px,
+                            static_cast<const uint16_t*>(p.w), p.ldw, items, pw, p.K, static_cast<int>(k8)))
+      return rc;
+    p.x = px;
+    p.w = pw;
+    p.ldx = p.ldw = k8 * 8;
+  }
+  const int sms = num_sms();
+  const int64_t big = ceil_div(p.M, 256) * ceil_div(p.n_out, p.gated ? 128 : 256);
+  if (big >= sms / 4) return p.gated ? launch_pair<true>(p, st) : launch_pair<false>(p, st);
+  const int bn = p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+  const int64_t tiles = ceil_div(p.M, bn) * ceil_div(p.n_out, p.gated ? 64 : 128), kb = ceil_div(p.K, kBK);
+  int splits = 1;
+  while (splits < 8 && tiles * splits * 2 <= sms && kb >= 8 * splits) splits *= 2;
+  if (bn == 32) return launch_split_bn<32>(p, splits, st);
+  if (bn == 64) return launch_split_bn<64>(p, splits, st);
+  return launch_split_bn<128>(p, splits, st);
+}
+
+}  // namespace w4a8
