@@ -46,7 +46,8 @@ def _check(lib, M, N, K, dtype="bf16", out="bf16", act="none", gated=False, bias
 SIZES = [(1, 1, 1), (1, 256, 1024), (1, 33, 77), (3, 17, 64), (8, 128, 4096), (9, 40, 513), (16, 512, 2048),
          (17, 16, 96), (33, 200, 1000), (64, 256, 1536), (65, 130, 320), (100, 72, 64), (128, 384, 512),
          (129, 257, 130), (255, 64, 1024), (256, 512, 256), (300, 300, 300), (513, 1000, 200), (1025, 48, 2056),
-         (2304, 1288, 320), (2305, 1283, 130), (4100, 700, 72), (520, 9000, 64)]
+         (2304, 1288, 320), (2305, 1283, 130), (4100, 700, 72), (520, 9000, 64),
+         (700, 260, 640), (390, 1032, 1300), (8192, 40, 1088)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -66,6 +67,40 @@ def test_whole_numbers_are_exact(lib, M, N, K, dtype):
     got = lib.dense_linear(x, w, out_dtype=torch.float32)
     want = x.cpu().double() @ w.cpu().double().t()
     assert torch.equal(got.cpu().double(), want)
+
+
+CONFIGS = [(256, 1), (256, 2), (256, 4), (128, 1), (128, 2), (128, 4), (64, 1), (64, 2), (64, 4), (64, 8), (32, 1),
+           (32, 2), (32, 4), (32, 8)]
+
+
+@pytest.fixture
+def config(lib, request):
+    clib = lib.load()
+    assert clib.w4a8_test_linear_config(*request.param) == 0
+    yield request.param
+    clib.w4a8_test_linear_config(0, 0)
+
+
+@pytest.mark.parametrize("config", CONFIGS, indirect=True)
+@pytest.mark.parametrize("M,N,K", [(17, 130, 520), (96, 264, 1100), (300, 520, 832), (1000, 1288, 640)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_every_configuration(lib, config, M, N, K, gated):
+    g = torch.Generator("cuda").manual_seed(M)
+    x, w = _mat(M, K, "bf16", g, ints=True), _mat(N, K, "bf16", g, ints=True)
+    got = lib.dense_linear(x, w, out_dtype=torch.float32)
+    assert torch.equal(got.cpu().double(), x.cpu().double() @ w.cpu().double().t())
+    _check(lib, M, N, K, gated=gated, act="silu" if gated else "gelu", bias="f32", residual=True, seed=N)
+    _check(lib, M, N, K, gated=gated, act="relu", out="f32", residual=True, opad=1, seed=N)
+
+
+def test_configuration_that_does_not_exist(lib):
+    x = torch.zeros((64, 64), dtype=torch.bfloat16, device="cuda")
+    lib.load().w4a8_test_linear_config(96, 1)
+    try:
+        with pytest.raises(lib.W4A8Error, match="no configuration"):
+            lib.dense_linear(x, x)
+    finally:
+        lib.load().w4a8_test_linear_config(0, 0)
 
 
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])

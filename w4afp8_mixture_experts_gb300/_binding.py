@@ -8,11 +8,12 @@ built library every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
 
-from .build import LIB
+from .build import EXT, LIB
 
 _c_i64 = ctypes.c_int64
 _c_int = ctypes.c_int
@@ -68,6 +69,7 @@ _SIGS = {
     "dense_linear": (_c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_int, _c_vp, _c_int, _c_int, _c_int, _c_vp, _c_i64,
                               _c_vp, _c_i64, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_sz, _c_vp]),
     "dense_linear_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64]),
+    "w4a8_test_linear_config": (_c_int, [_c_int, _c_int]),
 }
 
 
@@ -400,49 +402,29 @@ def w4a8_moe_forward_noalloc(x, logits, k: int, w13, w13_s, w2, w2_s, out, renor
 
 
 # --- operators around the routed experts -----------------------------------------------------------------------
+# Their tensors are marshalled by the extension beside the library (csrc/torch_ops.cpp): the checks, the output
+# tensors and the stream lookup cost several times the smallest device times when done here.
 
-_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _NORMS = {"none": 0, "rms": 1, "layer": 2}
 _ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
-
-def _mat(t, name, dev, shape=None, dtypes=(torch.bfloat16, torch.float16, torch.float32)):
-    """Checks a CUDA matrix whose rows are contiguous (any row stride); returns (pointer, row stride, dtype id)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dimensions")
-    rows, cols = t.shape
-    if shape is not None and (rows, cols) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {(rows, cols)}")
-    rs, cs = t.stride()
-    if cs != 1 and cols > 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    if rows > 1 and rs < cols:
-        raise ValueError(f"{name} has overlapping rows (row stride {rs}, {cols} columns)")
-    return t.data_ptr(), max(rs, cols, 1), _DTYPES[t.dtype]
+_ops = None
 
 
-def _vec(t, name, dev, n, dtypes):
-    """Checks a contiguous CUDA vector of n elements (None passes); returns its pointer or None."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+def _load_ops():
+    """The extension module (once), after the library.  Raises if it has not been built."""
+    global _ops
+    if _ops is None:
+        load()
+        if not os.path.exists(EXT):
+            raise RuntimeError(f"{EXT} is missing: build it with w4afp8_mixture_experts_gb300.build.build()")
+        spec = importlib.util.spec_from_file_location("w4a8_torch_ops", EXT)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.init(_check)
+        _ops = mod
+    return _ops
 
 
 def _one_of(table, value, name):
@@ -457,17 +439,8 @@ def moe_route_grouped_topk(logits, k: int, bias=None, score: str = "sigmoid", n_
     """Grouped routing.  logits [T, E] fp32, bf16 or f16 (any row stride), bias fp32 [E] or None (choice only) ->
     (ids int32 [T, k], weights fp32 [T, k]).  A logit of -inf (or its type's lowest value, or NaN) takes its expert
     out; see moe_route_grouped_topk in include/w4a8moe.h for the rules."""
-    dev = logits.device if isinstance(logits, torch.Tensor) else None
-    lp, ld, ldt = _mat(logits, "logits", dev)
-    T, E = logits.shape
-    bp = _vec(bias, "bias", dev, E, (torch.float32,))
-    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-    w = torch.empty((T, k), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        _check(load().moe_route_grouped_topk(lp, ldt, ld, T, E, k, _one_of(_SCORES, score, "score"), bp, n_group,
-                                             topk_group, group_top, int(bool(renormalize)), scale, ids.data_ptr(),
-                                             w.data_ptr(), _stream(dev)))
-    return ids, w
+    return (_ops or _load_ops()).route(logits, k, bias, _one_of(_SCORES, score, "score"), n_group, topk_group,
+                                       group_top, renormalize, scale)
 
 
 def block_norm(f, residual=None, *, post: str = "none", w_post=None, b_post=None, gate=None, branch_scale: float = 1.0,
@@ -480,43 +453,9 @@ def block_norm(f, residual=None, *, post: str = "none", w_post=None, b_post=None
     default f's); gate [1 or B or T, H or 1] of f's dtype or fp32, B dividing T; w_*, b_* [H], all of f's dtype or all
     fp32.  post and pre are "none", "rms" or "layer".  Returns (h, y); h or y may be given as outputs (h may be
     residual and y may be f itself), and is None where want_h or want_y is false."""
-    dev = f.device if isinstance(f, torch.Tensor) else None
-    fp, ldf, fd = _mat(f, "f", dev)
-    T, H = f.shape
-    either = (f.dtype, torch.float32)
-    rp, ldr = None, 0
-    rdt = residual_dtype or f.dtype
-    if residual is not None:
-        rp, ldr, _ = _mat(residual, "residual", dev, (T, H), either)
-        if residual_dtype not in (None, residual.dtype):
-            raise ValueError(f"residual_dtype {residual_dtype} differs from the residual's {residual.dtype}")
-        rdt = residual.dtype
-    elif rdt not in either:
-        raise TypeError(f"residual_dtype must be one of {either}, got {rdt}")
-    params = [t for t in (w_post, b_post, w_pre, b_pre) if t is not None]
-    pdt = params[0].dtype if params else torch.float32
-    pts = [_vec(t, n, dev, H, either) for t, n in ((w_post, "w_post"), (b_post, "b_post"), (w_pre, "w_pre"),
-                                                   (b_pre, "b_pre"))]
-    if any(t.dtype != pdt for t in params):
-        raise TypeError("w_post, b_post, w_pre and b_pre must have one dtype")
-    gp, ldg, gr, gc, gd = None, 0, 1, 1, 2
-    if gate is not None:
-        gp, ldg, gd = _mat(gate, "gate", dev, None, either)
-        gr, gc = gate.shape
-    hp, ldh, yp, ldy = None, 0, None, 0
-    if want_h:
-        if h is None:
-            h = torch.empty((T, H), dtype=rdt, device=dev)
-        hp, ldh, _ = _mat(h, "h", dev, (T, H), (rdt,))
-    if want_y:
-        if y is None:
-            y = torch.empty((T, H), dtype=f.dtype, device=dev)
-        yp, ldy, _ = _mat(y, "y", dev, (T, H), (f.dtype,))
-    with torch.cuda.device(dev):
-        _check(load().block_norm(fp, ldf, fd, rp, ldr, _DTYPES[rdt], _one_of(_NORMS, post, "post"), pts[0], pts[1], gp,
-                                 ldg, gr, gc, gd, branch_scale, residual_scale, _one_of(_NORMS, pre, "pre"), pts[2],
-                                 pts[3], _DTYPES[pdt], eps, T, H, hp, ldh, yp, ldy, _stream(dev)))
-    return (h if want_h else None), (y if want_y else None)
+    return (_ops or _load_ops()).norm(f, residual, _one_of(_NORMS, post, "post"), w_post, b_post, gate, branch_scale,
+                                      residual_scale, _one_of(_NORMS, pre, "pre"), w_pre, b_pre, eps, residual_dtype,
+                                      want_h, want_y, h, y)
 
 
 def dense_linear(x, w, bias=None, act: str = "none", gated: bool = False, residual=None, out_dtype=None, out=None,
@@ -527,38 +466,11 @@ def dense_linear(x, w, bias=None, act: str = "none", gated: bool = False, residu
     result [M, N] ([M, N/2] when gated) of out_dtype: x's dtype (default) or fp32.  act is "none", "relu", "silu",
     "gelu" or "gelu_tanh".  out may be given, also as the residual itself; ws is a uint8 workspace of
     dense_linear_workspace_bytes(M, N, K) bytes, used where x or w is not 16-byte aligned (made here when needed)."""
-    dev = x.device if isinstance(x, torch.Tensor) else None
-    xp, ldx, xd = _mat(x, "x", dev, None, (torch.bfloat16, torch.float16))
-    wp, ldw, _ = _mat(w, "w", dev, None, (x.dtype,))
-    M, K = x.shape
-    N = w.shape[0]
-    if w.shape[1] != K:
-        raise ValueError(f"w must have {K} columns, got {w.shape[1]}")
-    if gated and N % 2:
-        raise ValueError(f"w must have an even number of rows when gated, got {N}")
-    either = (x.dtype, torch.float32)
-    odt = out_dtype or x.dtype
-    if odt not in either:
-        raise TypeError(f"out_dtype must be one of {either}, got {odt}")
-    n_out = N // 2 if gated else N
-    bp = _vec(bias, "bias", dev, N, either)
-    rp, ldr = None, 0
-    if residual is not None:
-        rp, ldr, _ = _mat(residual, "residual", dev, (M, n_out), (odt,))
-    if out is None:
-        out = torch.empty((M, n_out), dtype=odt, device=dev)
-    op, ldo, od = _mat(out, "out", dev, (M, n_out), (odt,))
-    if ws is None and (xp | wp | 2 * ldx | 2 * ldw) % 16:  # operands without 16-byte alignment are copied there
-        ws = torch.empty(dense_linear_workspace_bytes(M, N, K), dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        _check(load().dense_linear(xp, ldx, wp, ldw, xd, bp, 2 if bias is None else _DTYPES[bias.dtype],
-                                   _one_of(_ACTS, act, "act"), int(bool(gated)), rp, ldr, op, ldo, od, M, N, K,
-                                   None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                                   _stream(dev)))
-    return out
+    return (_ops or _load_ops()).linear(x, w, bias, _one_of(_ACTS, act, "act"), gated, residual, out_dtype, out, ws)
 
 
 def dense_linear_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Workspace of dense_linear where x or w is not 16-byte aligned (0: none)."""
     return int(load().dense_linear_workspace_bytes(M, N, K))
 
 

@@ -1,7 +1,9 @@
-"""Builds libw4a8moe.so (the CUDA library) in-tree with nvcc for sm_103a.
+"""Builds libw4a8moe.so (the CUDA library) in-tree with nvcc for sm_103a, and the Python extension beside it.
 
 Translation units are compiled in parallel and linked with the static CUDA
-runtime; the result lands in w4afp8_mixture_experts_gb300/_lib/.
+runtime; the results land in w4afp8_mixture_experts_gb300/_lib/.  The extension
+(w4a8_torch_ops) marshals the tensors of the operators around the routed experts;
+it links to the library and holds no device code.
 """
 from __future__ import annotations
 
@@ -10,12 +12,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libw4a8moe.so")
+EXT = os.path.join(LIBDIR, "w4a8_torch_ops.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
                 "-diag-suppress", "177"]
@@ -56,10 +60,49 @@ def build_shared(srcs, out, deps, extra=(), jobs=None) -> str:
     return out
 
 
+def _torch_paths():
+    """(root of the installed torch, its C++ ABI flag), read without importing it where that is not needed."""
+    import torch
+    return os.path.dirname(torch.__file__), int(torch._C._GLIBCXX_USE_CXX11_ABI)
+
+
+def _compile_torch_ops() -> str:
+    """The object of the Python extension (host code only; the toolkit's headers come from nvcc's own root)."""
+    src, obj = os.path.join(CSRC, "torch_ops.cpp"), os.path.join(LIBDIR, "torch_ops.o")
+    deps = [src] + glob.glob(os.path.join(ROOT, "include", "*.h"))
+    if os.path.exists(obj) and os.path.getmtime(obj) >= _newest(deps):
+        return obj
+    os.makedirs(LIBDIR, exist_ok=True)
+    root, abi = _torch_paths()
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+           "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"), "-isystem",
+           os.path.join(root, "include", "torch", "csrc", "api", "include"), "-isystem", cuda, "-c", src, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_torch_ops(obj: str) -> str:
+    if not (os.path.exists(EXT) and os.path.getmtime(EXT) >= max(os.path.getmtime(obj), os.path.getmtime(LIB))):
+        lib = os.path.join(_torch_paths()[0], "lib")
+        cmd = ["g++", "-shared", "-o", EXT, obj, "-L" + LIBDIR, "-lw4a8moe", "-L" + lib, "-lc10", "-lc10_cuda",
+               "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    return EXT
+
+
 def build() -> str:
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     deps = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
-    return build_shared(srcs, LIB, deps)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:  # beside nvcc's own jobs
+        obj = ex.submit(_compile_torch_ops)
+        lib = build_shared(srcs, LIB, deps)
+        _link_torch_ops(obj.result())
+    return lib
 
 
 if __name__ == "__main__":

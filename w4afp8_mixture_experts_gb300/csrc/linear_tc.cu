@@ -15,6 +15,8 @@
 //
 // Every wait is bounded: on expiry the CTA raises its abort flag and the device error word, lets its copies and
 // products in flight finish (again with a limit), frees its tensor memory and returns.
+#include <atomic>
+
 #include "linear.cuh"
 
 namespace w4a8 {
@@ -27,24 +29,12 @@ constexpr int kMaxSmem = 227 * 1024;
 
 __device__ unsigned int g_linear_error;
 
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.b32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // Waits for a phase of `bar`, at most kTimeoutNs; gives up early when another role of the CTA has given up.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (try_wait_cluster(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t n = 0;; ++n) {
-    if (try_wait_cluster(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if ((n & 127u) == 127u) {
       if (*abort_flag) return false;
       if (globaltimer_ns() - t0 > kTimeoutNs) {
@@ -58,14 +48,31 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
 
 // Waits for an operation in flight after an abort, whatever the abort flag; bit 2 of the error word on expiry.
 __device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
-  if (try_wait_cluster(bar, parity)) return;
+  if (mbar_try_wait(bar, parity)) return;
   const uint64_t t0 = globaltimer_ns();
-  while (!try_wait_cluster(bar, parity)) {
+  while (!mbar_try_wait(bar, parity)) {
     if (globaltimer_ns() - t0 > kTimeoutNs) {
       atomicOr(&g_linear_error, 4u);
       return;
     }
   }
+}
+
+// The same by a whole warp; the same answer on all its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag));
+}
+// One lane of a converged warp.  The producer and product warps run their loops as whole warps and elect a lane
+// around each TMA or tcgen05 instruction: with the loop inside a single-lane branch the operands of those
+// instructions are not known to be uniform over the warp, and every product cost its issuer ~120 cycles.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -80,8 +87,10 @@ __device__ __forceinline__ uint32_t map_to_cta(uint32_t saddr, uint32_t cta) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(cta));
   return r;
 }
+// An arrival on a barrier of another CTA that hands over tensor memory only (ordered by the tcgen05 fences): with a
+// release at cluster scope each arrival waited for the warp's outstanding global stores as well.
 __device__ __forceinline__ void remote_arrive(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // shared-memory operand: K-major, 128-byte swizzle, 8-row groups 1024 B apart
@@ -111,11 +120,11 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
         : "memory");
 }
 // arrives on `bar` of both CTAs of the pair when every product issued so far has completed
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint16_t ctas) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
+      "h"(ctas)
       : "memory");
 }
 // a box of a matrix into this CTA's shared memory, signalled on a barrier of either CTA of the pair
@@ -127,25 +136,56 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* m, u
       : "memory");
 }
 
-__device__ __forceinline__ void activate_all(float (&v)[32], int act) {
-  switch (act) {  // one branch for the 32 values
+// a box of a matrix into L2 only
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* m, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void activate_all(float (&v)[N], int act) {
+  switch (act) {  // one branch for the N values
     case W4A8_ACT_RELU:
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = activate(v[i], W4A8_ACT_RELU);
+      for (int i = 0; i < N; ++i) v[i] = activate(v[i], W4A8_ACT_RELU);
       break;
     case W4A8_ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = activate(v[i], W4A8_ACT_SILU);
+      for (int i = 0; i < N; ++i) v[i] = activate(v[i], W4A8_ACT_SILU);
       break;
     case W4A8_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = activate(v[i], W4A8_ACT_GELU);
+      for (int i = 0; i < N; ++i) v[i] = activate(v[i], W4A8_ACT_GELU);
       break;
     case W4A8_ACT_GELU_TANH:
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = activate(v[i], W4A8_ACT_GELU_TANH);
+      for (int i = 0; i < N; ++i) v[i] = activate(v[i], W4A8_ACT_GELU_TANH);
       break;
     default: break;
+  }
+}
+
+// 32 bytes of one row, as two 16-byte accesses or one
+__device__ __forceinline__ void load32b(const void* p, bool whole, uint32_t (&w)[8]) {
+  if (whole) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
+  } else {
+    const uint4 a = static_cast<const uint4*>(p)[0], b = static_cast<const uint4*>(p)[1];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+}
+__device__ __forceinline__ void store32b(void* p, bool whole, const uint32_t (&w)[8]) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
@@ -166,7 +206,7 @@ static_assert(kPairOffBar % 8 == 0, "barrier alignment");
 struct PairPlan {
   int tiles_m, tiles_n, tiles, kblocks;
   int out_cols;  // output columns of a tile: 256, or 128 when gated
-  int vec_out;   // out and residual rows take 16-byte accesses
+  int vec_out;   // out and residual rows take 16-byte accesses (1) or 32-byte ones (2)
 };
 
 // Tiles in an order that keeps the rows and columns in flight compact: bands of 8 row blocks, columns in turn.
@@ -179,103 +219,126 @@ __device__ __forceinline__ void pair_tile(const PairPlan& pl, int i, int& tm, in
   tm = band * kBand + in - tn * rows;
 }
 
-// 32 output columns of this thread's row, from column n on
-__device__ __forceinline__ void store_row32(const LinearParams& p, const PairPlan& pl, float (&v)[32], int m0, int row,
-                                            int n, float* stg) {
-  if (pl.vec_out && n + 32 <= p.n_out) {
-    const int m = m0 + row;
+// N (16 or 32) output columns of this thread's row m0 + lane, from column n on; `res`: the residual's 32-byte
+// pieces when `have` (a 16-bit residual read ahead)
+template <int N>
+__device__ __forceinline__ void store_row(const LinearParams& p, const PairPlan& pl, float (&v)[N], int m0, int n,
+                                          bool have, const uint32_t (*res)[8], float* stg) {
+  const int lane = threadIdx.x & 31;
+  const bool whole = pl.vec_out == 2;
+  if (pl.vec_out && n + N <= p.n_out) {
+    const int m = m0 + lane;
     if (m >= p.M) return;
+    uint32_t w[8];
     if (p.out_dtype == W4A8_DTYPE_F32) {
       float* o = static_cast<float*>(p.out) + m * p.ldo + n;
-      if (p.residual) {
-        const float4* r = reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + m * p.ldr + n);
+      const float* r = static_cast<const float*>(p.residual) + (p.residual ? m * p.ldr + n : 0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 a = r[i];
-          v[4 * i] += a.x;
-          v[4 * i + 1] += a.y;
-          v[4 * i + 2] += a.z;
-          v[4 * i + 3] += a.w;
+      for (int i = 0; i < N / 8; ++i) {
+        if (p.residual) {
+          load32b(r + 8 * i, whole, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[8 * i + j] += __uint_as_float(w[j]);
         }
-      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        reinterpret_cast<float4*>(o)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * i + j]);
+        store32b(o + 8 * i, whole, w);
+      }
       return;
     }
     uint16_t* o = static_cast<uint16_t*>(p.out) + m * p.ldo + n;
-    const uint4* r =
-        p.residual ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.residual) + m * p.ldr + n) : nullptr;
     const bool bf16 = p.out_dtype == W4A8_DTYPE_BF16;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t w[4];
-      if (r) {
-        const uint4 a = r[i];
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    for (int i = 0; i < N / 16; ++i) {
+      if (have) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float2 f;
-          if (bf16) {
-            f = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
-          } else {
-            f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-          }
-          v[8 * i + 2 * j] += f.x;
-          v[8 * i + 2 * j + 1] += f.y;
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t q = res[i][j];
+          const float2 f = bf16 ? make_float2(__uint_as_float(q << 16), __uint_as_float(q & 0xFFFF0000u))
+                                : __half22float2(*reinterpret_cast<const __half2*>(&q));
+          v[16 * i + 2 * j] += f.x;
+          v[16 * i + 2 * j + 1] += f.y;
         }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 8; ++j) {
         if (bf16) {
-          w[j] = bf16x2_bits(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+          w[j] = bf16x2_bits(v[16 * i + 2 * j], v[16 * i + 2 * j + 1]);
         } else {
-          const __half2 h = __floats2half2_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+          const __half2 h = __floats2half2_rn(v[16 * i + 2 * j], v[16 * i + 2 * j + 1]);
           w[j] = *reinterpret_cast<const uint32_t*>(&h);
         }
       }
-      reinterpret_cast<uint4*>(o)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      store32b(o + 16 * i, whole, w);
     }
     return;
   }
   // rows without alignment, or a tile's last columns: 16 columns at a time through shared memory, so that the
   // lanes of a warp touch neighbouring columns of two rows instead of 32 rows
-  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < N / 16; ++h) {
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 16; ++i) stg[lane * kStageRow + i] = v[16 * h + i];
     __syncwarp();
     const int c = n + 16 * h + (lane & 15);
-    if (c < p.n_out) {
-#pragma unroll 4
-      for (int i = lane >> 4; i < 32; i += 2) {
-        const int m = m0 + i;
-        if (m >= p.M) break;
-        float a = stg[i * kStageRow + (lane & 15)];
-        if (p.residual) a += load_any(p.residual, m * p.ldr + c, p.out_dtype);
-        store_any(p.out, m * p.ldo + c, a, p.out_dtype);
+    if (c >= p.n_out) continue;
+    const int row = lane >> 4;  // rows row, row + 2, ...
+    float a[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a[i] = stg[(row + 2 * i) * kStageRow + (lane & 15)];
+    // every load before the first use, and the type's branch around all of them
+    if (p.out_dtype == W4A8_DTYPE_F32) {
+      if (p.residual) {
+        const float* r = static_cast<const float*>(p.residual) + c;
+        float f[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = m0 + row + 2 * i < p.M ? r[(m0 + row + 2 * i) * p.ldr] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) a[i] += f[i];
       }
+      float* o = static_cast<float*>(p.out) + c;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (m0 + row + 2 * i < p.M) o[(m0 + row + 2 * i) * p.ldo] = a[i];
+    } else {
+      const bool bf16 = p.out_dtype == W4A8_DTYPE_BF16;
+      if (p.residual) {
+        const uint16_t* r = static_cast<const uint16_t*>(p.residual) + c;
+        uint16_t f[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = m0 + row + 2 * i < p.M ? r[(m0 + row + 2 * i) * p.ldr] : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) a[i] += bf16 ? bf16_bits_to_float(f[i]) : __half2float(__ushort_as_half(f[i]));
+      }
+      uint16_t* o = static_cast<uint16_t*>(p.out) + c;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (m0 + row + 2 * i < p.M)
+          o[(m0 + row + 2 * i) * p.ldo] = bf16 ? float_to_bf16_bits(a[i]) : __half_as_ushort(__float2half_rn(a[i]));
     }
   }
 }
 
-template <bool GATED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+// PARTS = 1: persistent over tiles, the accumulator double buffered.  PARTS > 1: a cluster of PARTS pairs computes
+// one tile, each pair a piece of K, and finishes 1 / PARTS of its columns: the other pairs push their partial
+// products of those columns into its (by then idle) operand stages.
+template <bool GATED, int PARTS>
+__global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw,
                        const LinearParams p, const PairPlan pl) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairOffBar);  // the first CTA's count for both
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairOffBar);  // the pair's first CTA counts for both
   uint64_t* empty = full + kPairStages;
   uint64_t* tfull = empty + kPairStages;  // [2] accumulator ready, in both CTAs
   uint64_t* tempty = tfull + 2;           // [2] accumulator read by both CTAs (the first CTA's)
   uint64_t* mdrain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int crank = static_cast<int>(cluster_rank());
+  const int rank = crank & 1, part = crank >> 1, lead = crank & ~1;
   pdl_trigger();
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tx);
@@ -304,117 +367,229 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
 
-  const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
-  if (warp == 0) {
-    if (lane == 0) {  // TMA producer of this CTA's half of every stage
-      uint32_t it = 0;
-      for (int i = first; i < pl.tiles; i += stride) {
-        int tm, tn;
-        pair_tile(pl, i, tm, tn);
-        const int m = tm * 256 + rank * 128;
-        const int n = GATED ? rank * p.n_out + tn * 128 : tn * 256 + rank * 128;
-        for (int kb = 0; kb < pl.kblocks; ++kb, ++it) {
-          const int s = it % kPairStages;
-          if (!wait_bar(&empty[s], ((it / kPairStages) & 1) ^ 1, abort_flag)) goto stop;
+  const int first = blockIdx.x / (2 * PARTS), stride = PARTS > 1 ? pl.tiles : gridDim.x / 2;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(part) * pl.kblocks / PARTS);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(part + 1) * pl.kblocks / PARTS);
+  if (warp == 0) {  // TMA producer of this CTA's half of every stage
+    uint32_t it = 0;
+    bool ok = true;
+    for (int i = first; ok && i < pl.tiles; i += stride) {
+      int tm, tn;
+      pair_tile(pl, i, tm, tn);
+      const int m = tm * 256 + rank * 128;
+      const int n = GATED ? rank * p.n_out + tn * 128 : tn * 256 + rank * 128;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const int s = it % kPairStages;
+        if (!(ok = warp_wait(&empty[s], ((it / kPairStages) & 1) ^ 1, abort_flag))) break;
+        if (elect_one()) {
           uint8_t* at = smem + s * kPairStageBytes;
-          const uint32_t bar = map_to_cta(smem_u32(&full[s]), 0);
+          const uint32_t bar = map_to_cta(smem_u32(&full[s]), lead);
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStageBytes);
           tma_load_pair(at, &tx, bar, kb * kBK, m);
           tma_load_pair(at + kATile, &tw, bar, kb * kBK, n);
         }
-      }
-    stop:
-      // the last stages' slots are released before the CTA may go (and, after an abort, their loads have landed)
-      const uint32_t n = it < kPairStages ? it : kPairStages;
-      for (uint32_t j = it - n; j < it; ++j) {
-        const uint32_t s = j % kPairStages, ph = (j / kPairStages) & 1;
-        if ((*abort_flag || !wait_bar(&empty[s], ph, abort_flag)) && rank == 0) drain_bar(&full[s], ph);
+        __syncwarp();
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {  // the pair's products
-      const uint32_t idesc = idesc_f16(p.dtype == W4A8_DTYPE_BF16, 256, 256);
-      uint32_t it = 0;
-      int n = 0;
-      for (int i = first; i < pl.tiles; i += stride, ++n) {
-        const int buf = n & 1;
-        if (!wait_bar(&tempty[buf], ((n >> 1) & 1) ^ 1, abort_flag)) break;
+    // the last stages' slots are released before the CTA may go (and, after an abort, their loads have landed)
+    const uint32_t n = it < kPairStages ? it : kPairStages;
+    for (uint32_t j = it - n; j < it; ++j) {
+      const uint32_t s = j % kPairStages, ph = (j / kPairStages) & 1;
+      if (!(ok && (ok = warp_wait(&empty[s], ph, abort_flag))) && rank == 0) drain_bar(&full[s], ph);
+    }
+  } else if (warp == 1 && rank == 0) {  // the pair's products
+    const uint32_t idesc = idesc_f16(p.dtype == W4A8_DTYPE_BF16, 256, 256);
+    const uint16_t both = static_cast<uint16_t>(3 << lead);
+    uint32_t it = 0;
+    int n = 0;
+    bool ok = true;
+    for (int i = first; ok && i < pl.tiles; i += stride, ++n) {
+      const int buf = n & 1;
+      if (!(ok = warp_wait(&tempty[buf], ((n >> 1) & 1) ^ 1, abort_flag))) break;
+      tc_fence_after();
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const int s = it % kPairStages;
+        if (!(ok = warp_wait(&full[s], (it / kPairStages) & 1, abort_flag))) break;
         tc_fence_after();
-        bool ok = true;
-        for (int kb = 0; kb < pl.kblocks; ++kb, ++it) {
-          const int s = it % kPairStages;
-          if (!(ok = wait_bar(&full[s], (it / kPairStages) & 1, abort_flag))) break;
-          tc_fence_after();
-          const uint32_t at = smem_u32(smem + s * kPairStageBytes);
-          const uint64_t a = operand_desc(at), b = operand_desc(at + kATile);
+        const uint32_t at = smem_u32(smem + s * kPairStageBytes);
+        const uint64_t a = operand_desc(at), b = operand_desc(at + kATile);
+        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k) mma_f16<2>(tmem + buf * 256, a + 2 * k, b + 2 * k, idesc, kb > 0 || k > 0);
-          commit_pair(&empty[s]);
+          for (int k = 0; k < kBK / 16; ++k)
+            mma_f16<2>(tmem + buf * 256, a + 2 * k, b + 2 * k, idesc, kb > kb0 || k > 0);
+          commit_pair(&empty[s], both);
+          if (kb + 1 == kb1) commit_pair(&tfull[buf], both);
         }
-        if (!ok) break;
-        commit_pair(&tfull[buf]);
+        __syncwarp();
       }
-      if (*abort_flag) {
+    }
+    if (!ok) {
+      if (elect_one())
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(mdrain))
                      : "memory");
-        drain_bar(mdrain, 0);
+      __syncwarp();
+      drain_bar(mdrain, 0);
+    }
+  }
+
+  // epilogue: warp e reads lane quarter e % 4 (its tokens) and, by e / 4, one half of the columns that this CTA
+  // finishes; a turn is kN columns
+  constexpr int kCols = (GATED ? 64 : 128) / PARTS;  // output columns of a warp
+  constexpr int kN = kCols < 32 ? kCols : 32;
+  constexpr int kHalf = GATED ? 128 : 0;             // where the other half's products lie
+  const int e = warp - 4, quarter = warp & 3, half = e >> 2;
+  float* bias = reinterpret_cast<float*>(smem + kPairOffBias) + e * 128;
+  float* stg = reinterpret_cast<float*>(smem + kPairOffStg) + e * 32 * kStageRow;
+  const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+  const int bd = p.bias_f32 ? W4A8_DTYPE_F32 : p.dtype;
+  const int nh = part * 2 * kCols + half * kCols;  // first column of this warp within the tile
+
+  auto load_bias = [&](int n0) {
+    __syncwarp();
+    for (int c = lane; c < (GATED ? 2 : 1) * kCols; c += 32) {
+      const int other = GATED && c >= kCols;
+      const int col = n0 + c - other * kCols;
+      bias[c] = col < p.n_out ? load_any(p.bias, col + other * p.n_out, bd) : 0.f;
+    }
+    __syncwarp();
+  };
+  // bias, activation and gating of columns c ... of this warp
+  auto apply = [&](float (&v)[kN], float (&u)[kN], int c) {
+    if (p.bias) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) v[j] += bias[c + j];
+    }
+    activate_all<kN>(v, p.act);
+    if (GATED) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) v[j] *= p.bias ? u[j] + bias[kCols + c + j] : u[j];
+    }
+  };
+  constexpr int kPieces = kCols / 16;  // 32-byte pieces of a 16-bit residual
+  auto read_ahead = [&](int m, int n0, uint32_t (&res)[kPieces][8]) {
+    const uint16_t* r = static_cast<const uint16_t*>(p.residual) + m * p.ldr + n0;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (m < p.M && n0 + 16 * i + 16 <= p.n_out) load32b(r + 16 * i, pl.vec_out == 2, res[i]);
+  };
+  const bool ahead = p.residual && pl.vec_out && p.out_dtype != W4A8_DTYPE_F32;
+
+  if constexpr (PARTS == 1) {
+    if (warp >= 4) {
+      const uint32_t tempty0 = map_to_cta(smem_u32(tempty), lead);
+      int n = 0;
+      for (int i = first; i < pl.tiles; i += stride, ++n) {
+        int tm, tn;
+        pair_tile(pl, i, tm, tn);
+        const int buf = n & 1;
+        const int n0 = tn * pl.out_cols + nh;
+        const int m0 = tm * 256 + rank * 128 + quarter * 32;
+        uint32_t res[kPieces][8];
+        if (ahead) read_ahead(m0 + lane, n0, res);
+        if (p.bias) load_bias(n0);
+        if (__any_sync(0xffffffffu, !wait_bar(&tfull[buf], (n >> 1) & 1, abort_flag))) break;
+        tc_fence_after();
+        const uint32_t at = tmem + buf * 256 + lanes + nh;
+#pragma unroll 1
+        for (int c = 0; c < kCols; c += 32) {
+          float v[32], u[32];
+          __syncwarp();
+          tmem_ld32(at + c, reinterpret_cast<uint32_t*>(v));
+          if (GATED) tmem_ld32(at + kHalf + c, reinterpret_cast<uint32_t*>(u));
+          tmem_wait_ld_pin<32>(reinterpret_cast<uint32_t*>(v));
+          if (GATED) tmem_wait_ld_pin<32>(reinterpret_cast<uint32_t*>(u));
+          if (c + 32 == kCols) {  // every value is in registers: the accumulator is free
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) remote_arrive(tempty0 + buf * 8);
+          }
+          if (n0 + c >= p.n_out) continue;
+          apply(v, u, c);
+          store_row<32>(p, pl, v, m0, n0 + c, ahead, res, stg);
+#pragma unroll
+          for (int j = 0; j + 2 < kPieces; ++j)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) res[j][q] = res[j + 2][q];
+        }
       }
     }
-  } else if (warp >= 4) {  // epilogue: warp e reads lane quarter e % 4, columns by e / 4
-    const int e = warp - 4, quarter = warp & 3, half = e >> 2;
-    float* bias = reinterpret_cast<float*>(smem + kPairOffBias) + e * 128;
-    float* stg = reinterpret_cast<float*>(smem + kPairOffStg) + e * 32 * kStageRow;
-    const uint32_t tempty0 = map_to_cta(smem_u32(tempty), 0);
-    const int bd = p.bias_f32 ? W4A8_DTYPE_F32 : p.dtype;
-    constexpr int kCols = GATED ? 64 : 128;  // output columns of this warp
-    int n = 0;
-    for (int i = first; i < pl.tiles; i += stride, ++n) {
-      int tm, tn;
-      pair_tile(pl, i, tm, tn);
-      const int buf = n & 1;
-      const int n0 = tn * pl.out_cols + half * kCols;
-      const int m0 = tm * 256 + rank * 128 + quarter * 32;
-      if (p.bias) {  // [0, 64) gate, [64, 128) other half when gated
-        __syncwarp();
-        for (int c = lane; c < 128; c += 32) {
-          const int col = n0 + (GATED ? c & 63 : c);
-          bias[c] = col < p.n_out ? load_any(p.bias, col + (GATED && c >= 64 ? p.n_out : 0), bd) : 0.f;
-        }
-        __syncwarp();
-      }
-      if (__any_sync(0xffffffffu, !wait_bar(&tfull[buf], (n >> 1) & 1, abort_flag))) break;
-      tc_fence_after();
-      const uint32_t at = tmem + buf * 256 + (static_cast<uint32_t>(quarter * 32) << 16) + half * kCols;
+  } else {
+    constexpr int kPart = 2 * kCols * (GATED ? 2 : 1);  // columns of products that a CTA finishes: 256 / PARTS
+    float* recv = reinterpret_cast<float*>(smem);       // [PARTS - 1][kPart][128 tokens]
+    static_assert((PARTS - 1) * kPart * 128 * 4 <= kPairStages * kPairStageBytes, "partial products in the stages");
+    int tm, tn;
+    pair_tile(pl, first, tm, tn);
+    const int n0 = tn * pl.out_cols + nh;
+    const int m0 = tm * 256 + rank * 128 + quarter * 32;
+    uint32_t res[kPieces][8];
+    if (warp >= 4) {
+      if (ahead) read_ahead(m0 + lane, n0, res);
+      if (p.bias) load_bias(n0);
+    }
+    __syncwarp();
+    const bool ok = !__any_sync(0xffffffffu, !wait_bar(&tfull[0], 0, abort_flag));
+    tc_fence_after();
+    cluster_arrive();  // every pair's products are done: no operand stage is in use any more
+    cluster_wait();
+    if (warp >= 4 && ok) {
+      const uint32_t to0 = smem_u32(recv) + (quarter * 32 + lane) * 4;
 #pragma unroll 1
-      for (int c = 0; c < kCols; c += 32) {
-        float v[32], u[32];
-        __syncwarp();
-        tmem_ld32(at + c, reinterpret_cast<uint32_t*>(v));
-        if (GATED) tmem_ld32(at + 128 + c, reinterpret_cast<uint32_t*>(u));
-        tmem_wait_ld_pin<32>(reinterpret_cast<uint32_t*>(v));
-        if (GATED) tmem_wait_ld_pin<32>(reinterpret_cast<uint32_t*>(u));
-        if (c + 32 == kCols) {  // every value is in registers: the accumulator is free
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) remote_arrive(tempty0 + buf * 8);
-        }
-        if (n0 + c >= p.n_out) continue;
-        if (p.bias) {
+      for (int q = 0; q < PARTS; ++q) {
+        if (q == part) continue;
+        const uint32_t to = map_to_cta(to0 + (part < q ? part : part - 1) * kPart * 512, 2 * q + rank);
+#pragma unroll 1
+        for (int c = 0; c < kCols; c += kN) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 b = *reinterpret_cast<const float4*>(bias + c + 4 * j);
-            v[4 * j] += b.x;
-            v[4 * j + 1] += b.y;
-            v[4 * j + 2] += b.z;
-            v[4 * j + 3] += b.w;
+          for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+            float v[kN];
+            __syncwarp();
+            const uint32_t at = tmem + lanes + h * kHalf + q * 2 * kCols + half * kCols + c;
+            if constexpr (kN == 32)
+              tmem_ld32(at, reinterpret_cast<uint32_t*>(v));
+            else
+              tmem_ld16(at, reinterpret_cast<uint32_t*>(v));
+            tmem_wait_ld_pin<kN>(reinterpret_cast<uint32_t*>(v));
+#pragma unroll
+            for (int j = 0; j < kN; ++j)
+              asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + (h * 2 * kCols + half * kCols + c + j) * 512),
+                           "f"(v[j])
+                           : "memory");
           }
         }
-        activate_all(v, p.act);
-        if (GATED) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] *= p.bias ? u[j] + bias[64 + c + j] : u[j];
+      }
+    }
+    cluster_arrive();
+    cluster_wait();
+    if (warp >= 4 && ok && n0 < p.n_out) {
+      const float* mine = recv + quarter * 32 + lane;
+#pragma unroll 1
+      for (int c = 0; c < kCols; c += kN) {
+        float v[kN], u[kN];
+        __syncwarp();
+        const uint32_t at = tmem + lanes + nh + c;
+        if constexpr (kN == 32) {
+          tmem_ld32(at, reinterpret_cast<uint32_t*>(v));
+          if (GATED) tmem_ld32(at + kHalf, reinterpret_cast<uint32_t*>(u));
+        } else {
+          tmem_ld16(at, reinterpret_cast<uint32_t*>(v));
+          if (GATED) tmem_ld16(at + kHalf, reinterpret_cast<uint32_t*>(u));
         }
-        store_row32(p, pl, v, m0, lane, n0 + c, stg);
+        tmem_wait_ld_pin<kN>(reinterpret_cast<uint32_t*>(v));
+        if (GATED) tmem_wait_ld_pin<kN>(reinterpret_cast<uint32_t*>(u));
+#pragma unroll
+        for (int q = 0; q < PARTS - 1; ++q)
+#pragma unroll
+          for (int j = 0; j < kN; ++j) {
+            v[j] += mine[(q * kPart + half * kCols + c + j) * 128];
+            if (GATED) u[j] += mine[(q * kPart + 2 * kCols + half * kCols + c + j) * 128];
+          }
+        if (n0 + c >= p.n_out) continue;
+        apply(v, u, c);
+        store_row<kN>(p, pl, v, m0, n0 + c, ahead, res, stg);
+#pragma unroll
+        for (int j = 0; j + kN / 16 < kPieces; ++j)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) res[j][q] = res[j + kN / 16][q];
       }
     }
   }
@@ -439,6 +614,7 @@ struct SplitCfg {
   static constexpr int kOffRed = kStages * kStageBytes;       // [source CTA][token of mine][128 W rows] fp32
   static constexpr int kOffBar = kOffRed + BN * 128 * 4;
   static constexpr int kSmem = kOffBar + (2 * kStages + 2) * 8 + 16 + 1024;
+  static constexpr int kAhead = 24;
   static constexpr uint32_t kTmemCols = BN;
   static_assert(kSmem <= kMaxSmem, "shared memory");
 };
@@ -457,7 +633,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   uint64_t* mdrain = done + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = splits > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int n0 = (blockIdx.x / splits) * kOutCols, m0 = blockIdx.y * BN;
   pdl_trigger();
@@ -486,40 +662,55 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
 
   const int kb0 = static_cast<int>(static_cast<int64_t>(rank) * kblocks / splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * kblocks / splits);
-  int issued = 0;  // stages whose loads this thread has issued
-  if (warp == 0 && lane == 0) {
-    int& it = issued;
-    for (int kb = kb0; kb < kb1; ++kb, ++it) {
-      const int s = it % C::kStages;
-      if (!wait_bar(&empty[s], ((it / C::kStages) & 1) ^ 1, abort_flag)) break;
-      uint8_t* at = smem + s * C::kStageBytes;
-      mbar_arrive_expect_tx(&full[s], C::kStageBytes);
-      if (GATED) {
-        tma_load_2d(at, &tw, &full[s], kb * kBK, n0);
-        tma_load_2d(at + kATile / 2, &tw, &full[s], kb * kBK, p.n_out + n0);
-      } else {
-        tma_load_2d(at, &tw, &full[s], kb * kBK, n0);
+  int issued = 0;  // stages whose loads this warp has issued
+  if (warp == 0) {
+    // The ring alone holds too few bytes in flight for the memory's latency: once it is filled, the loads are
+    // announced to L2 kAhead stages early.
+    int pre = kb0 + C::kStages;
+    for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+      const int s = issued % C::kStages;
+      if (issued + 1 >= C::kStages) {
+        if (elect_one()) {
+          for (int q = pre; q < kb1 && q <= kb + C::kAhead; ++q) {
+            tma_prefetch_2d(&tw, q * kBK, n0);
+            if (GATED) tma_prefetch_2d(&tw, q * kBK, p.n_out + n0);
+            tma_prefetch_2d(&tx, q * kBK, m0);
+          }
+        }
+        __syncwarp();
+        pre = max(pre, min(kb1, kb + C::kAhead + 1));
       }
-      tma_load_2d(at + kATile, &tx, &full[s], kb * kBK, m0);
+      if (!warp_wait(&empty[s], ((issued / C::kStages) & 1) ^ 1, abort_flag)) break;
+      if (elect_one()) {
+        uint8_t* at = smem + s * C::kStageBytes;
+        mbar_arrive_expect_tx(&full[s], C::kStageBytes);
+        tma_load_2d(at, &tw, &full[s], kb * kBK, n0);
+        if (GATED) tma_load_2d(at + kATile / 2, &tw, &full[s], kb * kBK, p.n_out + n0);
+        tma_load_2d(at + kATile, &tx, &full[s], kb * kBK, m0);
+      }
+      __syncwarp();
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     const uint32_t idesc = idesc_f16(p.dtype == W4A8_DTYPE_BF16, 128, BN);
     int it = 0;
     bool ok = true;
     for (int kb = kb0; kb < kb1; ++kb, ++it) {
       const int s = it % C::kStages;
-      if (!(ok = wait_bar(&full[s], (it / C::kStages) & 1, abort_flag))) break;
+      if (!(ok = warp_wait(&full[s], (it / C::kStages) & 1, abort_flag))) break;
       tc_fence_after();
       const uint32_t at = smem_u32(smem + s * C::kStageBytes);
       const uint64_t a = operand_desc(at), b = operand_desc(at + kATile);
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < kBK / 16; ++k) mma_f16<1>(tmem, a + 2 * k, b + 2 * k, idesc, it > 0 || k > 0);
-      mma_commit(&empty[s]);
+        for (int k = 0; k < kBK / 16; ++k) mma_f16<1>(tmem, a + 2 * k, b + 2 * k, idesc, it > 0 || k > 0);
+        mma_commit(&empty[s]);
+        if (kb + 1 == kb1) mma_commit(done);
+      }
+      __syncwarp();
     }
-    if (ok) {
-      mma_commit(done);
-    } else {
-      mma_commit(mdrain);
+    if (!ok) {
+      if (elect_one()) mma_commit(mdrain);
+      __syncwarp();
       drain_bar(mdrain, 0);
     }
   }
@@ -533,7 +724,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   if (splits > 1) cluster_wait();
   // this CTA's partial products to the owners of their tokens: warp w reads lane quarter w % 4 (W rows), half
   // w / 4 of the tokens
-  const int own = BN / splits;  // tokens of an owner
+  const int own_log = 31 - __clz(BN / splits), own = 1 << own_log;  // tokens of an owner
   const int quarter = warp & 3, f = quarter * 32 + lane;
   if (ok) {
     constexpr int kCols = BN / 2;
@@ -549,7 +740,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       tmem_wait_ld_pin<kStep>(reinterpret_cast<uint32_t*>(v));
 #pragma unroll
       for (int j = 0; j < kStep; ++j) {
-        const int q = (c + j) / own, tok = (c + j) - q * own;
+        const int q = (c + j) >> own_log, tok = (c + j) & (own - 1);
         const uint32_t to = red + ((rank * own + tok) * 128 + f) * 4;
         if (splits > 1)
           asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_to_cta(to, q)), "f"(v[j]) : "memory");
@@ -580,18 +771,26 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.f;
     for (int s = 0; s < splits; ++s) {
-      const float* src = red + (s * own + tok) * 128 + col;
+      const float4* src = reinterpret_cast<const float4*>(red + (s * own + tok) * 128 + col);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] += src[j];
-        if (GATED) u[j] += src[64 + j];
+      for (int j = 0; j < 2; ++j) {
+        const float4 a = src[j];
+        v[4 * j] += a.x, v[4 * j + 1] += a.y, v[4 * j + 2] += a.z, v[4 * j + 3] += a.w;
+        if (GATED) {
+          const float4 b = src[16 + j];
+          u[4 * j] += b.x, u[4 * j + 1] += b.y, u[4 * j + 2] += b.z, u[4 * j + 3] += b.w;
+        }
       }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const bool in = n + j < p.n_out;
       if (p.bias && in) v[j] += load_any(p.bias, n + j, bd);
-      v[j] = activate(v[j], p.act);
+    }
+    activate_all<8>(v, p.act);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool in = n + j < p.n_out;
       if (GATED) v[j] *= p.bias && in ? u[j] + load_any(p.bias, p.n_out + n + j, bd) : u[j];
     }
     if (vec_out && n + 8 <= p.n_out) {
@@ -630,11 +829,28 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + m * p.ldo + n) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     } else {
+      const int left = min(8, p.n_out - n);
+      if (p.out_dtype == W4A8_DTYPE_F32) {
+        float* o = static_cast<float*>(p.out) + m * p.ldo + n;
+        const float* r = static_cast<const float*>(p.residual) + m * p.ldr + n;
+        float f[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (n + j >= p.n_out) break;
-        if (p.residual) v[j] += load_any(p.residual, m * p.ldr + n + j, p.out_dtype);
-        store_any(p.out, m * p.ldo + n + j, v[j], p.out_dtype);
+        for (int j = 0; j < 8; ++j) f[j] = p.residual && j < left ? r[j] : 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < left) o[j] = v[j] + f[j];
+      } else {
+        const bool bf16 = p.out_dtype == W4A8_DTYPE_BF16;
+        uint16_t* o = static_cast<uint16_t*>(p.out) + m * p.ldo + n;
+        const uint16_t* r = static_cast<const uint16_t*>(p.residual) + m * p.ldr + n;
+        uint16_t f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = p.residual && j < left ? r[j] : 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float a = v[j] + (bf16 ? bf16_bits_to_float(f[j]) : __half2float(__ushort_as_half(f[j])));
+          if (j < left) o[j] = bf16 ? float_to_bf16_bits(a) : __half_as_ushort(__float2half_rn(a));
+        }
       }
     }
   }
@@ -712,84 +928,178 @@ struct Registrar {
   Registrar() { register_device_error_reader(&read_linear_error); }
 } registrar;
 
-bool vec_rows(const LinearParams& p) {
-  const int64_t size = static_cast<int64_t>(dtype_size(p.out_dtype));
-  return aligned16(p.out) && p.ldo * size % 16 == 0 &&
-         (!p.residual || (aligned16(p.residual) && p.ldr * size % 16 == 0));
+// widest access that out's and the residual's rows take: 2 = 32 bytes, 1 = 16 bytes, 0 = single elements
+int vec_rows(const LinearParams& p) {
+  const uint64_t size = dtype_size(p.out_dtype);
+  uint64_t bits = reinterpret_cast<uintptr_t>(p.out) | p.ldo * size;
+  if (p.residual) bits |= reinterpret_cast<uintptr_t>(p.residual) | p.ldr * size;
+  return bits % 32 == 0 ? 2 : bits % 16 == 0 ? 1 : 0;
 }
 
-template <class... KArgs, class... Args>
-int launch_cluster(const char* what, void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, int cluster,
-                   cudaStream_t st, Args&&... args) {
-  cudaLaunchConfig_t lc = {};
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  lc.gridDim = grid;
-  lc.blockDim = dim3(threads);
-  lc.dynamicSmemBytes = smem;
-  lc.stream = st;
-  lc.attrs = attr;
-  lc.numAttrs = cluster > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&lc, kern, static_cast<KArgs>(args)...);
-  if (e != cudaSuccess) return set_error(W4A8_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-  return check_launch(what);
-}
+// What a launch of one kernel instance needs, and how many of its clusters the current device runs at once
+// (clusters of 8 leave SMs of a graphics-processing cluster unused, so this is not SMs / size).
+class Launcher {
+ public:
+  template <class... KArgs>
+  int prepare(void (*kern)(KArgs...), size_t smem, int threads, int cluster) {
+    return once_.run([&] {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+        return check_launch("cudaFuncSetAttribute(linear)");
+      cudaLaunchAttribute attr[1];
+      cudaLaunchConfig_t lc = config(dim3(cluster), threads, smem, cluster, nullptr, attr);
+      int n = 0, dev = 0;
+      if (cudaGetDevice(&dev) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, kern, &lc) != cudaSuccess)
+        return check_launch("cudaOccupancyMaxActiveClusters(linear)");
+      if (dev >= 0 && dev < 64) clusters_[dev] = n > 0 ? n : 1;
+      return static_cast<int>(W4A8_OK);
+    });
+  }
+  int clusters() const {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 && clusters_[dev] ? clusters_[dev] : 1;
+  }
+  static cudaLaunchConfig_t config(dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st,
+                                   cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t lc = {};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    lc.gridDim = grid;
+    lc.blockDim = dim3(threads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = st;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return lc;
+  }
+  template <class... KArgs, class... Args>
+  static int launch(const char* what, void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, int cluster,
+                    cudaStream_t st, Args&&... args) {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t lc = config(grid, threads, smem, cluster, st, attr);
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    lc.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&lc, kern, static_cast<KArgs>(args)...);
+    if (e != cudaSuccess) return set_error(W4A8_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    return check_launch(what);
+  }
 
-template <bool GATED>
-int launch_pair(const LinearParams& p, cudaStream_t st) {
-  static DeviceOnce attrs;
-  auto kern = linear_pair_kernel<GATED>;
-  if (int rc = attrs.run([&] {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem) != cudaSuccess)
-          return check_launch("cudaFuncSetAttribute(linear_pair)");
-        return static_cast<int>(W4A8_OK);
-      }))
+ private:
+  DeviceOnce once_;
+  int clusters_[64] = {0};
+};
+
+// One configuration of the two kernels: how many clusters run at once, and the launch itself.
+struct Option {
+  int (*ready)(int* clusters);  // status; makes the configuration ready on this device
+  int (*launch)(const LinearParams& p, cudaStream_t st);
+  double fixed_us;  // a launch of one tile per cluster without its stages
+  int rows, cols;   // x rows and W rows of a tile
+  int parts;        // pieces of K
+  bool persistent;
+};
+
+template <bool GATED, int PARTS>
+struct Pair {
+  static Launcher& launcher() {
+    static Launcher l;
+    return l;
+  }
+  static int ready(int* clusters) {
+    const int rc = launcher().prepare(linear_pair_kernel<GATED, PARTS>, kPairSmem, kPairThreads, 2 * PARTS);
+    *clusters = launcher().clusters();
     return rc;
-  CUtensorMap tx, tw;
-  int rc;
-  if ((rc = row_map(&tx, p.x, p.dtype, p.M, p.K, p.ldx, 128, "x"))) return rc;
-  if ((rc = row_map(&tw, p.w, p.dtype, p.N, p.K, p.ldw, 128, "w"))) return rc;
-  PairPlan pl;
-  pl.out_cols = GATED ? 128 : 256;
-  pl.tiles_m = static_cast<int>(ceil_div(p.M, 256));
-  pl.tiles_n = static_cast<int>(ceil_div(p.n_out, pl.out_cols));
-  const int64_t tiles = static_cast<int64_t>(pl.tiles_m) * pl.tiles_n;
-  pl.tiles = static_cast<int>(tiles);
-  pl.kblocks = static_cast<int>(ceil_div(p.K, kBK));
-  pl.vec_out = vec_rows(p);
-  const int64_t pairs = tiles < num_sms() / 2 ? tiles : num_sms() / 2;
-  return launch_cluster("linear_pair_kernel", kern, dim3(static_cast<unsigned>(2 * pairs)), kPairThreads, kPairSmem, 1,
-                        st, tx, tw, p, pl);
-}
+  }
+  static int launch(const LinearParams& p, cudaStream_t st) {
+    CUtensorMap tx, tw;
+    int rc, clusters;
+    if ((rc = ready(&clusters))) return rc;
+    if ((rc = row_map(&tx, p.x, p.dtype, p.M, p.K, p.ldx, 128, "x"))) return rc;
+    if ((rc = row_map(&tw, p.w, p.dtype, p.N, p.K, p.ldw, 128, "w"))) return rc;
+    PairPlan pl;
+    pl.out_cols = GATED ? 128 : 256;
+    pl.tiles_m = static_cast<int>(ceil_div(p.M, 256));
+    pl.tiles_n = static_cast<int>(ceil_div(p.n_out, pl.out_cols));
+    pl.tiles = pl.tiles_m * pl.tiles_n;  // below 2^25 for M, N <= 2^20
+    pl.kblocks = static_cast<int>(ceil_div(p.K, kBK));
+    pl.vec_out = vec_rows(p);
+    const int n = PARTS > 1 || pl.tiles < clusters ? pl.tiles : clusters;
+    return Launcher::launch("linear_pair_kernel", linear_pair_kernel<GATED, PARTS>, dim3(2 * PARTS * n), kPairThreads,
+                            kPairSmem, 2 * PARTS, st, tx, tw, p, pl);
+  }
+};
 
-template <int BN, bool GATED>
-int launch_split(const LinearParams& p, int splits, cudaStream_t st) {
+template <int BN, bool GATED, int SPLITS>
+struct Split {
   using C = SplitCfg<BN>;
-  static DeviceOnce attrs;
-  auto kern = linear_split_kernel<BN, GATED>;
-  if (int rc = attrs.run([&] {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
-          return check_launch("cudaFuncSetAttribute(linear_split)");
-        return static_cast<int>(W4A8_OK);
-      }))
+  static Launcher& launcher() {
+    static Launcher l;
+    return l;
+  }
+  static int ready(int* clusters) {
+    const int rc = launcher().prepare(linear_split_kernel<BN, GATED>, C::kSmem, kSplitThreads, SPLITS);
+    *clusters = launcher().clusters();
     return rc;
-  CUtensorMap tx, tw;
-  int rc;
-  if ((rc = row_map(&tx, p.x, p.dtype, p.M, p.K, p.ldx, BN, "x"))) return rc;
-  if ((rc = row_map(&tw, p.w, p.dtype, p.N, p.K, p.ldw, GATED ? 64 : 128, "w"))) return rc;
-  const int64_t nb = ceil_div(p.n_out, GATED ? 64 : 128), mb = ceil_div(p.M, BN);
-  return launch_cluster("linear_split_kernel", kern, dim3(static_cast<unsigned>(nb * splits), static_cast<unsigned>(mb)),
-                        kSplitThreads, C::kSmem, splits, st, tx, tw, p, splits, static_cast<int>(ceil_div(p.K, kBK)),
-                        static_cast<int>(vec_rows(p)));
+  }
+  static int launch(const LinearParams& p, cudaStream_t st) {
+    CUtensorMap tx, tw;
+    int rc, clusters;
+    if ((rc = ready(&clusters))) return rc;
+    if ((rc = row_map(&tx, p.x, p.dtype, p.M, p.K, p.ldx, BN, "x"))) return rc;
+    if ((rc = row_map(&tw, p.w, p.dtype, p.N, p.K, p.ldw, GATED ? 64 : 128, "w"))) return rc;
+    const unsigned nb = static_cast<unsigned>(ceil_div(p.n_out, GATED ? 64 : 128));
+    return Launcher::launch("linear_split_kernel", linear_split_kernel<BN, GATED>,
+                            dim3(nb * SPLITS, static_cast<unsigned>(ceil_div(p.M, BN))), kSplitThreads, C::kSmem, SPLITS,
+                            st, tx, tw, p, SPLITS, static_cast<int>(ceil_div(p.K, kBK)), vec_rows(p));
+  }
+};
+
+template <bool GATED, int PARTS>
+Option pair_option(double fixed) {
+  return {Pair<GATED, PARTS>::ready, Pair<GATED, PARTS>::launch, fixed, 256, 256, PARTS, PARTS == 1};
+}
+template <int BN, bool GATED, int SPLITS>
+Option split_option(double fixed) {
+  return {Split<BN, GATED, SPLITS>::ready, Split<BN, GATED, SPLITS>::launch, fixed, BN, 128, SPLITS, false};
 }
 
-template <int BN>
-int launch_split_bn(const LinearParams& p, int splits, cudaStream_t st) {
-  return p.gated ? launch_split<BN, true>(p, splits, st) : launch_split<BN, false>(p, splits, st);
+// Configuration asked for by a test (rows of a tile * 16 + pieces of K), 0: none.
+std::atomic<int> g_force{0};
+
+// The configuration with the smallest estimate
+//   fixed + 0.26 us * (64-k stages of a piece) * waves + (waves - 1) * (fixed - 3 us, a launch; 0 when persistent)
+// 0.26 us is what a stage takes in every configuration that memory does not bound; the fixed times are launches of one
+// wave extrapolated to no stages, measured on a GB300 (M x N x K = 64 x 256 x 7168, 128 x 8192 x 7168,
+// 256 x 4096 x 7168 gated, 2048 x 256 x 7168, with 1 to 8 pieces).
+template <bool GATED>
+int launch_best(const LinearParams& p, cudaStream_t st) {
+  static const Option options[] = {
+      pair_option<GATED, 1>(8.0),          pair_option<GATED, 2>(8.0),          pair_option<GATED, 4>(9.3),
+      split_option<128, GATED, 1>(9.0),    split_option<128, GATED, 2>(9.3),    split_option<128, GATED, 4>(9.5),
+      split_option<64, GATED, 1>(5.3),     split_option<64, GATED, 2>(5.5),     split_option<64, GATED, 4>(5.5),
+      split_option<64, GATED, 8>(4.8),     split_option<32, GATED, 1>(3.3),     split_option<32, GATED, 2>(3.4),
+      split_option<32, GATED, 4>(3.4),     split_option<32, GATED, 8>(3.4),
+  };
+  const Option* best = nullptr;
+  double best_us = 0.0;
+  const int64_t kblocks = ceil_div(p.K, kBK);
+  const int force = g_force.load(std::memory_order_relaxed);
+  for (const Option& o : options) {
+    if (o.parts > kblocks || (force && force % 16 <= kblocks && force != o.rows * 16 + o.parts)) continue;
+    int clusters;
+    if (int rc = o.ready(&clusters)) return rc;
+    const int64_t tiles = ceil_div(p.M, o.rows) * ceil_div(p.N, o.cols);
+    const int64_t waves = ceil_div(tiles, clusters);
+    const double us = o.fixed_us + 0.26 * static_cast<double>(ceil_div(kblocks, o.parts) * waves) +
+                      (o.persistent ? 0.0 : (waves - 1) * (o.fixed_us - 3.0));
+    if (!best || us < best_us) {
+      best = &o;
+      best_us = us;
+    }
+  }
+  if (!best) return set_error(W4A8_ERR_UNSUPPORTED, "no configuration for K=%d", p.K);
+  return best->launch(p, st);
 }
 
 }  // namespace
@@ -813,16 +1123,12 @@ int launch_linear_tc(LinearParams p, void* ws, size_t ws_bytes, cudaStream_t st)
     p.w = pw;
     p.ldx = p.ldw = k8 * 8;
   }
-  const int sms = num_sms();
-  const int64_t big = ceil_div(p.M, 256) * ceil_div(p.n_out, p.gated ? 128 : 256);
-  if (big >= sms / 4) return p.gated ? launch_pair<true>(p, st) : launch_pair<false>(p, st);
-  const int bn = p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
-  const int64_t tiles = ceil_div(p.M, bn) * ceil_div(p.n_out, p.gated ? 64 : 128), kb = ceil_div(p.K, kBK);
-  int splits = 1;
-  while (splits < 8 && tiles * splits * 2 <= sms && kb >= 8 * splits) splits *= 2;
-  if (bn == 32) return launch_split_bn<32>(p, splits, st);
-  if (bn == 64) return launch_split_bn<64>(p, splits, st);
-  return launch_split_bn<128>(p, splits, st);
+  return p.gated ? launch_best<true>(p, st) : launch_best<false>(p, st);
 }
 
 }  // namespace w4a8
+
+extern "C" int w4a8_test_linear_config(int rows, int pieces) {
+  w4a8::g_force.store(rows > 0 ? rows * 16 + pieces : 0);
+  return W4A8_OK;
+}
