@@ -6,7 +6,6 @@
 // A row is held by the threads of one block (or one warp, for short rows: several rows to a block); the row's
 // sums are one block reduction each (the mean first, then the squared differences, for a LayerNorm).
 #include <algorithm>
-#include <type_traits>
 
 #include "block_ops.cuh"
 #include "common.cuh"
@@ -45,16 +44,6 @@ __device__ __forceinline__ void load_vec(const T* p, float (&o)[V]) {
   const Pack<T, V> a = *reinterpret_cast<const Pack<T, V>*>(p);
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = to_f32(a.v[i]);
-}
-// two fp32 values rounded to T and packed (16-bit types)
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (std::is_same<T, __half>::value) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    return bf16x2_bits(lo, hi);
-  }
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T* p, const float (&o)[V]) {

@@ -54,20 +54,6 @@ __device__ __forceinline__ float activate(float z, int act) {
   }
 }
 
-__device__ __forceinline__ float load_any(const void* p, int64_t at, int dtype) {
-  if (dtype == W4A8_DTYPE_F32) return static_cast<const float*>(p)[at];
-  if (dtype == W4A8_DTYPE_F16) return __half2float(static_cast<const __half*>(p)[at]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
-}
-__device__ __forceinline__ void store_any(void* p, int64_t at, float v, int dtype) {
-  if (dtype == W4A8_DTYPE_F32)
-    static_cast<float*>(p)[at] = v;
-  else if (dtype == W4A8_DTYPE_F16)
-    static_cast<__half*>(p)[at] = __float2half_rn(v);
-  else
-    static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
-}
-
 // out[m][n] from the accumulated products z (gate half) and z2 (other half, gated only)
 __device__ __forceinline__ void finish(const LinearParams& p, int m, int n, float z, float z2) {
   const int bd = p.bias_f32 ? W4A8_DTYPE_F32 : p.dtype;

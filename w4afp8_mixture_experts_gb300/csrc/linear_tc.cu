@@ -15,6 +15,7 @@
 //
 // Every wait is bounded: on expiry the CTA raises its abort flag and the device error word, lets its copies and
 // products in flight finish (again with a limit), frees its tensor memory and returns.
+#include <algorithm>
 #include <atomic>
 
 #include "linear.cuh"
@@ -136,11 +137,19 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* m, u
       : "memory");
 }
 
-// a box of a matrix into L2 only
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* m, int32_t x, int32_t y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(m)),
-               "r"(x), "r"(y)
-               : "memory");
+// Asks L2 for a block of the residual, `rows` x `cols` at (m, n), with `count` threads of which this is number `i`:
+// issued before the products, it takes the memory's latency out of the epilogue's loads.
+__device__ __forceinline__ void prefetch_residual(const LinearParams& p, int m, int n, int rows, int cols, int i, int count) {
+  const int size = p.out_dtype == W4A8_DTYPE_F32 ? 4 : 2;
+  rows = min(rows, p.M - m);
+  const int bytes = min(cols, p.n_out - n) * size;
+  if (bytes <= 0) return;
+  const int segs = (bytes + 127) / 128 + 1;  // a row may start anywhere in a 128-byte line
+  for (; i < rows * segs; i += count) {
+    const int row = i / segs, at = min(i % segs * 128, bytes - 1);
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p.residual) +
+                                                  ((m + row) * p.ldr + n) * size + at));
+  }
 }
 
 template <int N>
@@ -432,6 +441,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   }
 
+  if (PARTS > 1 && (warp == 2 || warp == 3) && p.residual && !pl.vec_out) {  // aligned rows are read ahead below
+    int tm, tn;
+    pair_tile(pl, first, tm, tn);
+    prefetch_residual(p, tm * 256 + rank * 128, tn * pl.out_cols + part * (pl.out_cols / PARTS), 128,
+                      pl.out_cols / PARTS, threadIdx.x - 64, 64);
+  }
+
   // epilogue: warp e reads lane quarter e % 4 (its tokens) and, by e / 4, one half of the columns that this CTA
   // finishes; a turn is kN columns
   constexpr int kCols = (GATED ? 64 : 128) / PARTS;  // output columns of a warp
@@ -610,14 +626,160 @@ constexpr int kSplitThreads = 256;
 template <int BN>
 struct SplitCfg {
   static constexpr int kStageBytes = kATile + BN * kBK * 2;
-  static constexpr int kStages = BN == 128 ? 4 : BN == 64 ? 6 : 7;
+  static constexpr int kStages = BN == 128 ? 4 : BN == 64 ? 6 : 8;
   static constexpr int kOffRed = kStages * kStageBytes;       // [source CTA][token of mine][128 W rows] fp32
   static constexpr int kOffBar = kOffRed + BN * 128 * 4;
-  static constexpr int kSmem = kOffBar + (2 * kStages + 2) * 8 + 16 + 1024;
-  static constexpr int kAhead = 24;
-  static constexpr uint32_t kTmemCols = BN;
+  static constexpr int kSmem = kOffBar + (2 * kStages + 5) * 8 + 16 + 1024;
+  // MMA warps: warp m issues the products of stages it % kMma == m into an accumulator of its own.  One warp spends
+  // ~330 cycles a stage on the hand-over (wait, fence, commit), several times what the products take; together they
+  // overlap it, and the sums over K are shorter.
+  static constexpr int kMma = 2;
+  // A warp waits for every phase of the slots that it uses, in order, only if a slot always falls to the same warp:
+  // otherwise its parity wait is satisfied by the phase before the one it needs.
+  static_assert(kStages % kMma == 0, "ring depth a multiple of the MMA warps");
+  static constexpr int kTurns = BN * 16 / kSplitThreads;  // tokens of a thread in the epilogue, at most
+  static constexpr uint32_t kTmemCols = kMma * BN;
   static_assert(kSmem <= kMaxSmem, "shared memory");
 };
+
+// The epilogue's threads: with aligned rows a thread finishes 8 neighbouring columns of every kStep-th token, without
+// alignment one column of them (so that a warp touches neighbours).
+template <bool GATED>
+struct SplitMap {
+  static constexpr int kOutCols = GATED ? 64 : 128;
+  static constexpr int kOct = kOutCols / 8;
+  static constexpr int kOctStep = kSplitThreads / kOct, kColStep = kSplitThreads / kOutCols;
+};
+
+// The biases of this thread's columns and the aligned 16-bit residual of all its tokens.
+template <int BN, bool GATED>
+__device__ __forceinline__ void read_ahead_split(const LinearParams& p, int m, int n0, int own, int vec_out,
+                                                 float (&bias)[8], float (&bias2)[8], uint4 (&res)[SplitCfg<BN>::kTurns]) {
+  using Map = SplitMap<GATED>;
+  const int n = n0 + (vec_out ? threadIdx.x % Map::kOct * 8 : threadIdx.x % Map::kOutCols);
+  const int bd = p.bias_f32 ? W4A8_DTYPE_F32 : p.dtype;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const bool in = p.bias && n + j < p.n_out && (vec_out || j == 0);
+    bias[j] = in ? load_any(p.bias, n + j, bd) : 0.f;
+    bias2[j] = in && GATED ? load_any(p.bias, p.n_out + n + j, bd) : 0.f;
+  }
+  if (!p.residual || !vec_out || p.out_dtype == W4A8_DTYPE_F32 || n + 8 > p.n_out) return;
+  const int left = min(own, p.M - m);
+  const uint16_t* r = static_cast<const uint16_t*>(p.residual) + n;
+#pragma unroll
+  for (int i = 0; i < SplitCfg<BN>::kTurns; ++i) {
+    const int tok = threadIdx.x / Map::kOct + i * Map::kOctStep;
+    if (tok < left) res[i] = *reinterpret_cast<const uint4*>(r + (m + tok) * p.ldr);
+  }
+}
+
+// Adds a CTA's partial products for its tokens in rank order and writes them: red [split][own][128 W rows].
+template <int BN, bool GATED, typename T>
+__device__ __forceinline__ void finish_tokens(const LinearParams& p, const float* red, int splits, int own, int left, int m,
+                                              int n0, int vec_out, const float (&bias)[8], const float (&bias2)[8],
+                                              const uint4 (&res)[SplitCfg<BN>::kTurns]) {
+  using Map = SplitMap<GATED>;
+  const T* residual = static_cast<const T*>(p.residual);
+  T* out = static_cast<T*>(p.out);
+  if (!vec_out) {
+    constexpr int kN = 16;  // tokens at a time: every load before the first use
+    const int f = threadIdx.x % Map::kOutCols, n = n0 + f;
+    if (n >= p.n_out) return;
+#pragma unroll 1
+    for (int tok0 = threadIdx.x / Map::kOutCols; tok0 < left; tok0 += kN * Map::kColStep) {
+      const int64_t row = m + tok0;
+      const int count = (left - tok0 + Map::kColStep - 1) / Map::kColStep;  // tokens of this turn, if fewer than kN
+      float v[kN], u[kN];
+      T r[kN];
+      if (p.residual) {
+        const T* rp = residual + row * p.ldr + n;
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+          if (j < count) r[j] = rp[j * Map::kColStep * p.ldr];
+      }
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        v[j] = bias[0];
+        u[j] = bias2[0];
+      }
+#pragma unroll 1
+      for (int s = 0; s < splits; ++s) {
+        const float* src = red + (s * own + tok0) * 128 + f;
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+          if (j < count) {
+            v[j] += src[j * Map::kColStep * 128];
+            if (GATED) u[j] += src[j * Map::kColStep * 128 + 64];
+          }
+      }
+      activate_all<kN>(v, p.act);
+      T* o = out + row * p.ldo + n;
+#pragma unroll
+      for (int j = 0; j < kN; ++j)
+        if (j < count) {
+          if (GATED) v[j] *= u[j];
+          if (p.residual) v[j] += to_f32(r[j]);
+          o[j * Map::kColStep * p.ldo] = from_f32<T>(v[j]);
+        }
+    }
+    return;
+  }
+  const int col = threadIdx.x % Map::kOct * 8, n = n0 + col;
+  if (n >= p.n_out) return;
+  const bool whole = n + 8 <= p.n_out;
+#pragma unroll
+  for (int i = 0; i < SplitCfg<BN>::kTurns; ++i) {
+    const int tok = threadIdx.x / Map::kOct + i * Map::kOctStep;
+    if (tok >= left) break;
+    float v[8], u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = bias[j];
+      u[j] = bias2[j];
+    }
+#pragma unroll 1
+    for (int s = 0; s < splits; ++s) {
+      const float4* src = reinterpret_cast<const float4*>(red + (s * own + tok) * 128 + col);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float4 a = src[j];
+        v[4 * j] += a.x, v[4 * j + 1] += a.y, v[4 * j + 2] += a.z, v[4 * j + 3] += a.w;
+        if (GATED) {
+          const float4 b = src[16 + j];
+          u[4 * j] += b.x, u[4 * j + 1] += b.y, u[4 * j + 2] += b.z, u[4 * j + 3] += b.w;
+        }
+      }
+    }
+    activate_all<8>(v, p.act);
+    if (GATED) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= u[j];
+    }
+    const T* r = residual + (p.residual ? (m + tok) * p.ldr + n : 0);
+    T* o = out + (m + tok) * p.ldo + n;
+    if (!whole) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (n + j < p.n_out) o[j] = from_f32<T>(p.residual ? v[j] + to_f32(r[j]) : v[j]);
+    } else if constexpr (sizeof(T) == 4) {
+      if (p.residual) {
+        const float4 a = reinterpret_cast<const float4*>(r)[0], b = reinterpret_cast<const float4*>(r)[1];
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+      }
+      reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      if (p.residual) {
+        const T* h = reinterpret_cast<const T*>(&res[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += to_f32(h[j]);
+      }
+      *reinterpret_cast<uint4*>(o) = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]),
+                                                pack2<T>(v[6], v[7]));
+    }
+  }
+}
 
 template <int BN, bool GATED>
 __global__ void __launch_bounds__(kSplitThreads, 1)
@@ -630,8 +792,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* empty = full + C::kStages;
   uint64_t* done = empty + C::kStages;
-  uint64_t* mdrain = done + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 1);
+  uint64_t* mdrain = done + 1;  // [4]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = splits > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -644,8 +806,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    mbar_init(done, 1);
-    mbar_init(mdrain, 1);
+    mbar_init(done, C::kMma);
+    for (int i = 0; i < C::kMma; ++i) mbar_init(&mdrain[i], 1);
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -662,24 +824,15 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
 
   const int kb0 = static_cast<int>(static_cast<int64_t>(rank) * kblocks / splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * kblocks / splits);
+  const int own_log = 31 - __clz(BN / splits), own = 1 << own_log;  // tokens that a CTA finishes
+  // what the epilogue needs besides the products is read ahead of them
+  float bias[8], bias2[8];
+  uint4 res[SplitCfg<BN>::kTurns];
+  read_ahead_split<BN, GATED>(p, m0 + rank * own, n0, own, vec_out, bias, bias2, res);
   int issued = 0;  // stages whose loads this warp has issued
   if (warp == 0) {
-    // The ring alone holds too few bytes in flight for the memory's latency: once it is filled, the loads are
-    // announced to L2 kAhead stages early.
-    int pre = kb0 + C::kStages;
     for (int kb = kb0; kb < kb1; ++kb, ++issued) {
       const int s = issued % C::kStages;
-      if (issued + 1 >= C::kStages) {
-        if (elect_one()) {
-          for (int q = pre; q < kb1 && q <= kb + C::kAhead; ++q) {
-            tma_prefetch_2d(&tw, q * kBK, n0);
-            if (GATED) tma_prefetch_2d(&tw, q * kBK, p.n_out + n0);
-            tma_prefetch_2d(&tx, q * kBK, m0);
-          }
-        }
-        __syncwarp();
-        pre = max(pre, min(kb1, kb + C::kAhead + 1));
-      }
       if (!warp_wait(&empty[s], ((issued / C::kStages) & 1) ^ 1, abort_flag)) break;
       if (elect_one()) {
         uint8_t* at = smem + s * C::kStageBytes;
@@ -690,11 +843,13 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       }
       __syncwarp();
     }
-  } else if (warp == 1) {
+  } else if (warp == 2 || warp == 3) {
+    if (p.residual && (!vec_out || p.out_dtype == W4A8_DTYPE_F32)) prefetch_residual(p, m0 + rank * own, n0, own, kOutCols, threadIdx.x - 64, 64);
+  } else if (warp >= 4 && warp < 4 + C::kMma) {
     const uint32_t idesc = idesc_f16(p.dtype == W4A8_DTYPE_BF16, 128, BN);
-    int it = 0;
+    const int m = warp - 4, stages = kb1 - kb0;
     bool ok = true;
-    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+    for (int it = m; it < stages; it += C::kMma) {
       const int s = it % C::kStages;
       if (!(ok = warp_wait(&full[s], (it / C::kStages) & 1, abort_flag))) break;
       tc_fence_after();
@@ -702,17 +857,14 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       const uint64_t a = operand_desc(at), b = operand_desc(at + kATile);
       if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kBK / 16; ++k) mma_f16<1>(tmem, a + 2 * k, b + 2 * k, idesc, it > 0 || k > 0);
+        for (int k = 0; k < kBK / 16; ++k) mma_f16<1>(tmem + m * BN, a + 2 * k, b + 2 * k, idesc, it > m || k > 0);
         mma_commit(&empty[s]);
-        if (kb + 1 == kb1) mma_commit(done);
       }
       __syncwarp();
     }
-    if (!ok) {
-      if (elect_one()) mma_commit(mdrain);
-      __syncwarp();
-      drain_bar(mdrain, 0);
-    }
+    if (elect_one()) mma_commit(ok ? done : &mdrain[m]);
+    __syncwarp();
+    if (!ok) drain_bar(&mdrain[m], 0);
   }
   __syncwarp();
   const bool ok = !__any_sync(0xffffffffu, !wait_bar(done, 0, abort_flag));
@@ -724,7 +876,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   if (splits > 1) cluster_wait();
   // this CTA's partial products to the owners of their tokens: warp w reads lane quarter w % 4 (W rows), half
   // w / 4 of the tokens
-  const int own_log = 31 - __clz(BN / splits), own = 1 << own_log;  // tokens of an owner
   const int quarter = warp & 3, f = quarter * 32 + lane;
   if (ok) {
     constexpr int kCols = BN / 2;
@@ -733,11 +884,19 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
 #pragma unroll 1
     for (int c = (warp >> 2) * kCols; c < (warp >> 2) * kCols + kCols; c += kStep) {
       float v[kStep];
-      if constexpr (kStep == 32)
-        tmem_ld32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c, reinterpret_cast<uint32_t*>(v));
-      else
-        tmem_ld16(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c, reinterpret_cast<uint32_t*>(v));
-      tmem_wait_ld_pin<kStep>(reinterpret_cast<uint32_t*>(v));
+#pragma unroll
+      for (int m = 0; m < C::kMma; ++m) {
+        if (m > 0 && m >= kb1 - kb0) break;  // fewer stages than MMA warps: no products in that accumulator
+        float w[kStep];
+        const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + m * BN + c;
+        if constexpr (kStep == 32)
+          tmem_ld32(at, reinterpret_cast<uint32_t*>(w));
+        else
+          tmem_ld16(at, reinterpret_cast<uint32_t*>(w));
+        tmem_wait_ld_pin<kStep>(reinterpret_cast<uint32_t*>(w));
+#pragma unroll
+        for (int j = 0; j < kStep; ++j) v[j] = m > 0 ? v[j] + w[j] : w[j];
+      }
 #pragma unroll
       for (int j = 0; j < kStep; ++j) {
         const int q = (c + j) >> own_log, tok = (c + j) & (own - 1);
@@ -760,105 +919,21 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     tmem_dealloc(tmem, C::kTmemCols);
   }
   if (!ok) return;
-  // 8 output columns of one of this CTA's tokens per thread and turn
   const float* red = reinterpret_cast<const float*>(smem + C::kOffRed);
-  const int bd = p.bias_f32 ? W4A8_DTYPE_F32 : p.dtype;
-  for (int i = threadIdx.x; i < own * (kOutCols / 8); i += kSplitThreads) {
-    const int tok = i / (kOutCols / 8), col = i % (kOutCols / 8) * 8;
-    const int m = m0 + rank * own + tok, n = n0 + col;
-    if (m >= p.M || n >= p.n_out) continue;
-    float v[8], u[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.f;
-    for (int s = 0; s < splits; ++s) {
-      const float4* src = reinterpret_cast<const float4*>(red + (s * own + tok) * 128 + col);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float4 a = src[j];
-        v[4 * j] += a.x, v[4 * j + 1] += a.y, v[4 * j + 2] += a.z, v[4 * j + 3] += a.w;
-        if (GATED) {
-          const float4 b = src[16 + j];
-          u[4 * j] += b.x, u[4 * j + 1] += b.y, u[4 * j + 2] += b.z, u[4 * j + 3] += b.w;
-        }
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const bool in = n + j < p.n_out;
-      if (p.bias && in) v[j] += load_any(p.bias, n + j, bd);
-    }
-    activate_all<8>(v, p.act);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const bool in = n + j < p.n_out;
-      if (GATED) v[j] *= p.bias && in ? u[j] + load_any(p.bias, p.n_out + n + j, bd) : u[j];
-    }
-    if (vec_out && n + 8 <= p.n_out) {
-      if (p.out_dtype == W4A8_DTYPE_F32) {
-        float* o = static_cast<float*>(p.out) + m * p.ldo + n;
-        if (p.residual) {
-          const float* r = static_cast<const float*>(p.residual) + m * p.ldr + n;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] += r[j];
-        }
-        reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
-      } else {
-        if (p.residual) {
-          const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.residual) + m * p.ldr + n);
-          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 r = p.out_dtype == W4A8_DTYPE_BF16
-                                 ? make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u))
-                                 : __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-            v[2 * j] += r.x;
-            v[2 * j + 1] += r.y;
-          }
-        }
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (p.out_dtype == W4A8_DTYPE_BF16) {
-            w[j] = bf16x2_bits(v[2 * j], v[2 * j + 1]);
-          } else {
-            const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
-            w[j] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-        }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + m * p.ldo + n) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    } else {
-      const int left = min(8, p.n_out - n);
-      if (p.out_dtype == W4A8_DTYPE_F32) {
-        float* o = static_cast<float*>(p.out) + m * p.ldo + n;
-        const float* r = static_cast<const float*>(p.residual) + m * p.ldr + n;
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = p.residual && j < left ? r[j] : 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < left) o[j] = v[j] + f[j];
-      } else {
-        const bool bf16 = p.out_dtype == W4A8_DTYPE_BF16;
-        uint16_t* o = static_cast<uint16_t*>(p.out) + m * p.ldo + n;
-        const uint16_t* r = static_cast<const uint16_t*>(p.residual) + m * p.ldr + n;
-        uint16_t f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = p.residual && j < left ? r[j] : 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float a = v[j] + (bf16 ? bf16_bits_to_float(f[j]) : __half2float(__ushort_as_half(f[j])));
-          if (j < left) o[j] = bf16 ? float_to_bf16_bits(a) : __half_as_ushort(__float2half_rn(a));
-        }
-      }
-    }
-  }
+  const int left = min(own, p.M - m0 - rank * own);  // tokens of mine that exist
+  if (p.out_dtype == W4A8_DTYPE_F32)
+    finish_tokens<BN, GATED, float>(p, red, splits, own, left, m0 + rank * own, n0, vec_out, bias, bias2, res);
+  else if (p.out_dtype == W4A8_DTYPE_F16)
+    finish_tokens<BN, GATED, __half>(p, red, splits, own, left, m0 + rank * own, n0, vec_out, bias, bias2, res);
+  else
+    finish_tokens<BN, GATED, __nv_bfloat16>(p, red, splits, own, left, m0 + rank * own, n0, vec_out, bias, bias2, res);
 }
 
 // --- operands without 16-byte alignment ------------------------------------------------------------------------
 
-// Rows of x and w to 16-byte-aligned rows of the workspace (zeros past K), 8 elements per thread.
+// Rows of x and of w (those of the two that need it) to 16-byte-aligned rows of the workspace, zeros past K; 8 elements
+// per thread.  Inside a row they come in as 32-bit words, shifted into place where the row starts in the middle of one;
+// a row's ends are read element by element, so that nothing beside it is touched.
 __global__ void __launch_bounds__(256) linear_repack_kernel(const uint16_t* x, int64_t ldx, int64_t items_x, uint16_t* px,
                                                             const uint16_t* w, int64_t ldw, int64_t items, uint16_t* pw,
                                                             int K, int k8) {
@@ -867,14 +942,25 @@ __global__ void __launch_bounds__(256) linear_repack_kernel(const uint16_t* x, i
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < items; i += gridDim.x * 256ll) {
     const bool is_x = i < items_x;
     const int64_t j = is_x ? i : i - items_x;
-    const int64_t row = j / k8;
-    const int k = static_cast<int>(j - row * k8) * 8;
+    const uint32_t row = static_cast<uint32_t>(static_cast<uint64_t>(j) / static_cast<uint32_t>(k8));
+    const int k = static_cast<int>(j - static_cast<int64_t>(row) * k8) * 8;
     const uint16_t* src = (is_x ? x + row * ldx : w + row * ldw) + k;
     uint32_t v[4];
+    if (k > 0 && k + 8 < K) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(src);
+      const uint32_t* words = reinterpret_cast<const uint32_t*>(a & ~uintptr_t(3));
+      uint32_t in[5];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t lo = k + 2 * c < K ? src[2 * c] : 0, hi = k + 2 * c + 1 < K ? src[2 * c + 1] : 0;
-      v[c] = lo | (hi << 16);
+      for (int c = 0; c < 4; ++c) in[c] = words[c];
+      in[4] = a & 2 ? words[4] : 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = __funnelshift_r(in[c], in[c + 1], static_cast<uint32_t>(a & 2) * 8);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t lo = k + 2 * c < K ? src[2 * c] : 0, hi = k + 2 * c + 1 < K ? src[2 * c + 1] : 0;
+        v[c] = lo | (hi << 16);
+      }
     }
     reinterpret_cast<uint4*>(is_x ? px : pw)[j] = make_uint4(v[0], v[1], v[2], v[3]);
   }
@@ -995,8 +1081,12 @@ struct Option {
   int (*ready)(int* clusters);  // status; makes the configuration ready on this device
   int (*launch)(const LinearParams& p, cudaStream_t st);
   double fixed_us;  // a launch of one tile per cluster without its stages
+  double stage_us;  // a 64-k stage of a CTA by itself
+  double l2_rate;   // bytes per us that L2 gives all CTAs together
+  int stage_bytes;
   int rows, cols;   // x rows and W rows of a tile
   int parts;        // pieces of K
+  int ctas, stages; // CTAs of a cluster, stages of a CTA's ring
   bool persistent;
 };
 
@@ -1057,29 +1147,36 @@ struct Split {
 
 template <bool GATED, int PARTS>
 Option pair_option(double fixed) {
-  return {Pair<GATED, PARTS>::ready, Pair<GATED, PARTS>::launch, fixed, 256, 256, PARTS, PARTS == 1};
+  return {Pair<GATED, PARTS>::ready, Pair<GATED, PARTS>::launch, fixed, 0.26, 18e6, kPairStageBytes, 256, 256, PARTS, 2 * PARTS, kPairStages,
+          PARTS == 1};
 }
 template <int BN, bool GATED, int SPLITS>
 Option split_option(double fixed) {
-  return {Split<BN, GATED, SPLITS>::ready, Split<BN, GATED, SPLITS>::launch, fixed, BN, 128, SPLITS, false};
+  return {Split<BN, GATED, SPLITS>::ready, Split<BN, GATED, SPLITS>::launch, fixed, BN == 32 ? 0.2 : 0.18, 12e6, SplitCfg<BN>::kStageBytes, BN, 128, SPLITS,
+          SPLITS,
+          SplitCfg<BN>::kStages, false};
 }
 
 // Configuration asked for by a test (rows of a tile * 16 + pieces of K), 0: none.
 std::atomic<int> g_force{0};
 
 // The configuration with the smallest estimate
-//   fixed + 0.26 us * (64-k stages of a piece) * waves + (waves - 1) * (fixed - 3 us, a launch; 0 when persistent)
-// 0.26 us is what a stage takes in every configuration that memory does not bound; the fixed times are launches of one
-// wave extrapolated to no stages, measured on a GB300 (M x N x K = 64 x 256 x 7168, 128 x 8192 x 7168,
-// 256 x 4096 x 7168 gated, 2048 x 256 x 7168, with 1 to 8 pieces).
+//   fixed + max(stage * (64-k stages of a piece), W / rate) * waves + (waves - 1) * (fixed - 3 us, a launch; 0 when
+//   persistent)
+// stage: what a stage takes where memory does not bound it, 0.26 us in the pair kernel (its products) and 0.18 to 0.2 us
+// in the split kernel (its loads), or what L2 needs for the stages of all CTAs (12 TB/s for the split kernel; 18 TB/s for
+// the pair kernel, which reads most lines for many CTAs at once).  rate: 6 TB/s of memory, or what the bytes in flight of
+// the CTAs give at 1.2 us of latency.  fixed: launches of one wave extrapolated to no stages.  Measured on a GB300 (M x N
+// x K = 64 x 256 x 7168, 64 x 4096 x 7168 and 256 x 4096 x 7168 gated, 128 x 7168 x 2048, 777 x 1001 x 1544,
+// 2048 x 256 x 7168, every configuration).
 template <bool GATED>
 int launch_best(const LinearParams& p, cudaStream_t st) {
   static const Option options[] = {
-      pair_option<GATED, 1>(8.0),          pair_option<GATED, 2>(8.0),          pair_option<GATED, 4>(9.3),
-      split_option<128, GATED, 1>(9.0),    split_option<128, GATED, 2>(9.3),    split_option<128, GATED, 4>(9.5),
-      split_option<64, GATED, 1>(5.3),     split_option<64, GATED, 2>(5.5),     split_option<64, GATED, 4>(5.5),
-      split_option<64, GATED, 8>(4.8),     split_option<32, GATED, 1>(3.3),     split_option<32, GATED, 2>(3.4),
-      split_option<32, GATED, 4>(3.4),     split_option<32, GATED, 8>(3.4),
+      pair_option<GATED, 1>(8.0),          pair_option<GATED, 2>(8.0),          pair_option<GATED, 4>(10.5),
+      split_option<128, GATED, 1>(7.4),    split_option<128, GATED, 2>(7.4),    split_option<128, GATED, 4>(7.4),
+      split_option<64, GATED, 1>(4.2),     split_option<64, GATED, 2>(4.2),     split_option<64, GATED, 4>(4.2),
+      split_option<64, GATED, 8>(4.3),     split_option<32, GATED, 1>(3.3),     split_option<32, GATED, 2>(3.4),
+      split_option<32, GATED, 4>(3.4),     split_option<32, GATED, 8>(3.5),
   };
   const Option* best = nullptr;
   double best_us = 0.0;
@@ -1091,7 +1188,12 @@ int launch_best(const LinearParams& p, cudaStream_t st) {
     if (int rc = o.ready(&clusters)) return rc;
     const int64_t tiles = ceil_div(p.M, o.rows) * ceil_div(p.N, o.cols);
     const int64_t waves = ceil_div(tiles, clusters);
-    const double us = o.fixed_us + 0.26 * static_cast<double>(ceil_div(kblocks, o.parts) * waves) +
+    const double ctas = static_cast<double>(std::min<int64_t>(tiles, clusters)) * o.ctas;
+    const double rate = std::min(6.0e6, ctas * o.stages * kATile / 1.2);  // bytes of W per us
+    const double w_us = 2.0 * p.N * p.K / rate / static_cast<double>(waves);
+    const double stage_us = std::max(o.stage_us, ctas * o.stage_bytes / o.l2_rate);
+    const double us = o.fixed_us +
+                      std::max(stage_us * static_cast<double>(ceil_div(kblocks, o.parts)), w_us) * waves +
                       (o.persistent ? 0.0 : (waves - 1) * (o.fixed_us - 3.0));
     if (!best || us < best_us) {
       best = &o;
@@ -1105,23 +1207,28 @@ int launch_best(const LinearParams& p, cudaStream_t st) {
 }  // namespace
 
 int launch_linear_tc(LinearParams p, void* ws, size_t ws_bytes, cudaStream_t st) {
-  if (!(aligned16(p.x) && aligned16(p.w) && p.ldx % 8 == 0 && p.ldw % 8 == 0)) {
-    const int64_t k8 = ceil_div(p.K, 8);
-    const size_t need = static_cast<size_t>(p.M + static_cast<int64_t>(p.N)) * k8 * 16;
+  const bool x_ok = aligned16(p.x) && p.ldx % 8 == 0, w_ok = aligned16(p.w) && p.ldw % 8 == 0;
+  if (!x_ok || !w_ok) {  // TMA takes rows on 16-byte boundaries only
+    const int64_t k8 = ceil_div(p.K, 8), items_x = x_ok ? 0 : p.M * k8, items = items_x + (w_ok ? 0 : p.N * k8);
+    const size_t need = static_cast<size_t>(items) * 16;
     W4A8_REQUIRE(ws && ws_bytes >= need && aligned16(ws),
                  "x and w without 16-byte alignment need %zu bytes of 16-byte aligned workspace", need);
     uint16_t* px = static_cast<uint16_t*>(ws);
-    uint16_t* pw = px + p.M * k8 * 8;
-    const int64_t items = (p.M + static_cast<int64_t>(p.N)) * k8;
+    uint16_t* pw = px + items_x * 8;
     const int64_t blocks = ceil_div(items, 256);
     if (int rc = launch_pdl("linear_repack_kernel", linear_repack_kernel,
                             dim3(static_cast<unsigned>(blocks < 32 * num_sms() ? blocks : 32 * num_sms())), dim3(256), 0,
-                            st, static_cast<const uint16_t*>(p.x), p.ldx, p.M * k8, px,
+                            st, static_cast<const uint16_t*>(p.x), p.ldx, items_x, px,
                             static_cast<const uint16_t*>(p.w), p.ldw, items, pw, p.K, static_cast<int>(k8)))
       return rc;
-    p.x = px;
-    p.w = pw;
-    p.ldx = p.ldw = k8 * 8;
+    if (!x_ok) {
+      p.x = px;
+      p.ldx = k8 * 8;
+    }
+    if (!w_ok) {
+      p.w = pw;
+      p.ldw = k8 * 8;
+    }
   }
   return p.gated ? launch_best<true>(p, st) : launch_best<false>(p, st);
 }
