@@ -368,6 +368,15 @@ int w4a8_moe_forward(const uint16_t* x, const float* logits, int64_t T, int64_t 
 size_t w4a8_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int k);
 
 /*
+ * The same layer with the routing given: steps (2) to (6) for topk_ids int32 [T][k] in [0, E) and topk_w fp32
+ * [T][k], such as moe_route_grouped_topk writes them.  The workspace is that of w4a8_moe_forward (its topk_ids and
+ * topk_w parts stay unused).  1 <= k <= min(E, 32).
+ */
+int w4a8_moe_forward_routed(const uint16_t* x, const int32_t* topk_ids, const float* topk_w, int64_t T, int64_t H,
+                            int64_t I, int64_t E, int k, const uint8_t* w13, const float* w13_s, const uint8_t* w2,
+                            const float* w2_s, uint16_t* out, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * One expert-parallel shard of the layer (PR #7762 page, ep-moe mode and the
  * expert_map review of ep_moe/layer.py): routing over all E experts, then
  * (2') with expert_map, and the rest over the pairs routed to this shard's

@@ -77,6 +77,12 @@ def _linear(L, x=P16, ldx=64, w=P16, ldw=64, dt=BF16, bias=NULL, bd=F32, act=0, 
     (lambda L: _linear(L, out=NULL), b"null"),
     (lambda L: _linear(L, w=P17), b"aligned"),
     (lambda L: _linear(L, od=F32, out=P18), b"aligned"),
+    (lambda L: L.w4a8_moe_forward_routed(P16, P16, P16, 4, 256, 256, 8, 9, P16, P16, P16, P16, P16, P16, 1 << 30, NULL),
+     b"k=9"),
+    (lambda L: L.w4a8_moe_forward_routed(P16, NULL, P16, 4, 256, 256, 8, 2, P16, P16, P16, P16, P16, P16, 1 << 30, NULL),
+     b"null"),
+    (lambda L: L.w4a8_moe_forward_routed(P16, P16, P16, 4, 256, 256, 8, 2, P16, P16, P16, P16, P16, P16, 10, NULL),
+     b"workspace too small"),
 ])
 def test_refused_before_launch(clib, call, msg):
     assert call(clib) == 1  # W4A8_ERR_INVALID_ARG

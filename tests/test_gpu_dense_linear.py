@@ -69,6 +69,19 @@ def test_whole_numbers_are_exact(lib, M, N, K, dtype):
     assert torch.equal(got.cpu().double(), want)
 
 
+@pytest.mark.parametrize("M,N,K", [(2, 64, 16384), (30, 128, 16384), (200, 512, 16384), (1300, 2000, 16384),
+                                   (600, 512, 8000)])
+def test_long_sums_stay_fp32(lib, M, N, K):
+    # Sums on the tensor core are cut off at every addition of 16 products, to one side.  With at most 64 additions
+    # (1024 products) to a sum before it is added up in fp32, each cut at most 2^-23 of its sum, the error stays below
+    # 64 * 2^-23 of the result's norm; a single sum over K = 16384 would be off by about 1024 / 3 * 2^-23.
+    g = torch.Generator("cuda").manual_seed(21)
+    x, w = _mat(M, K, "bf16", g), _mat(N, K, "bf16", g)
+    got = lib.dense_linear(x, w, out_dtype=torch.float32).double()
+    want = x.double() @ w.double().t()
+    assert (got - want).norm() <= 64 * 2.0 ** -23 * want.norm()
+
+
 CONFIGS = [(256, 1), (256, 2), (256, 4), (128, 1), (128, 2), (128, 4), (64, 1), (64, 2), (64, 4), (64, 8), (32, 1),
            (32, 2), (32, 4), (32, 8)]
 
@@ -91,6 +104,13 @@ def test_every_configuration(lib, config, M, N, K, gated):
     assert torch.equal(got.cpu().double(), x.cpu().double() @ w.cpu().double().t())
     _check(lib, M, N, K, gated=gated, act="silu" if gated else "gelu", bias="f32", residual=True, seed=N)
     _check(lib, M, N, K, gated=gated, act="relu", out="f32", residual=True, opad=1, seed=N)
+    # fp32 outputs of a long K: sums in pieces
+    x, w = _mat(M, 4224, "bf16", g, ints=True), _mat(N, 4224, "bf16", g, ints=True)
+    r = _mat(M, N // 2 if gated else N, "f32", g, ints=True)
+    z = x.cpu().double() @ w.cpu().double().t()
+    want = (z[:, :N // 2].clamp_min(0) * z[:, N // 2:] if gated else z.clamp_min(0)) + r.cpu().double()
+    got = lib.dense_linear(x, w, act="relu", gated=gated, residual=r, out_dtype=torch.float32).cpu().double()
+    assert torch.equal(got, want.float().double() if gated else want)
 
 
 def test_configuration_that_does_not_exist(lib):

@@ -61,6 +61,8 @@ _SIGS = {
     "w4a8_moe_forward_noalloc": (_c_int, [_c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_vp,
                                           _c_vp, _c_vp, _c_vp, _c_vp, _c_vp]),
     "w4a8_moe_noalloc_scratch_bytes": (_c_sz, []),
+    "w4a8_moe_forward_routed": (_c_int, [_c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_vp,
+                                         _c_vp, _c_vp, _c_vp, _c_vp, _c_sz, _c_vp]),
     "moe_route_grouped_topk": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_vp, _c_int, _c_int,
                                         _c_int, _c_int, _c_f32, _c_vp, _c_vp, _c_vp]),
     "block_norm": (_c_int, [_c_vp, _c_i64, _c_int, _c_vp, _c_i64, _c_int, _c_int, _c_vp, _c_vp, _c_vp, _c_i64,
@@ -356,6 +358,31 @@ def w4a8_moe_forward(x, logits, k: int, w13, w13_s, w2, w2_s, renormalize: bool 
         out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
     _check(load().w4a8_moe_forward(_p(x), _p(logits), T, H, I, E, k, int(bool(renormalize)), _p(w13), _p(w13_s),
                                    _p(w2), _p(w2_s), _p(out), _p(ws), ws.numel(), _stream()))
+    return out
+
+
+def w4a8_moe_forward_routed(x, topk_ids, topk_w, w13, w13_s, w2, w2_s, ws=None, out=None):
+    """The layer with its routing given (topk_ids int32 [T, k], topk_w fp32 [T, k], as moe_route_grouped_topk returns
+    them); everything else as in w4a8_moe_forward."""
+    _req(x, torch.bfloat16, "x", 2)
+    _req(topk_ids, torch.int32, "topk_ids", 2)
+    _req(topk_w, torch.float32, "topk_w", 2)
+    _req(w13, torch.uint8, "w13", 3)
+    _req(w2, torch.uint8, "w2", 3)
+    _req(w13_s, torch.float32, "w13_s", 3)
+    _req(w2_s, torch.float32, "w2_s", 3)
+    T, H = x.shape
+    k = topk_ids.shape[1]
+    E = w13.shape[0]
+    I = w13.shape[1] // 2
+    if topk_ids.shape != (T, k) or topk_w.shape != (T, k):
+        raise ValueError(f"topk_ids and topk_w must have {T} rows and the same shape")
+    if ws is None:
+        ws = torch.empty(int(load().w4a8_moe_workspace_bytes(T, H, I, E, k)), dtype=torch.uint8, device=x.device)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    _check(load().w4a8_moe_forward_routed(_p(x), _p(topk_ids), _p(topk_w), T, H, I, E, k, _p(w13), _p(w13_s), _p(w2),
+                                          _p(w2_s), _p(out), _p(ws), ws.numel(), _stream()))
     return out
 
 

@@ -128,10 +128,13 @@ extern "C" size_t w4a8_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int6
   return L.total;
 }
 
-extern "C" int w4a8_moe_forward(const uint16_t* x, const float* logits, int64_t T, int64_t H, int64_t I, int64_t E,
-                                int k, int renormalize, const uint8_t* w13, const float* w13_s, const uint8_t* w2,
-                                const float* w2_s, uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
-  using namespace w4a8;
+namespace w4a8 {
+namespace {
+
+// The layer with its routing: topk ids and weights given (ids, tw), or computed into the workspace from logits.
+int moe_layer(const uint16_t* x, const float* logits, const int32_t* ids, const float* tw, int64_t T, int64_t H,
+              int64_t I, int64_t E, int k, int renormalize, const uint8_t* w13, const float* w13_s, const uint8_t* w2,
+              const float* w2_s, uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
   w4a8_moe_layout L;
   int rc = layout_of(T, H, I, E, k, &L);
   if (rc) return rc;
@@ -139,8 +142,6 @@ extern "C" int w4a8_moe_forward(const uint16_t* x, const float* logits, int64_t 
   W4A8_REQUIRE((reinterpret_cast<uintptr_t>(ws) & 255) == 0, "workspace must be 256-byte aligned");
   if (T == 0) return W4A8_OK;
   uint8_t* b = static_cast<uint8_t*>(ws);
-  int32_t* ids = reinterpret_cast<int32_t*>(b + L.topk_ids);
-  float* tw = reinterpret_cast<float*>(b + L.topk_w);
   int64_t* seg = reinterpret_cast<int64_t*>(b + L.seg_indptr);
   int32_t* s2d = reinterpret_cast<int32_t*>(b + L.src2dst);
   int32_t* d2s = reinterpret_cast<int32_t*>(b + L.dst2src);
@@ -153,7 +154,13 @@ extern "C" int w4a8_moe_forward(const uint16_t* x, const float* logits, int64_t 
   float* hc = reinterpret_cast<float*>(b + L.hc);
   uint16_t* y2 = reinterpret_cast<uint16_t*>(b + L.y2);
   const int64_t P = T * k;
-  if ((rc = moe_route_topk(logits, T, E, k, renormalize, ids, tw, stream))) return rc;
+  if (!ids) {
+    int32_t* ws_ids = reinterpret_cast<int32_t*>(b + L.topk_ids);
+    float* ws_tw = reinterpret_cast<float*>(b + L.topk_w);
+    if ((rc = moe_route_topk(logits, T, E, k, renormalize, ws_ids, ws_tw, stream))) return rc;
+    ids = ws_ids;
+    tw = ws_tw;
+  }
   if ((rc = moe_permute(ids, T, k, E, seg, s2d, d2s, b + L.permute_ws, permute_ws_bytes(P, E), stream))) return rc;
   if ((rc = fp8_quant_scatter_per_token_group(x, T, H, s2d, k, P, xq, xs, xc, L.scale_ld, stream))) return rc;
   // w13, then SiLU-and-Mul requantisation in its own kernel: with the requantisation fused into w13's
@@ -165,6 +172,27 @@ extern "C" int w4a8_moe_forward(const uint16_t* x, const float* logits, int64_t 
   if ((rc = w4a8_grouped_gemm(hq, hs, hc, L.scale_ld, w2, w2_s, seg, E, H, I, P, y2, nullptr, 0, stream)))
     return rc;
   return moe_unpermute_combine(y2, s2d, tw, T, k, H, out, stream);
+}
+
+}  // namespace
+}  // namespace w4a8
+
+extern "C" int w4a8_moe_forward(const uint16_t* x, const float* logits, int64_t T, int64_t H, int64_t I, int64_t E,
+                                int k, int renormalize, const uint8_t* w13, const float* w13_s, const uint8_t* w2,
+                                const float* w2_s, uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
+  return w4a8::moe_layer(x, logits, nullptr, nullptr, T, H, I, E, k, renormalize, w13, w13_s, w2, w2_s, out, ws,
+                         ws_bytes, stream);
+}
+
+extern "C" int w4a8_moe_forward_routed(const uint16_t* x, const int32_t* topk_ids, const float* topk_w, int64_t T,
+                                       int64_t H, int64_t I, int64_t E, int k, const uint8_t* w13, const float* w13_s,
+                                       const uint8_t* w2, const float* w2_s, uint16_t* out, void* ws, size_t ws_bytes,
+                                       void* stream) {
+  using namespace w4a8;
+  W4A8_REQUIRE(E >= 1 && E <= 1024, "E=%lld must be in [1, 1024]", (long long)E);
+  W4A8_REQUIRE(k >= 1 && k <= 32 && k <= E, "k=%d must be in [1, min(E, 32)]", k);
+  W4A8_REQUIRE(T == 0 || (topk_ids && topk_w), "null pointer");
+  return moe_layer(x, nullptr, topk_ids, topk_w, T, H, I, E, k, 0, w13, w13_s, w2, w2_s, out, ws, ws_bytes, stream);
 }
 
 extern "C" int w4a8_moe_forward_ep(const uint16_t* x, const float* logits, int64_t T, int64_t H, int64_t I,

@@ -90,10 +90,35 @@ __global__ void __launch_bounds__(kWarps * 32) linear_stream_kernel(const Linear
 #pragma unroll
       for (int i = 0; i < 4; ++i) c[r][j][i] = 0.f;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  // pieces of 2 * kStep elements, dealt round-robin to the warps of all splits
+  // pieces of 2 * kStep elements, dealt round-robin to the warps of all splits.  The tensor core cuts off at every
+  // addition to its accumulator, so long sums drift: every kChunk pieces they move to sums that are rounded to nearest.
+  constexpr int kChunk = 16;
+  float sum[R][NT][4];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[r][j][i] = 0.f;
+  auto flush = [&] {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[r][j][i] += c[r][j][i];
+          c[r][j][i] = 0.f;
+        }
+  };
   const int pieces = (p.K + 2 * kStep - 1) / (2 * kStep);
+  int until_flush = kChunk;
 #pragma unroll 2
   for (int q = split * kWarps + warp; q < pieces; q += splits * kWarps) {
+    if (--until_flush < 0) {
+      flush();
+      until_flush = kChunk - 1;
+    }
     uint4 a[2][R][2], b[2][NT];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -116,6 +141,7 @@ __global__ void __launch_bounds__(kWarps * 32) linear_stream_kernel(const Linear
           mma16816<F16>(c[r][j], a0.z, a1.z, a0.w, a1.w, x.z, x.w);
         }
   }
+  flush();
   // partial products of the warps: [warp][r][token][16 columns]
   float* mine = smem + warp * kTile;
 #pragma unroll
@@ -124,7 +150,7 @@ __global__ void __launch_bounds__(kWarps * 32) linear_stream_kernel(const Linear
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        mine[(r * NT * 8 + j * 8 + 2 * t4 + (i & 1)) * 16 + g + 8 * (i >> 1)] = c[r][j][i];
+        mine[(r * NT * 8 + j * 8 + 2 * t4 + (i & 1)) * 16 + g + 8 * (i >> 1)] = sum[r][j][i];
   __syncthreads();
   if (splits > 1) {
     cluster_wait();

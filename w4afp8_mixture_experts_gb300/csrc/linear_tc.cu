@@ -329,10 +329,18 @@ __device__ __forceinline__ void store_row(const LinearParams& p, const PairPlan&
   }
 }
 
+// The tensor core cuts off what does not fit the accumulator at every addition, so a sum of n products of 16 k is off by
+// about n / 2 units of fp32 to one side (3.8e-6 of the result at K = 3584, where plain fp32 sums have 0.9e-6).  That does
+// not show in a 16-bit output; for an fp32 one, sums over kChunk stages are added up in registers, rounded to nearest.
+constexpr int kChunk = 16;
+constexpr int kRegsLaunch = 168;  // of a thread at launch (checked on the host)
+constexpr int kRegsRoles = 40, kRegsSums = 232;  // registers of warps 0-3 and of the epilogue's, which hold 128 sums
+static_assert(128 * kRegsRoles + 32 * kPairEpiWarps * kRegsSums <= kPairThreads * kRegsLaunch, "within the launch's registers");
+
 // PARTS = 1: persistent over tiles, the accumulator double buffered.  PARTS > 1: a cluster of PARTS pairs computes
 // one tile, each pair a piece of K, and finishes 1 / PARTS of its columns: the other pairs push their partial
-// products of those columns into its (by then idle) operand stages.
-template <bool GATED, int PARTS>
+// products of those columns into its (by then idle) operand stages.  CHUNKED: sums in pieces of kChunk stages.
+template <bool GATED, int PARTS, bool CHUNKED>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw,
                        const LinearParams p, const PairPlan pl) {
@@ -375,6 +383,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
+  if constexpr (CHUNKED) {
+    if (warp < 4) regs_release<kRegsRoles>();
+  }
 
   const int first = blockIdx.x / (2 * PARTS), stride = PARTS > 1 ? pl.tiles : gridDim.x / 2;
   const int kb0 = static_cast<int>(static_cast<int64_t>(part) * pl.kblocks / PARTS);
@@ -410,26 +421,30 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t idesc = idesc_f16(p.dtype == W4A8_DTYPE_BF16, 256, 256);
     const uint16_t both = static_cast<uint16_t>(3 << lead);
     uint32_t it = 0;
-    int n = 0;
+    int n = 0;  // accumulator fills so far
     bool ok = true;
-    for (int i = first; ok && i < pl.tiles; i += stride, ++n) {
-      const int buf = n & 1;
-      if (!(ok = warp_wait(&tempty[buf], ((n >> 1) & 1) ^ 1, abort_flag))) break;
-      tc_fence_after();
+    for (int i = first; ok && i < pl.tiles; i += stride) {
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int s = it % kPairStages;
+        const int s = it % kPairStages, at_chunk = CHUNKED ? (kb - kb0) % kChunk : kb - kb0;
+        const int buf = n & 1;
+        if (at_chunk == 0) {
+          if (!(ok = warp_wait(&tempty[buf], ((n >> 1) & 1) ^ 1, abort_flag))) break;
+          tc_fence_after();
+        }
         if (!(ok = warp_wait(&full[s], (it / kPairStages) & 1, abort_flag))) break;
         tc_fence_after();
         const uint32_t at = smem_u32(smem + s * kPairStageBytes);
         const uint64_t a = operand_desc(at), b = operand_desc(at + kATile);
+        const bool last = kb + 1 == kb1 || (CHUNKED && at_chunk == kChunk - 1);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k)
-            mma_f16<2>(tmem + buf * 256, a + 2 * k, b + 2 * k, idesc, kb > kb0 || k > 0);
+            mma_f16<2>(tmem + buf * 256, a + 2 * k, b + 2 * k, idesc, at_chunk > 0 || k > 0);
           commit_pair(&empty[s], both);
-          if (kb + 1 == kb1) commit_pair(&tfull[buf], both);
+          if (last) commit_pair(&tfull[buf], both);
         }
         __syncwarp();
+        n += last;
       }
     }
     if (!ok) {
@@ -488,23 +503,66 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     for (int i = 0; i < kPieces; ++i)
       if (m < p.M && n0 + 16 * i + 16 <= p.n_out) load32b(r + 16 * i, pl.vec_out == 2, res[i]);
   };
-  const bool ahead = p.residual && pl.vec_out && p.out_dtype != W4A8_DTYPE_F32;
+  const bool ahead = !CHUNKED && p.residual && pl.vec_out && p.out_dtype != W4A8_DTYPE_F32;  // CHUNKED: fp32 output
+  const uint32_t tempty0 = map_to_cta(smem_u32(tempty), lead);
+  int n = 0;  // accumulator fills so far
+  // Waits for the products of a tile and returns the accumulator that holds them (-1 after an abort).  CHUNKED: every
+  // thread adds up 128 columns of its row over the chunks and puts the sums back into the last chunk's accumulator.
+  auto products = [&]() -> int {
+    if constexpr (CHUNKED) {
+      const int chunks = (kb1 - kb0 + kChunk - 1) / kChunk;
+      float sum[4][32];
+      for (int ch = 0; ch < chunks; ++ch, ++n) {
+        const int buf = n & 1;
+        if (__any_sync(0xffffffffu, !wait_bar(&tfull[buf], (n >> 1) & 1, abort_flag))) return -1;
+        tc_fence_after();
+        if (chunks == 1) break;
+        const uint32_t at = tmem + buf * 256 + lanes + half * 128;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          float v[16];
+          tmem_ld16(at + 16 * q, reinterpret_cast<uint32_t*>(v));
+          tmem_wait_ld_pin<16>(reinterpret_cast<uint32_t*>(v));
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[q / 2][q % 2 * 16 + j] = ch > 0 ? sum[q / 2][q % 2 * 16 + j] + v[j] : v[j];
+        }
+        if (ch + 1 < chunks) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) remote_arrive(tempty0 + buf * 8);
+          continue;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_st32(at + 32 * q, reinterpret_cast<const uint32_t*>(sum[q]));
+        tmem_wait_st();
+        tc_fence_before();
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kPairEpiWarps) : "memory");  // the epilogue warps share columns
+        tc_fence_after();
+        break;
+      }
+      return n++ & 1;
+    } else {
+      const int buf = n & 1;
+      if (__any_sync(0xffffffffu, !wait_bar(&tfull[buf], (n >> 1) & 1, abort_flag))) return -1;
+      tc_fence_after();
+      ++n;
+      return buf;
+    }
+  };
 
   if constexpr (PARTS == 1) {
     if (warp >= 4) {
-      const uint32_t tempty0 = map_to_cta(smem_u32(tempty), lead);
-      int n = 0;
-      for (int i = first; i < pl.tiles; i += stride, ++n) {
+      if constexpr (CHUNKED) regs_claim<kRegsSums>();
+      for (int i = first; i < pl.tiles; i += stride) {
         int tm, tn;
         pair_tile(pl, i, tm, tn);
-        const int buf = n & 1;
         const int n0 = tn * pl.out_cols + nh;
         const int m0 = tm * 256 + rank * 128 + quarter * 32;
         uint32_t res[kPieces][8];
         if (ahead) read_ahead(m0 + lane, n0, res);
         if (p.bias) load_bias(n0);
-        if (__any_sync(0xffffffffu, !wait_bar(&tfull[buf], (n >> 1) & 1, abort_flag))) break;
-        tc_fence_after();
+        const int buf = products();
+        if (buf < 0) break;
         const uint32_t at = tmem + buf * 256 + lanes + nh;
 #pragma unroll 1
         for (int c = 0; c < kCols; c += 32) {
@@ -529,7 +587,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
       }
     }
-  } else {
+  } else if (warp >= 4) {
+    if constexpr (CHUNKED) regs_claim<kRegsSums>();
     constexpr int kPart = 2 * kCols * (GATED ? 2 : 1);  // columns of products that a CTA finishes: 256 / PARTS
     float* recv = reinterpret_cast<float*>(smem);       // [PARTS - 1][kPart][128 tokens]
     static_assert((PARTS - 1) * kPart * 128 * 4 <= kPairStages * kPairStageBytes, "partial products in the stages");
@@ -538,16 +597,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int n0 = tn * pl.out_cols + nh;
     const int m0 = tm * 256 + rank * 128 + quarter * 32;
     uint32_t res[kPieces][8];
-    if (warp >= 4) {
-      if (ahead) read_ahead(m0 + lane, n0, res);
-      if (p.bias) load_bias(n0);
-    }
+    if (ahead) read_ahead(m0 + lane, n0, res);
+    if (p.bias) load_bias(n0);
+    const int buf = products();
+    const bool ok = buf >= 0;
+    const uint32_t acc = tmem + lanes + max(buf, 0) * 256;
     __syncwarp();
-    const bool ok = !__any_sync(0xffffffffu, !wait_bar(&tfull[0], 0, abort_flag));
-    tc_fence_after();
+    tc_fence_before();
     cluster_arrive();  // every pair's products are done: no operand stage is in use any more
     cluster_wait();
-    if (warp >= 4 && ok) {
+    tc_fence_after();
+    if (ok) {
       const uint32_t to0 = smem_u32(recv) + (quarter * 32 + lane) * 4;
 #pragma unroll 1
       for (int q = 0; q < PARTS; ++q) {
@@ -559,7 +619,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           for (int h = 0; h < (GATED ? 2 : 1); ++h) {
             float v[kN];
             __syncwarp();
-            const uint32_t at = tmem + lanes + h * kHalf + q * 2 * kCols + half * kCols + c;
+            const uint32_t at = acc + h * kHalf + q * 2 * kCols + half * kCols + c;
             if constexpr (kN == 32)
               tmem_ld32(at, reinterpret_cast<uint32_t*>(v));
             else
@@ -576,13 +636,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     cluster_arrive();
     cluster_wait();
-    if (warp >= 4 && ok && n0 < p.n_out) {
+    if (ok && n0 < p.n_out) {
       const float* mine = recv + quarter * 32 + lane;
 #pragma unroll 1
       for (int c = 0; c < kCols; c += kN) {
         float v[kN], u[kN];
         __syncwarp();
-        const uint32_t at = tmem + lanes + nh + c;
+        const uint32_t at = acc + nh + c;
         if constexpr (kN == 32) {
           tmem_ld32(at, reinterpret_cast<uint32_t*>(v));
           if (GATED) tmem_ld32(at + kHalf, reinterpret_cast<uint32_t*>(u));
@@ -607,6 +667,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
           for (int q = 0; q < 8; ++q) res[j][q] = res[j + kN / 16][q];
       }
+    }
+  } else {  // warps 0-3 take part in the two cluster barriers
+    __syncwarp();
+    for (int i = 0; i < 2; ++i) {
+      cluster_arrive();
+      cluster_wait();
     }
   }
   __syncwarp();
@@ -638,7 +704,7 @@ struct SplitCfg {
   // otherwise its parity wait is satisfied by the phase before the one it needs.
   static_assert(kStages % kMma == 0, "ring depth a multiple of the MMA warps");
   static constexpr int kTurns = BN * 16 / kSplitThreads;  // tokens of a thread in the epilogue, at most
-  static constexpr uint32_t kTmemCols = kMma * BN;
+  static constexpr uint32_t kTmemCols = 2 * kMma * BN;  // an fp32 output spreads its sums over two accumulators a warp
   static_assert(kSmem <= kMaxSmem, "shared memory");
 };
 
@@ -829,6 +895,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   float bias[8], bias2[8];
   uint4 res[SplitCfg<BN>::kTurns];
   read_ahead_split<BN, GATED>(p, m0 + rank * own, n0, own, vec_out, bias, bias2, res);
+  const int accs = (p.out_dtype == W4A8_DTYPE_F32 ? 2 : 1) * C::kMma;
   int issued = 0;  // stages whose loads this warp has issued
   if (warp == 0) {
     for (int kb = kb0; kb < kb1; ++kb, ++issued) {
@@ -848,6 +915,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   } else if (warp >= 4 && warp < 4 + C::kMma) {
     const uint32_t idesc = idesc_f16(p.dtype == W4A8_DTYPE_BF16, 128, BN);
     const int m = warp - 4, stages = kb1 - kb0;
+    const int second = accs > C::kMma ? C::kMma * BN : 0;  // the second accumulator, every other time
     bool ok = true;
     for (int it = m; it < stages; it += C::kMma) {
       const int s = it % C::kStages;
@@ -857,7 +925,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       const uint64_t a = operand_desc(at), b = operand_desc(at + kATile);
       if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kBK / 16; ++k) mma_f16<1>(tmem + m * BN, a + 2 * k, b + 2 * k, idesc, it > m || k > 0);
+        for (int k = 0; k < kBK / 16; ++k)
+          mma_f16<1>(tmem + m * BN + (it / C::kMma % 2) * second, a + 2 * k, b + 2 * k, idesc, it >= accs || k > 0);
         mma_commit(&empty[s]);
       }
       __syncwarp();
@@ -885,8 +954,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     for (int c = (warp >> 2) * kCols; c < (warp >> 2) * kCols + kCols; c += kStep) {
       float v[kStep];
 #pragma unroll
-      for (int m = 0; m < C::kMma; ++m) {
-        if (m > 0 && m >= kb1 - kb0) break;  // fewer stages than MMA warps: no products in that accumulator
+      for (int m = 0; m < 2 * C::kMma; ++m) {
+        if (m >= accs || (m > 0 && m >= kb1 - kb0)) break;  // fewer stages than accumulators: no products in that one
         float w[kStep];
         const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + m * BN + c;
         if constexpr (kStep == 32)
@@ -1027,8 +1096,16 @@ int vec_rows(const LinearParams& p) {
 class Launcher {
  public:
   template <class... KArgs>
-  int prepare(void (*kern)(KArgs...), size_t smem, int threads, int cluster) {
+  int prepare(void (*kern)(KArgs...), size_t smem, int threads, int cluster, int least_regs = 0) {
     return once_.run([&] {
+      // setmaxnreg.inc waits until the released registers cover the request: they must be there
+      cudaFuncAttributes fa;
+      if (least_regs) {
+        if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return check_launch("cudaFuncGetAttributes(linear)");
+        if (fa.numRegs < least_regs)
+          return set_error(W4A8_ERR_UNSUPPORTED, "linear kernel built with %d registers per thread: %d are needed",
+                           fa.numRegs, least_regs);
+      }
       if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return check_launch("cudaFuncSetAttribute(linear)");
       cudaLaunchAttribute attr[1];
@@ -1090,18 +1167,21 @@ struct Option {
   bool persistent;
 };
 
-template <bool GATED, int PARTS>
+template <bool GATED, int PARTS, bool CHUNKED>
 struct Pair {
   static Launcher& launcher() {
     static Launcher l;
     return l;
   }
   static int ready(int* clusters) {
-    const int rc = launcher().prepare(linear_pair_kernel<GATED, PARTS>, kPairSmem, kPairThreads, 2 * PARTS);
+    const int rc = launcher().prepare(linear_pair_kernel<GATED, PARTS, CHUNKED>, kPairSmem, kPairThreads, 2 * PARTS,
+                                      CHUNKED ? kRegsLaunch : 0);
     *clusters = launcher().clusters();
     return rc;
   }
   static int launch(const LinearParams& p, cudaStream_t st) {
+    if (!CHUNKED && p.out_dtype == W4A8_DTYPE_F32 && p.K > kChunk * kBK * PARTS)
+      return Pair<GATED, PARTS, true>::launch(p, st);
     CUtensorMap tx, tw;
     int rc, clusters;
     if ((rc = ready(&clusters))) return rc;
@@ -1115,7 +1195,7 @@ struct Pair {
     pl.kblocks = static_cast<int>(ceil_div(p.K, kBK));
     pl.vec_out = vec_rows(p);
     const int n = PARTS > 1 || pl.tiles < clusters ? pl.tiles : clusters;
-    return Launcher::launch("linear_pair_kernel", linear_pair_kernel<GATED, PARTS>, dim3(2 * PARTS * n), kPairThreads,
+    return Launcher::launch("linear_pair_kernel", linear_pair_kernel<GATED, PARTS, CHUNKED>, dim3(2 * PARTS * n), kPairThreads,
                             kPairSmem, 2 * PARTS, st, tx, tw, p, pl);
   }
 };
@@ -1147,7 +1227,7 @@ struct Split {
 
 template <bool GATED, int PARTS>
 Option pair_option(double fixed) {
-  return {Pair<GATED, PARTS>::ready, Pair<GATED, PARTS>::launch, fixed, 0.26, 18e6, kPairStageBytes, 256, 256, PARTS, 2 * PARTS, kPairStages,
+  return {Pair<GATED, PARTS, false>::ready, Pair<GATED, PARTS, false>::launch, fixed, 0.26, 18e6, kPairStageBytes, 256, 256, PARTS, 2 * PARTS, kPairStages,
           PARTS == 1};
 }
 template <int BN, bool GATED, int SPLITS>
@@ -1183,6 +1263,8 @@ int launch_best(const LinearParams& p, cudaStream_t st) {
   const int64_t kblocks = ceil_div(p.K, kBK);
   const int force = g_force.load(std::memory_order_relaxed);
   for (const Option& o : options) {
+    // an fp32 output's sums are kept short (see kChunk): the split kernel has four accumulators for a piece of K
+    if (!force && o.rows < 256 && p.out_dtype == W4A8_DTYPE_F32 && kblocks > 4 * kChunk * o.parts) continue;
     if (o.parts > kblocks || (force && force % 16 <= kblocks && force != o.rows * 16 + o.parts)) continue;
     int clusters;
     if (int rc = o.ready(&clusters)) return rc;
