@@ -234,34 +234,47 @@ __global__ void __launch_bounds__(256) route_grouped_kernel(const RouteParams p)
       for (int i = 1; i < EPL; ++i) mx = fmaxf(mx, l[i]);
       mx = lanes_max<S>(mx);
       total = 0.f;
+      if (mx < INFINITY) {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) total += softmax_term(l[i], mx);
+        for (int i = 0; i < EPL; ++i) total += __expf(l[i] - mx);
+      } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) total += softmax_term(l[i], mx);
+      }
       if (mx == -INFINITY) total = 0.f;  // nothing is left
       total = lanes_sum<S>(total);
     }
     uint32_t key[EPL];
+    if (p.softmax && !p.bias) {
+      // ranked by its logits: the same order as the scores', without ties made by rounding
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      float c = l[i];
-      if (!p.softmax) c = sigmoid_score(c);
-      // a softmax without a bias is ranked by its logits: the same order, without ties made by rounding
-      if (p.bias) c = __fadd_rn(p.softmax ? __fdiv_rn(softmax_term(c, mx), total) : c, bias[i]);
-      c += 0.0f;  // -0 and +0 are equal
-      key[i] = l[i] > -INFINITY ? order_key(c) : kKeyOut;
-      if (i >= n) key[i] = 0;
+      for (int i = 0; i < EPL; ++i) key[i] = order_key(l[i] + 0.0f);  // -0 and +0 are equal
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        float c = p.softmax ? __fdiv_rn(softmax_term(l[i], mx), total) : sigmoid_score(l[i]);
+        if (p.bias) c = __fadd_rn(c, bias[i]);  // never -0: scores are not negative
+        key[i] = l[i] > -INFINITY ? order_key(c) : kKeyOut;
+      }
     }
     uint64_t v[L];
     if constexpr (GROUPS) {
-      uint32_t k1 = 0, k2 = 0;  // the group's two largest keys
+      uint32_t k1 = kKeyOut, k2 = kKeyOut;  // the group's two largest keys (places without an expert have kKeyOut)
+      if (p.group_top == 1) {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        k2 = max(k2, min(k1, key[i]));
-        k1 = max(k1, key[i]);
-      }
-      for (int o = 1; o < lpg; o <<= 1) {
-        const uint32_t o1 = __shfl_xor_sync(0xffffffffu, k1, o), o2 = __shfl_xor_sync(0xffffffffu, k2, o);
-        k2 = max(min(k1, o1), max(k2, o2));
-        k1 = max(k1, o1);
+        for (int i = 0; i < EPL; ++i) k1 = max(k1, key[i]);
+        for (int o = 1; o < lpg; o <<= 1) k1 = max(k1, __shfl_xor_sync(0xffffffffu, k1, o));
+      } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          k2 = max(k2, min(k1, key[i]));
+          k1 = max(k1, key[i]);
+        }
+        for (int o = 1; o < lpg; o <<= 1) {
+          const uint32_t o1 = __shfl_xor_sync(0xffffffffu, k1, o), o2 = __shfl_xor_sync(0xffffffffu, k2, o);
+          k2 = max(min(k1, o1), max(k2, o2));
+          k1 = max(k1, o1);
+        }
       }
       uint32_t gk = 0;  // on a group's first lane: its score
       if (sub == 0 && g < p.n_group) {
