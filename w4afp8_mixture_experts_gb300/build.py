@@ -88,7 +88,7 @@ def _link_torch_ops(obj: str) -> str:
     if not (os.path.exists(EXT) and os.path.getmtime(EXT) >= max(os.path.getmtime(obj), os.path.getmtime(LIB))):
         lib = os.path.join(_torch_paths()[0], "lib")
         cmd = ["g++", "-shared", "-o", EXT, obj, "-L" + LIBDIR, "-lw4a8moe", "-L" + lib, "-lc10", "-lc10_cuda",
-               "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+               "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")

@@ -590,7 +590,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else if (warp >= 4) {
     if constexpr (CHUNKED) regs_claim<kRegsSums>();
     constexpr int kPart = 2 * kCols * (GATED ? 2 : 1);  // columns of products that a CTA finishes: 256 / PARTS
-    float* recv = reinterpret_cast<float*>(smem);       // [PARTS - 1][kPart][128 tokens]
+    // [PARTS - 1][kPart / 4][128 tokens][4]: a thread pushes and takes 4 columns of its token at a time
+    float4* recv = reinterpret_cast<float4*>(smem);
     static_assert((PARTS - 1) * kPart * 128 * 4 <= kPairStages * kPairStageBytes, "partial products in the stages");
     int tm, tn;
     pair_tile(pl, first, tm, tn);
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     cluster_wait();
     tc_fence_after();
     if (ok) {
-      const uint32_t to0 = smem_u32(recv) + (quarter * 32 + lane) * 4;
+      const uint32_t to0 = smem_u32(recv) + (quarter * 32 + lane) * 16;
 #pragma unroll 1
       for (int q = 0; q < PARTS; ++q) {
         if (q == part) continue;
@@ -626,9 +627,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               tmem_ld16(at, reinterpret_cast<uint32_t*>(v));
             tmem_wait_ld_pin<kN>(reinterpret_cast<uint32_t*>(v));
 #pragma unroll
-            for (int j = 0; j < kN; ++j)
-              asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + (h * 2 * kCols + half * kCols + c + j) * 512),
-                           "f"(v[j])
+            for (int j = 0; j < kN; j += 4)
+              asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               to + (h * 2 * kCols + half * kCols + c + j) * 512),
+                           "f"(v[j]), "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3])
                            : "memory");
           }
         }
@@ -637,7 +639,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     cluster_arrive();
     cluster_wait();
     if (ok && n0 < p.n_out) {
-      const float* mine = recv + quarter * 32 + lane;
+      const float4* mine = recv + quarter * 32 + lane;
 #pragma unroll 1
       for (int c = 0; c < kCols; c += kN) {
         float v[kN], u[kN];
@@ -655,9 +657,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
         for (int q = 0; q < PARTS - 1; ++q)
 #pragma unroll
-          for (int j = 0; j < kN; ++j) {
-            v[j] += mine[(q * kPart + half * kCols + c + j) * 128];
-            if (GATED) u[j] += mine[(q * kPart + 2 * kCols + half * kCols + c + j) * 128];
+          for (int j = 0; j < kN; j += 4) {
+            const float4 a = mine[(q * kPart + half * kCols + c + j) / 4 * 128];
+            v[j] += a.x, v[j + 1] += a.y, v[j + 2] += a.z, v[j + 3] += a.w;
+            if (GATED) {
+              const float4 b = mine[(q * kPart + 2 * kCols + half * kCols + c + j) / 4 * 128];
+              u[j] += b.x, u[j + 1] += b.y, u[j + 2] += b.z, u[j + 3] += b.w;
+            }
           }
         if (n0 + c >= p.n_out) continue;
         apply(v, u, c);
@@ -1091,35 +1097,31 @@ int vec_rows(const LinearParams& p) {
   return bits % 32 == 0 ? 2 : bits % 16 == 0 ? 1 : 0;
 }
 
-// What a launch of one kernel instance needs, and how many of its clusters the current device runs at once
-// (clusters of 8 leave SMs of a graphics-processing cluster unused, so this is not SMs / size).
+// What a launch of one kernel instance needs, and how many of its clusters a device runs at once (clusters of 8 leave
+// SMs of a graphics-processing cluster unused, so this is not SMs / size).
 class Launcher {
  public:
   template <class... KArgs>
-  int prepare(void (*kern)(KArgs...), size_t smem, int threads, int cluster, int least_regs = 0) {
-    return once_.run([&] {
-      // setmaxnreg.inc waits until the released registers cover the request: they must be there
+  int prepare(int dev, int* clusters, void (*kern)(KArgs...), size_t smem, int threads, int cluster, int least_regs = 0) {
+    const bool known = dev >= 0 && dev < 64;
+    if (known && (*clusters = clusters_[dev].load(std::memory_order_acquire)) > 0) return W4A8_OK;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+      return check_launch("cudaFuncSetAttribute(linear)");
+    if (least_regs) {  // setmaxnreg.inc waits until the released registers cover the request: they must be there
       cudaFuncAttributes fa;
-      if (least_regs) {
-        if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return check_launch("cudaFuncGetAttributes(linear)");
-        if (fa.numRegs < least_regs)
-          return set_error(W4A8_ERR_UNSUPPORTED, "linear kernel built with %d registers per thread: %d are needed",
-                           fa.numRegs, least_regs);
-      }
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-        return check_launch("cudaFuncSetAttribute(linear)");
-      cudaLaunchAttribute attr[1];
-      cudaLaunchConfig_t lc = config(dim3(cluster), threads, smem, cluster, nullptr, attr);
-      int n = 0, dev = 0;
-      if (cudaGetDevice(&dev) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, kern, &lc) != cudaSuccess)
-        return check_launch("cudaOccupancyMaxActiveClusters(linear)");
-      if (dev >= 0 && dev < 64) clusters_[dev] = n > 0 ? n : 1;
-      return static_cast<int>(W4A8_OK);
-    });
-  }
-  int clusters() const {
-    int dev = 0;
-    return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 && clusters_[dev] ? clusters_[dev] : 1;
+      if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return check_launch("cudaFuncGetAttributes(linear)");
+      if (fa.numRegs < least_regs)
+        return set_error(W4A8_ERR_UNSUPPORTED, "linear kernel built with %d registers per thread: %d are needed",
+                         fa.numRegs, least_regs);
+    }
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t lc = config(dim3(cluster), threads, smem, cluster, nullptr, attr);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &lc) != cudaSuccess)
+      return check_launch("cudaOccupancyMaxActiveClusters(linear)");
+    *clusters = n > 0 ? n : 1;
+    if (known) clusters_[dev].store(*clusters, std::memory_order_release);
+    return W4A8_OK;
   }
   static cudaLaunchConfig_t config(dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st,
                                    cudaLaunchAttribute* attr) {
@@ -1149,14 +1151,13 @@ class Launcher {
   }
 
  private:
-  DeviceOnce once_;
-  int clusters_[64] = {0};
+  std::atomic<int> clusters_[64] = {};  // 0: not prepared on that device
 };
 
 // One configuration of the two kernels: how many clusters run at once, and the launch itself.
 struct Option {
-  int (*ready)(int* clusters);  // status; makes the configuration ready on this device
-  int (*launch)(const LinearParams& p, cudaStream_t st);
+  int (*ready)(int dev, int* clusters);  // status; makes the configuration ready on the current device
+  int (*launch)(const LinearParams& p, int dev, cudaStream_t st);
   double fixed_us;  // a launch of one tile per cluster without its stages
   double stage_us;  // a 64-k stage of a CTA by itself
   double l2_rate;   // bytes per us that L2 gives all CTAs together
@@ -1173,18 +1174,16 @@ struct Pair {
     static Launcher l;
     return l;
   }
-  static int ready(int* clusters) {
-    const int rc = launcher().prepare(linear_pair_kernel<GATED, PARTS, CHUNKED>, kPairSmem, kPairThreads, 2 * PARTS,
-                                      CHUNKED ? kRegsLaunch : 0);
-    *clusters = launcher().clusters();
-    return rc;
+  static int ready(int dev, int* clusters) {
+    return launcher().prepare(dev, clusters, linear_pair_kernel<GATED, PARTS, CHUNKED>, kPairSmem, kPairThreads,
+                              2 * PARTS, CHUNKED ? kRegsLaunch : 0);
   }
-  static int launch(const LinearParams& p, cudaStream_t st) {
+  static int launch(const LinearParams& p, int dev, cudaStream_t st) {
     if (!CHUNKED && p.out_dtype == W4A8_DTYPE_F32 && p.K > kChunk * kBK * PARTS)
-      return Pair<GATED, PARTS, true>::launch(p, st);
+      return Pair<GATED, PARTS, true>::launch(p, dev, st);
     CUtensorMap tx, tw;
     int rc, clusters;
-    if ((rc = ready(&clusters))) return rc;
+    if ((rc = ready(dev, &clusters))) return rc;
     if ((rc = row_map(&tx, p.x, p.dtype, p.M, p.K, p.ldx, 128, "x"))) return rc;
     if ((rc = row_map(&tw, p.w, p.dtype, p.N, p.K, p.ldw, 128, "w"))) return rc;
     PairPlan pl;
@@ -1207,15 +1206,13 @@ struct Split {
     static Launcher l;
     return l;
   }
-  static int ready(int* clusters) {
-    const int rc = launcher().prepare(linear_split_kernel<BN, GATED>, C::kSmem, kSplitThreads, SPLITS);
-    *clusters = launcher().clusters();
-    return rc;
+  static int ready(int dev, int* clusters) {
+    return launcher().prepare(dev, clusters, linear_split_kernel<BN, GATED>, C::kSmem, kSplitThreads, SPLITS);
   }
-  static int launch(const LinearParams& p, cudaStream_t st) {
+  static int launch(const LinearParams& p, int dev, cudaStream_t st) {
     CUtensorMap tx, tw;
     int rc, clusters;
-    if ((rc = ready(&clusters))) return rc;
+    if ((rc = ready(dev, &clusters))) return rc;
     if ((rc = row_map(&tx, p.x, p.dtype, p.M, p.K, p.ldx, BN, "x"))) return rc;
     if ((rc = row_map(&tw, p.w, p.dtype, p.N, p.K, p.ldw, GATED ? 64 : 128, "w"))) return rc;
     const unsigned nb = static_cast<unsigned>(ceil_div(p.n_out, GATED ? 64 : 128));
@@ -1258,6 +1255,8 @@ int launch_best(const LinearParams& p, cudaStream_t st) {
       split_option<64, GATED, 8>(4.3),     split_option<32, GATED, 1>(3.3),     split_option<32, GATED, 2>(3.4),
       split_option<32, GATED, 4>(3.4),     split_option<32, GATED, 8>(3.5),
   };
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return check_launch("cudaGetDevice");
   const Option* best = nullptr;
   double best_us = 0.0;
   const int64_t kblocks = ceil_div(p.K, kBK);
@@ -1267,7 +1266,7 @@ int launch_best(const LinearParams& p, cudaStream_t st) {
     if (!force && o.rows < 256 && p.out_dtype == W4A8_DTYPE_F32 && kblocks > 4 * kChunk * o.parts) continue;
     if (o.parts > kblocks || (force && force % 16 <= kblocks && force != o.rows * 16 + o.parts)) continue;
     int clusters;
-    if (int rc = o.ready(&clusters)) return rc;
+    if (int rc = o.ready(dev, &clusters)) return rc;
     const int64_t tiles = ceil_div(p.M, o.rows) * ceil_div(p.N, o.cols);
     const int64_t waves = ceil_div(tiles, clusters);
     const double ctas = static_cast<double>(std::min<int64_t>(tiles, clusters)) * o.ctas;
@@ -1283,7 +1282,7 @@ int launch_best(const LinearParams& p, cudaStream_t st) {
     }
   }
   if (!best) return set_error(W4A8_ERR_UNSUPPORTED, "no configuration for K=%d", p.K);
-  return best->launch(p, st);
+  return best->launch(p, dev, st);
 }
 
 }  // namespace
