@@ -80,6 +80,20 @@ def test_strides_and_alignment(lib, pad, shift, H):
     _check(lib, 9, H, pad=pad, shift=shift, gate=(9, H), seed=4)
 
 
+@pytest.mark.parametrize("T", [1, 5, 1000, 4001])
+@pytest.mark.parametrize("H", [8, 60, 64, 65, 128, 136, 250, 256])
+def test_narrow_rows(lib, T, H):
+    _check(lib, T, H, post="layer", pre="rms", gate=(T, 1), bias=True, seed=H)
+    _check(lib, T, H, dtype="f32", rdtype="f32", post="rms", pre="layer", gate=(1, H), seed=H)
+
+
+@pytest.mark.parametrize("T,H,pad", [(1, 13942, 0), (1, 20001, 0), (1, 777, 0), (5, 777, 7), (400, 777, 7), (3, 12345, 7),
+                                     (2, 16385, 7), (2, 32767, 1)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_aligned_rows_of_odd_width(lib, T, H, pad, dtype):
+    _check(lib, T, H, dtype=dtype, rdtype="f32", post="layer", pre="layer", gate=(1, H), bias=True, pad=pad, seed=8)
+
+
 def test_parameters_in_the_activations_type(lib):
     _check(lib, 6, 640, pdtype="bf16", post="layer", pre="layer", bias=True)
     _check(lib, 6, 641, dtype="f16", rdtype="f16", pdtype="f16", post="rms", pre="layer", bias=True)

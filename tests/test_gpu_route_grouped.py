@@ -52,6 +52,14 @@ CASES = [
     (510, 8, dict(score="sigmoid", n_group=17, topk_group=5, group_top=2), False),
     (300, 9, dict(score="sigmoid", n_group=1), False),
     (320, 16, dict(score="sigmoid", n_group=32, topk_group=7, group_top=2), True),
+    (384, 6, dict(score="sigmoid", n_group=16, topk_group=4), False),
+    (384, 8, dict(score="sigmoid"), True),
+    (454, 6, dict(score="softmax"), False),
+    (900, 12, dict(score="sigmoid", n_group=2, topk_group=1), False),
+    (160, 16, dict(score="softmax", n_group=2, topk_group=1, renormalize=False), False),
+    (24, 3, dict(score="sigmoid", n_group=8, topk_group=3), True),
+    (40, 8, dict(score="softmax", n_group=5, topk_group=4, group_top=2), True),
+    (96, 12, dict(score="sigmoid", n_group=4, topk_group=3, group_top=2), False),
 ]
 
 

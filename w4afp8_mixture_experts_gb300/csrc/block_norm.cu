@@ -1,636 +1,8 @@
-// The norms after and before a block in one pass over a token's row, with the block's gate and residual:
-//   u = norm_post(f)      h = residual_scale * r + branch_scale * gate * u      y = norm_pre(h)
-// norm in {none, rms, layer}; sums and the values between the two norms stay in fp32 registers, h and y are
-// each rounded once (y from the unrounded h).
-//
-// A row is held by the threads of one block (or one warp, for short rows: several rows to a block); the row's
-// sums are one block reduction each (the mean first, then the squared differences, for a LayerNorm).
-#include <algorithm>
-
-#include "block_ops.cuh"
-#include "common.cuh"
+// block_norm: argument checks and the fp32 kernels (block_norm.cuh).
+#include "block_norm.cuh"
 
 namespace w4a8 {
-namespace {
-
-constexpr int kMaxH = 32768;
-
-struct NormParams {
-  const void* f;
-  const void* r;       // nullptr: no residual
-  const void* gate;    // nullptr: 1
-  const void* w_post;  // nullptr: 1
-  const void* b_post;  // nullptr: 0
-  const void* w_pre;
-  const void* b_pre;
-  void* h;  // nullptr: not wanted
-  void* y;  // nullptr: not wanted
-  int64_t ldf, ldr, ldg, ldh, ldy;
-  int T, H;
-  int post, pre;      // w4a8_norm
-  int rows_per_gate;  // row t uses gate row t / rows_per_gate
-  int gate_scalar;    // one gate value per gate row
-  int gate_f32, w_f32;
-  float branch_scale, residual_scale, eps;
-};
-
-template <typename T, int V>
-struct alignas(V * sizeof(T) > 16 ? 16 : V * sizeof(T)) Pack {
-  T v[V];
-};
-
-template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T* p, float (&o)[V]) {
-  const Pack<T, V> a = *reinterpret_cast<const Pack<T, V>*>(p);
-#pragma unroll
-  for (int i = 0; i < V; ++i) o[i] = to_f32(a.v[i]);
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_vec(T* p, const float (&o)[V]) {
-  if constexpr (V == 8 && sizeof(T) == 2) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(o[0], o[1]), pack2<T>(o[2], o[3]), pack2<T>(o[4], o[5]),
-                                              pack2<T>(o[6], o[7]));
-  } else {
-    Pack<T, V> a;
-#pragma unroll
-    for (int i = 0; i < V; ++i) a.v[i] = from_f32<T>(o[i]);
-    *reinterpret_cast<Pack<T, V>*>(p) = a;
-  }
-}
-// a parameter vector: fp32 or the activations' type
-template <typename X, int V>
-__device__ __forceinline__ void load_param(const void* p, int f32, int64_t at, float (&o)[V]) {
-  if (f32)
-    load_vec<float, V>(static_cast<const float*>(p) + at, o);
-  else
-    load_vec<X, V>(static_cast<const X*>(p) + at, o);
-}
-
-// Sum over the row's threads; the same value on all of them.  `slot` alternates between two halves of the
-// scratch so that one barrier per reduction is enough.
-__device__ __forceinline__ float row_sum(float v, float* scratch, int& slot) {
-  v = warp_sum(v);
-  const int warps = blockDim.x >> 5;
-  if (warps == 1) return v;
-  float* s = scratch + slot;
-  slot ^= 32;
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  const int lane = threadIdx.x & 31;
-  return warp_sum(lane < warps ? s[lane] : 0.f);
-}
-
-template <int V, int VPT>
-__device__ __forceinline__ void normalise(float (&u)[VPT][V], int kind, int H, float eps, float* scratch, int& slot) {
-  float s = 0.f;
-  if (kind == W4A8_NORM_LAYER) {
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) s += u[j][i];
-    const float mean = row_sum(s, scratch, slot) / H;
-    s = 0.f;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const bool in = (j * blockDim.x + threadIdx.x) * V < H;
-#pragma unroll
-      for (int i = 0; i < V; ++i) u[j][i] = in ? u[j][i] - mean : 0.f;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < VPT; ++j)
-#pragma unroll
-    for (int i = 0; i < V; ++i) s = fmaf(u[j][i], u[j][i], s);
-  const float inv = rsqrtf(row_sum(s, scratch, slot) / H + eps);
-#pragma unroll
-  for (int j = 0; j < VPT; ++j)
-#pragma unroll
-    for (int i = 0; i < V; ++i) u[j][i] *= inv;
-}
-
-template <typename X, int V, int VPT>
-__device__ __forceinline__ void scale_shift(float (&u)[VPT][V], const void* w, const void* b, int f32, int H) {
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int c = (j * blockDim.x + threadIdx.x) * V;
-    if (c >= H) continue;
-    float a[V];
-    if (w) {
-      load_param<X, V>(w, f32, c, a);
-#pragma unroll
-      for (int i = 0; i < V; ++i) u[j][i] *= a[i];
-    }
-    if (b) {
-      load_param<X, V>(b, f32, c, a);
-#pragma unroll
-      for (int i = 0; i < V; ++i) u[j][i] += a[i];
-    }
-  }
-}
-
-__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {  // all but the N newest groups have landed
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// u = f -> u = norm_post(f), scaled and shifted
-template <typename X, int V, int VPT>
-__device__ __forceinline__ void post_norm(const NormParams& p, float (&u)[VPT][V], float* scratch, int& slot) {
-  if (p.post == W4A8_NORM_NONE) return;
-  normalise<V, VPT>(u, p.post, p.H, p.eps, scratch, slot);
-  scale_shift<X, V, VPT>(u, p.w_post, p.b_post, p.w_f32, p.H);
-}
-
-// u -> branch_scale * gate * u + residual_scale * r, where residual(j) gives the thread's r of vector j; stores h
-template <typename X, typename R, int V, int VPT, class Residual>
-__device__ __forceinline__ void join_residual(const NormParams& p, float (&u)[VPT][V], int64_t t, Residual&& residual) {
-  const int64_t grow = p.gate ? (t / p.rows_per_gate) * p.ldg : 0;
-  float gs = p.branch_scale;
-  if (p.gate && p.gate_scalar) {
-    float a[1];
-    load_param<X, 1>(p.gate, p.gate_f32, grow, a);
-    gs *= a[0];
-  }
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int c = (j * blockDim.x + threadIdx.x) * V;
-    if (c >= p.H) continue;
-    float a[V];
-    if (p.gate && !p.gate_scalar) {
-      load_param<X, V>(p.gate, p.gate_f32, grow + c, a);
-#pragma unroll
-      for (int i = 0; i < V; ++i) u[j][i] *= a[i];
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) u[j][i] *= gs;
-    if (p.r) {
-      residual(j, c, a);
-#pragma unroll
-      for (int i = 0; i < V; ++i) u[j][i] = fmaf(p.residual_scale, a[i], u[j][i]);
-    }
-    if (p.h) store_vec<R, V>(static_cast<R*>(p.h) + t * p.ldh + c, u[j]);
-  }
-}
-
-// h = u -> y
-template <typename X, int V, int VPT>
-__device__ __forceinline__ void pre_norm(const NormParams& p, float (&u)[VPT][V], int64_t t, float* scratch, int& slot) {
-  if (!p.y) return;
-  if (p.pre != W4A8_NORM_NONE) {
-    normalise<V, VPT>(u, p.pre, p.H, p.eps, scratch, slot);
-    scale_shift<X, V, VPT>(u, p.w_pre, p.b_pre, p.w_f32, p.H);
-  }
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int c = (j * blockDim.x + threadIdx.x) * V;
-    if (c < p.H) store_vec<X, V>(static_cast<X*>(p.y) + t * p.ldy + c, u[j]);
-  }
-}
-
-// A block to a row (or eight rows of a warp each): blockDim.x threads hold a row, VPT vectors of V elements each.
-template <typename X, typename R, int V, int VPT>
-__global__ void __launch_bounds__(1024) block_norm_row_kernel(const NormParams p) {
-  __shared__ float scratch[64];
-  pdl_trigger();
-  pdl_wait();
-  int slot = 0;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-  if (t >= p.T) return;  // whole warps, where several rows share a block
-  float u[VPT][V];
-  Pack<R, V> res[VPT];
-  const X* f = static_cast<const X*>(p.f) + t * p.ldf;
-  const R* r = static_cast<const R*>(p.r) + t * p.ldr;
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int c = (j * blockDim.x + threadIdx.x) * V;
-#pragma unroll
-    for (int i = 0; i < V; ++i) u[j][i] = 0.f;
-    if (c < p.H) {
-      load_vec<X, V>(f + c, u[j]);
-      if (p.r) res[j] = *reinterpret_cast<const Pack<R, V>*>(r + c);
-    }
-  }
-  post_norm<X, V, VPT>(p, u, scratch, slot);
-  join_residual<X, R, V, VPT>(p, u, t, [&](int j, int, float (&a)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) a[i] = to_f32(res[j].v[i]);
-  });
-  pre_norm<X, V, VPT>(p, u, t, scratch, slot);
-}
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t pair(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 split(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
-// Many rows: blocks stay and stride over them, 16 or 8 elements of a row to a thread and ROWS rows at a time (their
-// reductions share the barriers and hide each other's latency).  The weights and biases stay in registers (with
-// branch_scale, and a gate that all rows share, multiplied into the first pair), and the rows to come are copied to a
-// ring of two or three stages in shared memory asynchronously: registers would not hold enough bytes in flight to cover the
-// memory's latency beside the rows that are being worked on.
-//   V = 8: rows of whole aligned vectors.  Every thread copies its own pieces and alone reads them back, so there is
-//     nothing to synchronise.
-//   V = 1: rows without 16-byte alignment, or of a width that is no multiple of 8.  The block copies the aligned
-//     16-byte pieces that cover a row, and threads take single elements from there.  A piece that reaches outside the
-//     matrix (only its first and last one can) is copied element by element.
-template <typename T>
-__device__ __forceinline__ void fetch_window(uint8_t* dst, const void* base, int64_t ld, int64_t rows, int64_t t, int H) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(base), hi = lo + ((rows - 1) * ld + H) * sizeof(T);
-  const uintptr_t b0 = lo + t * ld * sizeof(T), w0 = b0 & ~uintptr_t(15);
-  const int pieces = static_cast<int>((b0 - w0 + H * sizeof(T) + 15) >> 4);
-  if (w0 >= lo && w0 + 16 * static_cast<uintptr_t>(pieces) <= hi) {
-    for (int i = threadIdx.x; i < pieces; i += blockDim.x)
-      copy16_async(dst + 16 * i, reinterpret_cast<const void*>(w0 + 16 * i));
-    return;
-  }
-  for (int i = threadIdx.x; i < pieces; i += blockDim.x) {
-    const uintptr_t a = w0 + 16 * static_cast<uintptr_t>(i);
-    if (a >= lo && a + 16 <= hi) {
-      copy16_async(dst + 16 * i, reinterpret_cast<const void*>(a));
-    } else {
-      for (uintptr_t e = a; e < a + 16; e += sizeof(T))
-        if (e >= lo && e < hi) *reinterpret_cast<T*>(dst + (e - w0)) = *reinterpret_cast<const T*>(e);
-    }
-  }
-}
-
-// One stage of the ring (ROWS rows): byte offsets of its parts, and of one row within a part.  V = 8: a thread's
-// 16-byte pieces lie 16 * threads apart.
-struct NormStage {
-  int stages, bytes, r_at, g_at;
-  int f_row, r_row, g_row;
-  bool gate_rows;  // the gate differs between rows and has H columns: it goes through the ring too
-};
-
-// Threads of an SM that the registers allow with kE elements to a thread (16: two rows of them in registers).
-__host__ __device__ constexpr int max_threads(int elems) { return elems == 16 ? 512 : 768; }
-
-template <typename X, typename R, int V, bool BIAS, int kE>
-__global__ void __launch_bounds__(max_threads(kE), 1) block_norm_stream_kernel(const NormParams p, const NormStage st) {
-  constexpr int kP = kE / 2;  // pairs of a thread's elements
-  constexpr int ROWS = 2;
-  extern __shared__ uint8_t ring[];
-  __shared__ float2 scratch[2][max_threads(kE) / 32];
-  const int threads = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + threadIdx.x;
-  const int tx = threadIdx.x, nx = blockDim.x, H = p.H;
-  // column of element i: V = 8: two vectors nx * 8 apart; V = 1: elements nx apart.  Elements i < mine exist.
-  const int mine = V == 8 ? ((tx * 8 < H) + ((nx + tx) * 8 < H)) * 8 : max(0, (H - tx + nx - 1) / nx);
-  auto col = [&](int i) { return V == 8 ? ((i / 8) * nx + tx) * 8 + i % 8 : i * nx + tx; };
-  auto in = [&](int i) { return (V == 8 ? i / 8 * 8 : i) < mine; };
-  pdl_trigger();
-  pdl_wait();
-  uint64_t w_post[kP], w_pre[kP];
-  // the biases: this thread's pairs in shared memory behind the ring, b_post then b_pre (registers hold no more)
-  uint64_t* biases = reinterpret_cast<uint64_t*>(ring + st.stages * st.bytes) + tid;
-#pragma unroll
-  for (int j = 0; j < kP; ++j) {
-    float wq[2] = {0.f, 0.f}, bq[2] = {0.f, 0.f}, wp[2] = {0.f, 0.f}, bp[2] = {0.f, 0.f};
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = 2 * j + h;
-      float a[1];
-      if (!in(i)) continue;
-      wp[h] = p.branch_scale;
-      wq[h] = 1.f;
-      if (p.gate && !p.gate_scalar && !st.gate_rows) {
-        load_param<X, 1>(p.gate, p.gate_f32, col(i), a);
-        wp[h] *= a[0];
-      }
-      if (BIAS && p.b_post) {
-        load_param<X, 1>(p.b_post, p.w_f32, col(i), a);
-        bp[h] = wp[h] * a[0];
-      }
-      if (p.w_post) {
-        load_param<X, 1>(p.w_post, p.w_f32, col(i), a);
-        wp[h] *= a[0];
-      }
-      if (p.w_pre) {
-        load_param<X, 1>(p.w_pre, p.w_f32, col(i), a);
-        wq[h] = a[0];
-      }
-      if (BIAS && p.b_pre) {
-        load_param<X, 1>(p.b_pre, p.w_f32, col(i), a);
-        bq[h] = a[0];
-      }
-    }
-    w_post[j] = pair(wp[0], wp[1]);
-    w_pre[j] = pair(wq[0], wq[1]);
-    if (BIAS) {
-      biases[j * threads] = pair(bp[0], bp[1]);
-      biases[(kP + j) * threads] = pair(bq[0], bq[1]);
-    }
-  }
-
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;  // between the rows of a thread
-  auto gate_index = [&](int64_t t) { return static_cast<int64_t>(static_cast<uint32_t>(t) / p.rows_per_gate); };
-  auto piece = [&](uint8_t* at, int q) { return at + q * (16 * threads) + 16 * tid; };
-  // copies one row of a matrix of T into its place in the ring
-  auto fetch_part = [&](auto type, const void* base, int64_t ld, int64_t rows, int64_t t, uint8_t* at) {
-    using T = decltype(type);
-    if constexpr (V == 8) {
-      constexpr int Q = sizeof(T) / 2;  // 16-byte pieces of a vector
-      const char* src = reinterpret_cast<const char*>(static_cast<const T*>(base) + t * ld + tx * 8);
-#pragma unroll
-      for (int j = 0; j < kE / 8; ++j)
-        if (in(8 * j)) {
-#pragma unroll
-          for (int q = 0; q < Q; ++q) copy16_async(piece(at, j * Q + q), src + j * nx * 16 * Q + 16 * q);
-        }
-    } else {
-      fetch_window<T>(at, base, ld, rows, t, H);
-    }
-  };
-  auto fetch = [&](int64_t t0, uint8_t* at) {
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const int64_t t = t0 + r * step;
-      if (t >= p.T) break;
-      fetch_part(X(), p.f, p.ldf, p.T, t, at + r * st.f_row);
-      if (p.r) fetch_part(R(), p.r, p.ldr, p.T, t, at + st.r_at + r * st.r_row);
-      if (st.gate_rows) {
-        uint8_t* g = at + st.g_at + r * st.g_row;
-        if (p.gate_f32)
-          fetch_part(float(), p.gate, p.ldg, p.T / p.rows_per_gate, gate_index(t), g);
-        else
-          fetch_part(X(), p.gate, p.ldg, p.T / p.rows_per_gate, gate_index(t), g);
-      }
-    }
-    copy_commit();
-  };
-  // this thread's elements of one row of the ring; zeros where there are none
-  auto take = [&](auto type, const void* base, int64_t ld, int64_t t, uint8_t* at, uint64_t* o) {
-    using T = decltype(type);
-    if constexpr (V == 8) {
-      constexpr int Q = sizeof(T) / 2;
-#pragma unroll
-      for (int j = 0; j < kE / 8; ++j) {
-        Pack<T, 8> a;
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-          reinterpret_cast<uint4*>(&a)[q] = in(8 * j) ? *reinterpret_cast<const uint4*>(piece(at, j * Q + q))
-                                                      : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[4 * j + i] = pair(to_f32(a.v[2 * i]), to_f32(a.v[2 * i + 1]));
-      }
-    } else {
-      const T* row =
-          reinterpret_cast<const T*>(at + ((reinterpret_cast<uintptr_t>(base) + t * ld * sizeof(T)) & 15)) + tx;
-#pragma unroll
-      for (int i = 0; i < kP; ++i)
-        o[i] = pair(in(2 * i) ? to_f32(row[2 * i * nx]) : 0.f, in(2 * i + 1) ? to_f32(row[(2 * i + 1) * nx]) : 0.f);
-    }
-  };
-  auto put = [&](auto type, void* base, int64_t ld, int64_t t, const uint64_t* o) {
-    using T = decltype(type);
-    T* row = static_cast<T*>(base) + t * ld;
-    if constexpr (V == 8) {
-#pragma unroll
-      for (int j = 0; j < kE / 8; ++j) {
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 a = split(o[4 * j + i]);
-          v[2 * i] = a.x;
-          v[2 * i + 1] = a.y;
-        }
-        if (in(8 * j)) store_vec<T, 8>(row + (j * nx + tx) * 8, v);
-      }
-    } else {
-      row += tx;
-#pragma unroll
-      for (int i = 0; i < kP; ++i) {
-        const float2 a = split(o[i]);
-        if (in(2 * i)) row[2 * i * nx] = from_f32<T>(a.x);
-        if (in(2 * i + 1)) row[(2 * i + 1) * nx] = from_f32<T>(a.y);
-      }
-    }
-  };
-  int turn = 0;
-  auto reduce = [&](float (&v)[ROWS]) {  // sums over the row's threads, one barrier
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) v[r] = warp_sum(v[r]);
-    const int warps = nx >> 5, lane = tx & 31;
-    if (warps == 1) return;
-    float2* at = scratch[turn];
-    turn ^= 1;
-    if (lane == 0) at[tx >> 5] = make_float2(v[0], v[ROWS - 1]);
-    __syncthreads();
-    const float2 a = lane < warps ? at[lane] : make_float2(0.f, 0.f);
-    v[0] = warp_sum(a.x);
-    if (ROWS == 2) v[ROWS - 1] = warp_sum(a.y);
-  };
-  const float inv_h = 1.0f / H;
-  auto normalise_rows = [&](uint64_t (&u)[ROWS][kP], int kind) {
-    float s[ROWS];
-    if (kind == W4A8_NORM_LAYER) {
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        uint64_t a = u[r][0];
-#pragma unroll
-        for (int i = 1; i < kP; ++i) a = add2(a, u[r][i]);
-        const float2 b = split(a);
-        s[r] = b.x + b.y;
-      }
-      reduce(s);
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        const float m = -s[r] * inv_h;
-#pragma unroll
-        for (int i = 0; i < kP; ++i) u[r][i] = add2(u[r][i], pair(in(2 * i) ? m : 0.f, in(2 * i + 1) ? m : 0.f));
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      uint64_t a = mul2(u[r][0], u[r][0]);
-#pragma unroll
-      for (int i = 1; i < kP; ++i) a = fma2(u[r][i], u[r][i], a);
-      const float2 b = split(a);
-      s[r] = b.x + b.y;
-    }
-    reduce(s);
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const float inv = rsqrtf(fmaf(s[r], inv_h, p.eps));
-#pragma unroll
-      for (int i = 0; i < kP; ++i) u[r][i] = mul2(u[r][i], pair(inv, inv));
-    }
-  };
-  auto scale_rows = [&](uint64_t (&u)[ROWS][kP], const uint64_t (&w)[kP], const uint64_t* b) {
-#pragma unroll
-    for (int i = 0; i < kP; ++i) {
-      const uint64_t bi = BIAS ? b[i * threads] : 0;
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r) u[r][i] = BIAS ? fma2(u[r][i], w[i], bi) : mul2(u[r][i], w[i]);
-    }
-  };
-  auto scalar_gate = [&](int64_t t) {
-    float a[1] = {1.f};
-    if (p.gate_scalar && t < p.T) load_param<X, 1>(p.gate, p.gate_f32, gate_index(t) * p.ldg, a);
-    return a[0];
-  };
-
-  int64_t t0 = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-  for (int s = 0; s < st.stages; ++s) fetch(t0 + s * ROWS * step, ring + s * st.bytes);
-  float gs[ROWS];
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r) gs[r] = scalar_gate(t0 + r * step);
-  int s = 0;
-  const uint64_t rs = pair(p.residual_scale, p.residual_scale);
-  for (; t0 < p.T; t0 += ROWS * step) {
-    uint8_t* at = ring + s * st.bytes;
-    if (st.stages == 3)
-      copy_wait<2>();
-    else
-      copy_wait<1>();
-    if (V == 1) __syncthreads();
-    uint64_t u[ROWS][kP];
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) take(X(), p.f, p.ldf, t0 + r * step, at + r * st.f_row, u[r]);
-    if (p.post != W4A8_NORM_NONE) normalise_rows(u, p.post);
-    scale_rows(u, w_post, biases);
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const int64_t t = t0 + r * step;
-      if (p.gate_scalar) {
-#pragma unroll
-        for (int i = 0; i < kP; ++i) u[r][i] = mul2(u[r][i], pair(gs[r], gs[r]));
-        gs[r] = scalar_gate(t + ROWS * step);
-      }
-      if (st.gate_rows) {
-        uint64_t a[kP];
-        uint8_t* g = at + st.g_at + r * st.g_row;
-        if (p.gate_f32)
-          take(float(), p.gate, p.ldg, gate_index(t), g, a);
-        else
-          take(X(), p.gate, p.ldg, gate_index(t), g, a);
-#pragma unroll
-        for (int i = 0; i < kP; ++i) u[r][i] = mul2(u[r][i], a[i]);
-      }
-      if (p.r) {
-        uint64_t a[kP];
-        take(R(), p.r, p.ldr, t, at + st.r_at + r * st.r_row, a);
-#pragma unroll
-        for (int i = 0; i < kP; ++i) u[r][i] = fma2(rs, a[i], u[r][i]);
-      }
-      if (p.h && t < p.T) put(R(), p.h, p.ldh, t, u[r]);
-    }
-    if (V == 1) __syncthreads();  // every thread has read the stage
-    fetch(t0 + st.stages * ROWS * step, at);
-    s = s + 1 == st.stages ? 0 : s + 1;
-    if (!p.y) continue;
-    if (p.pre != W4A8_NORM_NONE) normalise_rows(u, p.pre);
-    scale_rows(u, w_pre, biases + kP * threads);
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r)
-      if (t0 + r * step < p.T) put(X(), p.y, p.ldy, t0 + r * step, u[r]);
-  }
-  copy_wait<0>();
-}
-
-template <typename X, typename R, int V, int VPT>
-int launch_row(const NormParams& p, cudaStream_t st) {
-  const int64_t per = ceil_div(ceil_div(p.H, V * VPT), 32) * 32;  // threads of a row
-  const int rows = per == 32 ? 8 : 1;
-  return launch_pdl("block_norm_row_kernel", block_norm_row_kernel<X, R, V, VPT>,
-                    dim3(static_cast<unsigned>(ceil_div(p.T, rows))), dim3(static_cast<unsigned>(per), rows), 0, st, p);
-}
-
-constexpr int kMaxSmem = 227 * 1024;
-
-template <typename X, typename R, int V, bool BIAS, int kE>
-int launch_stream(const NormParams& p, const NormStage& stage, int threads, int rows, cudaStream_t st) {
-  auto kern = block_norm_stream_kernel<X, R, V, BIAS, kE>;
-  static DeviceOnce once;
-  if (int rc = once.run([&] {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024) != cudaSuccess)
-          return check_launch("cudaFuncSetAttribute(block_norm)");
-        return static_cast<int>(W4A8_OK);
-      }))
-    return rc;
-  // as many blocks as run at once: max_threads(kE) threads have registers, and shared memory takes the ring (with the
-  // kernel's static part and the 1 KB that a block costs)
-  const int64_t smem = static_cast<int64_t>(stage.stages) * stage.bytes + (BIAS ? threads * rows * kE * 8 : 0);
-  const int64_t per_sm =
-      std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(max_threads(kE) / (threads * rows), kMaxSmem / (smem + 1280)), 16));
-  const int64_t blocks = std::min(ceil_div(p.T, rows), per_sm * num_sms());
-  return launch_pdl("block_norm_stream_kernel", kern, dim3(static_cast<unsigned>(blocks)), dim3(threads, rows),
-                    static_cast<size_t>(smem), st, p, stage);
-}
-
-// Whether the rows fit the streaming kernel (two stages of them in shared memory); *rc is the launch's status then.
-template <typename X, typename R, int V, int kE>
-bool try_stream(const NormParams& p, cudaStream_t st, int* rc) {
-  if (p.H > kE * max_threads(kE)) return false;
-  const bool bias = p.b_post || p.b_pre;
-  const int threads = static_cast<int>(ceil_div(ceil_div(p.H, kE), 32) * 32);
-  const int rows = V == 8 && threads == 32 ? 4 : 1;
-  constexpr int turn = 2;  // rows of a stage
-  NormStage stage;
-  stage.gate_rows = p.gate && !p.gate_scalar && p.rows_per_gate < p.T;
-  // one row of a part: the block's vectors, or the 16-byte pieces that cover a row
-  const auto part = [&](int size) { return V == 8 ? threads * rows * kE * size : (p.H * size + 15) / 16 * 16 + 16; };
-  stage.f_row = part(sizeof(X));
-  stage.r_row = p.r ? part(sizeof(R)) : 0;
-  stage.g_row = stage.gate_rows ? part(p.gate_f32 ? 4 : static_cast<int>(sizeof(X))) : 0;
-  stage.r_at = turn * stage.f_row;
-  stage.g_at = stage.r_at + turn * stage.r_row;
-  stage.bytes = stage.g_at + turn * stage.g_row;
-  const int room = kMaxSmem - 1280 - (bias ? threads * rows * kE * 8 : 0);
-  if (2 * stage.bytes > room) return false;
-  stage.stages = 3 * stage.bytes <= room ? 3 : 2;
-  *rc = bias ? launch_stream<X, R, V, true, kE>(p, stage, threads, rows, st)
-             : launch_stream<X, R, V, false, kE>(p, stage, threads, rows, st);
-  return true;
-}
-
-template <typename X, typename R>
-int dispatch(const NormParams& p, bool vec, cudaStream_t st) {
-  // Rows that a block works through in turn pay for the ring from the second one on; with few rows, and with rows too
-  // long for it, each gets a block of its own.
-  int rc;
-  if (p.T > 2 * num_sms()) {
-    if (vec && try_stream<X, R, 8, 16>(p, st, &rc)) return rc;
-    // single elements cost more instructions and latency each, which twice the warps hide where they fit (3001 x 5119
-    // f16 with an fp32 residual: 73 us, and 77 us with 16 elements to a thread)
-    if (!vec && (try_stream<X, R, 1, 8>(p, st, &rc) || try_stream<X, R, 1, 16>(p, st, &rc))) return rc;
-  }
-  if (vec) {
-    if (p.H <= 8192) return launch_row<X, R, 8, 1>(p, st);
-    if (p.H <= 16384) return launch_row<X, R, 8, 2>(p, st);
-    return launch_row<X, R, 8, 4>(p, st);
-  }
-  if (p.H <= 4096) return launch_row<X, R, 1, 4>(p, st);
-  if (p.H <= 8192) return launch_row<X, R, 1, 8>(p, st);
-  return launch_row<X, R, 1, 32>(p, st);
-}
-
-}  // namespace
+int launch_norm_f32(const NormParams& p, bool vec, cudaStream_t st) { return dispatch<float, float>(p, vec, st); }
 }  // namespace w4a8
 
 extern "C" int block_norm(const void* f, int64_t ldf, int dtype, const void* residual, int64_t ldr, int residual_dtype,
@@ -667,13 +39,13 @@ extern "C" int block_norm(const void* f, int64_t ldf, int dtype, const void* res
   W4A8_REQUIRE(h || y, "h and y are both null: nothing to compute");
   const int64_t sx = static_cast<int64_t>(dtype_size(dtype)), sr = static_cast<int64_t>(dtype_size(residual_dtype));
   const int64_t sp = static_cast<int64_t>(dtype_size(param_dtype)), sg = static_cast<int64_t>(dtype_size(gate_dtype));
-  bool vec = H % 8 == 0;
+  bool vec = true;  // rows start on 16-byte boundaries
   bool elem = true;
   auto look = [&](const void* q, int64_t ld, int64_t size) {
     if (!q) return;
     const uintptr_t a = reinterpret_cast<uintptr_t>(q);
     elem = elem && a % size == 0;
-    vec = vec && a % 16 == 0 && ld * size % 16 == 0;
+    vec = vec && a % 16 == 0 && (T == 1 || ld * size % 16 == 0);
   };
   look(f, ldf, sx);
   look(residual, ldr, sr);
@@ -716,7 +88,6 @@ extern "C" int block_norm(const void* f, int64_t ldf, int dtype, const void* res
   p.eps = eps;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool r32 = residual_dtype == W4A8_DTYPE_F32;
-  if (dtype == W4A8_DTYPE_F32) return dispatch<float, float>(p, vec, st);
-  if (dtype == W4A8_DTYPE_F16) return r32 ? dispatch<__half, float>(p, vec, st) : dispatch<__half, __half>(p, vec, st);
-  return r32 ? dispatch<__nv_bfloat16, float>(p, vec, st) : dispatch<__nv_bfloat16, __nv_bfloat16>(p, vec, st);
+  if (dtype == W4A8_DTYPE_F32) return launch_norm_f32(p, vec, st);
+  return dtype == W4A8_DTYPE_F16 ? launch_norm_f16(p, r32, vec, st) : launch_norm_bf16(p, r32, vec, st);
 }

@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(kWarps * 32) linear_stream_kernel(const Linear
   };
   const int pieces = (p.K + 2 * kStep - 1) / (2 * kStep);
   int until_flush = kChunk;
-#pragma unroll 2
+  constexpr int kUnroll = NT == 1 ? 2 : 1;  // with 16 tokens, two pieces at a time take the registers of two more blocks
+#pragma unroll kUnroll
   for (int q = split * kWarps + warp; q < pieces; q += splits * kWarps) {
     if (--until_flush < 0) {
       flush();

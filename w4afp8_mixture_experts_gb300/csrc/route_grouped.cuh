@@ -136,11 +136,19 @@ __device__ __forceinline__ void choose(uint64_t (&v)[L], int k, int lane, uint32
         v[L - 1] = 0;
       }
     }
-  } else {  // sorting this many would cost more than looking at them k times
-    for (int j = 0; j < k; ++j) {
-      uint64_t best = 0;
+  } else {  // several sorted lists: sorting as one would cost more than comparing their heads
+    constexpr int kLists = L <= 16 ? 2 : L / 8, kLen = (L + kLists - 1) / kLists;
+    uint64_t w[kLists][kLen];
 #pragma unroll
-      for (int i = 0; i < L; ++i) best = v[i] > best ? v[i] : best;
+    for (int a = 0; a < kLists; ++a) {
+#pragma unroll
+      for (int i = 0; i < kLen; ++i) w[a][i] = a * kLen + i < L ? v[a * kLen + i] : 0;
+      sort_descending<kLen>(w[a]);
+    }
+    for (int j = 0; j < k; ++j) {
+      uint64_t best = w[0][0];
+#pragma unroll
+      for (int a = 1; a < kLists; ++a) best = w[a][0] > best ? w[a][0] : best;
       const uint32_t key = static_cast<uint32_t>(best >> 32), low = static_cast<uint32_t>(best);
       const uint32_t m = lanes_max<S>(key);
       const uint32_t c = lanes_max<S>(key == m ? low : 0u);
@@ -149,8 +157,12 @@ __device__ __forceinline__ void choose(uint64_t (&v)[L], int k, int lane, uint32
         my_pos = static_cast<int>(~c);
       }
 #pragma unroll
-      for (int i = 0; i < L; ++i)
-        if (v[i] == (static_cast<uint64_t>(m) << 32 | c)) v[i] = 0;
+      for (int a = 0; a < kLists; ++a)
+        if (w[a][0] == (static_cast<uint64_t>(m) << 32 | c)) {
+#pragma unroll
+          for (int i = 0; i + 1 < kLen; ++i) w[a][i] = w[a][i + 1];
+          w[a][kLen - 1] = 0;
+        }
     }
   }
 }
@@ -390,6 +402,7 @@ int launch_lanes(const RouteParams& p, cudaStream_t st) {
   if (p.epl <= 8) return launch_epl<S, 8>(p, st);
   if constexpr (S == 16) return launch_epl<S, 10>(p, st);
   if constexpr (S == 32) {
+    if (p.epl <= 12) return launch_epl<S, 12>(p, st);
     if (p.epl <= 16) return launch_epl<S, 16>(p, st);
     if (p.epl <= 32) return launch_epl<S, 32>(p, st);
     return launch_epl<S, 64>(p, st);
