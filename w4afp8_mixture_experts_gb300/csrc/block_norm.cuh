@@ -1,10 +1,13 @@
 // The norms after and before a block in one pass over a token's row, with the block's gate and residual:
 //   u = norm_post(f)      h = residual_scale * r + branch_scale * gate * u      y = norm_pre(h)
 // norm in {none, rms, layer}; sums and the values between the two norms stay in fp32 registers, h and y are
-// each rounded once (y from the unrounded h).
+// each rounded once (y from the unrounded h).  A LayerNorm takes the mean first, then the squared differences from it.
 //
-// A row is held by the threads of one block (or one warp, for short rows: several rows to a block); the row's
-// sums are one block reduction each (the mean first, then the squared differences, for a LayerNorm).
+// Bound by memory (each of f, r, h and y once).  Two kernels:
+//   row kernel: a row to a block, or to 8, 16 or 32 lanes.  64 x 7168 bf16 takes 3.6 us, of which a launch is 2.5.
+//   streaming kernel (16-bit rows, many of them): blocks stay and copy the rows to come into a ring in shared memory.
+//     8192 x 7168 bf16 with a channel gate: 82 us, 5.7 TB/s (a row to a block: 134 us).  3001 x 5119 f16 with an fp32
+//     residual, two LayerNorms and no alignment: 69 us, 2.7 TB/s; there it is bound by instructions, ~85 for an element.
 #pragma once
 
 #include <algorithm>
@@ -630,9 +633,14 @@ bool try_stream(const NormParams& p, cudaStream_t st, int* rc) {
   stage.r_at = turn * stage.f_row;
   stage.g_at = stage.r_at + turn * stage.r_row;
   stage.bytes = stage.g_at + turn * stage.g_row;
-  const int room = kMaxSmem - 1280 - (bias ? threads * rows * kE * 8 : 0);
-  if (2 * stage.bytes > room) return false;
-  stage.stages = 3 * stage.bytes <= room ? 3 : 2;
+  // three stages where that leaves an SM as many blocks as two do (8192 x 4096 bf16 with an fp32 residual: one block of 256
+  // threads with three, two with two)
+  const auto blocks = [&](int stages) {
+    const int smem = stages * stage.bytes + (bias ? threads * rows * kE * 8 : 0) + 1280;
+    return std::min(max_threads(kE) / (threads * rows), kMaxSmem / smem);
+  };
+  if (blocks(2) < 1) return false;
+  stage.stages = blocks(3) < blocks(2) ? 2 : 3;
   *rc = bias ? launch_stream<X, R, V, true, kE>(p, stage, threads, rows, st)
              : launch_stream<X, R, V, false, kE>(p, stage, threads, rows, st);
   return true;
@@ -645,15 +653,22 @@ int dispatch(const NormParams& p, bool vec, cudaStream_t st) {
   int rc;
   // rows of up to 256 elements go to a warp or a part of one, however many they are
   if (vec && p.H <= 256) return launch_row<X, R, 8, 1>(p, st);
-  if (p.T > 2 * num_sms()) {
-    if (vec && p.H % 8 == 0 && try_stream<X, R, 8, 16>(p, st, &rc)) return rc;
+  // fp32 rows fill the memory's pipes from registers, and the ring would take the threads' room (9000 x 1024: 24.5 us a row
+  // to a block, 41.0 us with the ring; bf16, 16384 x 1024: 35.7 and 23.4 us)
+  const bool stream = p.T > 2 * num_sms() && !(vec && sizeof(X) == 4);
+  if (stream) {
+    if constexpr (sizeof(X) != 4) {
+      if (vec && p.H % 8 == 0 && try_stream<X, R, 8, 16>(p, st, &rc)) return rc;
+    }
     // single elements cost more instructions and latency each, which twice the warps hide where they fit (3001 x 5119
     // f16 with an fp32 residual: 73 us, and 77 us with 16 elements to a thread)
     if ((!vec || p.H % 8) && (try_stream<X, R, 1, 8>(p, st, &rc) || try_stream<X, R, 1, 16>(p, st, &rc))) return rc;
   }
   if (vec) {
-    if (p.H <= 8192) return launch_row<X, R, 8, 1>(p, st);
-    if (p.H <= 16384) return launch_row<X, R, 8, 2>(p, st);
+    // few rows: as many threads to a row as possible; many: half as many, so that two rows share an SM
+    const bool many = p.T > 2 * num_sms();
+    if (p.H <= (many ? 4096 : 8192)) return launch_row<X, R, 8, 1>(p, st);
+    if (p.H <= (many ? 8192 : 16384)) return launch_row<X, R, 8, 2>(p, st);
     return launch_row<X, R, 8, 4>(p, st);
   }
   if (p.H <= 4096) return launch_row<X, R, 1, 4>(p, st);

@@ -6,12 +6,17 @@
 //   rows on M, 128 per CTA; W rows on N, each CTA loads half of them).  Persistent, the accumulator double
 //   buffered over the whole tensor memory, so that the epilogue of one tile runs under the products of the
 //   next.  When gated, one CTA loads 128 gate rows and the other the 128 matching rows of the other half: both
-//   CTAs then hold, for their 128 tokens, the two halves of 128 output columns side by side.
+//   CTAs then hold, for their 128 tokens, the two halves of 128 output columns side by side.  With few tiles, two or
+//   four pairs of a cluster share a tile by pieces of K.
+//     8192 x 4096 x 7168 gated: 240 us, 2.0 PFLOP/s, by itself, and 1.7 PFLOP/s under the power limit (products);
+//     8192 x 7168 x 2048 with a residual: 133-145 us (products, then the residual's read and the output's write);
+//     8192 x 256 x 7168, fp32 out, two pieces of K: 33 us (x at 4 TB/s, then 6 us of exchange and epilogue).
 //
 //   split kernel (few rows, or few tiles): a CTA computes a 128 x BN tile with W rows on M and tokens on N over
 //   one piece of K; the CTAs of a cluster take the pieces of one tile, push their partial products into the
 //   shared memory of the CTA that owns a token, and every owner adds its parts in rank order and finishes its
 //   tokens.  One launch, no workspace, and a result that does not depend on timing.
+//     64 x 4096 x 7168 gated: 14.3 us, W at 4.1 TB/s; 64 x 256 x 7168: 6.2 us (8 pieces of K; launch and latency).
 //
 // Every wait is bounded: on expiry the CTA raises its abort flag and the device error word, lets its copies and
 // products in flight finish (again with a limit), frees its tensor memory and returns.
@@ -333,6 +338,7 @@ __device__ __forceinline__ void store_row(const LinearParams& p, const PairPlan&
 // about n / 2 units of fp32 to one side (3.8e-6 of the result at K = 3584, where plain fp32 sums have 0.9e-6).  That does
 // not show in a 16-bit output; for an fp32 one, sums over kChunk stages are added up in registers, rounded to nearest.
 constexpr int kChunk = 16;
+constexpr int kPrefetchStages = 16;  // K up to which the pair kernel's epilogue prefetches the next residual
 constexpr int kRegsLaunch = 168;  // of a thread at launch (checked on the host)
 constexpr int kRegsRoles = 40, kRegsSums = 232;  // registers of warps 0-3 and of the epilogue's, which hold 128 sums
 static_assert(128 * kRegsRoles + 32 * kPairEpiWarps * kRegsSums <= kPairThreads * kRegsLaunch, "within the launch's registers");
@@ -383,85 +389,106 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
-  if constexpr (CHUNKED) {
-    if (warp < 4) regs_release<kRegsRoles>();
-  }
-
   const int first = blockIdx.x / (2 * PARTS), stride = PARTS > 1 ? pl.tiles : gridDim.x / 2;
   const int kb0 = static_cast<int>(static_cast<int64_t>(part) * pl.kblocks / PARTS);
   const int kb1 = static_cast<int>(static_cast<int64_t>(part + 1) * pl.kblocks / PARTS);
-  if (warp == 0) {  // TMA producer of this CTA's half of every stage
-    uint32_t it = 0;
-    bool ok = true;
-    for (int i = first; ok && i < pl.tiles; i += stride) {
-      int tm, tn;
-      pair_tile(pl, i, tm, tn);
-      const int m = tm * 256 + rank * 128;
-      const int n = GATED ? rank * p.n_out + tn * 128 : tn * 256 + rank * 128;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int s = it % kPairStages;
-        if (!(ok = warp_wait(&empty[s], ((it / kPairStages) & 1) ^ 1, abort_flag))) break;
-        if (elect_one()) {
-          uint8_t* at = smem + s * kPairStageBytes;
-          const uint32_t bar = map_to_cta(smem_u32(&full[s]), lead);
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStageBytes);
-          tma_load_pair(at, &tx, bar, kb * kBK, m);
-          tma_load_pair(at + kATile, &tw, bar, kb * kBK, n);
+  // no CTA of the cluster leaves while another may still signal it or read its operands
+  auto leave = [&] {
+    __syncwarp();
+    tc_fence_before();
+    cluster_arrive();
+    cluster_wait();
+  };
+  // Warps 0-3 end inside this branch: with CHUNKED they hold fewer registers than the code behind it is built for.
+  if (warp < 4) {
+    if constexpr (CHUNKED) regs_release<kRegsRoles>();
+    if (warp == 0) {  // TMA producer of this CTA's half of every stage
+      uint32_t it = 0;
+      bool ok = true;
+      for (int i = first; ok && i < pl.tiles; i += stride) {
+        int tm, tn;
+        pair_tile(pl, i, tm, tn);
+        const int m = tm * 256 + rank * 128;
+        const int n = GATED ? rank * p.n_out + tn * 128 : tn * 256 + rank * 128;
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const int s = it % kPairStages;
+          if (!(ok = warp_wait(&empty[s], ((it / kPairStages) & 1) ^ 1, abort_flag))) break;
+          if (elect_one()) {
+            uint8_t* at = smem + s * kPairStageBytes;
+            const uint32_t bar = map_to_cta(smem_u32(&full[s]), lead);
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStageBytes);
+            tma_load_pair(at, &tx, bar, kb * kBK, m);
+            tma_load_pair(at + kATile, &tw, bar, kb * kBK, n);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
-    }
-    // the last stages' slots are released before the CTA may go (and, after an abort, their loads have landed)
-    const uint32_t n = it < kPairStages ? it : kPairStages;
-    for (uint32_t j = it - n; j < it; ++j) {
-      const uint32_t s = j % kPairStages, ph = (j / kPairStages) & 1;
-      if (!(ok && (ok = warp_wait(&empty[s], ph, abort_flag))) && rank == 0) drain_bar(&full[s], ph);
-    }
-  } else if (warp == 1 && rank == 0) {  // the pair's products
-    const uint32_t idesc = idesc_f16(p.dtype == W4A8_DTYPE_BF16, 256, 256);
-    const uint16_t both = static_cast<uint16_t>(3 << lead);
-    uint32_t it = 0;
-    int n = 0;  // accumulator fills so far
-    bool ok = true;
-    for (int i = first; ok && i < pl.tiles; i += stride) {
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int s = it % kPairStages, at_chunk = CHUNKED ? (kb - kb0) % kChunk : kb - kb0;
-        const int buf = n & 1;
-        if (at_chunk == 0) {
-          if (!(ok = warp_wait(&tempty[buf], ((n >> 1) & 1) ^ 1, abort_flag))) break;
+      // the last stages' slots are released before the CTA may go (and, after an abort, their loads have landed)
+      const uint32_t n = it < kPairStages ? it : kPairStages;
+      for (uint32_t j = it - n; j < it; ++j) {
+        const uint32_t s = j % kPairStages, ph = (j / kPairStages) & 1;
+        if (!(ok && (ok = warp_wait(&empty[s], ph, abort_flag))) && rank == 0) drain_bar(&full[s], ph);
+      }
+    } else if (warp == 1 && rank == 0) {  // the pair's products
+      const uint32_t idesc = idesc_f16(p.dtype == W4A8_DTYPE_BF16, 256, 256);
+      const uint16_t both = static_cast<uint16_t>(3 << lead);
+      uint32_t it = 0;
+      int n = 0;  // accumulator fills so far
+      bool ok = true;
+      for (int i = first; ok && i < pl.tiles; i += stride) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const int s = it % kPairStages, at_chunk = CHUNKED ? (kb - kb0) % kChunk : kb - kb0;
+          const int buf = n & 1;
+          if (at_chunk == 0) {
+            if (!(ok = warp_wait(&tempty[buf], ((n >> 1) & 1) ^ 1, abort_flag))) break;
+            tc_fence_after();
+          }
+          if (!(ok = warp_wait(&full[s], (it / kPairStages) & 1, abort_flag))) break;
           tc_fence_after();
-        }
-        if (!(ok = warp_wait(&full[s], (it / kPairStages) & 1, abort_flag))) break;
-        tc_fence_after();
-        const uint32_t at = smem_u32(smem + s * kPairStageBytes);
-        const uint64_t a = operand_desc(at), b = operand_desc(at + kATile);
-        const bool last = kb + 1 == kb1 || (CHUNKED && at_chunk == kChunk - 1);
-        if (elect_one()) {
+          const uint32_t at = smem_u32(smem + s * kPairStageBytes);
+          const uint64_t a = operand_desc(at), b = operand_desc(at + kATile);
+          const bool last = kb + 1 == kb1 || (CHUNKED && at_chunk == kChunk - 1);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k)
-            mma_f16<2>(tmem + buf * 256, a + 2 * k, b + 2 * k, idesc, at_chunk > 0 || k > 0);
-          commit_pair(&empty[s], both);
-          if (last) commit_pair(&tfull[buf], both);
+            for (int k = 0; k < kBK / 16; ++k)
+              mma_f16<2>(tmem + buf * 256, a + 2 * k, b + 2 * k, idesc, at_chunk > 0 || k > 0);
+            commit_pair(&empty[s], both);
+            if (last) commit_pair(&tfull[buf], both);
+          }
+          __syncwarp();
+          n += last;
         }
+      }
+      if (!ok) {
+        if (elect_one())
+          asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(mdrain))
+                       : "memory");
         __syncwarp();
-        n += last;
+        drain_bar(mdrain, 0);
       }
     }
-    if (!ok) {
-      if (elect_one())
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(mdrain))
-                     : "memory");
-      __syncwarp();
-      drain_bar(mdrain, 0);
-    }
-  }
 
-  if (PARTS > 1 && (warp == 2 || warp == 3) && p.residual && !pl.vec_out) {  // aligned rows are read ahead below
-    int tm, tn;
-    pair_tile(pl, first, tm, tn);
-    prefetch_residual(p, tm * 256 + rank * 128, tn * pl.out_cols + part * (pl.out_cols / PARTS), 128,
-                      pl.out_cols / PARTS, threadIdx.x - 64, 64);
+    if (PARTS > 1 && (warp == 2 || warp == 3) && p.residual && !pl.vec_out) {  // aligned rows are read ahead below
+      int tm, tn;
+      pair_tile(pl, first, tm, tn);
+      prefetch_residual(p, tm * 256 + rank * 128, tn * pl.out_cols + part * (pl.out_cols / PARTS), 128,
+                        pl.out_cols / PARTS, threadIdx.x - 64, 64);
+    }
+    if constexpr (PARTS > 1) {  // the exchange's two barriers
+      __syncwarp();
+      for (int i = 0; i < 2; ++i) {
+        cluster_arrive();
+        cluster_wait();
+      }
+    }
+    leave();
+    if (warp == 2) {
+      tc_fence_after();
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+    return;
   }
+  if constexpr (CHUNKED) regs_claim<kRegsSums>();
 
   // epilogue: warp e reads lane quarter e % 4 (its tokens) and, by e / 4, one half of the columns that this CTA
   // finishes; a turn is kN columns
@@ -551,44 +578,47 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   };
 
   if constexpr (PARTS == 1) {
-    if (warp >= 4) {
-      if constexpr (CHUNKED) regs_claim<kRegsSums>();
-      for (int i = first; i < pl.tiles; i += stride) {
-        int tm, tn;
-        pair_tile(pl, i, tm, tn);
-        const int n0 = tn * pl.out_cols + nh;
-        const int m0 = tm * 256 + rank * 128 + quarter * 32;
-        uint32_t res[kPieces][8];
-        if (ahead) read_ahead(m0 + lane, n0, res);
-        if (p.bias) load_bias(n0);
-        const int buf = products();
-        if (buf < 0) break;
-        const uint32_t at = tmem + buf * 256 + lanes + nh;
+    for (int i = first; i < pl.tiles; i += stride) {
+      int tm, tn;
+      pair_tile(pl, i, tm, tn);
+      const int n0 = tn * pl.out_cols + nh;
+      const int m0 = tm * 256 + rank * 128 + quarter * 32;
+      uint32_t res[kPieces][8];
+      if (ahead) read_ahead(m0 + lane, n0, res);
+      if (p.bias) load_bias(n0);
+      const int buf = products();
+      if (buf < 0) break;
+      // With a short K the epilogue is the longer part, and the residual's latency shows: the next tile's goes to L2
+      // now (8192 x 7168 x 512: 73.8 -> 68.6 us, K = 1024: 84.6 -> 82.1; K = 1536: 104.3 -> 106.9, so not there).
+      if (p.residual && pl.kblocks <= kPrefetchStages && i + stride < pl.tiles) {
+        int um, un;
+        pair_tile(pl, i + stride, um, un);
+        prefetch_residual(p, um * 256 + rank * 128 + quarter * 32, un * pl.out_cols + nh, 32, kCols, lane, 32);
+      }
+      const uint32_t at = tmem + buf * 256 + lanes + nh;
 #pragma unroll 1
-        for (int c = 0; c < kCols; c += 32) {
-          float v[32], u[32];
+      for (int c = 0; c < kCols; c += 32) {
+        float v[32], u[32];
+        __syncwarp();
+        tmem_ld32(at + c, reinterpret_cast<uint32_t*>(v));
+        if (GATED) tmem_ld32(at + kHalf + c, reinterpret_cast<uint32_t*>(u));
+        tmem_wait_ld_pin<32>(reinterpret_cast<uint32_t*>(v));
+        if (GATED) tmem_wait_ld_pin<32>(reinterpret_cast<uint32_t*>(u));
+        if (c + 32 == kCols) {  // every value is in registers: the accumulator is free
+          tc_fence_before();
           __syncwarp();
-          tmem_ld32(at + c, reinterpret_cast<uint32_t*>(v));
-          if (GATED) tmem_ld32(at + kHalf + c, reinterpret_cast<uint32_t*>(u));
-          tmem_wait_ld_pin<32>(reinterpret_cast<uint32_t*>(v));
-          if (GATED) tmem_wait_ld_pin<32>(reinterpret_cast<uint32_t*>(u));
-          if (c + 32 == kCols) {  // every value is in registers: the accumulator is free
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) remote_arrive(tempty0 + buf * 8);
-          }
-          if (n0 + c >= p.n_out) continue;
-          apply(v, u, c);
-          store_row<32>(p, pl, v, m0, n0 + c, ahead, res, stg);
-#pragma unroll
-          for (int j = 0; j + 2 < kPieces; ++j)
-#pragma unroll
-            for (int q = 0; q < 8; ++q) res[j][q] = res[j + 2][q];
+          if (lane == 0) remote_arrive(tempty0 + buf * 8);
         }
+        if (n0 + c >= p.n_out) continue;
+        apply(v, u, c);
+        store_row<32>(p, pl, v, m0, n0 + c, ahead, res, stg);
+#pragma unroll
+        for (int j = 0; j + 2 < kPieces; ++j)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) res[j][q] = res[j + 2][q];
       }
     }
-  } else if (warp >= 4) {
-    if constexpr (CHUNKED) regs_claim<kRegsSums>();
+  } else {
     constexpr int kPart = 2 * kCols * (GATED ? 2 : 1);  // columns of products that a CTA finishes: 256 / PARTS
     // [PARTS - 1][kPart / 4][128 tokens][4]: a thread pushes and takes 4 columns of its token at a time
     float4* recv = reinterpret_cast<float4*>(smem);
@@ -674,21 +704,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           for (int q = 0; q < 8; ++q) res[j][q] = res[j + kN / 16][q];
       }
     }
-  } else {  // warps 0-3 take part in the two cluster barriers
-    __syncwarp();
-    for (int i = 0; i < 2; ++i) {
-      cluster_arrive();
-      cluster_wait();
-    }
   }
-  __syncwarp();
-  tc_fence_before();
-  cluster_arrive();  // no CTA leaves while the other may still signal it or read its operands
-  cluster_wait();
-  if (warp == 2) {
-    tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
-  }
+  leave();
 }
 
 // --- split kernel --------------------------------------------------------------------------------------------
@@ -1182,7 +1199,7 @@ struct Pair {
     if (!CHUNKED && p.out_dtype == W4A8_DTYPE_F32 && p.K > kChunk * kBK * PARTS)
       return Pair<GATED, PARTS, true>::launch(p, dev, st);
     CUtensorMap tx, tw;
-    int rc, clusters;
+    int rc, clusters = 1;
     if ((rc = ready(dev, &clusters))) return rc;
     if ((rc = row_map(&tx, p.x, p.dtype, p.M, p.K, p.ldx, 128, "x"))) return rc;
     if ((rc = row_map(&tw, p.w, p.dtype, p.N, p.K, p.ldw, 128, "w"))) return rc;
@@ -1211,7 +1228,7 @@ struct Split {
   }
   static int launch(const LinearParams& p, int dev, cudaStream_t st) {
     CUtensorMap tx, tw;
-    int rc, clusters;
+    int rc, clusters = 1;
     if ((rc = ready(dev, &clusters))) return rc;
     if ((rc = row_map(&tx, p.x, p.dtype, p.M, p.K, p.ldx, BN, "x"))) return rc;
     if ((rc = row_map(&tw, p.w, p.dtype, p.N, p.K, p.ldw, GATED ? 64 : 128, "w"))) return rc;
@@ -1265,7 +1282,7 @@ int launch_best(const LinearParams& p, cudaStream_t st) {
     // an fp32 output's sums are kept short (see kChunk): the split kernel has four accumulators for a piece of K
     if (!force && o.rows < 256 && p.out_dtype == W4A8_DTYPE_F32 && kblocks > 4 * kChunk * o.parts) continue;
     if (o.parts > kblocks || (force && force % 16 <= kblocks && force != o.rows * 16 + o.parts)) continue;
-    int clusters;
+    int clusters = 1;
     if (int rc = o.ready(dev, &clusters)) return rc;
     const int64_t tiles = ceil_div(p.M, o.rows) * ceil_div(p.N, o.cols);
     const int64_t waves = ceil_div(tiles, clusters);
