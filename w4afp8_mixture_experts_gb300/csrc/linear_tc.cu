@@ -710,10 +710,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
 // --- split kernel --------------------------------------------------------------------------------------------
 
-constexpr int kSplitThreads = 256;
 
 template <int BN>
 struct SplitCfg {
+  // 16 warps share the epilogue's latencies (128 x 7168 x 2048: 13.0 us with 8 warps, 11.5 with 16), but for 32 tokens it
+  // is short, and the larger launch costs more (64 x 256 x 7168: 6.25 and 6.7 us)
+  static constexpr int kThreads = BN == 32 ? 256 : 512;
   static constexpr int kStageBytes = kATile + BN * kBK * 2;
   static constexpr int kStages = BN == 128 ? 4 : BN == 64 ? 6 : 8;
   static constexpr int kOffRed = kStages * kStageBytes;       // [source CTA][token of mine][128 W rows] fp32
@@ -726,25 +728,25 @@ struct SplitCfg {
   // A warp waits for every phase of the slots that it uses, in order, only if a slot always falls to the same warp:
   // otherwise its parity wait is satisfied by the phase before the one it needs.
   static_assert(kStages % kMma == 0, "ring depth a multiple of the MMA warps");
-  static constexpr int kTurns = BN * 16 / kSplitThreads;  // tokens of a thread in the epilogue, at most
+  static constexpr int kTurns = BN * 16 / kThreads;  // tokens of a thread in the epilogue, at most
   static constexpr uint32_t kTmemCols = 2 * kMma * BN;  // an fp32 output spreads its sums over two accumulators a warp
   static_assert(kSmem <= kMaxSmem, "shared memory");
 };
 
 // The epilogue's threads: with aligned rows a thread finishes 8 neighbouring columns of every kStep-th token, without
 // alignment one column of them (so that a warp touches neighbours).
-template <bool GATED>
+template <int BN, bool GATED>
 struct SplitMap {
   static constexpr int kOutCols = GATED ? 64 : 128;
   static constexpr int kOct = kOutCols / 8;
-  static constexpr int kOctStep = kSplitThreads / kOct, kColStep = kSplitThreads / kOutCols;
+  static constexpr int kOctStep = SplitCfg<BN>::kThreads / kOct, kColStep = SplitCfg<BN>::kThreads / kOutCols;
 };
 
 // The biases of this thread's columns and the aligned 16-bit residual of all its tokens.
 template <int BN, bool GATED>
 __device__ __forceinline__ void read_ahead_split(const LinearParams& p, int m, int n0, int own, int vec_out,
                                                  float (&bias)[8], float (&bias2)[8], uint4 (&res)[SplitCfg<BN>::kTurns]) {
-  using Map = SplitMap<GATED>;
+  using Map = SplitMap<BN, GATED>;
   const int n = n0 + (vec_out ? threadIdx.x % Map::kOct * 8 : threadIdx.x % Map::kOutCols);
   const int bd = p.bias_f32 ? W4A8_DTYPE_F32 : p.dtype;
 #pragma unroll
@@ -768,7 +770,7 @@ template <int BN, bool GATED, typename T>
 __device__ __forceinline__ void finish_tokens(const LinearParams& p, const float* red, int splits, int own, int left, int m,
                                               int n0, int vec_out, const float (&bias)[8], const float (&bias2)[8],
                                               const uint4 (&res)[SplitCfg<BN>::kTurns]) {
-  using Map = SplitMap<GATED>;
+  using Map = SplitMap<BN, GATED>;
   const T* residual = static_cast<const T*>(p.residual);
   T* out = static_cast<T*>(p.out);
   if (!vec_out) {
@@ -871,7 +873,7 @@ __device__ __forceinline__ void finish_tokens(const LinearParams& p, const float
 }
 
 template <int BN, bool GATED>
-__global__ void __launch_bounds__(kSplitThreads, 1)
+__global__ void __launch_bounds__(SplitCfg<BN>::kThreads, 1)
     linear_split_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw,
                         const LinearParams p, int splits, int kblocks, int vec_out) {
   using C = SplitCfg<BN>;
@@ -966,11 +968,11 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   __syncwarp();
   tc_fence_after();
   if (splits > 1) cluster_wait();
-  // this CTA's partial products to the owners of their tokens: warp w reads lane quarter w % 4 (W rows), half
-  // w / 4 of the tokens
+  // this CTA's partial products to the owners of their tokens: warp w reads lane quarter w % 4 (W rows) and the tokens
+  // of its turn w / 4
   const int quarter = warp & 3, f = quarter * 32 + lane;
   if (ok) {
-    constexpr int kCols = BN / 2;
+    constexpr int kCols = BN / (C::kThreads / 128);  // of a warp; its lane quarter is a fourth of the W rows
     constexpr int kStep = kCols < 32 ? kCols : 32;
     const uint32_t red = smem_u32(smem + C::kOffRed);
 #pragma unroll 1
@@ -983,8 +985,10 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
         const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + m * BN + c;
         if constexpr (kStep == 32)
           tmem_ld32(at, reinterpret_cast<uint32_t*>(w));
-        else
+        else if constexpr (kStep == 16)
           tmem_ld16(at, reinterpret_cast<uint32_t*>(w));
+        else
+          tmem_ld8(at, reinterpret_cast<uint32_t(&)[8]>(w));
         tmem_wait_ld_pin<kStep>(reinterpret_cast<uint32_t*>(w));
 #pragma unroll
         for (int j = 0; j < kStep; ++j) v[j] = m > 0 ? v[j] + w[j] : w[j];
@@ -1224,7 +1228,7 @@ struct Split {
     return l;
   }
   static int ready(int dev, int* clusters) {
-    return launcher().prepare(dev, clusters, linear_split_kernel<BN, GATED>, C::kSmem, kSplitThreads, SPLITS);
+    return launcher().prepare(dev, clusters, linear_split_kernel<BN, GATED>, C::kSmem, C::kThreads, SPLITS);
   }
   static int launch(const LinearParams& p, int dev, cudaStream_t st) {
     CUtensorMap tx, tw;
@@ -1234,7 +1238,7 @@ struct Split {
     if ((rc = row_map(&tw, p.w, p.dtype, p.N, p.K, p.ldw, GATED ? 64 : 128, "w"))) return rc;
     const unsigned nb = static_cast<unsigned>(ceil_div(p.n_out, GATED ? 64 : 128));
     return Launcher::launch("linear_split_kernel", linear_split_kernel<BN, GATED>,
-                            dim3(nb * SPLITS, static_cast<unsigned>(ceil_div(p.M, BN))), kSplitThreads, C::kSmem, SPLITS,
+                            dim3(nb * SPLITS, static_cast<unsigned>(ceil_div(p.M, BN))), C::kThreads, C::kSmem, SPLITS,
                             st, tx, tw, p, SPLITS, static_cast<int>(ceil_div(p.K, kBK)), vec_rows(p));
   }
 };
