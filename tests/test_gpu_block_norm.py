@@ -183,3 +183,49 @@ def test_refusals(lib):
         lib.block_norm(f, post="rms", w_post=w, pre="rms", w_pre=w.to(torch.bfloat16))
     with pytest.raises(ValueError, match="w_pre"):
         lib.block_norm(f, w_pre=torch.ones(63, device="cuda"))
+
+
+@pytest.mark.parametrize("pad,shift", [(0, 0), (1, 1), (0, 3), (5, 2), (8, 7), (2, 4)])
+@pytest.mark.parametrize("T,H", [(2, 705), (401, 705), (401, 2047), (309, 3999), (3, 7001), (330, 7680), (401, 7682),
+                                 (307, 9001)])
+@pytest.mark.parametrize("dtype,rdtype", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f32")])
+def test_rows_that_start_alike_in_every_matrix(lib, dtype, rdtype, T, H, pad, shift):
+    # whole aligned vectors and the single elements beside them, for every start of a row within 16 bytes
+    _check(lib, T, H, dtype=dtype, rdtype=rdtype, post="layer", pre="rms", gate=(T, H), bias=True, pad=pad, shift=shift,
+           alias=True, seed=11)
+    _check(lib, T, H, dtype=dtype, rdtype=rdtype, post="rms", pre="layer", gate=(T, 1), pad=pad, shift=shift, alias=True,
+           seed=12)
+
+
+@pytest.mark.parametrize("T,H,groups", [(400, 1003, 4), (400, 1000, 8), (2, 1003, 2)])
+@pytest.mark.parametrize("pad,shift", [(5, 0), (5, 3), (0, 1)])
+def test_gates_of_several_rows(lib, T, H, groups, pad, shift):
+    _check(lib, T, H, gate=(groups, H), pad=pad, shift=shift, alias=True, seed=13)
+    _check(lib, T, H, dtype="f16", rdtype="f32", gate=(groups, H), pad=pad, shift=shift, alias=True, seed=14)
+
+
+@pytest.mark.parametrize("T,H,pad,shift", [(2, 1001, 0, 1), (401, 1001, 3, 3), (401, 771, 0, 5), (350, 5119, 2, 6)])
+@pytest.mark.parametrize("dtype,rdtype", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f32")])
+def test_nothing_beside_the_rows_is_written_or_counted(lib, dtype, rdtype, T, H, pad, shift):
+    g = torch.Generator("cuda").manual_seed(15)
+    bufs, views = [], []
+    for dt in (dtype, rdtype):
+        buf = torch.full((T * (H + pad) + shift + 16,), float("inf"), dtype=DT[dt], device="cuda")
+        v = buf[shift:shift + T * (H + pad)].view(T, H + pad)[:, :H]
+        v.copy_(torch.randn((T, H), device="cuda", generator=g).to(DT[dt]))
+        bufs.append(buf)
+        views.append(v)
+    beside = [torch.ones_like(b, dtype=torch.bool) for b in bufs]
+    for m in beside:
+        m[shift:shift + T * (H + pad)].view(T, H + pad)[:, :H] = False
+    f, r = views
+    h0, y0 = lib.block_norm(f.contiguous(), r.contiguous(), post="layer", pre="layer", residual_dtype=DT[rdtype])
+    lib.block_norm(f, r, post="layer", pre="layer", residual_dtype=DT[rdtype], h=r, y=f)
+    torch.cuda.synchronize()
+    for b, m in zip(bufs, beside):
+        assert torch.isinf(b[m]).all()
+    assert torch.isfinite(r).all() and torch.isfinite(f).all()
+    # the sums' order differs with a row's start: a few units in the last place of fp32, then each type's rounding
+    eps = {"bf16": 2.0**-7, "f16": 2.0**-9, "f32": 2.0**-18}
+    assert torch.all((r.double() - h0.double()).abs() <= eps[rdtype] * (1 + h0.double().abs()))
+    assert torch.all((f.double() - y0.double()).abs() <= eps[dtype] * (1 + y0.double().abs()))

@@ -5,12 +5,14 @@
 //
 // Bound by memory (each of f, r, h and y once).  Two kernels:
 //   row kernel: a row to a block, or to 8, 16 or 32 lanes.  64 x 7168 bf16 takes 3.6 us, of which a launch is 2.5.
-//   streaming kernel (16-bit rows, many of them): blocks stay and copy the rows to come into a ring in shared memory.
-//     8192 x 7168 bf16 with a channel gate: 82 us, 5.7 TB/s (a row to a block: 134 us).  3001 x 5119 f16 with an fp32
-//     residual, two LayerNorms and no alignment: 69 us, 2.7 TB/s; there it is bound by instructions, ~85 for an element.
+//   streaming kernel (many rows): blocks stay and copy the rows to come into a ring in shared memory.
+//     8192 x 7168 bf16 with a channel gate: 78 us, 6.0 TB/s (a row to a block: 134 us).  3001 x 5119 f16 with an fp32
+//     residual, two LayerNorms and no alignment: 47 us, 3.9 TB/s; there it is bound by instructions: two LayerNorms'
+//     reductions and 10 rounds of two rows to each block.
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "block_ops.cuh"
 #include "common.cuh"
@@ -61,6 +63,8 @@ __device__ __forceinline__ void store_vec(T* p, const float (&o)[V]) {
   if constexpr (V == 8 && sizeof(T) == 2) {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(o[0], o[1]), pack2<T>(o[2], o[3]), pack2<T>(o[4], o[5]),
                                               pack2<T>(o[6], o[7]));
+  } else if constexpr (V == 4 && sizeof(T) == 2) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(o[0], o[1]), pack2<T>(o[2], o[3]));
   } else {
     Pack<T, V> a;
 #pragma unroll
@@ -115,8 +119,10 @@ __device__ __forceinline__ float row_sum(float v, float* scratch, int& slot) {
   return warp_sum(lane < warps ? s[lane] : 0.f);
 }
 
-template <int V, int VPT>
-__device__ __forceinline__ void normalise(float (&u)[VPT][V], int kind, int H, float eps, float* scratch, int& slot) {
+// `count(j)`: how many elements of this thread's vector j are the row's (at least V: all)
+template <int V, int VPT, class C>
+__device__ __forceinline__ void normalise(float (&u)[VPT][V], int kind, int H, float eps, float* scratch, int& slot,
+                                          C&& count) {
   float s = 0.f;
   if (kind == W4A8_NORM_LAYER) {
 #pragma unroll
@@ -127,7 +133,7 @@ __device__ __forceinline__ void normalise(float (&u)[VPT][V], int kind, int H, f
     s = 0.f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int left = H - (j * blockDim.x + threadIdx.x) * V;
+      const int left = count(j);
 #pragma unroll
       for (int i = 0; i < V; ++i) u[j][i] = i < left ? u[j][i] - mean : 0.f;
     }
@@ -143,44 +149,13 @@ __device__ __forceinline__ void normalise(float (&u)[VPT][V], int kind, int H, f
     for (int i = 0; i < V; ++i) u[j][i] *= inv;
 }
 
-// A parameter row over this thread's columns, given to f(j, values) vector by vector.  Single elements are loaded 8 at a
-// time, inside one branch on the type: a branch around each of them waited for each load by itself.
-template <typename X, int V, int VPT, class F>
-__device__ __forceinline__ void with_param(const void* p, int f32, int64_t at, int H, F&& f) {
-  constexpr int kAtOnce = V == 8 ? 1 : VPT < 8 ? VPT : 8;
-#pragma unroll
-  for (int j0 = 0; j0 < VPT; j0 += kAtOnce) {
-    float a[kAtOnce][V];
-    if (f32) {
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j)
-        load_cut<float, V>(static_cast<const float*>(p) + at, ((j0 + j) * blockDim.x + threadIdx.x) * V, H, a[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j)
-        load_cut<X, V>(static_cast<const X*>(p) + at, ((j0 + j) * blockDim.x + threadIdx.x) * V, H, a[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) f(j0 + j, a[j]);
-  }
-}
-
-template <typename X, int V, int VPT>
-__device__ __forceinline__ void scale_shift(float (&u)[VPT][V], const void* w, const void* b, int f32, int H) {
-  if (w)
-    with_param<X, V, VPT>(w, f32, 0, H, [&](int j, const float (&a)[V]) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) u[j][i] *= a[i];
-    });
-  if (b)
-    with_param<X, V, VPT>(b, f32, 0, H, [&](int j, const float (&a)[V]) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) u[j][i] += a[i];
-    });
-}
-
-__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+template <int N>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  static_assert(N == 4 || N == 8 || N == 16);
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(N) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -188,9 +163,11 @@ __device__ __forceinline__ void copy_wait() {  // all but the N newest groups ha
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A row to a block (or, for short rows, to 8, 16 or 32 threads): blockDim.x threads hold a row, VPT vectors of V elements
-// each.  V = 8 takes aligned rows; their last vector may be cut short.
-template <typename X, typename R, int V, int VPT>
+// A row to a block (or, for short rows, to 8, 16 or 32 threads): VPT vectors of V elements to a thread.
+//   V > 1: aligned rows; their last vector may be cut short.
+//   V > 1, CUT: rows of any start, as long as f, r, h and y agree on where the row starts within V elements: the whole
+//     aligned vectors go to the row's threads, and the up to 2 * (V - 1) elements beside them to one more warp's lanes.
+template <typename X, typename R, int V, bool CUT, int VPT>
 __global__ void __launch_bounds__(1024) block_norm_row_kernel(const NormParams p) {
   __shared__ float scratch[64];
   pdl_trigger();
@@ -200,18 +177,92 @@ __global__ void __launch_bounds__(1024) block_norm_row_kernel(const NormParams p
   const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const bool here = row < p.T;  // where several rows share a warp, all of its lanes stay for the shuffles
   const int64_t t = here ? row : p.T - 1;
-  const auto col = [&](int j) { return static_cast<int>((j * blockDim.x + threadIdx.x) * V); };
-  constexpr bool kEarly = V * VPT <= 16;  // the residual is loaded with f, where registers hold both
+  const int tx = threadIdx.x, nx = blockDim.x - (CUT ? 32 : 0);
+  const int64_t start = static_cast<int64_t>(reinterpret_cast<uintptr_t>(p.f) / sizeof(X)) + t * p.ldf;
+  const int head = CUT ? min(static_cast<int>(-start & (V - 1)), H) : 0;
+  const int vectors = (H - head) / V;  // CUT: whole ones
+  const bool single = CUT && tx >= nx;
+  // this thread's first column
+  const int first = !single ? head + tx * V : tx - nx + (tx - nx < head ? 0 : vectors * V);
+  const auto col = [&](int j) { return CUT ? first + j * nx * V : static_cast<int>((j * blockDim.x + tx) * V); };
+  const auto count = [&](int j) {  // the row's elements in vector j
+    if (!CUT) return H - col(j);
+    return single ? (j == 0 && first < H ? 1 : 0) : j * nx + tx < vectors ? V : 0;
+  };
+  // a vector of a matrix's row, or of a parameter (which CUT may leave unaligned); zeros beside the row
+  const auto load = [&](auto type, const void* q, int64_t at, int j, bool aligned, float (&o)[V])
+                        __attribute__((always_inline)) {
+    using T = decltype(type);
+    const T* from = static_cast<const T*>(q) + at;
+    if constexpr (!CUT) {
+      load_cut<T, V>(from, col(j), H, o);
+    } else if (aligned && !single) {
+      if (count(j)) {
+        load_vec<T, V>(from + col(j), o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = 0.f;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = i < count(j) ? to_f32(from[col(j) + i]) : 0.f;
+    }
+  };
+  const auto store = [&](auto type, void* q, int64_t at, int j, const float (&o)[V]) __attribute__((always_inline)) {
+    using T = decltype(type);
+    T* to = static_cast<T*>(q) + at;
+    if constexpr (!CUT) {
+      store_cut<T, V>(to, col(j), H, o);
+    } else if (!single) {
+      if (count(j)) store_vec<T, V>(to + col(j), o);
+    } else {
+      if (count(j)) to[first] = from_f32<T>(o[0]);
+    }
+  };
+  // A parameter or matrix row over this thread's columns, given to f(j, values) vector by vector.  Single elements are
+  // loaded 8 at a time, inside one branch on the type: a branch around each of them waited for each load by itself.
+  const auto with = [&](const void* q, int f32, int64_t at, bool aligned, auto&& f) __attribute__((always_inline)) {
+    constexpr int kAtOnce = V > 1 ? 1 : VPT > 8 ? 4 : VPT;
+#pragma unroll
+    for (int j0 = 0; j0 < VPT; j0 += kAtOnce) {
+      float a[kAtOnce][V];
+      if (f32) {
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) load(float(), q, at, j0 + j, aligned, a[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) load(X(), q, at, j0 + j, aligned, a[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) f(j0 + j, a[j]);
+    }
+  };
+  constexpr bool kEarly = V * VPT <= (V > 1 ? 16 : 8);  // the residual is loaded with f, where registers hold both
   float u[VPT][V], r[kEarly ? VPT : 1][V];
 #pragma unroll
-  for (int j = 0; j < VPT; ++j) load_cut<X, V>(static_cast<const X*>(p.f) + t * p.ldf, col(j), H, u[j]);
+  for (int j = 0; j < VPT; ++j) load(X(), p.f, t * p.ldf, j, true, u[j]);
   if (kEarly && p.r) {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) load_cut<R, V>(static_cast<const R*>(p.r) + t * p.ldr, col(j), H, r[j]);
+    for (int j = 0; j < VPT; ++j) load(R(), p.r, t * p.ldr, j, true, r[j]);
   }
+  const auto scale = [&](const void* q, int f32, int64_t at) __attribute__((always_inline)) {
+    if (q)
+      with(q, f32, at, false, [&](int j, const float (&a)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) u[j][i] *= a[i];
+      });
+  };
+  const auto shift = [&](const void* b) __attribute__((always_inline)) {
+    if (b)
+      with(b, p.w_f32, 0, false, [&](int j, const float (&a)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) u[j][i] += a[i];
+      });
+  };
   if (p.post != W4A8_NORM_NONE) {
-    normalise<V, VPT>(u, p.post, H, p.eps, scratch, slot);
-    scale_shift<X, V, VPT>(u, p.w_post, p.b_post, p.w_f32, H);
+    normalise<V, VPT>(u, p.post, H, p.eps, scratch, slot, count);
+    scale(p.w_post, p.w_f32, 0);
+    shift(p.b_post);
   }
   float gs = p.branch_scale;
   if (p.gate) {
@@ -221,10 +272,7 @@ __global__ void __launch_bounds__(1024) block_norm_row_kernel(const NormParams p
       load_param<X, 1>(p.gate, p.gate_f32, grow, a);
       gs *= a[0];
     } else {
-      with_param<X, V, VPT>(p.gate, p.gate_f32, grow, H, [&](int j, const float (&a)[V]) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) u[j][i] *= a[i];
-      });
+      scale(p.gate, p.gate_f32, grow);
     }
   }
 #pragma unroll
@@ -235,22 +283,23 @@ __global__ void __launch_bounds__(1024) block_norm_row_kernel(const NormParams p
       if (kEarly && p.r) u[j][i] = fmaf(p.residual_scale, r[kEarly ? j : 0][i], u[j][i]);
     }
   if (!kEarly && p.r)
-    with_param<R, V, VPT>(p.r, 0, t * p.ldr, H, [&](int j, const float (&a)[V]) {
+    with(p.r, sizeof(R) == 4, t * p.ldr, true, [&](int j, const float (&a)[V]) {
 #pragma unroll
       for (int i = 0; i < V; ++i) u[j][i] = fmaf(p.residual_scale, a[i], u[j][i]);
     });
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    if (p.h && here) store_cut<R, V>(static_cast<R*>(p.h) + t * p.ldh, col(j), H, u[j]);
+    if (p.h && here) store(R(), p.h, t * p.ldh, j, u[j]);
   }
   if (!p.y) return;
   if (p.pre != W4A8_NORM_NONE) {
-    normalise<V, VPT>(u, p.pre, H, p.eps, scratch, slot);
-    scale_shift<X, V, VPT>(u, p.w_pre, p.b_pre, p.w_f32, H);
+    normalise<V, VPT>(u, p.pre, H, p.eps, scratch, slot, count);
+    scale(p.w_pre, p.w_f32, 0);
+    shift(p.b_pre);
   }
 #pragma unroll
   for (int j = 0; j < VPT; ++j)
-    if (here) store_cut<X, V>(static_cast<X*>(p.y) + t * p.ldy, col(j), H, u[j]);
+    if (here) store(X(), p.y, t * p.ldy, j, u[j]);
 }
 
 // Two fp32 operations in one instruction.
@@ -285,8 +334,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // branch_scale, and a gate that all rows share, multiplied into the first pair), and the rows to come are copied to a
 // ring of two or three stages in shared memory asynchronously: registers would not hold enough bytes in flight to cover the
 // memory's latency beside the rows that are being worked on.
-//   V = 8: rows of whole aligned vectors.  Every thread copies its own pieces and alone reads them back, so there is
-//     nothing to synchronise.
+//   V > 1: rows of whole aligned vectors, of 8 elements, or of 4 beside fp32 ones (every access of a warp then covers whole
+//     sectors).  Every thread copies its own pieces and alone reads them back, so there is nothing to synchronise.
+//   V > 1, CUT: rows of any width and start, as long as f, r, h and y agree on where a row starts within V elements.  That
+//     repeats after 8 rows at most, and the number of blocks is a multiple of 8: a block's rows all start alike, and the
+//     weights still stay in registers.  The whole aligned vectors of a row go to its threads as before, and the up to
+//     2 * (V - 1) elements before and after them to the lanes of one more warp.
 //   V = 1: rows without 16-byte alignment, or of a width that is no multiple of 8.  The block copies the aligned
 //     16-byte pieces that cover a row, and threads take single elements from there.  A piece that reaches outside the
 //     matrix (only its first and last one can) is copied element by element.
@@ -297,13 +350,13 @@ __device__ __forceinline__ void fetch_window(uint8_t* dst, const void* base, int
   const int pieces = static_cast<int>((b0 - w0 + H * sizeof(T) + 15) >> 4);
   if (w0 >= lo && w0 + 16 * static_cast<uintptr_t>(pieces) <= hi) {
     for (int i = threadIdx.x; i < pieces; i += blockDim.x)
-      copy16_async(dst + 16 * i, reinterpret_cast<const void*>(w0 + 16 * i));
+      copy_async<16>(dst + 16 * i, reinterpret_cast<const void*>(w0 + 16 * i));
     return;
   }
   for (int i = threadIdx.x; i < pieces; i += blockDim.x) {
     const uintptr_t a = w0 + 16 * static_cast<uintptr_t>(i);
     if (a >= lo && a + 16 <= hi) {
-      copy16_async(dst + 16 * i, reinterpret_cast<const void*>(a));
+      copy_async<16>(dst + 16 * i, reinterpret_cast<const void*>(a));
     } else {
       for (uintptr_t e = a; e < a + 16; e += sizeof(T))
         if (e >= lo && e < hi) *reinterpret_cast<T*>(dst + (e - w0)) = *reinterpret_cast<const T*>(e);
@@ -311,8 +364,8 @@ __device__ __forceinline__ void fetch_window(uint8_t* dst, const void* base, int
   }
 }
 
-// One stage of the ring (ROWS rows): byte offsets of its parts, and of one row within a part.  V = 8: a thread's
-// 16-byte pieces lie 16 * threads apart.
+// One stage of the ring (ROWS rows): byte offsets of its parts, and of one row within a part.  V > 1: a thread's
+// pieces lie threads of them apart.
 struct NormStage {
   int stages, bytes, r_at, g_at;
   int f_row, r_row, g_row;
@@ -322,34 +375,57 @@ struct NormStage {
 // Threads of an SM that the registers allow with kE elements to a thread (16: two rows of them in registers).
 __host__ __device__ constexpr int max_threads(int elems) { return elems == 16 ? 512 : 768; }
 
-template <typename X, typename R, int V, bool BIAS, int kE>
+template <typename X, typename R, int V, bool CUT, bool BIAS, int kE>
 __global__ void __launch_bounds__(max_threads(kE), 1) block_norm_stream_kernel(const NormParams p, const NormStage st) {
   constexpr int kP = kE / 2;  // pairs of a thread's elements
   constexpr int ROWS = 2;
   extern __shared__ uint8_t ring[];
   __shared__ float2 scratch[2][max_threads(kE) / 32];
   const int threads = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + threadIdx.x;
-  const int tx = threadIdx.x, nx = blockDim.x, H = p.H;
-  // column of element i: V = 8: two vectors nx * 8 apart; V = 1: elements nx apart.  Elements i < mine exist.
-  const int mine = V == 8 ? ((tx * 8 < H) + ((nx + tx) * 8 < H)) * 8 : max(0, (H - tx + nx - 1) / nx);
-  auto col = [&](int i) { return V == 8 ? ((i / 8) * nx + tx) * 8 + i % 8 : i * nx + tx; };
-  auto in = [&](int i) { return (V == 8 ? i / 8 * 8 : i) < mine; };
+  const int tx = threadIdx.x, nx = blockDim.x - (CUT ? 32 : 0), H = p.H;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;  // between the rows of a thread
+  int64_t t0 = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  // CUT: elements before the first whole vector, whole vectors, and whether this thread is of the warp for the others
+  const int64_t start = static_cast<int64_t>(reinterpret_cast<uintptr_t>(p.f) / sizeof(X)) + t0 * p.ldf;
+  const int head = CUT ? min(static_cast<int>(-start & (V - 1)), H) : 0;
+  const int vectors = CUT ? (H - head) / V : (H + V - 1) / V;
+  const bool single = CUT && tx >= nx;
+  // column of element i: V > 1: vectors nx * V apart; V = 1: elements nx apart.  Elements i < mine exist.
+  const int first = !single ? head + tx * V : tx - nx + (tx - nx < head ? 0 : vectors * V);
+  int mine = single ? first < H : 0;
+#pragma unroll
+  for (int i = 0; i < kE; i += V) mine += !single && i / V * nx + tx < vectors ? V : 0;
+  auto col = [&](int i) { return first + i / V * nx * V + i % V; };
+  auto in = [&](int i) { return i / V * V < mine; };  // for single: of element 0 only
+  auto valid = [&](int i) { return CUT ? i < mine : in(i); };
   pdl_trigger();
   pdl_wait();
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;  // between the rows of a thread
   auto gate_index = [&](int64_t t) { return static_cast<int64_t>(static_cast<uint32_t>(t) / p.rows_per_gate); };
-  auto piece = [&](uint8_t* at, int q) { return at + q * (16 * threads) + 16 * tid; };
-  // copies one row of a matrix of T into its place in the ring
+  const bool odd = (start + first) & 1;  // single, 16 bits: the element is the upper half of its four bytes
+  // Copies one row of a matrix of T into its place in the ring.  V > 1: each vector is a piece of 8 or 16 bytes, or two.
+  auto piece = [&](uint8_t* at, int bytes, int q) { return at + bytes * (q * threads + tid); };
   auto fetch_part = [&](auto type, const void* base, int64_t ld, int64_t rows, int64_t t, uint8_t* at) {
     using T = decltype(type);
-    if constexpr (V == 8) {
-      constexpr int Q = sizeof(T) / 2;  // 16-byte pieces of a vector
-      const char* src = reinterpret_cast<const char*>(static_cast<const T*>(base) + t * ld + tx * 8);
+    if constexpr (V > 1) {
+      constexpr int kBytes = V * sizeof(T), kPiece = kBytes < 16 ? kBytes : 16, Q = kBytes / kPiece;
+      const char* src = reinterpret_cast<const char*>(static_cast<const T*>(base) + t * ld + first);
+      if (single) {  // the four bytes around the element, but nothing outside the matrix
+        if (!mine) return;
+        uint8_t* to = piece(at, kPiece, 0);
+        const char* word = src - (sizeof(T) == 2 && odd ? 2 : 0);
+        const bool out = sizeof(T) == 2 && (odd ? t == 0 && first == 0 : t == rows - 1 && first == H - 1);
+        if (out)
+          *reinterpret_cast<T*>(to + (odd ? 2 : 0)) = *reinterpret_cast<const T*>(src);
+        else
+          copy_async<4>(to, word);
+        return;
+      }
 #pragma unroll
-      for (int j = 0; j < kE / 8; ++j)
-        if (in(8 * j)) {
+      for (int j = 0; j < kE / V; ++j)
+        if (in(V * j)) {
 #pragma unroll
-          for (int q = 0; q < Q; ++q) copy16_async(piece(at, j * Q + q), src + j * nx * 16 * Q + 16 * q);
+          for (int q = 0; q < Q; ++q)
+            copy_async<kPiece>(piece(at, kPiece, j * Q + q), src + j * nx * kBytes + kPiece * q);
         }
     } else {
       fetch_window<T>(at, base, ld, rows, t, H);
@@ -375,17 +451,25 @@ __global__ void __launch_bounds__(max_threads(kE), 1) block_norm_stream_kernel(c
   // this thread's elements of one row of the ring; zeros where there are none
   auto take = [&](auto type, const void* base, int64_t ld, int64_t t, uint8_t* at, uint64_t* o) {
     using T = decltype(type);
-    if constexpr (V == 8) {
-      constexpr int Q = sizeof(T) / 2;
+    if constexpr (V > 1) {
+      constexpr int kBytes = V * sizeof(T), kPiece = kBytes < 16 ? kBytes : 16, Q = kBytes / kPiece;
+      using Piece = std::conditional_t<kPiece == 16, uint4, uint2>;
+      if (single) {
+        const uint8_t* from = piece(at, kPiece, 0) + (sizeof(T) == 2 && odd ? 2 : 0);
+        o[0] = pair(mine ? to_f32(*reinterpret_cast<const T*>(from)) : 0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < kE / 8; ++j) {
-        Pack<T, 8> a;
+        for (int i = 1; i < kP; ++i) o[i] = 0;
+        return;
+      }
+#pragma unroll
+      for (int j = 0; j < kE / V; ++j) {
+        Pack<T, V> a;
 #pragma unroll
         for (int q = 0; q < Q; ++q)
-          reinterpret_cast<uint4*>(&a)[q] = in(8 * j) ? *reinterpret_cast<const uint4*>(piece(at, j * Q + q))
-                                                      : make_uint4(0, 0, 0, 0);
+          reinterpret_cast<Piece*>(&a)[q] =
+              in(V * j) ? *reinterpret_cast<const Piece*>(piece(at, kPiece, j * Q + q)) : Piece{};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[4 * j + i] = pair(to_f32(a.v[2 * i]), to_f32(a.v[2 * i + 1]));
+        for (int i = 0; i < V / 2; ++i) o[V / 2 * j + i] = pair(to_f32(a.v[2 * i]), to_f32(a.v[2 * i + 1]));
       }
     } else {
       const T* row =
@@ -398,17 +482,21 @@ __global__ void __launch_bounds__(max_threads(kE), 1) block_norm_stream_kernel(c
   auto put = [&](auto type, void* base, int64_t ld, int64_t t, const uint64_t* o) {
     using T = decltype(type);
     T* row = static_cast<T*>(base) + t * ld;
-    if constexpr (V == 8) {
+    if constexpr (V > 1) {
+      if (single) {
+        if (mine) row[first] = from_f32<T>(split(o[0]).x);
+        return;
+      }
 #pragma unroll
-      for (int j = 0; j < kE / 8; ++j) {
-        float v[8];
+      for (int j = 0; j < kE / V; ++j) {
+        float v[V];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 a = split(o[4 * j + i]);
-          v[2 * i] = a.x;
-          v[2 * i + 1] = a.y;
+        for (int i = 0; i < V; i += 2) {
+          const float2 a = split(o[(V * j + i) / 2]);
+          v[i] = a.x;
+          v[i + 1] = a.y;
         }
-        if (in(8 * j)) store_vec<T, 8>(row + (j * nx + tx) * 8, v);
+        if (in(V * j)) store_vec<T, V>(row + col(V * j), v);
       }
     } else {
       row += tx;
@@ -424,7 +512,7 @@ __global__ void __launch_bounds__(max_threads(kE), 1) block_norm_stream_kernel(c
   auto reduce = [&](float (&v)[ROWS]) {  // sums over the row's threads, one barrier
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) v[r] = warp_sum(v[r]);
-    const int warps = nx >> 5, lane = tx & 31;
+    const int warps = blockDim.x >> 5, lane = tx & 31;
     if (warps == 1) return;
     float2* at = scratch[turn];
     turn ^= 1;
@@ -452,6 +540,11 @@ __global__ void __launch_bounds__(max_threads(kE), 1) block_norm_stream_kernel(c
         const float m = -s[r] * inv_h;
 #pragma unroll
         for (int i = 0; i < kP; ++i) u[r][i] = add2(u[r][i], pair(in(2 * i) ? m : 0.f, in(2 * i + 1) ? m : 0.f));
+        if (single) {
+          u[r][0] = pair(split(u[r][0]).x, 0.f);
+#pragma unroll
+          for (int i = 1; i < V / 2; ++i) u[r][i] = 0;
+        }
       }
     }
 #pragma unroll
@@ -484,49 +577,52 @@ __global__ void __launch_bounds__(max_threads(kE), 1) block_norm_stream_kernel(c
     return a[0];
   };
 
-  int64_t t0 = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   for (int s = 0; s < st.stages; ++s) fetch(t0 + s * ROWS * step, ring + s * st.bytes);
   // while the first rows are on their way
   uint64_t w_post[kP], w_pre[kP];
   // the biases: this thread's pairs in shared memory behind the ring, b_post then b_pre (registers hold no more)
   uint64_t* biases = reinterpret_cast<uint64_t*>(ring + st.stages * st.bytes) + tid;
+  {
+    // a parameter at this thread's columns: all loads inside one branch on the type, so that none waits for another
+    auto param = [&](const void* q, int f32, float* a) {
+      if (f32) {
 #pragma unroll
-  for (int j = 0; j < kP; ++j) {
-    float wq[2] = {0.f, 0.f}, bq[2] = {0.f, 0.f}, wp[2] = {0.f, 0.f}, bp[2] = {0.f, 0.f};
+        for (int i = 0; i < kE; ++i) a[i] = valid(i) ? static_cast<const float*>(q)[col(i)] : 0.f;
+      } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = 2 * j + h;
-      float a[1];
-      if (!in(i)) continue;
-      wp[h] = p.branch_scale;
-      wq[h] = 1.f;
-      if (p.gate && !p.gate_scalar && !st.gate_rows) {
-        load_param<X, 1>(p.gate, p.gate_f32, col(i), a);
-        wp[h] *= a[0];
+        for (int i = 0; i < kE; ++i) a[i] = valid(i) ? to_f32(static_cast<const X*>(q)[col(i)]) : 0.f;
       }
-      if (BIAS && p.b_post) {
-        load_param<X, 1>(p.b_post, p.w_f32, col(i), a);
-        bp[h] = wp[h] * a[0];
-      }
-      if (p.w_post) {
-        load_param<X, 1>(p.w_post, p.w_f32, col(i), a);
-        wp[h] *= a[0];
-      }
-      if (p.w_pre) {
-        load_param<X, 1>(p.w_pre, p.w_f32, col(i), a);
-        wq[h] = a[0];
-      }
-      if (BIAS && p.b_pre) {
-        load_param<X, 1>(p.b_pre, p.w_f32, col(i), a);
-        bq[h] = a[0];
-      }
+    };
+    auto keep_bias = [&](int at, const void* q, const float* w) {
+      float a[kE];
+#pragma unroll
+      for (int i = 0; i < kE; ++i) a[i] = 0.f;
+      if (q) param(q, p.w_f32, a);
+#pragma unroll
+      for (int j = 0; j < kP; ++j) biases[(at + j) * threads] = pair(a[2 * j] * w[2 * j], a[2 * j + 1] * w[2 * j + 1]);
+    };
+    float w[kE], a[kE];
+#pragma unroll
+    for (int i = 0; i < kE; ++i) w[i] = valid(i) ? p.branch_scale : 0.f;
+    if (p.gate && !p.gate_scalar && !st.gate_rows) {
+      param(p.gate, p.gate_f32, a);
+#pragma unroll
+      for (int i = 0; i < kE; ++i) w[i] *= a[i];
     }
-    w_post[j] = pair(wp[0], wp[1]);
-    w_pre[j] = pair(wq[0], wq[1]);
-    if (BIAS) {
-      biases[j * threads] = pair(bp[0], bp[1]);
-      biases[(kP + j) * threads] = pair(bq[0], bq[1]);
+    if (BIAS) keep_bias(0, p.b_post, w);
+    if (p.w_post) {
+      param(p.w_post, p.w_f32, a);
+#pragma unroll
+      for (int i = 0; i < kE; ++i) w[i] *= a[i];
     }
+#pragma unroll
+    for (int j = 0; j < kP; ++j) w_post[j] = pair(w[2 * j], w[2 * j + 1]);
+#pragma unroll
+    for (int i = 0; i < kE; ++i) w[i] = valid(i) ? 1.f : 0.f;
+    if (BIAS) keep_bias(kP, p.b_pre, w);
+    if (p.w_pre) param(p.w_pre, p.w_f32, w);
+#pragma unroll
+    for (int j = 0; j < kP; ++j) w_pre[j] = pair(w[2 * j], w[2 * j + 1]);
   }
   float gs[ROWS];
 #pragma unroll
@@ -584,20 +680,20 @@ __global__ void __launch_bounds__(max_threads(kE), 1) block_norm_stream_kernel(c
   copy_wait<0>();
 }
 
-template <typename X, typename R, int V, int VPT>
+template <typename X, typename R, int V, bool CUT, int VPT>
 int launch_row(const NormParams& p, cudaStream_t st) {
-  const int64_t need = ceil_div(p.H, V * VPT);
-  const int64_t per = need <= 8 ? 8 : need <= 16 ? 16 : ceil_div(need, 32) * 32;  // threads of a row
+  const int64_t need = ceil_div(p.H, V * VPT), warps = ceil_div(need, 32);
+  const int64_t per = CUT ? warps * 32 + 32 : need <= 8 ? 8 : need <= 16 ? 16 : warps * 32;  // threads of a row
   const int rows = per <= 32 ? 256 / static_cast<int>(per) : 1;
-  return launch_pdl("block_norm_row_kernel", block_norm_row_kernel<X, R, V, VPT>,
+  return launch_pdl("block_norm_row_kernel", block_norm_row_kernel<X, R, V, CUT, VPT>,
                     dim3(static_cast<unsigned>(ceil_div(p.T, rows))), dim3(static_cast<unsigned>(per), rows), 0, st, p);
 }
 
 constexpr int kMaxSmem = 227 * 1024;
 
-template <typename X, typename R, int V, bool BIAS, int kE>
+template <typename X, typename R, int V, bool CUT, bool BIAS, int kE>
 int launch_stream(const NormParams& p, const NormStage& stage, int threads, int rows, cudaStream_t st) {
-  auto kern = block_norm_stream_kernel<X, R, V, BIAS, kE>;
+  auto kern = block_norm_stream_kernel<X, R, V, CUT, BIAS, kE>;
   static DeviceOnce once;
   if (int rc = once.run([&] {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024) != cudaSuccess)
@@ -609,24 +705,25 @@ int launch_stream(const NormParams& p, const NormStage& stage, int threads, int 
   // kernel's static part and the 1 KB that a block costs)
   const int64_t smem = static_cast<int64_t>(stage.stages) * stage.bytes + (BIAS ? threads * rows * kE * 8 : 0);
   const int64_t per_sm =
-      std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(max_threads(kE) / (threads * rows), kMaxSmem / (smem + 1280)), 16));
-  const int64_t blocks = std::min(ceil_div(p.T, rows), per_sm * num_sms());
+      std::clamp<int64_t>(std::min<int64_t>(max_threads(kE) / (threads * rows), kMaxSmem / (smem + 1280)), 1, 16);
+  int64_t blocks = std::min(ceil_div(p.T, rows), per_sm * num_sms());
+  if (CUT) blocks = std::max<int64_t>(8, blocks / 8 * 8);  // all rows of a block start alike
   return launch_pdl("block_norm_stream_kernel", kern, dim3(static_cast<unsigned>(blocks)), dim3(threads, rows),
                     static_cast<size_t>(smem), st, p, stage);
 }
 
 // Whether the rows fit the streaming kernel (two stages of them in shared memory); *rc is the launch's status then.
-template <typename X, typename R, int V, int kE>
+template <typename X, typename R, int V, bool CUT, int kE>
 bool try_stream(const NormParams& p, cudaStream_t st, int* rc) {
-  if (p.H > kE * max_threads(kE)) return false;
   const bool bias = p.b_post || p.b_pre;
-  const int threads = static_cast<int>(ceil_div(ceil_div(p.H, kE), 32) * 32);
-  const int rows = V == 8 && threads == 32 ? 4 : 1;
+  const int threads = static_cast<int>(ceil_div(ceil_div(p.H, kE), 32) * 32) + (CUT ? 32 : 0);
+  if (threads > max_threads(kE)) return false;
+  const int rows = V > 1 && threads == 32 ? 4 : 1;
   constexpr int turn = 2;  // rows of a stage
   NormStage stage;
   stage.gate_rows = p.gate && !p.gate_scalar && p.rows_per_gate < p.T;
   // one row of a part: the block's vectors, or the 16-byte pieces that cover a row
-  const auto part = [&](int size) { return V == 8 ? threads * rows * kE * size : (p.H * size + 15) / 16 * 16 + 16; };
+  const auto part = [&](int size) { return V > 1 ? threads * rows * kE * size : (p.H * size + 15) / 16 * 16 + 16; };
   stage.f_row = part(sizeof(X));
   stage.r_row = p.r ? part(sizeof(R)) : 0;
   stage.g_row = stage.gate_rows ? part(p.gate_f32 ? 4 : static_cast<int>(sizeof(X))) : 0;
@@ -641,9 +738,21 @@ bool try_stream(const NormParams& p, cudaStream_t st, int* rc) {
   };
   if (blocks(2) < 1) return false;
   stage.stages = blocks(3) < blocks(2) ? 2 : 3;
-  *rc = bias ? launch_stream<X, R, V, true, kE>(p, stage, threads, rows, st)
-             : launch_stream<X, R, V, false, kE>(p, stage, threads, rows, st);
+  *rc = bias ? launch_stream<X, R, V, CUT, true, kE>(p, stage, threads, rows, st)
+             : launch_stream<X, R, V, CUT, false, kE>(p, stage, threads, rows, st);
   return true;
+}
+
+// Whether every row starts at the same place within V elements in all of the row's matrices.
+template <typename X, typename R>
+bool rows_agree(const NormParams& p, int V) {
+  const auto phase = [&](const void* q, int size) { return static_cast<int>(reinterpret_cast<uintptr_t>(q) / size % V); };
+  const auto like_f = [&](const void* q, int64_t ld, int size) {
+    return !q || (phase(q, size) == phase(p.f, sizeof(X)) && (p.T == 1 || (ld - p.ldf) % V == 0));
+  };
+  if (!like_f(p.r, p.ldr, sizeof(R)) || !like_f(p.h, p.ldh, sizeof(R)) || !like_f(p.y, p.ldy, sizeof(X))) return false;
+  if (!p.gate || p.gate_scalar || p.rows_per_gate >= p.T) return true;
+  return like_f(p.gate, p.ldg, p.gate_f32 ? 4 : static_cast<int>(sizeof(X))) && (p.rows_per_gate == 1 || p.ldg % V == 0);
 }
 
 template <typename X, typename R>
@@ -651,30 +760,46 @@ int dispatch(const NormParams& p, bool vec, cudaStream_t st) {
   // Rows that a block works through in turn pay for the ring from the second one on; with few rows, and with rows too
   // long for it, each gets a block of its own.
   int rc;
+  const bool many = p.T > 2 * num_sms();
   // rows of up to 256 elements go to a warp or a part of one, however many they are
-  if (vec && p.H <= 256) return launch_row<X, R, 8, 1>(p, st);
-  // fp32 rows fill the memory's pipes from registers, and the ring would take the threads' room (9000 x 1024: 24.5 us a row
-  // to a block, 41.0 us with the ring; bf16, 16384 x 1024: 35.7 and 23.4 us)
-  const bool stream = p.T > 2 * num_sms() && !(vec && sizeof(X) == 4);
-  if (stream) {
-    if constexpr (sizeof(X) != 4) {
-      if (vec && p.H % 8 == 0 && try_stream<X, R, 8, 16>(p, st, &rc)) return rc;
-    }
-    // single elements cost more instructions and latency each, which twice the warps hide where they fit (3001 x 5119
-    // f16 with an fp32 residual: 73 us, and 77 us with 16 elements to a thread)
-    if ((!vec || p.H % 8) && (try_stream<X, R, 1, 8>(p, st, &rc) || try_stream<X, R, 1, 16>(p, st, &rc))) return rc;
+  if (vec && p.H <= 256) return launch_row<X, R, 8, false, 1>(p, st);
+  // (60000 x 101 bf16: 26.7 us, with the ring 43.1; 40000 x 201: 36.1 and 30.9)
+  if (!vec && p.H <= 128) return launch_row<X, R, 1, false, 8>(p, st);
+  constexpr int V = sizeof(R) == 4 ? 4 : 8;
+  // (shorter rows leave the warps for whole vectors too little: 20000 x 643 bf16 36.3 us, 34.4 in single elements; 16000 x
+  // 771: 30.8 and 35.7)
+  const bool whole = vec && p.H % V == 0, cut = p.H > 704 && rows_agree<X, R>(p, V);
+  // fp32 rows of whole vectors fill the memory's pipes from registers, and the ring would take the threads' room (2837 x
+  // 7680: 54.7 us a row to a block, 62.6 us with the ring; bf16, 16384 x 1024: 35.7 and 23.5 us)
+  if (many && !(sizeof(X) == 4 && whole)) {
+    if (whole ? try_stream<X, R, V, false, 16>(p, st, &rc) : cut && try_stream<X, R, V, true, 16>(p, st, &rc)) return rc;
+    // Single elements cost more instructions and latency each, which twice the warps hide where they fit.  Rows that miss
+    // the ring above for their length alone are still faster this way without fp32 among them (1596 x 8191 bf16: 35.3 us,
+    // 39.3 a row to a block; with an fp32 residual 73.8 and 58.6).
+    if (!whole && (!cut || sizeof(R) != 4) &&
+        (try_stream<X, R, 1, false, 8>(p, st, &rc) || try_stream<X, R, 1, false, 16>(p, st, &rc)))
+      return rc;
   }
+  // Few rows: as many threads to a row as possible; many: half as many, so that two rows share an SM.  Many long rows of
+  // fp32 alone are read in vectors of 4, where each access covers whole sectors (2837 x 7680: 62.5 us in vectors of 8, 55.2
+  // of 4; but 3000 x 4096: 35.4 and 37.9); those beside 16-bit ones are not (1596 x 10048: 47.1 us, of 4 55.7).
   if (vec) {
-    // few rows: as many threads to a row as possible; many: half as many, so that two rows share an SM
-    const bool many = p.T > 2 * num_sms();
-    if (p.H <= (many ? 4096 : 8192)) return launch_row<X, R, 8, 1>(p, st);
-    if (p.H <= (many ? 8192 : 16384)) return launch_row<X, R, 8, 2>(p, st);
-    return launch_row<X, R, 8, 4>(p, st);
+    if (many && sizeof(X) == 4 && p.H > 4096)
+      return p.H <= 8192 ? launch_row<X, R, 4, false, 4>(p, st) : launch_row<X, R, 4, false, 8>(p, st);
+    if (p.H <= (many ? 4096 : 8192)) return launch_row<X, R, 8, false, 1>(p, st);
+    if (p.H <= (many ? 8192 : 16384)) return launch_row<X, R, 8, false, 2>(p, st);
+    return launch_row<X, R, 8, false, 4>(p, st);
   }
-  if (p.H <= 4096) return launch_row<X, R, 1, 4>(p, st);
-  if (p.H <= 8192) return launch_row<X, R, 1, 8>(p, st);
-  if (p.H <= 16384) return launch_row<X, R, 1, 16>(p, st);
-  return launch_row<X, R, 1, 32>(p, st);
+  // a block has at most 31 warps for whole vectors (1596 x 10047 bf16 with an fp32 residual: 52.6 us; single elements 134)
+  if (cut) {
+    if (p.H <= (many ? 3968 : 7936)) return launch_row<X, R, V, true, 8 / V>(p, st);
+    if (p.H <= (many ? 7936 : 15872)) return launch_row<X, R, V, true, 16 / V>(p, st);
+    if (p.H <= 31744) return launch_row<X, R, V, true, 32 / V>(p, st);
+  }
+  if (p.H <= 4096) return launch_row<X, R, 1, false, 4>(p, st);
+  if (p.H <= 8192) return launch_row<X, R, 1, false, 8>(p, st);
+  if (p.H <= 16384) return launch_row<X, R, 1, false, 16>(p, st);
+  return launch_row<X, R, 1, false, 32>(p, st);
 }
 
 }  // namespace
