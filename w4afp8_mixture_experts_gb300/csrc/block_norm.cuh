@@ -6,9 +6,9 @@
 // Bound by memory (each of f, r, h and y once).  Two kernels:
 //   row kernel: a row to a block, or to 8, 16 or 32 lanes.  64 x 7168 bf16 takes 3.6 us, of which a launch is 2.5.
 //   streaming kernel (many rows): blocks stay and copy the rows to come into a ring in shared memory.
-//     8192 x 7168 bf16 with a channel gate: 78 us, 6.0 TB/s (a row to a block: 134 us).  3001 x 5119 f16 with an fp32
-//     residual, two LayerNorms and no alignment: 47 us, 3.9 TB/s; there it is bound by instructions: two LayerNorms'
-//     reductions and 10 rounds of two rows to each block.
+//     8192 x 7168 bf16 with a channel gate: 79 us, 5.9 TB/s (a row to a block: 134 us).  3001 x 5119 f16 with an fp32
+//     residual, two LayerNorms, a gate per token and no alignment: 44 us, 4.2 TB/s; there it is bound by the latency of
+//     four reductions a row, in 10 rounds of two rows to each block.
 #pragma once
 
 #include <algorithm>
@@ -163,6 +163,10 @@ __device__ __forceinline__ void copy_wait() {  // all but the N newest groups ha
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Threads of a row where the kernel's code fixes them (0: blockDim.x): with many single elements to a thread, columns that
+// are known offsets from the first leave registers for the elements.
+__host__ __device__ constexpr int row_threads(int V, int VPT) { return V == 1 && VPT > 8 ? 1024 : 0; }
+
 // A row to a block (or, for short rows, to 8, 16 or 32 threads): VPT vectors of V elements to a thread.
 //   V > 1: aligned rows; their last vector may be cut short.
 //   V > 1, CUT: rows of any start, as long as f, r, h and y agree on where the row starts within V elements: the whole
@@ -177,14 +181,14 @@ __global__ void __launch_bounds__(1024) block_norm_row_kernel(const NormParams p
   const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const bool here = row < p.T;  // where several rows share a warp, all of its lanes stay for the shuffles
   const int64_t t = here ? row : p.T - 1;
-  const int tx = threadIdx.x, nx = blockDim.x - (CUT ? 32 : 0);
+  const int tx = threadIdx.x, nx = row_threads(V, VPT) ? row_threads(V, VPT) : blockDim.x - (CUT ? 32 : 0);
   const int64_t start = static_cast<int64_t>(reinterpret_cast<uintptr_t>(p.f) / sizeof(X)) + t * p.ldf;
   const int head = CUT ? min(static_cast<int>(-start & (V - 1)), H) : 0;
   const int vectors = (H - head) / V;  // CUT: whole ones
   const bool single = CUT && tx >= nx;
   // this thread's first column
   const int first = !single ? head + tx * V : tx - nx + (tx - nx < head ? 0 : vectors * V);
-  const auto col = [&](int j) { return CUT ? first + j * nx * V : static_cast<int>((j * blockDim.x + tx) * V); };
+  const auto col = [&](int j) { return CUT ? first + j * nx * V : (j * nx + tx) * V; };
   const auto count = [&](int j) {  // the row's elements in vector j
     if (!CUT) return H - col(j);
     return single ? (j == 0 && first < H ? 1 : 0) : j * nx + tx < vectors ? V : 0;
@@ -571,10 +575,18 @@ __global__ void __launch_bounds__(max_threads(kE), 1) block_norm_stream_kernel(c
       for (int r = 0; r < ROWS; ++r) u[r][i] = BIAS ? fma2(u[r][i], w[i], bi) : mul2(u[r][i], w[i]);
     }
   };
-  auto scalar_gate = [&](int64_t t) {
-    float a[1] = {1.f};
-    if (p.gate_scalar && t < p.T) load_param<X, 1>(p.gate, p.gate_f32, gate_index(t) * p.ldg, a);
-    return a[0];
+  // a row's gate value, loaded a round ahead as it is: its conversion would wait for the load at once
+  auto gate_bits = [&](int64_t t) -> uint32_t {
+    if (!p.gate_scalar || t >= p.T) return 0;
+    const int64_t at = gate_index(t) * p.ldg;
+    return p.gate_f32 || sizeof(X) == 4 ? static_cast<const uint32_t*>(p.gate)[at]
+                                        : static_cast<const uint16_t*>(p.gate)[at];
+  };
+  auto gate_value = [&](uint32_t bits) {
+    if (p.gate_f32 || sizeof(X) == 4) return __uint_as_float(bits);
+    X x;
+    memcpy(&x, &bits, sizeof(X));
+    return to_f32(x);
   };
 
   for (int s = 0; s < st.stages; ++s) fetch(t0 + s * ROWS * step, ring + s * st.bytes);
@@ -624,9 +636,9 @@ __global__ void __launch_bounds__(max_threads(kE), 1) block_norm_stream_kernel(c
 #pragma unroll
     for (int j = 0; j < kP; ++j) w_pre[j] = pair(w[2 * j], w[2 * j + 1]);
   }
-  float gs[ROWS];
+  uint32_t gs[ROWS];
 #pragma unroll
-  for (int r = 0; r < ROWS; ++r) gs[r] = scalar_gate(t0 + r * step);
+  for (int r = 0; r < ROWS; ++r) gs[r] = gate_bits(t0 + r * step);
   int s = 0;
   const uint64_t rs = pair(p.residual_scale, p.residual_scale);
   for (; t0 < p.T; t0 += ROWS * step) {
@@ -645,9 +657,10 @@ __global__ void __launch_bounds__(max_threads(kE), 1) block_norm_stream_kernel(c
     for (int r = 0; r < ROWS; ++r) {
       const int64_t t = t0 + r * step;
       if (p.gate_scalar) {
+        const float g = gate_value(gs[r]);
 #pragma unroll
-        for (int i = 0; i < kP; ++i) u[r][i] = mul2(u[r][i], pair(gs[r], gs[r]));
-        gs[r] = scalar_gate(t + ROWS * step);
+        for (int i = 0; i < kP; ++i) u[r][i] = mul2(u[r][i], pair(g, g));
+        gs[r] = gate_bits(t + ROWS * step);
       }
       if (st.gate_rows) {
         uint64_t a[kP];
@@ -683,7 +696,11 @@ __global__ void __launch_bounds__(max_threads(kE), 1) block_norm_stream_kernel(c
 template <typename X, typename R, int V, bool CUT, int VPT>
 int launch_row(const NormParams& p, cudaStream_t st) {
   const int64_t need = ceil_div(p.H, V * VPT), warps = ceil_div(need, 32);
-  const int64_t per = CUT ? warps * 32 + 32 : need <= 8 ? 8 : need <= 16 ? 16 : warps * 32;  // threads of a row
+  const int64_t per = row_threads(V, VPT) ? row_threads(V, VPT)  // threads of a row
+                      : CUT               ? warps * 32 + 32
+                      : need <= 8         ? 8
+                      : need <= 16        ? 16
+                                          : warps * 32;
   const int rows = per <= 32 ? 256 / static_cast<int>(per) : 1;
   return launch_pdl("block_norm_row_kernel", block_norm_row_kernel<X, R, V, CUT, VPT>,
                     dim3(static_cast<unsigned>(ceil_div(p.T, rows))), dim3(static_cast<unsigned>(per), rows), 0, st, p);
