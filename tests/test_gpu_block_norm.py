@@ -229,3 +229,11 @@ def test_nothing_beside_the_rows_is_written_or_counted(lib, dtype, rdtype, T, H,
     eps = {"bf16": 2.0**-7, "f16": 2.0**-9, "f32": 2.0**-18}
     assert torch.all((r.double() - h0.double()).abs() <= eps[rdtype] * (1 + h0.double().abs()))
     assert torch.all((f.double() - y0.double()).abs() <= eps[dtype] * (1 + y0.double().abs()))
+
+
+@pytest.mark.parametrize("H", [129, 136, 200, 248, 255, 256, 257, 300, 504, 512, 513, 704])
+@pytest.mark.parametrize("dtype,rdtype", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f32")])
+def test_many_short_rows(lib, dtype, rdtype, H):
+    # more rows than the warps of the device take in one turn
+    _check(lib, 9001, H, dtype=dtype, rdtype=rdtype, post="layer", pre="rms", gate=(9001, 1), bias=True, seed=16)
+    _check(lib, 7500, H, dtype=dtype, rdtype=rdtype, post="rms", pre="layer", gate=(1, H), pad=8, alias=True, seed=17)

@@ -722,7 +722,7 @@ int launch_stream(const NormParams& p, const NormStage& stage, int threads, int 
   // kernel's static part and the 1 KB that a block costs)
   const int64_t smem = static_cast<int64_t>(stage.stages) * stage.bytes + (BIAS ? threads * rows * kE * 8 : 0);
   const int64_t per_sm =
-      std::clamp<int64_t>(std::min<int64_t>(max_threads(kE) / (threads * rows), kMaxSmem / (smem + 1280)), 1, 16);
+      std::max<int64_t>(1, std::min<int64_t>(max_threads(kE) / (threads * rows), kMaxSmem / (smem + 1280)));
   int64_t blocks = std::min(ceil_div(p.T, rows), per_sm * num_sms());
   if (CUT) blocks = std::max<int64_t>(8, blocks / 8 * 8);  // all rows of a block start alike
   return launch_pdl("block_norm_stream_kernel", kern, dim3(static_cast<unsigned>(blocks)), dim3(threads, rows),
@@ -778,24 +778,31 @@ int dispatch(const NormParams& p, bool vec, cudaStream_t st) {
   // long for it, each gets a block of its own.
   int rc;
   const bool many = p.T > 2 * num_sms();
-  // rows of up to 256 elements go to a warp or a part of one, however many they are
-  if (vec && p.H <= 256) return launch_row<X, R, 8, false, 1>(p, st);
-  // (60000 x 101 bf16: 26.7 us, with the ring 43.1; 40000 x 201: 36.1 and 30.9)
-  if (!vec && p.H <= 128) return launch_row<X, R, 1, false, 8>(p, st);
   constexpr int V = sizeof(R) == 4 ? 4 : 8;
-  // (shorter rows leave the warps for whole vectors too little: 20000 x 643 bf16 36.3 us, 34.4 in single elements; 16000 x
+  // (shorter rows leave the warps for whole vectors too little: 20000 x 643 bf16 36.3 us, 34.0 in single elements; 16000 x
   // 771: 30.8 and 35.7)
   const bool whole = vec && p.H % V == 0, cut = p.H > 704 && rows_agree<X, R>(p, V);
+  // Rows of up to 256 elements go to a warp each or, up to 128, to a part of one; from 129 on through the ring where a warp
+  // gets more than two of them (40000 x 200 bf16: 14.8 us, the row kernel 23.5; 4000 x 200: 4.6 and 4.2; 60000 x 128: 17.9
+  // and 14.8), and in single elements with any number (60000 x 101: 30.0 us, the row kernel 25.4; 40000 x 201: 22.1 and 36.1).
+  if (p.H <= 256) {
+    if (p.H > 128 && whole && p.T > 48 * num_sms() && try_stream<X, R, V, false, 8>(p, st, &rc)) return rc;
+    if (vec) return launch_row<X, R, 8, false, 1>(p, st);
+    if (p.H <= 128 || !many) return launch_row<X, R, 1, false, 8>(p, st);
+  }
   // fp32 rows of whole vectors fill the memory's pipes from registers, and the ring would take the threads' room (2837 x
   // 7680: 54.7 us a row to a block, 62.6 us with the ring; bf16, 16384 x 1024: 35.7 and 23.5 us)
   if (many && !(sizeof(X) == 4 && whole)) {
     if (whole ? try_stream<X, R, V, false, 16>(p, st, &rc) : cut && try_stream<X, R, V, true, 16>(p, st, &rc)) return rc;
-    // Single elements cost more instructions and latency each, which twice the warps hide where they fit.  Rows that miss
-    // the ring above for their length alone are still faster this way without fp32 among them (1596 x 8191 bf16: 35.3 us,
-    // 39.3 a row to a block; with an fp32 residual 73.8 and 58.6).
-    if (!whole && (!cut || sizeof(R) != 4) &&
-        (try_stream<X, R, 1, false, 8>(p, st, &rc) || try_stream<X, R, 1, false, 16>(p, st, &rc)))
-      return rc;
+    // Single elements cost more instructions and latency each, which twice the warps hide where they fit, but a row to one
+    // warp needs no barrier (40000 x 257 bf16: 35.5 us, with two warps 42.0).  Rows that miss the ring above for their
+    // length alone are still faster this way without fp32 among them (1596 x 8191 bf16: 35.3 us, 39.3 a row to a block;
+    // with an fp32 residual 73.8 and 58.6).
+    if (!whole && (!cut || sizeof(R) != 4)) {
+      const bool one_warp = p.H > 256 && p.H <= 512;
+      if (!one_warp && try_stream<X, R, 1, false, 8>(p, st, &rc)) return rc;
+      if (try_stream<X, R, 1, false, 16>(p, st, &rc)) return rc;
+    }
   }
   // Few rows: as many threads to a row as possible; many: half as many, so that two rows share an SM.  Many long rows of
   // fp32 alone are read in vectors of 4, where each access covers whole sectors (2837 x 7680: 62.5 us in vectors of 8, 55.2
