@@ -163,8 +163,8 @@ __device__ __forceinline__ void copy_wait() {  // all but the N newest groups ha
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Threads of a row where the kernel's code fixes them (0: blockDim.x): with many single elements to a thread, columns that
-// are known offsets from the first leave registers for the elements.
+// Threads of a row where the kernel's code fixes them (0: blockDim.x): with many single elements to a thread, columns
+// that are known offsets from the first leave registers for the elements.
 __host__ __device__ constexpr int row_threads(int V, int VPT) { return V == 1 && VPT > 8 ? 1024 : 0; }
 
 // A row to a block (or, for short rows, to 8, 16 or 32 threads): VPT vectors of V elements to a thread.
@@ -333,20 +333,8 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// Many rows: blocks stay and stride over them, 16 or 8 elements of a row to a thread and ROWS rows at a time (their
-// reductions share the barriers and hide each other's latency).  The weights and biases stay in registers (with
-// branch_scale, and a gate that all rows share, multiplied into the first pair), and the rows to come are copied to a
-// ring of two or three stages in shared memory asynchronously: registers would not hold enough bytes in flight to cover the
-// memory's latency beside the rows that are being worked on.
-//   V > 1: rows of whole aligned vectors, of 8 elements, or of 4 beside fp32 ones (every access of a warp then covers whole
-//     sectors).  Every thread copies its own pieces and alone reads them back, so there is nothing to synchronise.
-//   V > 1, CUT: rows of any width and start, as long as f, r, h and y agree on where a row starts within V elements.  That
-//     repeats after 8 rows at most, and the number of blocks is a multiple of 8: a block's rows all start alike, and the
-//     weights still stay in registers.  The whole aligned vectors of a row go to its threads as before, and the up to
-//     2 * (V - 1) elements before and after them to the lanes of one more warp.
-//   V = 1: rows without 16-byte alignment, or of a width that is no multiple of 8.  The block copies the aligned
-//     16-byte pieces that cover a row, and threads take single elements from there.  A piece that reaches outside the
-//     matrix (only its first and last one can) is copied element by element.
+// Copies the aligned 16-byte pieces that cover row t of a matrix.  A piece that reaches outside the matrix (only its
+// first and last one can) is copied element by element.
 template <typename T>
 __device__ __forceinline__ void fetch_window(uint8_t* dst, const void* base, int64_t ld, int64_t rows, int64_t t, int H) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(base), hi = lo + ((rows - 1) * ld + H) * sizeof(T);
@@ -368,6 +356,19 @@ __device__ __forceinline__ void fetch_window(uint8_t* dst, const void* base, int
   }
 }
 
+// Many rows: blocks stay and stride over them, 16 or 8 elements of a row to a thread and ROWS rows at a time (their
+// reductions share the barriers and hide each other's latency).  The weights and biases stay in registers (with
+// branch_scale, and a gate that all rows share, multiplied into the first pair), and the rows to come are copied to a ring
+// of two or three stages in shared memory asynchronously: registers would not hold enough bytes in flight to cover the
+// memory's latency beside the rows that are being worked on.
+//   V > 1: rows of whole aligned vectors, of 8 elements, or of 4 beside fp32 ones (every access of a warp then covers
+//     whole sectors).  Every thread copies its own pieces and alone reads them back, so there is nothing to synchronise.
+//   V > 1, CUT: rows of any width and start, as long as f, r, h and y agree on where a row starts within V elements.
+//     That repeats after 8 rows at most, and the number of blocks is a multiple of 8: a block's rows all start alike, and
+//     the weights still stay in registers.  The whole aligned vectors of a row go to its threads as before, and the up to
+//     2 * (V - 1) elements before and after them to the lanes of one more warp.
+//   V = 1: rows that start differently in f, r, h and y, and short or very long ones of odd width or start.  The block
+//     copies the 16-byte pieces that cover a row, and threads take single elements from there.
 // One stage of the ring (ROWS rows): byte offsets of its parts, and of one row within a part.  V > 1: a thread's
 // pieces lie threads of them apart.
 struct NormStage {
@@ -747,8 +748,8 @@ bool try_stream(const NormParams& p, cudaStream_t st, int* rc) {
   stage.r_at = turn * stage.f_row;
   stage.g_at = stage.r_at + turn * stage.r_row;
   stage.bytes = stage.g_at + turn * stage.g_row;
-  // three stages where that leaves an SM as many blocks as two do (8192 x 4096 bf16 with an fp32 residual: one block of 256
-  // threads with three, two with two)
+  // three stages where that leaves an SM as many blocks as two do (8192 x 4096 bf16 with an fp32 residual: one block of
+  // 256 threads with three, two with two)
   const auto blocks = [&](int stages) {
     const int smem = stages * stage.bytes + (bias ? threads * rows * kE * 8 : 0) + 1280;
     return std::min(max_threads(kE) / (threads * rows), kMaxSmem / smem);
@@ -782,9 +783,10 @@ int dispatch(const NormParams& p, bool vec, cudaStream_t st) {
   // (shorter rows leave the warps for whole vectors too little: 20000 x 643 bf16 36.3 us, 34.0 in single elements; 16000 x
   // 771: 30.8 and 35.7)
   const bool whole = vec && p.H % V == 0, cut = p.H > 704 && rows_agree<X, R>(p, V);
-  // Rows of up to 256 elements go to a warp each or, up to 128, to a part of one; from 129 on through the ring where a warp
-  // gets more than two of them (40000 x 200 bf16: 14.8 us, the row kernel 23.5; 4000 x 200: 4.6 and 4.2; 60000 x 128: 17.9
-  // and 14.8), and in single elements with any number (60000 x 101: 30.0 us, the row kernel 25.4; 40000 x 201: 22.1 and 36.1).
+  // Rows of up to 256 elements go to a warp each or, up to 128, to a part of one.  From 129 on they go through the ring
+  // where a warp gets more than two of them (40000 x 200 bf16: 14.8 us, the row kernel 23.5; 4000 x 200: 4.6 and 4.2;
+  // 60000 x 128: 17.9 and 14.8), in single elements where there are many (40000 x 201: 22.1 us, the row kernel 36.1; 60000
+  // x 101: 30.0 and 25.4).
   if (p.H <= 256) {
     if (p.H > 128 && whole && p.T > 48 * num_sms() && try_stream<X, R, V, false, 8>(p, st, &rc)) return rc;
     if (vec) return launch_row<X, R, 8, false, 1>(p, st);
