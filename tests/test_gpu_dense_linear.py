@@ -218,3 +218,19 @@ def test_refusals(lib):
         lib.dense_linear(x[:, :0], w[:, :0])
     with pytest.raises(TypeError, match="CUDA tensor"):
         lib.dense_linear(x.cpu(), w)
+
+
+@pytest.mark.parametrize("M,N,K", [(2501, 2056, 128), (2501, 2051, 128), (2500, 2048, 1600)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_fp32_residual_in_place(lib, M, N, K, gated):
+    if gated and N % 2:
+        N += 1
+    g = torch.Generator("cuda").manual_seed(21)
+    x = torch.randn((M, K), device="cuda", generator=g).to(torch.bfloat16)
+    w = (torch.randn((N, K), device="cuda", generator=g) / K**0.5).to(torch.bfloat16)
+    r = torch.randn((M, N // 2 if gated else N), device="cuda", generator=g)
+    apart = lib.dense_linear(x, w, act="relu", gated=gated, residual=r, out_dtype=torch.float32)
+    alone = lib.dense_linear(x, w, act="relu", gated=gated, out_dtype=torch.float32)
+    assert torch.equal(apart, alone + r)  # one fp32 addition
+    lib.dense_linear(x, w, act="relu", gated=gated, residual=r, out_dtype=torch.float32, out=r)
+    assert torch.equal(apart, r)

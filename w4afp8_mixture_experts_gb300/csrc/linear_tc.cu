@@ -234,8 +234,10 @@ __device__ __forceinline__ void pair_tile(const PairPlan& pl, int i, int& tm, in
 }
 
 // N (16 or 32) output columns of this thread's row m0 + lane, from column n on; `res`: the residual's 32-byte
-// pieces when `have` (a 16-bit residual read ahead)
-template <int N>
+// pieces when `have` (a 16-bit residual read ahead).  An fp32 residual is loaded here, ATONCE pieces before the first of
+// them is used: one by one each costs a latency (7582 x 6592 x 128: 147 us, 113 with 4; 8192 x 7168 x 2048: 218 and 193;
+// read ahead into registers like a 16-bit one it cost launches without a residual more than it gave, 44 -> 55 us).
+template <int N, int ATONCE>
 __device__ __forceinline__ void store_row(const LinearParams& p, const PairPlan& pl, float (&v)[N], int m0, int n,
                                           bool have, const uint32_t (*res)[8], float* stg) {
   const int lane = threadIdx.x & 31;
@@ -248,15 +250,21 @@ __device__ __forceinline__ void store_row(const LinearParams& p, const PairPlan&
       float* o = static_cast<float*>(p.out) + m * p.ldo + n;
       const float* r = static_cast<const float*>(p.residual) + (p.residual ? m * p.ldr + n : 0);
 #pragma unroll
-      for (int i = 0; i < N / 8; ++i) {
+      for (int i0 = 0; i0 < N / 8; i0 += ATONCE) {
+        static_assert(N / 8 % ATONCE == 0);
         if (p.residual) {
-          load32b(r + 8 * i, whole, w);
+          uint32_t f[ATONCE][8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[8 * i + j] += __uint_as_float(w[j]);
+          for (int i = 0; i < ATONCE; ++i) load32b(r + 8 * (i0 + i), whole, f[i]);
+#pragma unroll
+          for (int i = 0; i < 8 * ATONCE; ++i) v[8 * i0 + i] += __uint_as_float(f[i / 8][i % 8]);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * i + j]);
-        store32b(o + 8 * i, whole, w);
+        for (int i = i0; i < i0 + ATONCE; ++i) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * i + j]);
+          store32b(o + 8 * i, whole, w);
+        }
       }
       return;
     }
@@ -611,7 +619,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         if (n0 + c >= p.n_out) continue;
         apply(v, u, c);
-        store_row<32>(p, pl, v, m0, n0 + c, ahead, res, stg);
+        store_row<32, 4>(p, pl, v, m0, n0 + c, ahead, res, stg);
 #pragma unroll
         for (int j = 0; j + 2 < kPieces; ++j)
 #pragma unroll
@@ -697,7 +705,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
         if (n0 + c >= p.n_out) continue;
         apply(v, u, c);
-        store_row<kN>(p, pl, v, m0, n0 + c, ahead, res, stg);
+        store_row<kN, 1>(p, pl, v, m0, n0 + c, ahead, res, stg);
 #pragma unroll
         for (int j = 0; j + kN / 16 < kPieces; ++j)
 #pragma unroll
