@@ -341,6 +341,14 @@ int w4a8_test_tile_list_limit(int max_tiles);
  */
 int w4a8_test_linear_config(int rows, int pieces);
 
+/*
+ * Test of dense_linear's bounded waits where warps share a step: eight warps of one block wait, with the kernels' wait
+ * routine and a limit of limit_ns (at most 2e9), on a barrier each; that of warp `missing` (-1: none) is never completed.
+ * gave_up (device int[8]) gets, per warp, bit 0 where the warps together gave the step up and bit 1 where this warp's own
+ * wait ran out, which also raises bit 0 of the device error word.  No TMA or MMA is involved.
+ */
+int w4a8_test_linear_wait(int missing, uint64_t limit_ns, int* gave_up, void* stream);
+
 /* Operation ids for w4a8_workspace_bytes. */
 #define W4A8_OP_PERMUTE 1
 #define W4A8_OP_GROUPED_GEMM 2

@@ -93,3 +93,9 @@ def test_empty_calls_launch_nothing(clib):
     assert _route(clib, T=0, logits=NULL, ids=NULL, w=NULL) == 0
     assert _norm(clib, T=0) == 0
     assert _linear(clib, M=0) == 0 and _linear(clib, N=0) == 0
+
+
+def test_wait_test_refuses(clib):
+    assert clib.w4a8_test_linear_wait(8, 1000, P16, NULL) == 1 and b"missing=8" in clib.w4a8_last_error()
+    assert clib.w4a8_test_linear_wait(0, 3_000_000_000, P16, NULL) == 1 and b"limit_ns" in clib.w4a8_last_error()
+    assert clib.w4a8_test_linear_wait(0, 1000, NULL, NULL) == 1 and b"gave_up" in clib.w4a8_last_error()

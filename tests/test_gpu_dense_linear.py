@@ -1,4 +1,6 @@
 """dense_linear on the GPU against its definition in 64 bits."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -234,3 +236,24 @@ def test_fp32_residual_in_place(lib, M, N, K, gated):
     assert torch.equal(apart, alone + r)  # one fp32 addition
     lib.dense_linear(x, w, act="relu", gated=gated, residual=r, out_dtype=torch.float32, out=r)
     assert torch.equal(apart, r)
+
+
+@pytest.mark.parametrize("missing", [-1, 0, 3, 7])
+def test_warps_that_share_a_step_give_up_together(lib, missing):
+    # one warp's wait runs out (1 ms): every warp learns of it, the kernel ends, and the error word says so once
+    gave_up = torch.full((8,), -1, dtype=torch.int32, device="cuda")
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert lib.load().w4a8_test_linear_wait(missing, 1_000_000, ctypes.c_void_p(gave_up.data_ptr()), stream) == 0
+    torch.cuda.synchronize()
+    assert gave_up.tolist() == [(missing >= 0) | (2 if w == missing else 0) for w in range(8)]
+    assert lib.device_error() == (1 if missing >= 0 else 0)
+    assert lib.device_error() == 0
+    # a product whose sums are taken in pieces, through the same routine
+    g = torch.Generator("cuda").manual_seed(22)
+    x, w = _mat(520, 4224, "bf16", g, ints=True), _mat(264, 4224, "bf16", g, ints=True)
+    lib.load().w4a8_test_linear_config(256, 1)
+    try:
+        got = lib.dense_linear(x, w, out_dtype=torch.float32)
+    finally:
+        lib.load().w4a8_test_linear_config(0, 0)
+    assert torch.equal(got.double(), x.double() @ w.double().t()) and lib.device_error() == 0

@@ -72,6 +72,7 @@ _SIGS = {
                               _c_vp, _c_i64, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_sz, _c_vp]),
     "dense_linear_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64]),
     "w4a8_test_linear_config": (_c_int, [_c_int, _c_int]),
+    "w4a8_test_linear_wait": (_c_int, [_c_int, ctypes.c_uint64, _c_vp, _c_vp]),
 }
 
 

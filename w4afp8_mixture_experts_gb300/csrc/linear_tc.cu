@@ -35,15 +35,18 @@ constexpr int kMaxSmem = 227 * 1024;
 
 __device__ unsigned int g_linear_error;
 
-// Waits for a phase of `bar`, at most kTimeoutNs; gives up early when another role of the CTA has given up.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+// Waits for a phase of `bar`, at most limit_ns; gives up early when another role of the CTA has given up.  A thread that
+// was away for longer than the limit looks at the phase once more before it gives up.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                         uint64_t limit_ns = kTimeoutNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t n = 0;; ++n) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((n & 127u) == 127u) {
       if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > kTimeoutNs) {
+      if (globaltimer_ns() - t0 > limit_ns) {
+        if (mbar_try_wait(bar, parity)) return true;
         *abort_flag = 1;
         atomicOr(&g_linear_error, 1u);
         return false;
@@ -67,6 +70,22 @@ __device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
 // The same by a whole warp; the same answer on all its lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag));
+}
+// Whether the waits of all THREADS threads (whole warps) were satisfied: the same answer on all of them, once each has
+// arrived.  Warps that share a step decide on it together: one that gave up by itself would leave the others at their next
+// barrier for good.
+template <int THREADS>
+__device__ __forceinline__ bool all_satisfied(bool ok) {
+  uint32_t bad;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.eq.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.aligned.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(bad)
+      : "r"(static_cast<uint32_t>(ok)), "n"(THREADS)
+      : "memory");
+  return bad == 0;
 }
 // One lane of a converged warp.  The producer and product warps run their loops as whole warps and elect a lane
 // around each TMA or tcgen05 instruction: with the loop inside a single-lane branch the operands of those
@@ -542,14 +561,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t tempty0 = map_to_cta(smem_u32(tempty), lead);
   int n = 0;  // accumulator fills so far
   // Waits for the products of a tile and returns the accumulator that holds them (-1 after an abort).  CHUNKED: every
-  // thread adds up 128 columns of its row over the chunks and puts the sums back into the last chunk's accumulator.
+  // thread adds up 128 columns of its row over the chunks and puts the sums back into the last chunk's accumulator, where
+  // the epilogue warps read one another's columns: each of them arrives at their barrier once per tile, at its last chunk or
+  // when it gives up, and all go on or none.
   auto products = [&]() -> int {
     if constexpr (CHUNKED) {
       const int chunks = (kb1 - kb0 + kChunk - 1) / kChunk;
       float sum[4][32];
+      bool ok = true;
       for (int ch = 0; ch < chunks; ++ch, ++n) {
         const int buf = n & 1;
-        if (__any_sync(0xffffffffu, !wait_bar(&tfull[buf], (n >> 1) & 1, abort_flag))) return -1;
+        if (!(ok = warp_wait(&tfull[buf], (n >> 1) & 1, abort_flag))) break;
         tc_fence_after();
         if (chunks == 1) break;
         const uint32_t at = tmem + buf * 256 + lanes + half * 128;
@@ -571,14 +593,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int q = 0; q < 4; ++q) tmem_st32(at + 32 * q, reinterpret_cast<const uint32_t*>(sum[q]));
         tmem_wait_st();
         tc_fence_before();
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kPairEpiWarps) : "memory");  // the epilogue warps share columns
-        tc_fence_after();
         break;
       }
-      return n++ & 1;
+      if (chunks > 1) {
+        ok = all_satisfied<32 * kPairEpiWarps>(ok);
+        tc_fence_after();
+      }
+      return ok ? n++ & 1 : -1;
     } else {
       const int buf = n & 1;
-      if (__any_sync(0xffffffffu, !wait_bar(&tfull[buf], (n >> 1) & 1, abort_flag))) return -1;
+      if (!warp_wait(&tfull[buf], (n >> 1) & 1, abort_flag)) return -1;
       tc_fence_after();
       ++n;
       return buf;
@@ -1033,6 +1057,27 @@ __global__ void __launch_bounds__(SplitCfg<BN>::kThreads, 1)
     finish_tokens<BN, GATED, __nv_bfloat16>(p, red, splits, own, left, m0 + rank * own, n0, vec_out, bias, bias2, res);
 }
 
+// --- test of the epilogue warps' common outcome -----------------------------------------------------------------
+
+// The epilogue warps of one CTA, each waiting on a barrier of its own as in a tile's last chunk; that of warp `missing` is
+// never completed.  gave_up[w]: warp w was told that the tile is lost.
+__global__ void __launch_bounds__(32 * kPairEpiWarps) linear_wait_probe_kernel(int missing, uint64_t limit_ns, int* gave_up) {
+  __shared__ uint64_t bars[kPairEpiWarps];
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPairEpiWarps; ++i) mbar_init(&bars[i], 1);
+    abort_flag = 0;
+    mbar_fence_init();
+  }
+  __syncthreads();
+  if (lane == 0 && warp != missing) mbar_arrive(&bars[warp]);
+  __syncwarp();
+  const bool mine = __all_sync(0xffffffffu, wait_bar(&bars[warp], 0, &abort_flag, limit_ns));
+  const bool ok = all_satisfied<32 * kPairEpiWarps>(mine);
+  if (lane == 0) gave_up[warp] = (ok ? 0 : 1) | (mine ? 0 : 2);
+}
+
 // --- operands without 16-byte alignment ------------------------------------------------------------------------
 
 // Rows of x and of w (those of the two that need it) to 16-byte-aligned rows of the workspace, zeros past K; 8 elements
@@ -1348,4 +1393,13 @@ int launch_linear_tc(LinearParams p, void* ws, size_t ws_bytes, cudaStream_t st)
 extern "C" int w4a8_test_linear_config(int rows, int pieces) {
   w4a8::g_force.store(rows > 0 ? rows * 16 + pieces : 0);
   return W4A8_OK;
+}
+
+extern "C" int w4a8_test_linear_wait(int missing, uint64_t limit_ns, int* gave_up, void* stream) {
+  using namespace w4a8;
+  W4A8_REQUIRE(gave_up != nullptr && (reinterpret_cast<uintptr_t>(gave_up) & 3) == 0, "gave_up must be an int[8]");
+  W4A8_REQUIRE(missing >= -1 && missing < kPairEpiWarps, "missing=%d must be in [-1, 8)", missing);
+  W4A8_REQUIRE(limit_ns > 0 && limit_ns <= kTimeoutNs, "limit_ns must be in (0, 2e9]");
+  linear_wait_probe_kernel<<<1, 32 * kPairEpiWarps, 0, static_cast<cudaStream_t>(stream)>>>(missing, limit_ns, gave_up);
+  return check_launch("linear_wait_probe_kernel");
 }
