@@ -99,3 +99,52 @@ def test_wait_test_refuses(clib):
     assert clib.w4a8_test_linear_wait(8, 1000, P16, NULL) == 1 and b"missing=8" in clib.w4a8_last_error()
     assert clib.w4a8_test_linear_wait(0, 3_000_000_000, P16, NULL) == 1 and b"limit_ns" in clib.w4a8_last_error()
     assert clib.w4a8_test_linear_wait(0, 1000, NULL, NULL) == 1 and b"gave_up" in clib.w4a8_last_error()
+
+
+def test_routed_layer_runs_on_its_tensors_device(clib, monkeypatch):
+    # the device and the stream are those of x, whatever the current device; a tensor of another device is refused
+    import contextlib
+
+    import torch
+
+    import w4afp8_mixture_experts_gb300._binding as b
+
+    class OnDevice1(torch.Tensor):  # CPU memory that says it lies on the second device
+        is_cuda = property(lambda self: True)
+        device = property(lambda self: torch.device("cuda", getattr(self, "place", 1)))
+
+    def make(*shape, dtype):
+        return torch.zeros(shape, dtype=dtype).as_subclass(OnDevice1)
+
+    calls = []
+
+    class Lib:
+        def w4a8_moe_forward_routed(self, *a):
+            calls.append(("call", a[-1].value))
+            return 0
+
+    @contextlib.contextmanager
+    def device(d):
+        calls.append(("enter", d))
+        yield
+        calls.append(("leave", d))
+
+    class Stream:
+        def __init__(self, d):
+            self.cuda_stream = 100 + (0 if d is None else torch.device(d).index)
+
+    monkeypatch.setattr(b, "load", lambda: Lib())
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: Stream(d))
+    T, H, I, E, k = 4, 256, 128, 8, 2
+    args = dict(x=make(T, H, dtype=torch.bfloat16), topk_ids=make(T, k, dtype=torch.int32),
+                topk_w=make(T, k, dtype=torch.float32), w13=make(E, 2 * I, H // 2, dtype=torch.uint8),
+                w13_s=make(E, H // 128, 2 * I, dtype=torch.float32), w2=make(E, H, I // 2, dtype=torch.uint8),
+                w2_s=make(E, I // 128, H, dtype=torch.float32), ws=make(1024, dtype=torch.uint8),
+                out=make(T, H, dtype=torch.bfloat16))
+    b.w4a8_moe_forward_routed(**args)
+    one = torch.device("cuda", 1)
+    assert calls == [("enter", one), ("call", 101), ("leave", one)]
+    args["w2"].place = 0
+    with pytest.raises(ValueError, match="w2 must be on cuda:1"):
+        b.w4a8_moe_forward_routed(**args)

@@ -94,3 +94,28 @@ def test_routed_refusals(lib):
         lib.w4a8_moe_forward_routed(x, ids, w, *block.experts, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
     out = lib.w4a8_moe_forward_routed(x[:0], ids[:0], w[:0], *block.experts)
     assert out.shape == (0, 256)
+
+
+def test_routed_refuses_what_does_not_fit_the_layer(lib):
+    # every one of these would be read or written out of range
+    import moe_block
+    block = moe_block.random_block(256, 128, 8, 2, shared=64, n_group=1, topk_group=1)
+    x = torch.zeros((4, 256), dtype=torch.bfloat16, device="cuda")
+    ids, w = torch.zeros((4, 2), dtype=torch.int32, device="cuda"), torch.zeros((4, 2), device="cuda")
+    w13, w13_s, w2, w2_s = block.experts
+    need = lib.moe_workspace_layout(4, 256, 128, 8, 2).total
+    args = dict(x=x, topk_ids=ids, topk_w=w, w13=w13, w13_s=w13_s, w2=w2, w2_s=w2_s, ws=None, out=None)
+    ws, out = torch.empty(need, dtype=torch.uint8, device="cuda"), torch.empty_like(x)
+    for name, bad in [("w13", w13[:, :, :64].contiguous()), ("w13", w13[:, :255].contiguous()), ("w2", w2[:7]),
+                      ("w2", w2[:, :128].contiguous()), ("w2", w2[:, :, :32].contiguous()), ("w13_s", w13_s[:7]),
+                      ("w13_s", w13_s[:, :1].contiguous()), ("w2_s", w2_s[:7]), ("w2_s", w2_s[:, :, :128].contiguous()),
+                      ("out", out[:3]), ("out", torch.empty((4, 512), dtype=torch.bfloat16, device="cuda")[:, :256]),
+                      ("ws", torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2]), ("topk_ids", ids[:, :1]),
+                      ("x", torch.zeros((4, 512), dtype=torch.bfloat16, device="cuda")[:, ::2])]:
+        with pytest.raises(ValueError, match=name):
+            lib.w4a8_moe_forward_routed(**{**args, name: bad})
+    for name, bad in [("out", out.half()), ("out", out.cpu()), ("ws", ws.int()), ("ws", ws.cpu()), ("w2", w2.int()),
+                      ("w2_s", w2_s.half()), ("topk_ids", ids.long()), ("topk_w", w.half()), ("topk_w", w.cpu())]:
+        with pytest.raises(TypeError, match=name):
+            lib.w4a8_moe_forward_routed(**{**args, name: bad})
+    assert lib.w4a8_moe_forward_routed(**{**args, "ws": ws, "out": out}) is out

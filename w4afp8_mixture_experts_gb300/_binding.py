@@ -364,26 +364,38 @@ def w4a8_moe_forward(x, logits, k: int, w13, w13_s, w2, w2_s, renormalize: bool 
 
 def w4a8_moe_forward_routed(x, topk_ids, topk_w, w13, w13_s, w2, w2_s, ws=None, out=None):
     """The layer with its routing given (topk_ids int32 [T, k], topk_w fp32 [T, k], as moe_route_grouped_topk returns
-    them); everything else as in w4a8_moe_forward."""
+    them); everything else as in w4a8_moe_forward.  Every tensor is contiguous and on x's device; ws is a uint8
+    workspace of moe_workspace_layout(T, H, I, E, k).total bytes, out bf16 [T, H]."""
     _req(x, torch.bfloat16, "x", 2)
     _req(topk_ids, torch.int32, "topk_ids", 2)
     _req(topk_w, torch.float32, "topk_w", 2)
     _req(w13, torch.uint8, "w13", 3)
-    _req(w2, torch.uint8, "w2", 3)
-    _req(w13_s, torch.float32, "w13_s", 3)
-    _req(w2_s, torch.float32, "w2_s", 3)
     T, H = x.shape
     k = topk_ids.shape[1]
-    E = w13.shape[0]
-    I = w13.shape[1] // 2
-    if topk_ids.shape != (T, k) or topk_w.shape != (T, k):
+    E, I = w13.shape[0], w13.shape[1] // 2
+    if topk_ids.shape[0] != T or topk_w.shape != topk_ids.shape:
         raise ValueError(f"topk_ids and topk_w must have {T} rows and the same shape")
-    if ws is None:
-        ws = torch.empty(int(load().w4a8_moe_workspace_bytes(T, H, I, E, k)), dtype=torch.uint8, device=x.device)
-    if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-    _check(load().w4a8_moe_forward_routed(_p(x), _p(topk_ids), _p(topk_w), T, H, I, E, k, _p(w13), _p(w13_s), _p(w2),
-                                          _p(w2_s), _p(out), _p(ws), ws.numel(), _stream()))
+    dev = x.device
+    for t, dtype, name, shape in ((topk_ids, torch.int32, "topk_ids", (T, k)), (topk_w, torch.float32, "topk_w", (T, k)),
+                                  (w13, torch.uint8, "w13", (E, 2 * I, H // 2)),
+                                  (w13_s, torch.float32, "w13_s", (E, H // 128, 2 * I)),
+                                  (w2, torch.uint8, "w2", (E, H, I // 2)),
+                                  (w2_s, torch.float32, "w2_s", (E, I // 128, H)),
+                                  (ws, torch.uint8, "ws", None), (out, torch.bfloat16, "out", (T, H))):
+        if t is None and name in ("ws", "out"):
+            continue
+        _req(t, dtype, name)
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+        if shape is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    with torch.cuda.device(dev):
+        if ws is None:
+            ws = torch.empty(int(load().w4a8_moe_workspace_bytes(T, H, I, E, k)), dtype=torch.uint8, device=dev)
+        if out is None:
+            out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        _check(load().w4a8_moe_forward_routed(_p(x), _p(topk_ids), _p(topk_w), T, H, I, E, k, _p(w13), _p(w13_s),
+                                              _p(w2), _p(w2_s), _p(out), _p(ws), ws.numel(), _stream(dev)))
     return out
 
 
