@@ -469,7 +469,8 @@ typedef enum {
  *   (equal c: lower id first);  w_j = s[ids_j], with renormalize != 0 divided by
  *   (their sum + 1e-20), times scale.
  * The bias takes part in the choice only.  A softmax without a bias is ranked
- * by the logits (the same order, without ties made by rounding).
+ * by the logits, and its groups of two by the logarithm of their sum (the same
+ * order, without ties made by rounding).
  * A logit that is -inf, the lowest finite value of its type or NaN takes its
  * expert out: s = 0, c = -inf.  When fewer than k experts are left, the places
  * are filled with the lowest ids among the experts that are out or in groups

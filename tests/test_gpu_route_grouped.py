@@ -173,3 +173,51 @@ def test_refusals(lib):
         lib.moe_route_grouped_topk(x.cpu(), 2)
     with pytest.raises(ValueError, match="contiguous rows"):
         lib.moe_route_grouped_topk(torch.zeros((16, 4), device="cuda").t(), 2)
+
+
+def _pairs_of_softmax(l, k, n_group, topk_group, away):
+    """(ids, distance of the logarithms of the group scores that decide): groups by the sum of their two largest softmax
+    scores, in 64 bits."""
+    ids, gap = [], []
+    for row, out in zip(np.asarray(l, np.float64), away):
+        e = np.where(out, 0.0, np.exp(np.where(out, 0.0, row - np.max(row[~out], initial=-1e300))))
+        with np.errstate(divide="ignore"):
+            c = np.where(out, -np.inf, e / e.sum() if e.sum() else e).reshape(n_group, -1)
+            two = np.log(np.maximum(np.sort(c, axis=1)[:, -2:].sum(axis=1), 0.0))
+        order = np.argsort(-two, kind="stable")
+        best = two[order]
+        gap.append(best[topk_group - 1] - best[topk_group] if topk_group < n_group and np.isfinite(best[topk_group - 1])
+                   else np.inf)
+        kept = np.isin(np.arange(n_group), order[:topk_group])
+        live = np.where(out | ~np.repeat(kept, c.shape[1]), -np.inf, row)
+        ids.append(np.argsort(-live, kind="stable")[:k])
+    return np.array(ids), np.array(gap)
+
+
+@pytest.mark.parametrize("E,k,G,keep", [(64, 6, 8, 3), (256, 8, 8, 4), (40, 8, 5, 4), (96, 3, 4, 1), (512, 8, 16, 5)])
+@pytest.mark.parametrize("spread,offset", [(2.0, 0.0), (0.3, 1000.0), (60.0, -50.0)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_groups_by_the_sum_of_two_softmax_scores(lib, E, k, G, keep, spread, offset, masked):
+    rng = np.random.default_rng(E + k)
+    l = (rng.standard_normal((300, E)) * spread + offset).astype(np.float32)
+    away = rng.random((300, E)) < (0.3 if masked else 0.0)
+    l[away] = -np.inf
+    ids, _ = _run(lib, l, k, score="softmax", n_group=G, topk_group=keep, group_top=2)
+    rid, gap = _pairs_of_softmax(l, k, G, keep, away)
+    # the logarithm is off by at most its subtraction, sum and 4 units of exp and log1p, all below 2^9 * 2^-24 = 4e-5
+    far = gap > 1e-4
+    assert far.mean() > 0.9
+    assert np.array_equal(ids[far], rid[far])
+    if offset == 0.0 and not masked:  # a bias of zeros changes no sum
+        with_bias, _ = _run(lib, l, k, bias=np.zeros(E, np.float32), score="softmax", n_group=G, topk_group=keep, group_top=2)
+        assert np.array_equal(np.sort(ids[far], 1), np.sort(with_bias[far], 1))
+
+
+def test_groups_of_two_with_infinite_logits(lib):
+    l = np.zeros((3, 12), np.float32)
+    l[0, [4, 9]] = np.inf          # one infinite logit in each of two groups: equal sums, lower group first
+    l[1, [8, 9, 4]] = np.inf       # two in the last group
+    l[1, 0:4] = 5.0                # finite scores are 0 beside an infinite one
+    l[2, :] = [3e38, -3e38, 0, 0, 3e38, 3e38, 0, 0, 1, 1, 1, 1]
+    ids, _ = _run(lib, l, 2, score="softmax", n_group=3, topk_group=1, group_top=2)
+    assert ids.tolist() == [[4, 5], [8, 9], [4, 5]]

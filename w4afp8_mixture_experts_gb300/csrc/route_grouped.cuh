@@ -64,6 +64,15 @@ __device__ __forceinline__ float sigmoid_score(float l) { return __frcp_rn(__fad
 // the last place.)
 __device__ __forceinline__ float softmax_term(float l, float mx) { return l == mx ? 1.0f : __expf(l - mx); }
 
+// Ranks groups by the sum of two softmax scores, given their logits a >= b and the token's largest logit: the sum's
+// logarithm (up to the token's denominator), which neither overflows nor leaves small sums equal.  With infinite logits,
+// the sum itself: how many of the two are.
+__device__ __forceinline__ float pair_score(float a, float b, float mx) {
+  if (b == -INFINITY) return -INFINITY;
+  if (mx == INFINITY) return softmax_term(a, mx) + softmax_term(b, mx);
+  return fmaxf(a - mx + log1pf(expf(b - a)), -FLT_MAX);
+}
+
 // Sorts v[0 .. N) in descending order: merge exchange (Batcher; Knuth, TAOCP vol. 3, algorithm 5.2.2M).
 template <int N>
 __device__ __forceinline__ void sort_descending(uint64_t (&v)[N]) {
@@ -292,7 +301,11 @@ __global__ void __launch_bounds__(256) route_grouped_kernel(const RouteParams p)
       if (sub == 0 && g < p.n_group) {
         float sc = key_value(k1);
         if (p.group_top == 2) {
-          sc = __fadd_rn(sc, key_value(k2));
+          const float sc2 = key_value(k2);
+          if (p.softmax && !p.bias)
+            sc = pair_score(sc, sc2, mx);
+          else
+            sc = __fadd_rn(sc, sc2);
           if (!(sc >= -INFINITY)) sc = -INFINITY;  // inf + -inf
         }
         gk = order_key(sc + 0.0f);
