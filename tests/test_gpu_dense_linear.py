@@ -257,3 +257,36 @@ def test_warps_that_share_a_step_give_up_together(lib, missing):
     finally:
         lib.load().w4a8_test_linear_config(0, 0)
     assert torch.equal(got.double(), x.double() @ w.double().t()) and lib.device_error() == 0
+
+
+@pytest.mark.parametrize("M,N,K,dtype", [(8, 64, 1 << 20, "f16"), (64, 256, 1 << 20, "f16"), (300, 512, 1 << 20, "f16"),
+                                         (64, 256, 131072, "f16"), (1300, 2000, 40000, "f16"), (300, 512, 1 << 20, "bf16")])
+def test_long_sums_of_16_bit_outputs(lib, M, N, K, dtype):
+    # Positive terms, where the cut-off of the tensor core's additions only adds up.  A sum in one accumulator may be off by
+    # a sixteenth of the output's own rounding, the joining of up to 1024 pieces in fp32 by another.
+    g = torch.Generator("cuda").manual_seed(23)
+    x, w = (((0.5 + 0.5 * torch.rand((n, K), device="cuda", generator=g)) * 2.0 ** -5).to(DT[dtype]) for n in (M, N))
+    got = lib.dense_linear(x, w).double()
+    want = torch.zeros((M, N), dtype=torch.float64, device="cuda")
+    for k in range(0, K, 65536):
+        want += x[:, k:k + 65536].double() @ w[:, k:k + 65536].double().t()
+    assert lib.device_error() == 0
+    assert torch.all((got - want).abs() <= (1 + 1 / 8) * ref.U[dtype] * want)
+
+
+@pytest.mark.parametrize("config,dtype,K", [((256, 1), "f16", 16520), ((256, 2), "f16", 33000), ((256, 4), "f16", 65800),
+                                            ((256, 1), "bf16", 131200)], indirect=["config"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("opad", [0, 8, 3])
+def test_sums_in_pieces_with_a_16_bit_residual(lib, config, dtype, K, gated, opad):
+    # whole numbers: the sums are exact, and the residual is added before the one rounding to the output's type
+    M, N = 300, 512
+    g = torch.Generator("cuda").manual_seed(24)
+    x, w = _mat(M, K, dtype, g, ints=True), _mat(N, K, dtype, g, ints=True)
+    r = _mat(M, N // 2 if gated else N, dtype, g, pad=opad, ints=True)
+    z = x.double() @ w.double().t()
+    want = (z[:, :N // 2].clamp_min(0) * z[:, N // 2:] if gated else z.clamp_min(0)) + r.double()
+    got = lib.dense_linear(x, w, act="relu", gated=gated, residual=r)
+    assert lib.device_error() == 0 and torch.equal(got, want.float().to(DT[dtype]))
+    lib.dense_linear(x, w, act="relu", gated=gated, residual=r, out=r)
+    assert torch.equal(r, got)

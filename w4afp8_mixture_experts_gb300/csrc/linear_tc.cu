@@ -253,10 +253,10 @@ __device__ __forceinline__ void pair_tile(const PairPlan& pl, int i, int& tm, in
 }
 
 // N (16 or 32) output columns of this thread's row m0 + lane, from column n on; `res`: the residual's 32-byte
-// pieces when `have` (a 16-bit residual read ahead).  An fp32 residual is loaded here, ATONCE pieces before the first of
-// them is used: one by one each costs a latency (7582 x 6592 x 128: 147 us, 113 with 4; 8192 x 7168 x 2048: 218 and 193;
+// pieces when `have` (a 16-bit residual read ahead).  Otherwise it is loaded here (LOADS: a 16-bit one too); an fp32 one ATONCE pieces before the
+// first of them is used: one by one each costs a latency (7582 x 6592 x 128: 147 us, 113 with 4; 8192 x 7168 x 2048: 218 and 193;
 // read ahead into registers like a 16-bit one it cost launches without a residual more than it gave, 44 -> 55 us).
-template <int N, int ATONCE>
+template <int N, int ATONCE, bool LOADS>
 __device__ __forceinline__ void store_row(const LinearParams& p, const PairPlan& pl, float (&v)[N], int m0, int n,
                                           bool have, const uint32_t (*res)[8], float* stg) {
   const int lane = threadIdx.x & 31;
@@ -291,10 +291,12 @@ __device__ __forceinline__ void store_row(const LinearParams& p, const PairPlan&
     const bool bf16 = p.out_dtype == W4A8_DTYPE_BF16;
 #pragma unroll
     for (int i = 0; i < N / 16; ++i) {
-      if (have) {
+      if (have || (LOADS && p.residual)) {
+        uint32_t own[8];
+        if (LOADS) load32b(static_cast<const uint16_t*>(p.residual) + m * p.ldr + n + 16 * i, whole, own);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const uint32_t q = res[i][j];
+          const uint32_t q = LOADS ? own[j] : res[i][j];
           const float2 f = bf16 ? make_float2(__uint_as_float(q << 16), __uint_as_float(q & 0xFFFF0000u))
                                 : __half22float2(*reinterpret_cast<const __half2*>(&q));
           v[16 * i + 2 * j] += f.x;
@@ -362,9 +364,16 @@ __device__ __forceinline__ void store_row(const LinearParams& p, const PairPlan&
 }
 
 // The tensor core cuts off what does not fit the accumulator at every addition, so a sum of n products of 16 k is off by
-// about n / 2 units of fp32 to one side (3.8e-6 of the result at K = 3584, where plain fp32 sums have 0.9e-6).  That does
-// not show in a 16-bit output; for an fp32 one, sums over kChunk stages are added up in registers, rounded to nearest.
+// about n / 2 units of 2^-24 to one side (3.8e-6 of the result at K = 3584, where plain fp32 sums have 0.9e-6; 8.5e-4 with
+// positive terms at K = 2^20).  A sum in one accumulator is therefore as long as its output's type hides that, and longer
+// ones are added up in registers every kChunk stages, rounded to nearest:
+//   fp32   kChunk stages, 1024 products (n / 2 = 32 units)
+//   f16    256 stages, 16384 products: off by at most 2^-15, a sixteenth of the output's own rounding (2^-11)
+//   bf16   2048 stages, 131072 products: 2^-12, a sixteenth of 2^-8
 constexpr int kChunk = 16;
+constexpr int longest_sum(int out_dtype) {  // in stages
+  return out_dtype == W4A8_DTYPE_F32 ? kChunk : out_dtype == W4A8_DTYPE_F16 ? 256 : 2048;
+}
 constexpr int kPrefetchStages = 16;  // K up to which the pair kernel's epilogue prefetches the next residual
 constexpr int kRegsLaunch = 168;  // of a thread at launch (checked on the host)
 constexpr int kRegsRoles = 40, kRegsSums = 232;  // registers of warps 0-3 and of the epilogue's, which hold 128 sums
@@ -557,7 +566,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     for (int i = 0; i < kPieces; ++i)
       if (m < p.M && n0 + 16 * i + 16 <= p.n_out) load32b(r + 16 * i, pl.vec_out == 2, res[i]);
   };
-  const bool ahead = !CHUNKED && p.residual && pl.vec_out && p.out_dtype != W4A8_DTYPE_F32;  // CHUNKED: fp32 output
+  const bool ahead = !CHUNKED && p.residual && pl.vec_out && p.out_dtype != W4A8_DTYPE_F32;  // CHUNKED: registers hold the sums
   const uint32_t tempty0 = map_to_cta(smem_u32(tempty), lead);
   int n = 0;  // accumulator fills so far
   // Waits for the products of a tile and returns the accumulator that holds them (-1 after an abort).  CHUNKED: every
@@ -643,7 +652,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         if (n0 + c >= p.n_out) continue;
         apply(v, u, c);
-        store_row<32, 4>(p, pl, v, m0, n0 + c, ahead, res, stg);
+        store_row<32, 4, CHUNKED>(p, pl, v, m0, n0 + c, ahead, res, stg);
 #pragma unroll
         for (int j = 0; j + 2 < kPieces; ++j)
 #pragma unroll
@@ -729,7 +738,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
         if (n0 + c >= p.n_out) continue;
         apply(v, u, c);
-        store_row<kN, 1>(p, pl, v, m0, n0 + c, ahead, res, stg);
+        store_row<kN, 1, CHUNKED>(p, pl, v, m0, n0 + c, ahead, res, stg);
 #pragma unroll
         for (int j = 0; j + kN / 16 < kPieces; ++j)
 #pragma unroll
@@ -742,6 +751,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
 // --- split kernel --------------------------------------------------------------------------------------------
 
+constexpr int kSplitMma = 2;
+// accumulators that share the sums over a CTA's piece of K
+__host__ __device__ constexpr int split_accumulators(int out_dtype) {
+  return (out_dtype == W4A8_DTYPE_F32 ? 2 : 1) * kSplitMma;
+}
 
 template <int BN>
 struct SplitCfg {
@@ -753,10 +767,10 @@ struct SplitCfg {
   static constexpr int kOffRed = kStages * kStageBytes;       // [source CTA][token of mine][128 W rows] fp32
   static constexpr int kOffBar = kOffRed + BN * 128 * 4;
   static constexpr int kSmem = kOffBar + (2 * kStages + 5) * 8 + 16 + 1024;
-  // MMA warps: warp m issues the products of stages it % kMma == m into an accumulator of its own.  One warp spends
+  // MMA warps (kSplitMma): warp m issues the products of stages it % kMma == m into an accumulator of its own.  One warp spends
   // ~330 cycles a stage on the hand-over (wait, fence, commit), several times what the products take; together they
   // overlap it, and the sums over K are shorter.
-  static constexpr int kMma = 2;
+  static constexpr int kMma = kSplitMma;
   // A warp waits for every phase of the slots that it uses, in order, only if a slot always falls to the same warp:
   // otherwise its parity wait is satisfied by the phase before the one it needs.
   static_assert(kStages % kMma == 0, "ring depth a multiple of the MMA warps");
@@ -952,7 +966,7 @@ __global__ void __launch_bounds__(SplitCfg<BN>::kThreads, 1)
   float bias[8], bias2[8];
   uint4 res[SplitCfg<BN>::kTurns];
   read_ahead_split<BN, GATED>(p, m0 + rank * own, n0, own, vec_out, bias, bias2, res);
-  const int accs = (p.out_dtype == W4A8_DTYPE_F32 ? 2 : 1) * C::kMma;
+  const int accs = split_accumulators(p.out_dtype);
   int issued = 0;  // stages whose loads this warp has issued
   if (warp == 0) {
     for (int kb = kb0; kb < kb1; ++kb, ++issued) {
@@ -1253,7 +1267,7 @@ struct Pair {
                               2 * PARTS, CHUNKED ? kRegsLaunch : 0);
   }
   static int launch(const LinearParams& p, int dev, cudaStream_t st) {
-    if (!CHUNKED && p.out_dtype == W4A8_DTYPE_F32 && p.K > kChunk * kBK * PARTS)
+    if (!CHUNKED && p.K > longest_sum(p.out_dtype) * kBK * PARTS)
       return Pair<GATED, PARTS, true>::launch(p, dev, st);
     CUtensorMap tx, tw;
     int rc, clusters = 1;
@@ -1336,8 +1350,8 @@ int launch_best(const LinearParams& p, cudaStream_t st) {
   const int64_t kblocks = ceil_div(p.K, kBK);
   const int force = g_force.load(std::memory_order_relaxed);
   for (const Option& o : options) {
-    // an fp32 output's sums are kept short (see kChunk): the split kernel has four accumulators for a piece of K
-    if (!force && o.rows < 256 && p.out_dtype == W4A8_DTYPE_F32 && kblocks > 4 * kChunk * o.parts) continue;
+    // sums are kept short (see longest_sum): the split kernel has split_accumulators for a piece of K
+    if (!force && o.rows < 256 && kblocks > split_accumulators(p.out_dtype) * longest_sum(p.out_dtype) * o.parts) continue;
     if (o.parts > kblocks || (force && force % 16 <= kblocks && force != o.rows * 16 + o.parts)) continue;
     int clusters = 1;
     if (int rc = o.ready(dev, &clusters)) return rc;
