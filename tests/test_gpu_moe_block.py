@@ -119,3 +119,35 @@ def test_routed_refuses_what_does_not_fit_the_layer(lib):
         with pytest.raises(TypeError, match=name):
             lib.w4a8_moe_forward_routed(**{**args, name: bad})
     assert lib.w4a8_moe_forward_routed(**{**args, "ws": ws, "out": out}) is out
+
+
+@pytest.mark.parametrize("T", [1, 8, 16, 64, 600])
+def test_calls_that_follow_their_producer_at_once(lib, T):
+    # each call reads what the one before it writes into the same memory, with nothing in between; the inputs change from
+    # turn to turn, so that a value read too early is another one
+    g = torch.Generator("cuda").manual_seed(T)
+    H, E, turns = 4096, 64, 40
+    w = (torch.randn((E, H), device="cuda", generator=g) * H ** -0.5).to(torch.bfloat16)
+    up = (torch.randn((H, E), device="cuda", generator=g) * E ** -0.5).to(torch.bfloat16)
+    attn = torch.randn((turns, T, H), device="cuda", generator=g).to(torch.bfloat16)
+    res = torch.randn((T, H), device="cuda", generator=g).to(torch.bfloat16)
+    h, x, f = torch.empty_like(res), torch.empty_like(res), torch.empty_like(res)
+    logits = torch.empty((T, E), device="cuda")
+    small = torch.empty((T, E), dtype=torch.bfloat16, device="cuda")
+
+    def turn(a, wait):
+        outs = []
+        for call in (lambda: lib.block_norm(a, res, post="rms", pre="rms", h=h, y=x),
+                     lambda: lib.dense_linear(x, w, out_dtype=torch.float32, out=logits),
+                     lambda: outs.extend(lib.moe_route_grouped_topk(logits, 4, n_group=8, topk_group=4, group_top=2)),
+                     lambda: lib.dense_linear(x, w, act="silu", out=small),
+                     lambda: lib.dense_linear(small, up, residual=h, out=f)):
+            call()
+            if wait:
+                torch.cuda.synchronize()
+        return outs + [f.clone()]
+
+    at_once = [turn(a, False) for a in attn]
+    for a, got in zip(attn, at_once):
+        assert all(torch.equal(p, q) for p, q in zip(got, turn(a, True)))
+    assert lib.device_error() == 0

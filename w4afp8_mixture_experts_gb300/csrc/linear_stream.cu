@@ -17,10 +17,11 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kStep = 32;  // k per pair of mma instructions
 
-// 8 consecutive elements [k, k + 8) of a row, zeros from K on
+// 8 consecutive elements [k, k + 8) of a row, zeros from K on.  An ordinary load: a non-coherent one asks for memory that
+// nothing writes during the kernel's whole life, and this kernel starts while its predecessor may still write x.
 template <bool ALIGNED>
 __device__ __forceinline__ uint4 load8(const uint16_t* row, int k, int K) {
-  if (ALIGNED && k + 8 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
+  if (ALIGNED && k + 8 <= K) return *reinterpret_cast<const uint4*>(row + k);
   uint32_t v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
