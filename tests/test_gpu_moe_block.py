@@ -151,3 +151,23 @@ def test_calls_that_follow_their_producer_at_once(lib, T):
     for a, got in zip(attn, at_once):
         assert all(torch.equal(p, q) for p, q in zip(got, turn(a, True)))
     assert lib.device_error() == 0
+
+
+@pytest.mark.parametrize("T", [1, 64, 3000])
+def test_outputs_are_tensors_of_their_own(lib, T):
+    # each output has its own memory, as large as itself: keeping, saving or resizing one does not concern the other
+    import io
+    f, r = torch.randn((T, 128), device="cuda").to(torch.bfloat16), torch.randn((T, 128), device="cuda")
+    for pair in (lib.block_norm(f, r), lib.moe_route_grouped_topk(r, 8)):
+        a, b = pair
+        assert a.untyped_storage().data_ptr() != b.untyped_storage().data_ptr()
+        for t in pair:
+            assert t.is_contiguous() and t.storage_offset() == 0
+            assert t.untyped_storage().nbytes() == t.numel() * t.element_size()
+        file = io.BytesIO()
+        torch.save(list(pair), file)
+        file.seek(0)
+        assert all(torch.equal(p, q) for p, q in zip(torch.load(file), pair))
+        keep = b.clone()
+        a.resize_(2 * T, a.shape[1]).zero_()
+        assert torch.equal(b, keep)

@@ -106,31 +106,6 @@ at::Tensor empty(int64_t rows, int64_t cols, at::ScalarType dt, const at::Device
   return at::Tensor(at::detail::empty_cuda({rows, cols}, dt, dev, std::nullopt));
 }
 
-// Two [rows, cols] outputs.  Small ones lie in one allocation, 512 bytes apart at least: an allocation and its release
-// cost 1.4 us of host time, a third of a small call.  Large ones have their own, so that each can be freed by itself.
-void empty_pair(int64_t rows, int64_t cols, at::ScalarType da, at::ScalarType db, const at::Device& dev, at::Tensor* a,
-                at::Tensor* b) {
-  constexpr int64_t kShared = 1 << 20;
-  const int64_t size_a = rows * cols * static_cast<int64_t>(c10::elementSize(da));
-  const int64_t size_b = rows * cols * static_cast<int64_t>(c10::elementSize(db));
-  const int64_t at_b = (size_a + 511) / 512 * 512;
-  if (at_b + size_b > kShared || size_a == 0) {
-    *a = empty(rows, cols, da, dev);
-    *b = empty(rows, cols, db, dev);
-    return;
-  }
-  const at::TensorBase both = at::detail::empty_cuda({at_b + size_b}, at::kByte, dev, std::nullopt);
-  const auto view = [&](at::ScalarType dt, int64_t offset) {
-    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(both.storage()), both.key_set(),
-                                                            c10::scalarTypeToTypeMeta(dt));
-    t.unsafeGetTensorImpl()->set_storage_offset(offset / static_cast<int64_t>(c10::elementSize(dt)));
-    t.unsafeGetTensorImpl()->set_sizes_contiguous({rows, cols});
-    return t;
-  };
-  *a = view(da, 0);
-  *b = view(db, at_b);
-}
-
 int64_t as_int(PyObject* o) {
   const long long v = PyLong_AsLongLong(o);
   if (v == -1 && PyErr_Occurred()) throw Bad{nullptr, ""};
@@ -204,8 +179,7 @@ PyObject* py_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* bias = vec(a[2], "bias", dev, l.cols, at::kFloat, at::kFloat, nullptr);
     const c10::cuda::CUDAGuard guard(dev);
     const int64_t cols = k > 0 ? k : 0;
-    at::Tensor ids, w;
-    empty_pair(l.rows, cols, at::kInt, at::kFloat, dev, &ids, &w);
+    at::Tensor ids = empty(l.rows, cols, at::kInt, dev), w = empty(l.rows, cols, at::kFloat, dev);
     check(moe_route_grouped_topk(l.p, dtype_id(l.dtype), l.ld, l.rows, l.cols, k, as_i32(a[3]),
                                  static_cast<const float*>(bias), as_i32(a[4]), as_i32(a[5]), as_i32(a[6]),
                                  as_bool(a[7]), as_float(a[8]), static_cast<int32_t*>(ids.data_ptr()),
@@ -268,13 +242,11 @@ PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Mat out[2];
     PyObject* res[2] = {Py_None, Py_None};
     static const char* const out_names[2] = {"h", "y"};
-    if (as_bool(a[13]) && as_bool(a[14]) && a[15] == Py_None && a[16] == Py_None)
-      empty_pair(T, H, rdt, f.dtype, dev, &made[0], &made[1]);
     for (int i = 0; i < 2; ++i) {
       if (!as_bool(a[13 + i])) continue;
       const at::ScalarType dt = i ? f.dtype : rdt;
       if (a[15 + i] == Py_None) {
-        if (!made[i].defined()) made[i] = empty(T, H, dt, dev);
+        made[i] = empty(T, H, dt, dev);
         out[i].p = made[i].data_ptr();
         out[i].ld = H > 1 ? H : 1;
       } else {
