@@ -12,7 +12,9 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -61,43 +63,70 @@ def build_shared(srcs, out, deps, extra=(), jobs=None) -> str:
 
 
 def _torch_paths():
-    """(root of the installed torch, its C++ ABI flag), read without importing it where that is not needed."""
+    """(root of the installed torch, its C++ ABI flag, its version)."""
     import torch
-    return os.path.dirname(torch.__file__), int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.dirname(torch.__file__), int(torch._C._GLIBCXX_USE_CXX11_ABI), torch.__version__
+
+
+def _torch_ops_headers() -> bool:
+    """Whether the headers that the Python extension needs are installed (the CUDA library needs none of them)."""
+    root = os.path.join(_torch_paths()[0], "include", "torch", "csrc")
+    return (os.path.exists(os.path.join(root, "autograd", "python_variable.h"))
+            and os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")))
+
+
+def _run_if_stale(cmd, out, deps, stamp) -> str:
+    """Runs cmd to make `out`, unless it is there, newer than deps, and made by this command with this stamp (which
+    stands for what cmd does not name: the versions of torch and Python)."""
+    key, told = "\n".join(cmd + [stamp]), out + ".cmd"
+    if os.path.exists(out) and os.path.exists(told) and os.path.getmtime(out) >= _newest(deps):
+        with open(told) as f:
+            if f.read() == key:
+                return out
+    os.makedirs(LIBDIR, exist_ok=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {out}:\n{r.stdout}\n{r.stderr}")
+    with open(told, "w") as f:
+        f.write(key)
+    return out
+
+
+def _stamp() -> str:
+    return f"torch {_torch_paths()[2]}, python {sys.version}"
 
 
 def _compile_torch_ops() -> str:
     """The object of the Python extension (host code only; the toolkit's headers come from nvcc's own root)."""
     src, obj = os.path.join(CSRC, "torch_ops.cpp"), os.path.join(LIBDIR, "torch_ops.o")
-    deps = [src] + glob.glob(os.path.join(ROOT, "include", "*.h"))
-    if os.path.exists(obj) and os.path.getmtime(obj) >= _newest(deps):
-        return obj
-    os.makedirs(LIBDIR, exist_ok=True)
-    root, abi = _torch_paths()
+    root, abi, _ = _torch_paths()
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "include")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
            "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"), "-isystem",
            os.path.join(root, "include", "torch", "csrc", "api", "include"), "-isystem", cuda, "-c", src, "-o", obj]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
-    return obj
+    return _run_if_stale(cmd, obj, [src] + glob.glob(os.path.join(ROOT, "include", "*.h")), _stamp())
 
 
 def _link_torch_ops(obj: str) -> str:
-    if not (os.path.exists(EXT) and os.path.getmtime(EXT) >= max(os.path.getmtime(obj), os.path.getmtime(LIB))):
-        lib = os.path.join(_torch_paths()[0], "lib")
-        cmd = ["g++", "-shared", "-o", EXT, obj, "-L" + LIBDIR, "-lw4a8moe", "-L" + lib, "-lc10", "-lc10_cuda",
-               "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    return EXT
+    lib = os.path.join(_torch_paths()[0], "lib")
+    cmd = ["g++", "-shared", "-o", EXT, obj, "-L" + LIBDIR, "-lw4a8moe", "-L" + lib, "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    return _run_if_stale(cmd, EXT, [obj, LIB], _stamp())
 
 
 def build() -> str:
+    """The CUDA library, which needs nvcc alone, and the Python extension beside it.  Where torch's or Python's headers are
+    not installed the extension is left out with a warning: the C ABI and the calls that ctypes makes need none, and the
+    calls that it makes raise."""
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     deps = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
+    if not _torch_ops_headers():
+        warnings.warn("torch's or Python's headers are missing: block_norm, dense_linear and moe_route_grouped_topk are "
+                      "built for the C ABI only, not for Python")
+        for stale in (EXT, EXT + ".cmd"):
+            if os.path.exists(stale):
+                os.remove(stale)
+        return build_shared(srcs, LIB, deps)
     with cf.ThreadPoolExecutor(max_workers=1) as ex:  # beside nvcc's own jobs
         obj = ex.submit(_compile_torch_ops)
         lib = build_shared(srcs, LIB, deps)
