@@ -332,12 +332,13 @@ int w4a8_test_wait_timeout(uint64_t limit_ns, int* gave_up, void* stream);
 int w4a8_test_tile_list_limit(int max_tiles);
 
 /*
- * Test of dense_linear's configurations: calls with more than 16 rows normally pick a tile and a number of K
- * pieces from an estimate of their times.  This call asks for the configuration with `rows` x rows to a tile
- * (256, 128, 64 or 32) and `pieces` of K (256: 1, 2 or 4; 128: 1, 2 or 4; 64 and 32: 1, 2, 4 or 8) for the calls
- * that follow, process-wide (rows = 0: the estimate again, the default); a call with fewer 64-element blocks of
- * K than pieces keeps to the estimate.  Configurations differ in the order of their fp32 sums only.  Returns
- * W4A8_OK; a configuration that does not exist makes those calls return W4A8_ERR_UNSUPPORTED.
+ * Test of dense_linear's configurations: calls with more than 16 rows, and those with fewer whose aligned weights are
+ * large (from 12 MiB for 9 to 16 rows, from 24 MiB for up to 8 when gated), normally pick a tile and a number of K pieces
+ * from an estimate of their times.  This call asks for the configuration with `rows` x rows to a tile (256, 128, 64 or 32)
+ * and `pieces` of K (256: 1, 2 or 4; 128: 1, 2 or 4; 64 and 32: 1, 2, 4 or 8) for those of the calls that follow,
+ * process-wide (rows = 0: the estimate again, the default); a call with fewer 64-element blocks of K than pieces keeps to
+ * the estimate.  Configurations differ in the order of their fp32 sums only.  Returns W4A8_OK; a configuration that does
+ * not exist makes those calls return W4A8_ERR_UNSUPPORTED.
  */
 int w4a8_test_linear_config(int rows, int pieces);
 

@@ -290,3 +290,27 @@ def test_sums_in_pieces_with_a_16_bit_residual(lib, config, dtype, K, gated, opa
     assert lib.device_error() == 0 and torch.equal(got, want.float().to(DT[dtype]))
     lib.dense_linear(x, w, act="relu", gated=gated, residual=r, out=r)
     assert torch.equal(r, got)
+
+
+# few rows: aligned weights from 12 MiB (9 to 16 rows) or 24 MiB (up to 8, gated) leave the streaming kernel for tiles of
+# which most rows do not exist; just below and just above, and the same without alignment
+@pytest.mark.parametrize("M,N,K,gated", [(1, 4096, 7168, True), (1, 1754, 7168, True), (5, 1756, 7168, True),
+                                         (8, 4096, 7168, True), (8, 8192, 4096, False), (9, 1535, 4096, False),
+                                         (9, 1536, 4096, False), (16, 2048, 4096, False), (16, 1024, 6152, True),
+                                         (16, 2050, 4100, True)])
+@pytest.mark.parametrize("dtype,out,residual", [("bf16", "bf16", True), ("bf16", "f32", False), ("f16", "f32", True)])
+def test_few_rows_with_large_weights(lib, M, N, K, gated, dtype, out, residual):
+    _check(lib, M, N, K, dtype=dtype, out=out, gated=gated, act="silu" if gated else "gelu", bias="f32", residual=residual,
+           seed=25)
+
+
+@pytest.mark.parametrize("config", CONFIGS, indirect=True)
+@pytest.mark.parametrize("M", [1, 13])
+def test_few_rows_in_every_configuration(lib, config, M):
+    N, K = (1800, 7168) if M == 1 else (1544, 4160)
+    g = torch.Generator("cuda").manual_seed(26)
+    x, w = _mat(M, K, "bf16", g, ints=True), _mat(N, K, "bf16", g, ints=True)
+    z = x.cpu().double() @ w.cpu().double().t()
+    got = lib.dense_linear(x, w, act="relu", gated=True, out_dtype=torch.float32)
+    assert torch.equal(got.cpu().double(), (z[:, :N // 2].clamp_min(0) * z[:, N // 2:]))
+    assert lib.device_error() == 0
