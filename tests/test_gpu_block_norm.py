@@ -237,3 +237,22 @@ def test_many_short_rows(lib, dtype, rdtype, H):
     # more rows than the warps of the device take in one turn
     _check(lib, 9001, H, dtype=dtype, rdtype=rdtype, post="layer", pre="rms", gate=(9001, 1), bias=True, seed=16)
     _check(lib, 7500, H, dtype=dtype, rdtype=rdtype, post="rms", pre="layer", gate=(1, H), pad=8, alias=True, seed=17)
+
+
+@pytest.mark.parametrize("T,H", [(1, 4096), (64, 1003), (2048, 4096), (1500, 1003)])
+def test_graph(lib, T, H):
+    g = torch.Generator("cuda").manual_seed(18)
+    f, r = (torch.randn((T, H), device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    want = lib.block_norm(f, r, post="rms", pre="layer")
+    given = torch.zeros_like(f)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        lib.block_norm(given, r, post="rms", pre="layer")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            got = lib.block_norm(given, r, post="rms", pre="layer")
+        given.copy_(f)
+        graph.replay()
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -221,3 +221,49 @@ def test_groups_of_two_with_infinite_logits(lib):
     l[2, :] = [3e38, -3e38, 0, 0, 3e38, 3e38, 0, 0, 1, 1, 1, 1]
     ids, _ = _run(lib, l, 2, score="softmax", n_group=3, topk_group=1, group_top=2)
     assert ids.tolist() == [[4, 5], [8, 9], [4, 5]]
+
+
+@pytest.mark.parametrize("T,E,k,kw,with_bias", [
+    (20011, 64, 4, dict(score="sigmoid", n_group=8, topk_group=4, group_top=2), True),        # 8 lanes to a token
+    (10003, 160, 6, dict(score="softmax", n_group=8, topk_group=3, renormalize=False), False),  # 16
+    (10003, 96, 12, dict(score="sigmoid", n_group=4, topk_group=3, group_top=2), False),
+    (5107, 256, 8, dict(score="sigmoid", n_group=8, topk_group=4, group_top=2, scale=2.5), True),  # 32
+    (5107, 454, 6, dict(score="softmax"), False),
+    (5107, 384, 8, dict(score="sigmoid"), True),
+])
+def test_more_tokens_than_the_device_holds(lib, T, E, k, kw, with_bias):
+    # every warp walks through several tokens: the first, some in between and the last against the definition, all of them
+    # against calls that are too short for that
+    rng = np.random.default_rng(E)
+    x = torch.randn((T, E), device="cuda", generator=torch.Generator("cuda").manual_seed(E)) * 2
+    bias = rng.standard_normal(E).astype(np.float32) * 0.1 if with_bias else None
+    dev_bias = None if bias is None else torch.from_numpy(bias).cuda()
+    ids, w = lib.moe_route_grouped_topk(x, k, bias=dev_bias, **kw)
+    for at in range(0, T, 2000):
+        i, v = lib.moe_route_grouped_topk(x[at:at + 2000], k, bias=dev_bias, **kw)
+        assert torch.equal(i, ids[at:at + 2000]) and torch.equal(v, w[at:at + 2000])
+    rows = np.r_[0:100, T // 2:T // 2 + 50, T - 250:T]
+    rid, rw, gap = ref.route(x.cpu().numpy()[rows], k, bias=bias, **kw)
+    far = gap > 2e-6  # as above
+    assert far.mean() > 0.4
+    assert np.array_equal(ids.cpu().numpy()[rows][far], rid[far])
+    assert np.all(np.abs(w.cpu().double().numpy()[rows][far] - rw[far]) <= 64 * 2.0 ** -24 * rw[far] + 1e-37)
+
+
+@pytest.mark.parametrize("T", [1, 40, 6000])
+def test_other_stream_and_graph(lib, T):
+    x = torch.randn((T, 256), device="cuda", generator=torch.Generator("cuda").manual_seed(2))
+    kw = dict(n_group=8, topk_group=4, group_top=2)
+    want = lib.moe_route_grouped_topk(x, 8, **kw)
+    given = torch.zeros_like(x)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        lib.moe_route_grouped_topk(given, 8, **kw)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            got = lib.moe_route_grouped_topk(given, 8, **kw)
+        given.copy_(x)
+        graph.replay()
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
