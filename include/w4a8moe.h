@@ -479,7 +479,7 @@ typedef enum {
  *   logits [T][ld] fp32, bf16 or f16 (ld >= E)   bias fp32 [E] or NULL
  *   topk_ids int32 [T][k]   topk_w fp32 [T][k]
  *   1 <= E <= 1024, 1 <= n_group <= 32 dividing E, 1 <= topk_group <= n_group,
- *   group_top <= E / n_group, 1 <= k <= min(32, topk_group * E / n_group), T >= 0.
+ *   group_top <= E / n_group, 1 <= k <= min(32, topk_group * E / n_group), 0 <= T < 2^26.
  */
 int moe_route_grouped_topk(const void* logits, int logits_dtype, int64_t ld, int64_t T, int64_t E, int k, int score,
                            const float* bias, int n_group, int topk_group, int group_top, int renormalize,
@@ -501,7 +501,7 @@ int moe_route_grouped_topk(const void* logits, int logits_dtype, int64_t ld, int
  *   gate [gate_rows][gate_cols] of `gate_dtype` (dtype or fp32) or NULL (1): gate_rows
  *     divides T and token t uses gate row t / (T / gate_rows); gate_cols is H or 1.
  *   w_post, b_post, w_pre, b_pre [H] of `param_dtype` (dtype or fp32), each may be NULL.
- *   1 <= H <= 32768.  h may be the residual's and y may be f's own memory (same
+ *   0 <= T < 2^31, 1 <= H <= 32768.  h may be the residual's and y may be f's own memory (same
  *   row stride); no other overlap.
  */
 int block_norm(const void* f, int64_t ldf, int dtype, const void* residual, int64_t ldr, int residual_dtype, int post,

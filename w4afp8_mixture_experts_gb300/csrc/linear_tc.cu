@@ -1331,9 +1331,10 @@ std::atomic<int> g_force{0};
 // stage: what a stage takes where memory does not bound it, 0.26 us in the pair kernel (its products) and 0.18 to 0.2 us
 // in the split kernel (its loads), or what L2 needs for the stages of all CTAs (12 TB/s for the split kernel; 18 TB/s for
 // the pair kernel, which reads most lines for many CTAs at once).  rate: 6 TB/s of memory, or what the bytes in flight of
-// the CTAs give at 1.2 us of latency.  fixed: launches of one wave extrapolated to no stages.  Measured on a GB300 (M x N
+// the CTAs give at 1.2 us of latency.  fixed: launches of one wave extrapolated to no stages.  Fitted on a GB300 (M x N
 // x K = 64 x 256 x 7168, 64 x 4096 x 7168 and 256 x 4096 x 7168 gated, 128 x 7168 x 2048, 777 x 1001 x 1544,
-// 2048 x 256 x 7168, every configuration).
+// 2048 x 256 x 7168, every configuration); of 24 other shapes it is within 10 % of the best on 22, and at worst 1.35 times
+// it (258 x 3776 x 1536: 12.5 us, 9.3 with tiles of 64 rows).
 template <bool GATED>
 int launch_best(const LinearParams& p, cudaStream_t st) {
   static const Option options[] = {

@@ -1,8 +1,9 @@
 // Grouped expert routing: softmax or sigmoid scores, a balance bias that only takes part in the choice, the
 // best groups of experts, the best experts of those groups, renormalised and scaled weights.
 //
-// The bytes are few (8192 x 256 fp32 logits: 1.3 us); what bounds it is instructions (8192 x 256 sigmoid, 8 groups, k = 8:
-// 11.1 us; 65531 x 160 softmax, k = 6: 30.9 us), so every step is made to cost few of them per token:
+// The bytes are few (8192 x 256 fp32 logits: 1.3 us); what bounds it is instructions and their latency (8192 x 256 sigmoid,
+// 8 groups, k = 8: 11.1 us, 852 a token or 6 us of issue; 65531 x 160 softmax, k = 6: 30.6 us), so every step is made to
+// cost few of them per token:
 //   * a token has S = 8, 16 or 32 lanes of a warp, the fewest that leave a lane few experts: what a step costs across
 //     lanes is then shared by up to four tokens;
 //   * a group's experts lie on LPG = 2^lpg_log of them (the largest power of two with LPG * n_group <= S), EPL
