@@ -521,6 +521,9 @@ int block_norm(const void* f, int64_t ldf, int dtype, const void* residual, int6
  *   and may be out's own memory (same row stride)
  *   bias [N] of `bias_dtype` (dtype or fp32) or NULL
  *   0 <= M, N <= 2^20, 1 <= K <= 2^20.
+ * The tensor core cuts off at each addition to an accumulator, so sums of more
+ * than 1024 products (fp32 output), 16384 (f16) or 131072 (bf16) are added up in
+ * pieces, rounded to nearest.
  * ws: needed only where x or w is not 16-byte aligned in its pointer and row
  * stride (copies of both with aligned rows): dense_linear_workspace_bytes(M, N,
  * K) bytes, 16-byte aligned; otherwise, or where that is 0, NULL will do.
