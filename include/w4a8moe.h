@@ -77,7 +77,8 @@ int w4a8_abi_version(void);
  * (synchronises the device).  Bit 0 (1): a kernel's bounded wait on an
  * mbarrier gave up (W4A8_ERR_TIMEOUT) and that kernel's outputs are invalid.
  * Bit 1 (2): a routed expert id or an expert_map entry was out of range and
- * those pairs were left out.  Bit 2 (4): after such a give-up, waiting for
+ * those pairs were left out; or a page id or a position was out of range for a
+ * paged cache.  Bit 2 (4): after such a give-up, waiting for
  * the GEMM's own in-flight MMAs also ran out of time.  For tests and
  * diagnostics, not for the hot path.
  */
@@ -532,6 +533,121 @@ int dense_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int dty
                  int act, int gated, const void* residual, int64_t ldr, void* out, int64_t ldo, int out_dtype,
                  int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes, void* stream);
 size_t dense_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/*
+ * The attention half of a block: rotary positions, a paged cache of keys and
+ * values, the attention of new tokens over it, and the FP8 projections.  The
+ * conventions above hold.  W4A8_DTYPE_E4M3 below stands for cache elements of 8
+ * bits; no other operator takes it.
+ */
+#define W4A8_DTYPE_E4M3 3
+
+/*
+ * Rotation by position.  Of a head's D elements, R from `start` on form R / 2
+ * pairs (a_i, b_i): elements start + i and start + R / 2 + i, or, interleaved,
+ * start + 2 i and start + 2 i + 1.  At position p
+ *   (a_i, b_i) -> scale * (a_i cos(t) - b_i sin(t), b_i cos(t) + a_i sin(t)),
+ *   t = p * f_i; the other elements stay as they are.
+ * inverse: t = -p * f_i, the transpose of the rotation and so its gradient.
+ * freqs[i] is f_i / (2 pi), turns per position, in units of 2^-64 (modulo whole
+ * turns): p * freqs[i] modulo 2^64 is then the angle's fraction of a turn, exact
+ * for every position.  Frequencies scaled for long contexts are the caller's.
+ */
+typedef struct {
+  const int64_t* freqs;   /* device [R / 2]; NULL: no rotation                       */
+  int64_t R, start;       /* R even, start >= 0, start + R <= D                     */
+  int interleaved, inverse;
+  float scale;            /* finite                                                  */
+  const void* positions;  /* device [T], int32 or int64, any sign                    */
+  int positions64;        /* whether they are int64                                  */
+} w4a8_rotary;
+
+/*
+ * (11) Rotary positions: out[t][h] = x[t][h] rotated at positions[t].
+ *   x, out [T][H][D] of `dtype` (bf16, f16, fp32): element d of head h of token t at
+ *   t * ld_t + h * ld_h + d.  out may be x with the same strides; no other overlap.
+ *   1 <= D <= 1024, T * H < 2^31.
+ */
+int rotary_embedding(const void* x, int64_t ldx_t, int64_t ldx_h, int dtype, int64_t T, int64_t H, int64_t D,
+                     const w4a8_rotary* rotary /* host pointer */, void* out, int64_t ldo_t, int64_t ldo_h,
+                     void* stream);
+
+/*
+ * A paged cache of B sequences.  Position p of sequence b lies in page
+ * page_table[b * table_ld + p / page_size], slot p % page_size; element d of its
+ * head h at page * k_page + slot * k_slot + h * k_head + d (strides in elements, any
+ * order of the dimensions, D contiguous).  With E4M3 a key is its code times
+ * k_scale[h], a value its code times v_scale[h] (NULL: 1).
+ * Entries of the page table that no position of seq_lens[b] reaches are not read.
+ * A page id outside [0, pages), or a position behind the table's last page, sets
+ * the device error word (code 2): nothing is stored there, and such a key and value
+ * read as zeros.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t k_page, k_slot, k_head, v_page, v_slot, v_head;
+  int dtype;                                          /* W4A8_DTYPE_BF16, F16 or E4M3 */
+  int64_t pages, page_size, heads, D;                 /* pages < 2^31, page_size <= 2^20 */
+  const int32_t* page_table;                          /* [B][table_ld], device          */
+  int64_t table_ld, table_pages;                      /* table_pages * page_size < 2^31 */
+  const int32_t* seq_lens;                            /* [B], device                    */
+  int64_t B;
+  const float* k_scale;                               /* [heads] or NULL, device        */
+  const float* v_scale;
+} w4a8_paged_cache;
+
+/*
+ * (12) Appends keys and values to a paged cache, keys rotated on the way.
+ * Row t < indptr[B] is a token of the sequence b with indptr[b] <= t < indptr[b + 1]
+ * (indptr int32 [B + 1], not decreasing, from 0; NULL: T = B and one token each), at
+ * position seq_lens[b] - (indptr[b + 1] - t): seq_lens counts the new tokens.  A row of a
+ * negative position or behind indptr[B] is left out (a padded batch).
+ *   k, v [T][heads][D] of `dtype` (bf16 or f16; a 16-bit cache has the same type)
+ *   rotary: positions NULL takes the cache position; rotary NULL, or freqs NULL: none.
+ *   E4M3: code = e4m3(x / scale) in fp32, to nearest even, saturating.
+ *   q [T][Hq][D] of `dtype`, or NULL: rotated like the keys, rounded once, into q_out
+ *   (which may be q, with the same strides); rows that are left out keep what q_out has.
+ * Two rows for one slot (pages shared by sequences) race.  1 <= D <= 1024,
+ * T * (Hq + 2 * heads) < 2^31.
+ */
+int paged_kv_append(const void* k, int64_t ldk_t, int64_t ldk_h, const void* v, int64_t ldv_t, int64_t ldv_h, int dtype,
+                    int64_t T, const int32_t* indptr, const w4a8_paged_cache* cache /* host pointer */,
+                    const w4a8_rotary* rotary /* host pointer */, const void* q, int64_t ldq_t, int64_t ldq_h,
+                    int64_t Hq, void* q_out, int64_t ldqo_t, int64_t ldqo_h, void* stream);
+
+/*
+ * (13) Attention of one new token per sequence over a paged cache:
+ *   s_p = scale * q[b][h] . K[b][p][h / (Hq / heads)],  p in [lo, seq_lens[b])
+ *   lo = max(0, seq_lens[b] - window), or 0 when window = 0
+ *   out[b][h] = sum_p softmax(s)_p V[b][p][..],  lse[b][h] = log sum_p exp(s_p)
+ * A sequence without positions (seq_lens[b] <= 0) gives zeros and -inf.  Nothing outside
+ * the positions named is read.  Scores, softmax and sums are fp32; the weights are taken
+ * to the values' product in two pieces of 16 bits (16-bit caches) or in f16 (E4M3).
+ *   q [B][Hq][D] of `dtype` (bf16 or f16; a 16-bit cache has the same type), element d of
+ *   head h of sequence b at b * ldq_b + h * ldq_h + d; out likewise; lse fp32 [B][Hq] or NULL
+ *   D: a multiple of 8 (of 16 with E4M3) up to 256; the cache's pointers and strides are
+ *   multiples of 16 bytes.  Hq a multiple of heads, Hq / heads <= 256, B * heads < 2^24.
+ *   ws: paged_attention_workspace_bytes() bytes, 16-byte aligned; its contents on entry do
+ *   not matter.
+ */
+int paged_attention_decode(const void* q, int64_t ldq_b, int64_t ldq_h, int dtype, int64_t Hq,
+                           const w4a8_paged_cache* cache /* host pointer */, float scale, int64_t window, void* out,
+                           int64_t ldo_b, int64_t ldo_h, float* lse, void* ws, size_t ws_bytes, void* stream);
+size_t paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t D);
+
+/*
+ * (14) FP8 Linear with a scale per block of 128:
+ *   out[m][n] = sum_g a_scales[g][m] * b_scales[n / 128][g] * sum_{k in g} e4m3(A[m][k]) e4m3(B[n][k])
+ * over the groups g of 128 k; sums of a group on the tensor core, across groups in fp32.
+ *   A [M][K] E4M3 codes, a_scales fp32 [K/128][lda_s] (as the quantisation calls write them)
+ *   B [N][K] E4M3 codes, b_scales fp32 [ceil(N/128)][K/128] (a scale per 128 x 128 weights)
+ *   out [M][ldo] of `out_dtype` (bf16, f16 or fp32)
+ *   K % 128 == 0, 0 <= M, N <= 2^20, 128 <= K <= 2^20, lda_s >= M and lda_s % 4 == 0; A, B and
+ *   a_scales 16-byte aligned.
+ */
+int fp8_block_linear(const uint8_t* A, const float* a_scales, int64_t lda_s, const uint8_t* B, const float* b_scales,
+                     int64_t M, int64_t N, int64_t K, void* out, int64_t ldo, int out_dtype, void* stream);
 
 #ifdef __cplusplus
 }

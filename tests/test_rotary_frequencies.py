@@ -1,0 +1,61 @@
+"""rotary_frequencies: turns per position in units of 2^-64 (no GPU)."""
+import math
+
+import pytest
+
+from w4afp8_mixture_experts_gb300 import rotary_frequencies, rotary_yarn_scale
+
+
+def _radians(t):
+    return [2 * math.pi * v * 2.0 ** -64 for v in t.tolist()]
+
+
+def _close(a, b):
+    # a fraction of a turn has 64 bits: 2 pi 2^-64 radians, beside fp64 roundings
+    return all(abs(x - y) <= 1e-15 * abs(y) + 4e-19 for x, y in zip(a, b)) and len(a) == len(b)
+
+
+@pytest.mark.parametrize("dim", [2, 64, 128])
+def test_plain_and_linear(dim):
+    want = [10000.0 ** (-2 * i / dim) for i in range(dim // 2)]
+    assert _close(_radians(rotary_frequencies(dim, device="cpu")), want)
+    assert _close(_radians(rotary_frequencies(dim, scaling="linear", factor=8.0, device="cpu")), [w / 8 for w in want])
+
+
+def test_ntk():
+    base = 5e5 * 4.0 ** (64 / 62)
+    want = [base ** (-2 * i / 64) for i in range(32)]
+    assert _close(_radians(rotary_frequencies(64, 5e5, scaling="ntk", factor=4.0, device="cpu")), want)
+
+
+def test_yarn_keeps_fast_and_divides_slow():
+    got = _radians(rotary_frequencies(64, scaling="yarn", factor=40.0, length=4096, device="cpu"))
+    plain = [10000.0 ** (-2 * i / 64) for i in range(32)]
+    for f, p in zip(got, plain):
+        turns = p * 4096 / (2 * math.pi)
+        # the ramp begins and ends at whole pairs, which lie 10000^(2 / 64) = 1.334 apart: at most 32 * 1.334 = 42.7 turns
+        # and at least 1 / 1.334 = 0.75
+        if turns > 42.7:
+            assert _close([f], [p])
+        elif turns < 0.74:
+            assert _close([f], [p / 40])
+        else:
+            assert p / 40 * (1 - 1e-12) <= f <= p * (1 + 1e-12)
+    assert rotary_yarn_scale(40.0) == pytest.approx(0.1 * math.log(40) + 1) and rotary_yarn_scale(1.0) == 1.0
+
+
+def test_given_frequencies_keep_whole_turns_out():
+    f = [0.5, 4.0, -1.0, 7.0]  # 7 radians are a turn and more, -1 a turn backwards
+    got = rotary_frequencies(8, inv_freq=f, device="cpu")
+    for t, v in zip(got.tolist(), f):
+        a = 2 * math.pi * t * 2.0 ** -64
+        assert abs(math.sin(a - v)) <= 1e-15 * 8 and math.cos(a - v) > 0
+
+
+@pytest.mark.parametrize("kw", [dict(dim=3), dict(dim=0), dict(dim=8, scaling="cubic"), dict(dim=8, factor=0.0),
+                                dict(dim=8, base=1.0), dict(dim=2, scaling="ntk"), dict(dim=8, inv_freq=[1.0]),
+                                dict(dim=4, inv_freq=[1.0, math.inf]), dict(dim=8, length=0),
+                                dict(dim=8, factor=math.nan)])
+def test_refusals(kw):
+    with pytest.raises(ValueError):
+        rotary_frequencies(device="cpu", **kw)

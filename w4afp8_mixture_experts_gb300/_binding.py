@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import math
 import os
 
 import torch
@@ -71,6 +72,16 @@ _SIGS = {
     "dense_linear": (_c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_int, _c_vp, _c_int, _c_int, _c_int, _c_vp, _c_i64,
                               _c_vp, _c_i64, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_sz, _c_vp]),
     "dense_linear_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64]),
+    "rotary_embedding": (_c_int, [_c_vp, _c_i64, _c_i64, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64,
+                                  _c_vp]),
+    "paged_kv_append": (_c_int, [_c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64, _c_int, _c_i64, _c_vp, _c_vp, _c_vp,
+                                 _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp]),
+    "paged_attention_decode": (_c_int, [_c_vp, _c_i64, _c_i64, _c_int, _c_i64, _c_vp, _c_f32, _c_i64, _c_vp, _c_i64,
+                                        _c_i64, _c_vp, _c_vp, _c_sz, _c_vp]),
+    "paged_attention_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i64]),
+    "fp8_block_linear": (_c_int, [_c_vp, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_int,
+                                  _c_vp]),
+    "w4a8_test_fp8_linear_config": (_c_int, [_c_int, _c_int]),
     "w4a8_test_linear_config": (_c_int, [_c_int, _c_int]),
     "w4a8_test_linear_wait": (_c_int, [_c_int, ctypes.c_uint64, _c_vp, _c_vp]),
 }
@@ -81,6 +92,21 @@ class MoeLayout(ctypes.Structure):
                                                "xq", "xs", "xc", "y13", "hq", "hs", "hc", "y2",
                                                "permute_ws")] + \
                [("scale_ld", ctypes.c_int64), ("total", ctypes.c_size_t)]
+
+
+class Rotary(ctypes.Structure):
+    """w4a8_rotary of the C ABI."""
+    _fields_ = [("freqs", _c_vp), ("R", _c_i64), ("start", _c_i64), ("interleaved", _c_int), ("inverse", _c_int),
+                ("scale", _c_f32), ("positions", _c_vp), ("positions64", _c_int)]
+
+
+class PagedCache(ctypes.Structure):
+    """w4a8_paged_cache of the C ABI."""
+    _fields_ = [("k", _c_vp), ("v", _c_vp)] + \
+               [(n, _c_i64) for n in ("k_page", "k_slot", "k_head", "v_page", "v_slot", "v_head")] + \
+               [("dtype", _c_int)] + [(n, _c_i64) for n in ("pages", "page_size", "heads", "D")] + \
+               [("page_table", _c_vp), ("table_ld", _c_i64), ("table_pages", _c_i64), ("seq_lens", _c_vp),
+                ("B", _c_i64), ("k_scale", _c_vp), ("v_scale", _c_vp)]
 
 
 _lib = None
@@ -512,6 +538,100 @@ def dense_linear(x, w, bias=None, act: str = "none", gated: bool = False, residu
 def dense_linear_workspace_bytes(M: int, N: int, K: int) -> int:
     """Workspace of dense_linear where x or w is not 16-byte aligned (0: none)."""
     return int(load().dense_linear_workspace_bytes(M, N, K))
+
+
+# --- the attention half of a block ------------------------------------------------------------------------------
+
+_SCALINGS = ("none", "linear", "ntk", "yarn")
+
+
+def rotary_frequencies(dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+                       length: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, inv_freq=None, device=None):
+    """The frequencies that rotary_embedding and paged_kv_append take, int64 [dim / 2]: turns per position in units of
+    2^-64, made once per model.
+
+    f_i = base^(-2 i / dim) radians per position (or inv_freq, a sequence of dim / 2 numbers), scaled for contexts
+    `factor` times longer than the `length` that a model was trained on: "linear" divides all by factor, "ntk" takes
+    base * factor^(dim / (dim - 2)), "yarn" divides those with fewer than beta_slow turns over `length`, keeps those
+    with more than beta_fast, and blends in between (its factor on the rotated values is rotary_yarn_scale)."""
+    if dim < 2 or dim % 2:
+        raise ValueError(f"dim must be even and positive, got {dim}")
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}, got {scaling!r}")
+    if not (factor > 0 and math.isfinite(factor)) or not (base > 1 and math.isfinite(base)) or length < 1:
+        raise ValueError("factor and length must be positive and base above 1")
+    half = dim // 2
+    if inv_freq is not None:
+        f = [float(v) for v in inv_freq]
+        if len(f) != half or not all(math.isfinite(v) for v in f):
+            raise ValueError(f"inv_freq must have {half} finite numbers")
+    else:
+        if scaling == "ntk":
+            if dim == 2:
+                raise ValueError("ntk scaling needs dim above 2")
+            base = base * factor ** (dim / (dim - 2))
+        f = [base ** (-2.0 * i / dim) for i in range(half)]
+    if scaling == "linear":
+        f = [v / factor for v in f]
+    elif scaling == "yarn":
+        def pair_of(turns):  # the pair that makes this many turns over `length`
+            return dim * math.log(length / (turns * 2 * math.pi)) / (2 * math.log(base))
+        lo, hi = max(math.floor(pair_of(beta_fast)), 0), min(math.ceil(pair_of(beta_slow)), dim - 1)
+        keep = [1.0 - min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0) for i in range(half)]
+        f = [v / factor * (1.0 - k) + v * k for v, k in zip(f, keep)]
+    turns = [int(math.fmod(v / (2 * math.pi), 1.0) * 2.0 ** 64) for v in f]
+    turns = [(t + 2 ** 63) % 2 ** 64 - 2 ** 63 for t in turns]
+    return torch.tensor(turns, dtype=torch.int64, device="cuda" if device is None else device)
+
+
+def rotary_yarn_scale(factor: float, mscale: float = 1.0) -> float:
+    """The factor on rotated queries and keys that goes with yarn frequencies: 0.1 mscale ln(factor) + 1."""
+    return 1.0 if factor <= 1 else 0.1 * mscale * math.log(factor) + 1.0
+
+
+def rotary_embedding(x, positions, freqs, *, interleaved: bool = False, start: int = 0, scale: float = 1.0,
+                     inverse: bool = False, out=None):
+    """x [T, H, D] bf16, f16 or fp32 (any strides, D contiguous) rotated at positions [T] (int32 or int64): elements
+    start ... start + 2 len(freqs) of each head in pairs (i, i + len(freqs)), or neighbours when interleaved, by the
+    angle position * f_i, times scale; the others as they are.  freqs from rotary_frequencies.  inverse turns back (the
+    transpose: the gradient with respect to x of a result's gradient).  out may be x."""
+    return (_ops or _load_ops()).rotary(x, positions, freqs, interleaved, start, scale, inverse, out)
+
+
+def paged_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, indptr=None, *, freqs=None, positions=None,
+                    interleaved: bool = False, start: int = 0, scale: float = 1.0, k_scale=None, v_scale=None, q=None,
+                    q_out=None):
+    """Writes k, v [T, Hkv, D] (bf16 or f16) into the caches [pages, page_size, Hkv, D] (that type or float8_e4m3fn, any
+    strides, D contiguous), keys rotated as in rotary_embedding when freqs is given, at the cache position or at
+    positions [T].  Rows indptr[b] ... indptr[b + 1] are the last tokens of sequence b, whose length seq_lens[b] (int32
+    [B]) counts them; indptr None: one token each.  page_table int32 [B, n].  Rows behind indptr[B], or of a sequence of
+    length 0, are left out.  k_scale, v_scale fp32 [Hkv]: an 8-bit cache holds x / scale.
+    q [T, Hq, D] is rotated like the keys into q_out (made when None; may be q) and returned."""
+    return (_ops or _load_ops()).append(k, v, k_cache, v_cache, page_table, seq_lens, indptr, freqs, positions,
+                                        interleaved, start, scale, k_scale, v_scale, q, q_out)
+
+
+def paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, *, scale=None, window: int = 0, k_scale=None,
+                           v_scale=None, return_lse: bool = False, out=None, ws=None):
+    """Attention of one new token per sequence, q [B, Hq, D] (bf16 or f16), over its seq_lens[b] tokens in a paged cache
+    (see paged_kv_append; Hq a multiple of Hkv, D a multiple of 8 up to 256, of 16 with 8-bit caches).  scale defaults
+    to D^-0.5; window > 0 sees the last `window` tokens only.  Returns out [B, Hq, D] of q's type, with return_lse
+    (out, fp32 [B, Hq] log-sums of the exponentials); an empty sequence gives zeros and -inf.  ws is a uint8 workspace
+    of paged_attention_workspace_bytes(B, Hq, Hkv, D) bytes (made when None)."""
+    return (_ops or _load_ops()).attend(q, k_cache, v_cache, page_table, seq_lens, scale, window, k_scale, v_scale,
+                                        return_lse, out, ws)
+
+
+def paged_attention_workspace_bytes(B: int, Hq: int, Hkv: int, D: int) -> int:
+    """Workspace of paged_attention_decode on the current device."""
+    return int(load().paged_attention_workspace_bytes(B, Hq, Hkv, D))
+
+
+def fp8_block_linear(A, a_scales, B, b_scales, *, out_dtype=None, out=None):
+    """A [M, K] times B [N, K]^T in E4M3 (uint8 codes or float8_e4m3fn), K a multiple of 128: a_scales fp32 [K/128, ld]
+    per token and 128 columns, as fp8_quant_per_token_group writes them, b_scales fp32 [ceil(N/128), K/128] per 128 x
+    128 weights -> [M, N] of out_dtype (bf16 by default, f16 or fp32)."""
+    return (_ops or _load_ops()).fp8_linear(A, a_scales, B, b_scales, out_dtype, out)
 
 
 def device_error() -> int:

@@ -1,0 +1,426 @@
+// rotary_embedding and paged_kv_append: rows of heads moved, and rotated by position on the way.
+//
+// Both are one kernel over rows (token, head): the heads of a token are its queries, then (append) its keys and its
+// values.  A block takes a run of neighbouring rows.  Each thread asks for its first vectors of them, the block works out
+// where its tokens go and the cosines and sines of their angles once for all heads, and then the vectors are turned and
+// stored.  Bound by memory; the angles of a token cost R / 2 sincospif and are shared by its heads.
+//
+// An angle is a fraction of a turn: position * freqs modulo 2^64 is the exact remainder of the product by whole turns,
+// and its upper 32 bits as a signed number are half-turns in [-1, 1) in units of 2^-31.  In fp32 they are within 2^-25
+// half-turns of the angle, 1e-7, whatever the position.
+#include <algorithm>
+
+#include "paged.cuh"
+
+namespace w4a8 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kAhead = 4;     // items of a thread asked for before the angles are known
+constexpr int kMaxCs = 2048;  // cosine and sine pairs of a block's tokens
+constexpr int kMaxTok = 64;   // tokens of a block
+
+__device__ unsigned int g_paged_error;
+
+struct RowParams {
+  const void *q, *k, *v;
+  void *qo, *kc, *vc;
+  int64_t q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h;
+  int64_t k_page, k_slot, k_head, v_page, v_slot, v_head;
+  const int32_t *table, *lens, *indptr;
+  int64_t table_ld, pages;
+  const void* positions;
+  const int64_t* freqs;
+  const float *k_scale, *v_scale;
+  int64_t rows;  // T * heads of a token
+  int T, B, Hq, Hkv, D, R, start, table_pages;
+  int rot_items, items;  // of a row: those with pairs to turn, all of them
+  int rows_per_block;
+  FastDiv by_items, by_heads, by_page, by_half;
+  float cos_scale, sin_scale;
+  bool interleaved, positions64;
+};
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+  T e[V];
+};
+
+template <typename TC>
+__device__ __forceinline__ TC to_cache(float v, float scale);
+template <>
+__device__ __forceinline__ __nv_bfloat16 to_cache(float v, float) { return from_f32<__nv_bfloat16>(v); }
+template <>
+__device__ __forceinline__ __half to_cache(float v, float) { return from_f32<__half>(v); }
+template <>
+__device__ __forceinline__ float to_cache(float v, float) { return v; }
+template <>
+__device__ __forceinline__ uint8_t to_cache(float v, float scale) {
+  return static_cast<uint8_t>(e4m3x2(__fdiv_rn(v, scale), 0.f) & 0xFF);
+}
+
+// Where the two vectors of an item lie in its row; the second may be missing (-1).
+// Turned items: V elements of the first halves of the pairs and V of the second ones, or V pairs of neighbours.
+// Others: two neighbouring vectors of the elements that stay.
+template <int V>
+__device__ __forceinline__ void places(const RowParams& p, int item, bool value, int& e0, int& e1) {
+  if (value) {
+    e0 = 2 * V * item;
+    e1 = e0 + V < p.D ? e0 + V : -1;
+    if (e0 >= p.D) e0 = -1;
+  } else if (item < p.rot_items) {
+    e0 = p.start + (p.interleaved ? 2 : 1) * V * item;
+    e1 = e0 + (p.interleaved ? V : p.R / 2);
+  } else {
+    const int at = 2 * V * (item - p.rot_items);
+    e0 = at < p.start ? at : at + p.R;
+    e1 = at + V < p.start ? at + V : at + V + p.R;
+    if (e1 >= p.D) e1 = -1;
+    if (e0 >= p.D) e0 = -1;
+  }
+}
+
+template <typename T, typename TC, int V>
+__device__ __forceinline__ void store_vec(TC* to, const float (&f)[V], float scale) {
+  Vec<TC, V> o;
+#pragma unroll
+  for (int j = 0; j < V; ++j) o.e[j] = to_cache<TC>(f[j], scale);
+  *reinterpret_cast<Vec<TC, V>*>(to) = o;
+}
+
+template <typename T, typename TC, int V, bool APPEND>
+__global__ void __launch_bounds__(kThreads) rotary_rows_kernel(const __grid_constant__ RowParams p) {
+  __shared__ float2 cs[kMaxCs];
+  __shared__ int64_t at_k[APPEND ? kMaxTok : 1], at_v[APPEND ? kMaxTok : 1];
+  __shared__ int at_pos[APPEND ? kMaxTok : 1];
+  __shared__ int first_seq;
+  const int heads = p.Hq + 2 * p.Hkv;  // of a token
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_block;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(p.rows_per_block), p.rows - r0));
+  const int tok0 = static_cast<int>(r0 / heads), in0 = static_cast<int>(r0 - static_cast<int64_t>(tok0) * heads);
+  const int toks = p.by_heads.div(in0 + rows - 1) + 1, count = rows * p.items;
+  const int tid = threadIdx.x;
+  pdl_trigger();
+  if (APPEND && tid == 0) first_seq = 0;
+  pdl_wait();
+
+  // the item `idx` of this block: its token (in the block), head, place in the row
+  auto item_at = [&](int idx, int& tok, int& head, int& item) {
+    const int row = p.by_items.div(idx, item);
+    tok = p.by_heads.div(in0 + row, head);
+  };
+  auto load = [&](int idx, Vec<T, V>& a, Vec<T, V>& b) {
+    int tok, head, item, e0, e1;
+    item_at(idx, tok, head, item);
+    places<V>(p, item, head >= p.Hq + p.Hkv, e0, e1);
+    const int64_t t = tok0 + tok;
+    const T* src = head < p.Hq            ? static_cast<const T*>(p.q) + t * p.q_t + head * p.q_h
+                   : head < p.Hq + p.Hkv  ? static_cast<const T*>(p.k) + t * p.k_t + (head - p.Hq) * p.k_h
+                                          : static_cast<const T*>(p.v) + t * p.v_t + (head - p.Hq - p.Hkv) * p.v_h;
+    if (e0 >= 0) a = *reinterpret_cast<const Vec<T, V>*>(src + e0);
+    if (e1 >= 0) b = *reinterpret_cast<const Vec<T, V>*>(src + e1);
+  };
+  Vec<T, V> a[kAhead], b[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (tid + u * kThreads < count) load(tid + u * kThreads, a[u], b[u]);
+
+  if constexpr (APPEND) {
+    if (p.indptr) {  // the sequence of the block's first token: how many end before it
+      __syncthreads();
+      int before = 0;
+      for (int j = 1 + tid; j <= p.B; j += kThreads) before += p.indptr[j] <= tok0;
+      before = __reduce_add_sync(0xffffffffu, before);
+      if ((tid & 31) == 0 && before) atomicAdd(&first_seq, before);
+      __syncthreads();
+    }
+    if (tid < toks) {
+      const int t = tok0 + tid;
+      int seq = t, end = t + 1;
+      bool in = t < p.B;
+      if (p.indptr) {
+        seq = first_seq;
+        while (seq < p.B && p.indptr[seq + 1] <= t) ++seq;
+        in = seq < p.B && p.indptr[seq] <= t;
+        if (in) end = p.indptr[seq + 1];
+      }
+      const int pos = in ? p.lens[seq] - (end - t) : -1;
+      int64_t place = -1;
+      int slot = 0;
+      if (pos >= 0) {
+        const int page = p.by_page.div(pos, slot);
+        if (page < p.table_pages) place = p.table[seq * p.table_ld + page];
+        if (place < 0 || place >= p.pages) {
+          atomicOr(&g_paged_error, 2u);
+          place = -1;
+        }
+      }
+      at_pos[tid] = pos;
+      at_k[tid] = place < 0 ? -1 : place * p.k_page + slot * p.k_slot;
+      at_v[tid] = place * p.v_page + slot * p.v_slot;
+    }
+    __syncthreads();
+  }
+  const int half = p.R / 2;
+  for (int i = tid; i < toks * half; i += kThreads) {
+    int f;
+    const int tok = p.by_half.div(i, f);
+    int64_t pos = 0;
+    if (p.positions)
+      pos = p.positions64 ? static_cast<const int64_t*>(p.positions)[tok0 + tok]
+                          : static_cast<const int32_t*>(p.positions)[tok0 + tok];
+    else if (APPEND)
+      pos = at_pos[tok];
+    const uint64_t turns = static_cast<uint64_t>(pos) * static_cast<uint64_t>(p.freqs[f]);
+    float s, c;
+    sincospif(static_cast<float>(static_cast<int32_t>(turns >> 32)) * 4.656612873e-10f, &s, &c);  // 2^-31
+    cs[i] = make_float2(c * p.cos_scale, s * p.sin_scale);
+  }
+  __syncthreads();
+
+  auto finish = [&](int idx, const Vec<T, V>& va, const Vec<T, V>& vb) {
+    int tok, head, item, e0, e1;
+    item_at(idx, tok, head, item);
+    const bool value = head >= p.Hq + p.Hkv, query = head < p.Hq;
+    places<V>(p, item, value, e0, e1);
+    float x[V], y[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      x[j] = e0 >= 0 ? to_f32(va.e[j]) : 0.f;
+      y[j] = e1 >= 0 ? to_f32(vb.e[j]) : 0.f;
+    }
+    if (!value && item < p.rot_items) {
+      const float2* t = cs + tok * half + item * V;
+      if (p.interleaved) {
+        float z[2 * V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) z[j] = x[j], z[V + j] = y[j];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float2 w = t[j];
+          const float r = z[2 * j] * w.x - z[2 * j + 1] * w.y, i = z[2 * j + 1] * w.x + z[2 * j] * w.y;
+          z[2 * j] = r;
+          z[2 * j + 1] = i;
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = z[j], y[j] = z[V + j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float2 w = t[j];
+          const float r = x[j] * w.x - y[j] * w.y, i = y[j] * w.x + x[j] * w.y;
+          x[j] = r;
+          y[j] = i;
+        }
+      }
+    }
+    const int64_t t = tok0 + tok;
+    if (!APPEND || query) {
+      if (APPEND && at_pos[tok] < 0) return;  // a row that belongs to no sequence
+      T* to = static_cast<T*>(p.qo) + t * p.o_t + head * p.o_h;
+      if (e0 >= 0) store_vec<T, T, V>(to + e0, x, 1.f);
+      if (e1 >= 0) store_vec<T, T, V>(to + e1, y, 1.f);
+      return;
+    }
+    if constexpr (APPEND) {
+      if (at_k[tok] < 0) return;
+      const int h = head - p.Hq - (value ? p.Hkv : 0);
+      TC* to = value ? static_cast<TC*>(p.vc) + at_v[tok] + h * p.v_head : static_cast<TC*>(p.kc) + at_k[tok] + h * p.k_head;
+      const float* scales = value ? p.v_scale : p.k_scale;
+      const float scale = scales ? scales[h] : 1.f;
+      if (e0 >= 0) store_vec<T, TC, V>(to + e0, x, scale);
+      if (e1 >= 0) store_vec<T, TC, V>(to + e1, y, scale);
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (tid + u * kThreads < count) finish(tid + u * kThreads, a[u], b[u]);
+  for (int idx = tid + kAhead * kThreads; idx < count; idx += kThreads) {
+    load(idx, a[0], b[0]);
+    finish(idx, a[0], b[0]);
+  }
+}
+
+template <typename T, typename TC, int V, bool APPEND>
+int launch_rows(RowParams p, cudaStream_t st) {
+  const int heads = p.Hq + 2 * p.Hkv, half = p.R / 2;
+  p.rot_items = half / V;
+  p.items = p.rot_items + static_cast<int>(ceil_div(p.D - p.R, 2 * V));
+  p.by_items = FastDiv(p.items);
+  p.by_heads = FastDiv(heads);
+  p.by_half = FastDiv(half > 0 ? half : 1);
+  // Rows of a block: what its threads ask for at once, fewer where that leaves SMs idle, and no more tokens than have room.
+  const int tokens = std::min(kMaxTok, half > 0 ? kMaxCs / half : kMaxTok);
+  int64_t rows = std::max<int64_t>(1, kAhead * kThreads / p.items);
+  rows = std::min(rows, ceil_div(p.rows, 2 * num_sms()));
+  rows = std::min(rows, static_cast<int64_t>(tokens - 1) * heads + 1);  // rows from anywhere in a token touch no more
+  p.rows_per_block = static_cast<int>(std::max<int64_t>(1, rows));
+  return launch_pdl("rotary_rows_kernel", rotary_rows_kernel<T, TC, V, APPEND>,
+                    dim3(static_cast<unsigned>(ceil_div(p.rows, p.rows_per_block))), dim3(kThreads), 0, st, p);
+}
+
+// Rows in vectors of 16 bytes, 8 bytes or single elements: the widest that every start, stride and part of a head allows.
+template <typename T, typename TC, bool APPEND>
+int launch_vec(const RowParams& p, uint64_t starts_t, uint64_t starts_c, uint64_t elems, cudaStream_t st) {
+  constexpr int kFull = 16 / sizeof(T), kHalf = 8 / sizeof(T);
+  const auto fits = [&](int v) {
+    return starts_t % (v * sizeof(T)) == 0 && starts_c % (v * sizeof(TC)) == 0 && elems % v == 0;
+  };
+  if (fits(kFull)) return launch_rows<T, TC, kFull, APPEND>(p, st);
+  if (fits(kHalf)) return launch_rows<T, TC, kHalf, APPEND>(p, st);
+  return launch_rows<T, TC, 1, APPEND>(p, st);
+}
+
+uint64_t bits_of(const void* q) { return static_cast<uint64_t>(reinterpret_cast<uintptr_t>(q)); }
+
+// A gcd by powers of two of everything that a vector's width has to divide: the lowest set bit of the union of the bits.
+uint64_t lowest(uint64_t bits) { return bits ? bits & (~bits + 1) : 1ull << 32; }
+
+int check_rotary(const w4a8_rotary* r, int64_t D, bool needs_positions) {
+  if (!r || !r->freqs) return W4A8_OK;
+  W4A8_REQUIRE(r->R >= 0 && r->R % 2 == 0 && r->start >= 0 && r->start + r->R <= D,
+               "R=%lld must be even and start=%lld + R at most D=%lld", (long long)r->R, (long long)r->start, (long long)D);
+  W4A8_REQUIRE(r->scale - r->scale == 0.f, "scale must be finite");
+  W4A8_REQUIRE(!needs_positions || r->positions, "null pointer: positions");
+  W4A8_REQUIRE(bits_of(r->freqs) % 8 == 0 && bits_of(r->positions) % (r->positions64 ? 8 : 4) == 0,
+               "freqs and positions must be aligned to their element size");
+  return W4A8_OK;
+}
+
+void set_rotary(RowParams& p, const w4a8_rotary* r) {
+  if (!r || !r->freqs) return;  // p.R stays 0: nothing is turned
+  p.R = static_cast<int>(r->R);
+  p.start = static_cast<int>(r->start);
+  p.freqs = r->freqs;
+  p.positions = r->positions;
+  p.positions64 = r->positions64 != 0;
+  p.interleaved = r->interleaved != 0;
+  p.cos_scale = r->scale;
+  p.sin_scale = r->inverse ? -r->scale : r->scale;
+}
+
+int read_paged_error() {
+  unsigned int v = 0;
+  cudaMemcpyFromSymbol(&v, g_paged_error, sizeof(v));
+  const unsigned int zero = 0;
+  cudaMemcpyToSymbol(g_paged_error, &zero, sizeof(zero));
+  return static_cast<int>(v);
+}
+
+struct Registrar {
+  Registrar() { register_device_error_reader(&read_paged_error); }
+} registrar;
+
+}  // namespace
+}  // namespace w4a8
+
+extern "C" int rotary_embedding(const void* x, int64_t ldx_t, int64_t ldx_h, int dtype, int64_t T, int64_t H, int64_t D,
+                                const w4a8_rotary* rotary, void* out, int64_t ldo_t, int64_t ldo_h, void* stream) {
+  using namespace w4a8;
+  W4A8_REQUIRE(dtype >= W4A8_DTYPE_BF16 && dtype <= W4A8_DTYPE_F32, "dtype=%d must be bf16, f16 or fp32", dtype);
+  W4A8_REQUIRE(D >= 1 && D <= 1024, "D=%lld must be in [1, 1024]", (long long)D);
+  W4A8_REQUIRE(T >= 0 && H >= 0 && T < (1ll << 31) && H < (1ll << 31) && T * H < (1ll << 31),
+               "T=%lld times H=%lld must be below 2^31", (long long)T, (long long)H);
+  W4A8_REQUIRE(ldx_t >= 0 && ldx_h >= 0 && ldo_t >= 0 && ldo_h >= 0, "strides must not be negative");
+  W4A8_REQUIRE(rotary && rotary->freqs, "null pointer: rotary, freqs");
+  if (T == 0 || H == 0) return W4A8_OK;
+  if (int rc = check_rotary(rotary, D, true)) return rc;
+  W4A8_REQUIRE(x && out, "null pointer");
+  const uint64_t size = dtype_size(dtype);
+  W4A8_REQUIRE((bits_of(x) | bits_of(out)) % size == 0, "x and out must be aligned to their element size");
+  RowParams p = {};
+  set_rotary(p, rotary);
+  p.q = x;
+  p.qo = out;
+  p.q_t = ldx_t;
+  p.q_h = ldx_h;
+  p.o_t = ldo_t;
+  p.o_h = ldo_h;
+  p.T = static_cast<int>(T);
+  p.Hq = static_cast<int>(H);
+  p.D = static_cast<int>(D);
+  p.rows = T * H;
+  const uint64_t starts = lowest(bits_of(x) | bits_of(out) | (T > 1 ? (ldx_t | ldo_t) * size : 0) |
+                                 (H > 1 ? (ldx_h | ldo_h) * size : 0));
+  const uint64_t elems = lowest(static_cast<uint64_t>(p.D | p.start | p.R / 2));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == W4A8_DTYPE_F32) return launch_vec<float, float, false>(p, starts, starts, elems, st);
+  if (dtype == W4A8_DTYPE_F16) return launch_vec<__half, __half, false>(p, starts, starts, elems, st);
+  return launch_vec<__nv_bfloat16, __nv_bfloat16, false>(p, starts, starts, elems, st);
+}
+
+extern "C" int paged_kv_append(const void* k, int64_t ldk_t, int64_t ldk_h, const void* v, int64_t ldv_t, int64_t ldv_h,
+                               int dtype, int64_t T, const int32_t* indptr, const w4a8_paged_cache* cache,
+                               const w4a8_rotary* rotary, const void* q, int64_t ldq_t, int64_t ldq_h, int64_t Hq,
+                               void* q_out, int64_t ldqo_t, int64_t ldqo_h, void* stream) {
+  using namespace w4a8;
+  if (int rc = check_cache(cache, dtype)) return rc;
+  const int64_t D = cache->D, H = cache->heads;
+  W4A8_REQUIRE(D >= 1 && D <= 1024, "D=%lld must be in [1, 1024]", (long long)D);
+  W4A8_REQUIRE(Hq >= 0 && Hq < (1 << 16) && (q || Hq == 0), "Hq=%lld must be in [0, 2^16), and 0 without q", (long long)Hq);
+  W4A8_REQUIRE(T >= 0 && T < (1ll << 31) && T * (Hq + 2 * H) < (1ll << 31), "T=%lld rows of %lld heads: below 2^31",
+               (long long)T, (long long)(Hq + 2 * H));
+  W4A8_REQUIRE(indptr || T == cache->B, "T=%lld must be B=%lld without indptr", (long long)T, (long long)cache->B);
+  W4A8_REQUIRE(bits_of(indptr) % 4 == 0, "indptr must be aligned to 4 bytes");
+  W4A8_REQUIRE(ldk_t >= 0 && ldk_h >= 0 && ldv_t >= 0 && ldv_h >= 0 && ldq_t >= 0 && ldq_h >= 0 && ldqo_t >= 0 && ldqo_h >= 0,
+               "strides must not be negative");
+  if (int rc = check_rotary(rotary, D, false)) return rc;
+  if (T == 0 || cache->B == 0) return W4A8_OK;
+  W4A8_REQUIRE(k && v && cache->seq_lens && (!q || Hq == 0 || q_out), "null pointer");
+  W4A8_REQUIRE(cache->table_pages == 0 || cache->page_table, "null pointer: page_table");
+  W4A8_REQUIRE(cache->pages == 0 || (cache->k && cache->v), "null pointer: k and v of the cache");
+  const bool fp8 = cache->dtype == W4A8_DTYPE_E4M3;
+  const uint64_t size = 2, csize = fp8 ? 1 : 2;
+  const uint64_t qs = q && Hq ? bits_of(q) | bits_of(q_out) : 0;
+  W4A8_REQUIRE((bits_of(k) | bits_of(v) | qs) % size == 0 && (bits_of(cache->k) | bits_of(cache->v)) % csize == 0,
+               "k, v, q, q_out and the cache must be aligned to their element size");
+  RowParams p = {};
+  p.cos_scale = p.sin_scale = 1.f;
+  set_rotary(p, rotary);
+  p.q = q;
+  p.qo = q_out;
+  p.k = k;
+  p.v = v;
+  p.kc = cache->k;
+  p.vc = cache->v;
+  p.q_t = ldq_t;
+  p.q_h = ldq_h;
+  p.o_t = ldqo_t;
+  p.o_h = ldqo_h;
+  p.k_t = ldk_t;
+  p.k_h = ldk_h;
+  p.v_t = ldv_t;
+  p.v_h = ldv_h;
+  p.k_page = cache->k_page;
+  p.k_slot = cache->k_slot;
+  p.k_head = cache->k_head;
+  p.v_page = cache->v_page;
+  p.v_slot = cache->v_slot;
+  p.v_head = cache->v_head;
+  p.table = cache->page_table;
+  p.table_ld = cache->table_ld;
+  p.table_pages = static_cast<int>(cache->table_pages);
+  p.pages = cache->pages;
+  p.lens = cache->seq_lens;
+  p.indptr = indptr;
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.by_page = FastDiv(cache->page_size);
+  p.T = static_cast<int>(T);
+  p.B = static_cast<int>(cache->B);
+  p.Hq = q ? static_cast<int>(Hq) : 0;
+  p.Hkv = static_cast<int>(H);
+  p.D = static_cast<int>(D);
+  p.rows = T * (p.Hq + 2 * H);
+  const uint64_t starts = lowest(bits_of(k) | bits_of(v) | qs | (ldk_t | ldk_h | ldv_t | ldv_h) * size |
+                                 (qs ? (ldq_t | ldq_h | ldqo_t | ldqo_h) * size : 0));
+  const uint64_t places = lowest(bits_of(cache->k) | bits_of(cache->v) |
+                                 (p.k_page | p.k_slot | p.k_head | p.v_page | p.v_slot | p.v_head) * csize);
+  const uint64_t elems = lowest(static_cast<uint64_t>(p.D | p.start | p.R / 2));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == W4A8_DTYPE_F16)
+    return fp8 ? launch_vec<__half, uint8_t, true>(p, starts, places, elems, st)
+               : launch_vec<__half, __half, true>(p, starts, places, elems, st);
+  return fp8 ? launch_vec<__nv_bfloat16, uint8_t, true>(p, starts, places, elems, st)
+             : launch_vec<__nv_bfloat16, __nv_bfloat16, true>(p, starts, places, elems, st);
+}

@@ -1,4 +1,4 @@
-// Python entry of the operators around the routed experts: tensor checks, output tensors and the current stream in
+// Python entry of the operators around the routed experts and of the attention half: tensor checks, output tensors and the current stream in
 // C++, then one call of the C ABI.  The same marshalling in Python cost 19-28 us a call (five tensors, 20 to 28
 // ctypes arguments), several times what the smallest of these operators take on the device.
 //
@@ -14,6 +14,9 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <array>
+#include <cmath>
 #include <cstdint>
 #include <string>
 
@@ -340,6 +343,313 @@ PyObject* py_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// --- the attention half ----------------------------------------------------------------------------------------
+
+// heads [rows][heads][D] with contiguous D and any strides
+struct Heads {
+  const void* p = nullptr;
+  int64_t rows = 0, heads = 0, D = 0, ld_t = 0, ld_h = 0;
+  at::ScalarType dtype = at::kFloat;
+};
+
+// Whether two places of a tensor that is written may be one: its dimensions, by stride, each step over all that is inside.
+template <size_t N>
+bool overlaps(std::array<std::pair<int64_t, int64_t>, N> dims, int64_t inner) {  // (stride, size), innermost extent
+  std::sort(dims.begin(), dims.end());
+  int64_t reach = inner;  // places that the dimensions so far cover
+  for (const auto& d : dims) {
+    if (d.second <= 1) continue;
+    if (d.first < reach) return true;
+    reach = d.first * (d.second - 1) + reach;
+  }
+  return false;
+}
+
+Heads heads_of(const at::Tensor& t, const char* name, const at::Device& dev, bool written) {
+  need_device(t, name, dev);
+  if (t.dim() != 3) value_error(std::string(name) + " must have 3 dimensions");
+  Heads h;
+  h.rows = t.size(0);
+  h.heads = t.size(1);
+  h.D = t.size(2);
+  if (h.D > 1 && t.stride(2) != 1) value_error(std::string(name) + " must have contiguous heads");
+  h.ld_t = h.rows > 1 ? t.stride(0) : 0;
+  h.ld_h = h.heads > 1 ? t.stride(1) : 0;
+  if (written && t.numel() > 0 && overlaps<2>({{{h.ld_t, h.rows}, {h.ld_h, h.heads}}}, h.D))
+    value_error(std::string(name) + " has overlapping heads");
+  h.p = t.data_ptr();
+  h.dtype = t.scalar_type();
+  return h;
+}
+void need_shape(const Heads& h, const char* name, int64_t rows, int64_t heads, int64_t D) {
+  if (h.rows != rows || h.heads != heads || h.D != D)
+    value_error(std::string(name) + " must have shape (" + std::to_string(rows) + ", " + std::to_string(heads) + ", " +
+                std::to_string(D) + "), got (" + std::to_string(h.rows) + ", " + std::to_string(h.heads) + ", " +
+                std::to_string(h.D) + ")");
+}
+
+at::Tensor empty3(int64_t a, int64_t b, int64_t c, at::ScalarType dt, const at::Device& dev) {
+  return at::Tensor(at::detail::empty_cuda({a, b, c}, dt, dev, std::nullopt));
+}
+
+// an optional rotation; returns whether there is one
+bool rotary_of(PyObject* freqs, PyObject* positions, PyObject* interleaved, PyObject* start, PyObject* scale,
+               const at::Device& dev, int64_t rows, w4a8_rotary* r) {
+  *r = w4a8_rotary{};
+  if (freqs == Py_None) {
+    if (positions != Py_None) value_error("positions given without freqs");
+    return false;
+  }
+  const at::Tensor& f = cuda_tensor(freqs, "freqs");
+  need_device(f, "freqs", dev);
+  need_dtype(f, "freqs", at::kLong, at::kLong);
+  if (f.dim() != 1 || !f.is_contiguous()) value_error("freqs must be a contiguous vector");
+  r->freqs = static_cast<const int64_t*>(f.data_ptr());
+  r->R = 2 * f.size(0);
+  r->start = as_int(start);
+  r->interleaved = as_bool(interleaved);
+  r->scale = as_float(scale);
+  if (r->R == 0) value_error("freqs must not be empty");
+  if (positions != Py_None) {
+    at::ScalarType dt = at::kInt;
+    r->positions = vec(positions, "positions", dev, rows, at::kInt, at::kLong, &dt);
+    r->positions64 = dt == at::kLong;
+  }
+  return true;
+}
+
+// k_cache, v_cache [pages, page_size, heads, D] of one type, page_table [B, n], seq_lens [B], scales [heads]
+w4a8_paged_cache cache_of(PyObject* k, PyObject* v, PyObject* table, PyObject* lens, PyObject* k_scale, PyObject* v_scale,
+                          const at::Device& dev, at::ScalarType dtype, bool written) {
+  w4a8_paged_cache c = {};
+  const at::Tensor& kt = cuda_tensor(k, "k_cache");
+  const at::Tensor& vt = cuda_tensor(v, "v_cache");
+  const at::Tensor* both[2] = {&kt, &vt};
+  static const char* const names[2] = {"k_cache", "v_cache"};
+  int64_t strides[2][3];
+  for (int i = 0; i < 2; ++i) {
+    const at::Tensor& t = *both[i];
+    need_device(t, names[i], dev);
+    need_dtype(t, names[i], dtype, at::kFloat8_e4m3fn);
+    if (t.dim() != 4) value_error(std::string(names[i]) + " must have 4 dimensions");
+    if (i && (t.sizes() != kt.sizes() || t.scalar_type() != kt.scalar_type()))
+      value_error("v_cache must have k_cache's shape and type, got " + shape_of(t) + " and " + shape_of(kt));
+    if (t.size(3) > 1 && t.stride(3) != 1) value_error(std::string(names[i]) + " must have contiguous heads");
+    for (int d = 0; d < 3; ++d) strides[i][d] = t.size(d) > 1 ? t.stride(d) : 0;
+    if (written && t.numel() > 0 &&
+        overlaps<3>({{{strides[i][0], t.size(0)}, {strides[i][1], t.size(1)}, {strides[i][2], t.size(2)}}}, t.size(3)))
+      value_error(std::string(names[i]) + " has overlapping heads");
+  }
+  c.k = kt.data_ptr();
+  c.v = vt.data_ptr();
+  c.k_page = strides[0][0], c.k_slot = strides[0][1], c.k_head = strides[0][2];
+  c.v_page = strides[1][0], c.v_slot = strides[1][1], c.v_head = strides[1][2];
+  c.pages = kt.size(0);
+  c.page_size = kt.size(1);
+  c.heads = kt.size(2);
+  c.D = kt.size(3);
+  c.dtype = kt.scalar_type() == at::kFloat8_e4m3fn ? W4A8_DTYPE_E4M3 : dtype_id(kt.scalar_type());
+  const at::Tensor& tt = cuda_tensor(table, "page_table");
+  need_dtype(tt, "page_table", at::kInt, at::kInt);
+  const Mat m = mat(tt, "page_table", dev);
+  c.page_table = static_cast<const int32_t*>(m.p);
+  c.table_ld = m.ld;
+  c.table_pages = m.cols;
+  c.B = m.rows;
+  c.seq_lens = static_cast<const int32_t*>(vec(lens, "seq_lens", dev, c.B, at::kInt, at::kInt, nullptr));
+  if (!c.seq_lens && c.B > 0) type_error("seq_lens must be a CUDA tensor");
+  c.k_scale = static_cast<const float*>(vec(k_scale, "k_scale", dev, c.heads, at::kFloat, at::kFloat, nullptr));
+  c.v_scale = static_cast<const float*>(vec(v_scale, "v_scale", dev, c.heads, at::kFloat, at::kFloat, nullptr));
+  return c;
+}
+
+// (x, positions, freqs, interleaved, start, scale, inverse, out) -> out
+PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> PyObject* {
+    const at::Tensor& xt = cuda_tensor(a[0], "x");
+    const at::Device dev = xt.device();
+    const Heads x = heads_of(xt, "x", dev, false);
+    if (dtype_id(x.dtype) < 0) type_error(std::string("x must be bf16, f16 or fp32, got ") + dtype_name(x.dtype));
+    cuda_tensor(a[1], "positions");
+    cuda_tensor(a[2], "freqs");
+    w4a8_rotary r;
+    rotary_of(a[2], a[1], a[3], a[4], a[5], dev, x.rows, &r);
+    r.inverse = as_bool(a[6]);
+    const c10::cuda::CUDAGuard guard(dev);
+    at::Tensor made;
+    Heads o;
+    if (a[7] == Py_None) {
+      made = empty3(x.rows, x.heads, x.D, x.dtype, dev);
+      o = heads_of(made, "out", dev, false);
+    } else {
+      const at::Tensor& ot = cuda_tensor(a[7], "out");
+      need_dtype(ot, "out", x.dtype, x.dtype);
+      o = heads_of(ot, "out", dev, true);
+      need_shape(o, "out", x.rows, x.heads, x.D);
+    }
+    check(rotary_embedding(x.p, x.ld_t, x.ld_h, dtype_id(x.dtype), x.rows, x.heads, x.D, &r, const_cast<void*>(o.p), o.ld_t,
+                           o.ld_h, c10::cuda::getCurrentCUDAStream(dev.index()).stream()));
+    return made.defined() ? THPVariable_Wrap(std::move(made)) : Py_NewRef(a[7]);
+  });
+}
+
+// (k, v, k_cache, v_cache, page_table, seq_lens, indptr, freqs, positions, interleaved, start, scale, k_scale, v_scale,
+//  q, q_out) -> q_out
+PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 16, [&]() -> PyObject* {
+    const at::Tensor& kt = cuda_tensor(a[0], "k");
+    const at::Device dev = kt.device();
+    need_dtype(kt, "k", at::kBFloat16, at::kHalf);
+    const Heads k = heads_of(kt, "k", dev, false);
+    const at::Tensor& vt = cuda_tensor(a[1], "v");
+    need_dtype(vt, "v", k.dtype, k.dtype);
+    const Heads v = heads_of(vt, "v", dev, false);
+    need_shape(v, "v", k.rows, k.heads, k.D);
+    const w4a8_paged_cache c = cache_of(a[2], a[3], a[4], a[5], a[12], a[13], dev, k.dtype, true);
+    if (c.heads != k.heads || c.D != k.D)
+      value_error("k_cache must have heads and head size (" + std::to_string(k.heads) + ", " + std::to_string(k.D) +
+                  "), got (" + std::to_string(c.heads) + ", " + std::to_string(c.D) + ")");
+    const int32_t* indptr =
+        static_cast<const int32_t*>(vec(a[6], "indptr", dev, c.B + 1, at::kInt, at::kInt, nullptr));
+    if (!indptr && k.rows != c.B)
+      value_error("k must have " + std::to_string(c.B) + " rows without indptr, got " + std::to_string(k.rows));
+    w4a8_rotary r;
+    rotary_of(a[7], a[8], a[9], a[10], a[11], dev, k.rows, &r);
+    const c10::cuda::CUDAGuard guard(dev);
+    at::Tensor made;
+    Heads q, o;
+    if (a[14] != Py_None) {
+      const at::Tensor& qt = cuda_tensor(a[14], "q");
+      need_dtype(qt, "q", k.dtype, k.dtype);
+      q = heads_of(qt, "q", dev, false);
+      need_shape(q, "q", k.rows, q.heads, k.D);
+      if (a[15] == Py_None) {
+        made = empty3(q.rows, q.heads, q.D, q.dtype, dev);
+        o = heads_of(made, "q_out", dev, false);
+      } else {
+        const at::Tensor& ot = cuda_tensor(a[15], "q_out");
+        need_dtype(ot, "q_out", k.dtype, k.dtype);
+        o = heads_of(ot, "q_out", dev, true);
+        need_shape(o, "q_out", q.rows, q.heads, q.D);
+      }
+    } else if (a[15] != Py_None) {
+      value_error("q_out given without q");
+    }
+    check(paged_kv_append(k.p, k.ld_t, k.ld_h, v.p, v.ld_t, v.ld_h, dtype_id(k.dtype), k.rows, indptr, &c, &r, q.p, q.ld_t,
+                          q.ld_h, q.heads, const_cast<void*>(o.p), o.ld_t, o.ld_h,
+                          c10::cuda::getCurrentCUDAStream(dev.index()).stream()));
+    return made.defined() ? THPVariable_Wrap(std::move(made)) : Py_NewRef(a[15]);
+  });
+}
+
+// (q, k_cache, v_cache, page_table, seq_lens, scale, window, k_scale, v_scale, return_lse, out, ws) -> out or (out, lse)
+PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> PyObject* {
+    const at::Tensor& qt = cuda_tensor(a[0], "q");
+    const at::Device dev = qt.device();
+    need_dtype(qt, "q", at::kBFloat16, at::kHalf);
+    const Heads q = heads_of(qt, "q", dev, false);
+    const w4a8_paged_cache c = cache_of(a[1], a[2], a[3], a[4], a[7], a[8], dev, q.dtype, false);
+    if (c.B != q.rows)
+      value_error("page_table must have " + std::to_string(q.rows) + " rows, got " + std::to_string(c.B));
+    if (c.D != q.D)
+      value_error("q must have heads of " + std::to_string(c.D) + " elements, got " + std::to_string(q.D));
+    const float scale = a[5] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(q.D))) : as_float(a[5]);
+    const c10::cuda::CUDAGuard guard(dev);
+    at::Tensor made, lse, room;
+    Heads o;
+    if (a[10] == Py_None) {
+      made = empty3(q.rows, q.heads, q.D, q.dtype, dev);
+      o = heads_of(made, "out", dev, false);
+    } else {
+      const at::Tensor& ot = cuda_tensor(a[10], "out");
+      need_dtype(ot, "out", q.dtype, q.dtype);
+      o = heads_of(ot, "out", dev, true);
+      need_shape(o, "out", q.rows, q.heads, q.D);
+    }
+    if (as_bool(a[9])) lse = empty(q.rows, q.heads, at::kFloat, dev);
+    void* ws = nullptr;
+    int64_t ws_bytes = 0;
+    if (a[11] != Py_None) {
+      const at::Tensor& t = cuda_tensor(a[11], "ws");
+      need_device(t, "ws", dev);
+      need_dtype(t, "ws", at::kByte, at::kByte);
+      if (!t.is_contiguous()) value_error("ws must be contiguous");
+      ws = t.data_ptr();
+      ws_bytes = t.numel();
+    } else {
+      ws_bytes = static_cast<int64_t>(paged_attention_workspace_bytes(c.B, q.heads, c.heads, c.D));
+      if (ws_bytes) {
+        room = empty(1, ws_bytes, at::kByte, dev);
+        ws = room.data_ptr();
+      }
+    }
+    check(paged_attention_decode(q.p, q.ld_t, q.ld_h, dtype_id(q.dtype), q.heads, &c, scale, as_int(a[6]),
+                                 const_cast<void*>(o.p), o.ld_t, o.ld_h,
+                                 lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, ws,
+                                 static_cast<size_t>(ws_bytes), c10::cuda::getCurrentCUDAStream(dev.index()).stream()));
+    PyObject* po = made.defined() ? THPVariable_Wrap(std::move(made)) : Py_NewRef(a[10]);
+    if (!po || !lse.defined()) return po;
+    PyObject* pl = THPVariable_Wrap(std::move(lse));
+    PyObject* r = pl ? PyTuple_Pack(2, po, pl) : nullptr;
+    Py_DECREF(po);
+    Py_XDECREF(pl);
+    return r;
+  });
+}
+
+// a contiguous matrix of E4M3 codes, as bytes or as float8_e4m3fn
+Mat codes(PyObject* o, const char* name, const at::Device& dev) {
+  const at::Tensor& t = cuda_tensor(o, name);
+  need_dtype(t, name, at::kByte, at::kFloat8_e4m3fn);
+  const Mat m = mat(t, name, dev);
+  if (!t.is_contiguous()) value_error(std::string(name) + " must be contiguous");
+  return m;
+}
+
+// (A, a_scales, B, b_scales, out_dtype, out) -> out
+PyObject* py_fp8_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 6, [&]() -> PyObject* {
+    const at::Device dev = cuda_tensor(a[0], "A").device();
+    const Mat A = codes(a[0], "A", dev), B = codes(a[2], "B", dev);
+    if (B.cols != A.cols)
+      value_error("B must have " + std::to_string(A.cols) + " columns, got " + std::to_string(B.cols));
+    const int64_t M = A.rows, N = B.rows, K = A.cols, G = K / 128;
+    const at::Tensor& at_ = cuda_tensor(a[1], "a_scales");
+    need_dtype(at_, "a_scales", at::kFloat, at::kFloat);
+    const Mat as = mat(at_, "a_scales", dev);
+    if (as.rows != G || as.cols < M)
+      value_error("a_scales must have shape (" + std::to_string(G) + ", at least " + std::to_string(M) + "), got " +
+                  shape_of(at_));
+    const at::Tensor& bt = cuda_tensor(a[3], "b_scales");
+    need_dtype(bt, "b_scales", at::kFloat, at::kFloat);
+    const Mat bs = mat(bt, "b_scales", dev);
+    need_shape(bs, "b_scales", (N + 127) / 128, G);
+    if (!bt.is_contiguous()) value_error("b_scales must be contiguous");
+    at::ScalarType odt = at::kBFloat16;
+    as_dtype(a[4], "out_dtype", &odt);
+    if (dtype_id(odt) < 0) type_error(std::string("out_dtype must be bf16, f16 or fp32, got ") + dtype_name(odt));
+    const c10::cuda::CUDAGuard guard(dev);
+    at::Tensor made;
+    Mat o;
+    if (a[5] == Py_None) {
+      made = empty(M, N, odt, dev);
+      o.p = made.data_ptr();
+      o.ld = N > 1 ? N : 1;
+    } else {
+      const at::Tensor& ot = cuda_tensor(a[5], "out");
+      need_dtype(ot, "out", odt, odt);
+      o = mat(ot, "out", dev);
+      need_shape(o, "out", M, N);
+    }
+    check(fp8_block_linear(static_cast<const uint8_t*>(A.p), static_cast<const float*>(as.p), as.ld,
+                           static_cast<const uint8_t*>(B.p), static_cast<const float*>(bs.p), M, N, K,
+                           const_cast<void*>(o.p), o.ld, dtype_id(odt),
+                           c10::cuda::getCurrentCUDAStream(dev.index()).stream()));
+    return made.defined() ? THPVariable_Wrap(std::move(made)) : Py_NewRef(a[5]);
+  });
+}
+
 template <class F>
 PyCFunction as_cfunction(F f) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
@@ -350,6 +660,10 @@ PyMethodDef methods[] = {
     {"route", as_cfunction(py_route), METH_FASTCALL, nullptr},
     {"norm", as_cfunction(py_norm), METH_FASTCALL, nullptr},
     {"linear", as_cfunction(py_linear), METH_FASTCALL, nullptr},
+    {"rotary", as_cfunction(py_rotary), METH_FASTCALL, nullptr},
+    {"append", as_cfunction(py_append), METH_FASTCALL, nullptr},
+    {"attend", as_cfunction(py_attend), METH_FASTCALL, nullptr},
+    {"fp8_linear", as_cfunction(py_fp8_linear), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 
