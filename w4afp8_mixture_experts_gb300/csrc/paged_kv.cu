@@ -1,9 +1,10 @@
 // rotary_embedding and paged_kv_append: rows of heads moved, and rotated by position on the way.
 //
 // Both are one kernel over rows (token, head): the heads of a token are its queries, then (append) its keys and its
-// values.  A block takes a run of neighbouring rows.  Each thread asks for its first vectors of them, the block works out
-// where its tokens go and the cosines and sines of their angles once for all heads, and then the vectors are turned and
-// stored.  Bound by memory; the angles of a token cost R / 2 sincospif and are shared by its heads.
+// values.  A block takes a run of neighbouring rows.  A thread has the same place in each of its rows (an item: two vectors
+// whose elements are turned with one another, or that stay), asks for the first of them, the block works out where its
+// tokens go and the cosines and sines of their angles once for all heads, and then the vectors are turned and stored.
+// Bound by memory; the angles of a token cost R / 2 sincospif and are shared by its heads.
 //
 // An angle is a fraction of a turn: position * freqs modulo 2^64 is the exact remainder of the product by whole turns,
 // and its upper 32 bits as a signed number are half-turns in [-1, 1) in units of 2^-31.  In fp32 they are within 2^-25
@@ -15,8 +16,9 @@
 namespace w4a8 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kAhead = 4;     // items of a thread asked for before the angles are known
+constexpr int kThreads = 128;
+constexpr int kBlocks = 8;   // of an SM
+constexpr int kRounds = 16;  // rows of a thread, at most
 constexpr int kMaxCs = 2048;  // cosine and sine pairs of a block's tokens
 constexpr int kMaxTok = 64;   // tokens of a block
 
@@ -36,7 +38,8 @@ struct RowParams {
   int T, B, Hq, Hkv, D, R, start, table_pages;
   int rot_items, items;  // of a row: those with pairs to turn, all of them
   int rows_per_block;
-  FastDiv by_items, by_heads, by_page, by_half;
+  int row_threads;       // threads of a row: its items, or all where there are more
+  FastDiv by_row, by_heads, by_page, by_half;
   float cos_scale, sin_scale;
   bool interleaved, positions64;
 };
@@ -46,17 +49,9 @@ struct alignas(sizeof(T) * V) Vec {
   T e[V];
 };
 
-template <typename TC>
-__device__ __forceinline__ TC to_cache(float v, float scale);
-template <>
-__device__ __forceinline__ __nv_bfloat16 to_cache(float v, float) { return from_f32<__nv_bfloat16>(v); }
-template <>
-__device__ __forceinline__ __half to_cache(float v, float) { return from_f32<__half>(v); }
-template <>
-__device__ __forceinline__ float to_cache(float v, float) { return v; }
-template <>
-__device__ __forceinline__ uint8_t to_cache(float v, float scale) {
-  return static_cast<uint8_t>(e4m3x2(__fdiv_rn(v, scale), 0.f) & 0xFF);
+// the correctly rounded quotient; where it is past what E4M3 holds its last bits do not matter
+__device__ __forceinline__ float over(float v, float scale, float r) {
+  return fabsf(v * r) < 512.f ? div_by_scale(v, scale, r) : v * r;
 }
 
 // Where the two vectors of an item lie in its row; the second may be missing (-1).
@@ -80,17 +75,24 @@ __device__ __forceinline__ void places(const RowParams& p, int item, bool value,
   }
 }
 
-template <typename T, typename TC, int V>
-__device__ __forceinline__ void store_vec(TC* to, const float (&f)[V], float scale) {
+template <typename TC, int V>
+__device__ __forceinline__ void store_vec(TC* to, const float (&f)[V], float scale, float r) {
   Vec<TC, V> o;
 #pragma unroll
-  for (int j = 0; j < V; ++j) o.e[j] = to_cache<TC>(f[j], scale);
+  for (int j = 0; j < V; ++j) {
+    if constexpr (sizeof(TC) != 1)
+      o.e[j] = from_f32<TC>(f[j]);
+    else if constexpr (V == 1)
+      o.e[j] = static_cast<uint8_t>(e4m3x2(over(f[j], scale, r), 0.f) & 0xFF);
+    else if (j % 2 == 0)
+      reinterpret_cast<uint16_t*>(o.e)[j / 2] = e4m3x2(over(f[j], scale, r), over(f[j + 1], scale, r));
+  }
   *reinterpret_cast<Vec<TC, V>*>(to) = o;
 }
 
 template <typename T, typename TC, int V, bool APPEND>
-__global__ void __launch_bounds__(kThreads) rotary_rows_kernel(const __grid_constant__ RowParams p) {
-  __shared__ float2 cs[kMaxCs];
+__global__ void __launch_bounds__(kThreads, kBlocks) rotary_rows_kernel(const __grid_constant__ RowParams p) {
+  __shared__ __align__(16) float2 cs[kMaxCs];
   __shared__ int64_t at_k[APPEND ? kMaxTok : 1], at_v[APPEND ? kMaxTok : 1];
   __shared__ int at_pos[APPEND ? kMaxTok : 1];
   __shared__ int first_seq;
@@ -98,32 +100,94 @@ __global__ void __launch_bounds__(kThreads) rotary_rows_kernel(const __grid_cons
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_block;
   const int rows = static_cast<int>(min(static_cast<int64_t>(p.rows_per_block), p.rows - r0));
   const int tok0 = static_cast<int>(r0 / heads), in0 = static_cast<int>(r0 - static_cast<int64_t>(tok0) * heads);
-  const int toks = p.by_heads.div(in0 + rows - 1) + 1, count = rows * p.items;
-  const int tid = threadIdx.x;
+  const int toks = p.by_heads.div(in0 + rows - 1) + 1;
+  const int tid = threadIdx.x, half = p.R / 2;
+  int item;
+  const int lane_row = p.by_row.div(tid, item), step = kThreads / p.row_threads;  // this thread's first row, and the next
   pdl_trigger();
   if (APPEND && tid == 0) first_seq = 0;
   pdl_wait();
 
-  // the item `idx` of this block: its token (in the block), head, place in the row
-  auto item_at = [&](int idx, int& tok, int& head, int& item) {
-    const int row = p.by_items.div(idx, item);
-    tok = p.by_heads.div(in0 + row, head);
+  struct Row {
+    Vec<T, V> a, b;
+    int tok, head;  // token in the block
   };
-  auto load = [&](int idx, Vec<T, V>& a, Vec<T, V>& b) {
-    int tok, head, item, e0, e1;
-    item_at(idx, tok, head, item);
-    places<V>(p, item, head >= p.Hq + p.Hkv, e0, e1);
-    const int64_t t = tok0 + tok;
-    const T* src = head < p.Hq            ? static_cast<const T*>(p.q) + t * p.q_t + head * p.q_h
-                   : head < p.Hq + p.Hkv  ? static_cast<const T*>(p.k) + t * p.k_t + (head - p.Hq) * p.k_h
-                                          : static_cast<const T*>(p.v) + t * p.v_t + (head - p.Hq - p.Hkv) * p.v_h;
-    if (e0 >= 0) a = *reinterpret_cast<const Vec<T, V>*>(src + e0);
-    if (e1 >= 0) b = *reinterpret_cast<const Vec<T, V>*>(src + e1);
+  auto load = [&](Row& r, int row, int e0, int e1, int v0, int v1) {
+    if (row >= rows) return;
+    r.tok = p.by_heads.div(in0 + row, r.head);
+    const int64_t t = tok0 + r.tok;
+    const T* src;
+    if (!APPEND || r.head < p.Hq) {
+      src = static_cast<const T*>(p.q) + t * p.q_t + r.head * p.q_h;
+    } else if (r.head < p.Hq + p.Hkv) {
+      src = static_cast<const T*>(p.k) + t * p.k_t + (r.head - p.Hq) * p.k_h;
+    } else {
+      src = static_cast<const T*>(p.v) + t * p.v_t + (r.head - p.Hq - p.Hkv) * p.v_h;
+      e0 = v0, e1 = v1;
+    }
+    if (e0 >= 0) r.a = *reinterpret_cast<const Vec<T, V>*>(src + e0);
+    if (e1 >= 0) r.b = *reinterpret_cast<const Vec<T, V>*>(src + e1);
   };
-  Vec<T, V> a[kAhead], b[kAhead];
+  auto finish = [&](Row& w, int row, int e0, int e1, int v0, int v1) {
+    if (row >= rows) return;
+    const bool value = APPEND && w.head >= p.Hq + p.Hkv;
+    float x[V], y[V];
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u)
-    if (tid + u * kThreads < count) load(tid + u * kThreads, a[u], b[u]);
+    for (int j = 0; j < V; ++j) x[j] = to_f32(w.a.e[j]), y[j] = to_f32(w.b.e[j]);
+    if (value) {
+      e0 = v0, e1 = v1;
+    } else if (item < p.rot_items) {
+      const float2* t = cs + w.tok * half + item * V;
+      if (p.interleaved) {
+        float z[2 * V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) z[j] = x[j], z[V + j] = y[j];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float2 f = t[j];
+          const float re = z[2 * j] * f.x - z[2 * j + 1] * f.y, im = z[2 * j + 1] * f.x + z[2 * j] * f.y;
+          z[2 * j] = re;
+          z[2 * j + 1] = im;
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = z[j], y[j] = z[V + j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float2 f = t[j];
+          const float re = x[j] * f.x - y[j] * f.y, im = y[j] * f.x + x[j] * f.y;
+          x[j] = re;
+          y[j] = im;
+        }
+      }
+    }
+    const int64_t t = tok0 + w.tok;
+    if (!APPEND || w.head < p.Hq) {
+      if (APPEND && at_pos[w.tok] < 0) return;  // a row that belongs to no sequence
+      T* to = static_cast<T*>(p.qo) + t * p.o_t + w.head * p.o_h;
+      if (e0 >= 0) store_vec<T, V>(to + e0, x, 1.f, 1.f);
+      if (e1 >= 0) store_vec<T, V>(to + e1, y, 1.f, 1.f);
+      return;
+    }
+    if constexpr (APPEND) {
+      if (at_k[w.tok] < 0) return;
+      const int h = w.head - p.Hq - (value ? p.Hkv : 0);
+      TC* to = value ? static_cast<TC*>(p.vc) + at_v[w.tok] + h * p.v_head
+                     : static_cast<TC*>(p.kc) + at_k[w.tok] + h * p.k_head;
+      const float* scales = value ? p.v_scale : p.k_scale;
+      const float scale = sizeof(TC) == 1 && scales ? scales[h] : 1.f, r = sizeof(TC) == 1 ? __frcp_rn(scale) : 1.f;
+      if (e0 >= 0) store_vec<TC, V>(to + e0, x, scale, r);
+      if (e1 >= 0) store_vec<TC, V>(to + e1, y, scale, r);
+    }
+  };
+
+  int e0, e1, v0, v1;
+  places<V>(p, item, false, e0, e1);
+  places<V>(p, item, true, v0, v1);
+  Row w;
+  const bool mine = lane_row < step;  // the last threads may be no whole row
+  const int first = mine ? lane_row : rows;
+  load(w, first, e0, e1, v0, v1);
 
   if constexpr (APPEND) {
     if (p.indptr) {  // the sequence of the block's first token: how many end before it
@@ -161,7 +225,6 @@ __global__ void __launch_bounds__(kThreads) rotary_rows_kernel(const __grid_cons
     }
     __syncthreads();
   }
-  const int half = p.R / 2;
   for (int i = tid; i < toks * half; i += kThreads) {
     int f;
     const int tok = p.by_half.div(i, f);
@@ -178,66 +241,21 @@ __global__ void __launch_bounds__(kThreads) rotary_rows_kernel(const __grid_cons
   }
   __syncthreads();
 
-  auto finish = [&](int idx, const Vec<T, V>& va, const Vec<T, V>& vb) {
-    int tok, head, item, e0, e1;
-    item_at(idx, tok, head, item);
-    const bool value = head >= p.Hq + p.Hkv, query = head < p.Hq;
-    places<V>(p, item, value, e0, e1);
-    float x[V], y[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      x[j] = e0 >= 0 ? to_f32(va.e[j]) : 0.f;
-      y[j] = e1 >= 0 ? to_f32(vb.e[j]) : 0.f;
+  // 32 warps of an SM hide one another's loads.  8192 x 72 x 128: 54 us; two rows of a thread on their way take registers
+  // from other warps (64 us), as do 4 blocks of 256 threads with as many rounds (59).
+#pragma unroll 1
+  for (int row = first; row < rows; row += step) {
+    finish(w, row, e0, e1, v0, v1);
+    load(w, row + step, e0, e1, v0, v1);
+  }
+  // rows of more items than threads: the items behind the first kThreads
+  for (item += kThreads; item < p.items; item += kThreads) {
+    places<V>(p, item, false, e0, e1);
+    places<V>(p, item, true, v0, v1);
+    for (int row = 0; row < rows; ++row) {
+      load(w, row, e0, e1, v0, v1);
+      finish(w, row, e0, e1, v0, v1);
     }
-    if (!value && item < p.rot_items) {
-      const float2* t = cs + tok * half + item * V;
-      if (p.interleaved) {
-        float z[2 * V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) z[j] = x[j], z[V + j] = y[j];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float2 w = t[j];
-          const float r = z[2 * j] * w.x - z[2 * j + 1] * w.y, i = z[2 * j + 1] * w.x + z[2 * j] * w.y;
-          z[2 * j] = r;
-          z[2 * j + 1] = i;
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) x[j] = z[j], y[j] = z[V + j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float2 w = t[j];
-          const float r = x[j] * w.x - y[j] * w.y, i = y[j] * w.x + x[j] * w.y;
-          x[j] = r;
-          y[j] = i;
-        }
-      }
-    }
-    const int64_t t = tok0 + tok;
-    if (!APPEND || query) {
-      if (APPEND && at_pos[tok] < 0) return;  // a row that belongs to no sequence
-      T* to = static_cast<T*>(p.qo) + t * p.o_t + head * p.o_h;
-      if (e0 >= 0) store_vec<T, T, V>(to + e0, x, 1.f);
-      if (e1 >= 0) store_vec<T, T, V>(to + e1, y, 1.f);
-      return;
-    }
-    if constexpr (APPEND) {
-      if (at_k[tok] < 0) return;
-      const int h = head - p.Hq - (value ? p.Hkv : 0);
-      TC* to = value ? static_cast<TC*>(p.vc) + at_v[tok] + h * p.v_head : static_cast<TC*>(p.kc) + at_k[tok] + h * p.k_head;
-      const float* scales = value ? p.v_scale : p.k_scale;
-      const float scale = scales ? scales[h] : 1.f;
-      if (e0 >= 0) store_vec<T, TC, V>(to + e0, x, scale);
-      if (e1 >= 0) store_vec<T, TC, V>(to + e1, y, scale);
-    }
-  };
-#pragma unroll
-  for (int u = 0; u < kAhead; ++u)
-    if (tid + u * kThreads < count) finish(tid + u * kThreads, a[u], b[u]);
-  for (int idx = tid + kAhead * kThreads; idx < count; idx += kThreads) {
-    load(idx, a[0], b[0]);
-    finish(idx, a[0], b[0]);
   }
 }
 
@@ -246,13 +264,16 @@ int launch_rows(RowParams p, cudaStream_t st) {
   const int heads = p.Hq + 2 * p.Hkv, half = p.R / 2;
   p.rot_items = half / V;
   p.items = p.rot_items + static_cast<int>(ceil_div(p.D - p.R, 2 * V));
-  p.by_items = FastDiv(p.items);
+  p.row_threads = std::min(p.items, kThreads);
+  p.by_row = FastDiv(p.row_threads);
   p.by_heads = FastDiv(heads);
   p.by_half = FastDiv(half > 0 ? half : 1);
-  // Rows of a block: what its threads ask for at once, fewer where that leaves SMs idle, and no more tokens than have room.
+  // Rows of a block: as many rounds for each thread as make whole waves of blocks, up to kRounds (a block's start, with its
+  // angles, costs about two rounds; 8192 x 72 x 128 takes 55 us with 8 rounds, 59 with 4), and no more tokens than have room.
   const int tokens = std::min(kMaxTok, half > 0 ? kMaxCs / half : kMaxTok);
-  int64_t rows = std::max<int64_t>(1, kAhead * kThreads / p.items);
-  rows = std::min(rows, ceil_div(p.rows, 2 * num_sms()));
+  const int64_t step = kThreads / p.row_threads, slots = kBlocks * num_sms();
+  const int64_t rounds = ceil_div(ceil_div(p.rows, step), slots), waves = ceil_div(rounds, kRounds);
+  int64_t rows = ceil_div(rounds, waves) * step;
   rows = std::min(rows, static_cast<int64_t>(tokens - 1) * heads + 1);  // rows from anywhere in a token touch no more
   p.rows_per_block = static_cast<int>(std::max<int64_t>(1, rows));
   return launch_pdl("rotary_rows_kernel", rotary_rows_kernel<T, TC, V, APPEND>,
