@@ -4,14 +4,14 @@
 namespace w4a8 {
 namespace {
 
-// Workspace: units before each sequence, then (m, l) and O of two parts of every block.
+// Workspace: places before each sequence, then (m, l) and O of two parts of every warp.
 struct AttendLayout {
   size_t ml, o, total;
 };
 AttendLayout attend_layout(int64_t B, int64_t G, int64_t D) {
   const auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
   const int DT = attend_dt(D);
-  const size_t rows = static_cast<size_t>(attend_blocks(DT)) * 2 * 16 * attend_mt(DT, static_cast<int>(G));
+  const size_t rows = static_cast<size_t>(attend_warps(DT)) * 2 * 16 * attend_mt(DT, static_cast<int>(G));
   AttendLayout L;
   L.ml = up(static_cast<size_t>(B + 1) * 8);
   L.o = L.ml + up(rows * 8);
@@ -35,13 +35,14 @@ extern "C" int paged_attention_decode(const void* q, int64_t ldq_b, int64_t ldq_
                fp8 ? 16 : 8);
   W4A8_REQUIRE(Hq >= 1 && Hq % H == 0 && Hq / H <= 256, "Hq=%lld must be a multiple of heads=%lld, at most 256 times it",
                (long long)Hq, (long long)H);
-  W4A8_REQUIRE(B * H < (1ll << 24), "B=%lld times heads=%lld must be below 2^24", (long long)B, (long long)H);
+  W4A8_REQUIRE(B * H < (1ll << 24) && B * Hq < (1ll << 31), "B=%lld times heads=%lld must be below 2^24, times Hq=%lld below 2^31",
+               (long long)B, (long long)H, (long long)Hq);
   W4A8_REQUIRE(window >= 0, "window=%lld must not be negative", (long long)window);
   W4A8_REQUIRE(scale - scale == 0.f, "scale must be finite");
   W4A8_REQUIRE(ldq_b >= 0 && ldq_h >= 0 && ldo_b >= 0 && ldo_h >= 0, "strides must not be negative");
   const int DT = attend_dt(D), G = static_cast<int>(Hq / H), rows = 16 * attend_mt(DT, G);
   const int64_t max_len = cache->table_pages * cache->page_size;
-  W4A8_REQUIRE(B * H * ceil_div(G, rows) * ceil_div(max_len + 1, 64) < (1ll << 38),
+  W4A8_REQUIRE(B * H * ceil_div(G, rows) * (ceil_div(max_len + 1, 16) + 1) < (1ll << 38),
                "B=%lld sequences of up to %lld tokens are too many for one call", (long long)B, (long long)max_len);
   if (B == 0) return W4A8_OK;
   W4A8_REQUIRE(q && out && cache->seq_lens, "null pointer");
@@ -91,6 +92,8 @@ extern "C" int paged_attention_decode(const void* q, int64_t ldq_b, int64_t ldq_
   p.scale = scale * 1.44269504089f;
   p.by_page = FastDiv(cache->page_size);
   p.q_f16 = dtype == W4A8_DTYPE_F16;
+  p.q_vec = (bits_of(q) | static_cast<uint64_t>(ldq_b | ldq_h) * 2) % 16 == 0;
+  p.same_places = p.k_page == p.v_page && p.k_slot == p.v_slot && p.k_head == p.v_head;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (fp8) return launch_attend_fp8(p, st);
   return p.q_f16 ? launch_attend_f16(p, st) : launch_attend_bf16(p, st);

@@ -1,14 +1,16 @@
 // paged_attention_decode: one query token per sequence against its cached keys and values.
 //
-// The work is a list of units: a unit is 4 * NT neighbouring tokens of one sequence for one key-value head and up to
-// 16 * MT of its query heads, and the list goes through all sequences, heads and units in order.  A launch has as many
-// blocks as stay resident, and each takes an equal run of the list, so that long and short sequences fill the machine
-// alike.  Its 4 warps take NT tokens of each unit.  A warp has its own ring of key and value tiles in shared memory,
-// filled by asynchronous 16-byte copies through the page table and read by ldmatrix, and walks on into the next sequence
-// without a pause: scores S = Q K^T by mma.sync (16 query heads to a fragment), running maximum and sum per row, weights
-// in registers as the next product's left operand, O += P V.  Where a sequence ends (or the block's run does) the
-// 4 warps join their rows in shared memory; a sequence's only block writes the result, others leave (m, l, O) in the
-// workspace, which a second kernel joins in the order of the blocks.
+// The work is a list of tiles: NT neighbouring tokens of one sequence for one key-value head and up to 16 * MT of its query
+// heads, through all sequences, heads and tiles in order.  A launch has as many warps as stay resident, and each takes an
+// equal run of the list, so that long and short sequences fill the machine alike; the start of an item (a sequence's head)
+// counts as kExtra tiles.  A warp works by itself: it has a ring of key and value tiles in shared memory, filled by
+// asynchronous 16-byte copies through the page table and read by ldmatrix, and its copies run on into the next item while it
+// finishes one: scores S = Q K^T by mma.sync (16 query heads to a fragment), running maximum and sum per row, weights in
+// registers as the next product's left operand, O += P V.  What a warp has whole it writes; of an item that several warps
+// share each leaves (m, l, O) in the workspace, and a second kernel joins them in the warps' order.
+//
+// (Blocks whose 4 warps shared a run, joined in shared memory at each item's end: 4.5 us an item, 39 us for 32 sequences of
+// up to 1024 tokens, whose bytes take 10.)
 //
 // Bound by memory: 2 D bytes a token and key-value head are read once and meet 4 G D operations for G query heads.  mma.sync
 // covers that: a tile of 16 rows by 16 tokens costs 48 products of 16 x 8 x 16 for 8 KB of cache.
@@ -37,14 +39,14 @@ struct AttendParams {
   int64_t q_b, q_h, o_b, o_h;
   int64_t k_page, k_slot, k_head, v_page, v_slot, v_head;  // bytes
   int64_t table_ld, pages, max_len;  // max_len: positions that the table reaches
-  int64_t* prefix;                   // [B + 1] units before each sequence
-  float2* part_ml;                   // [blocks][2][16 MT]
-  float* part_o;                     // [blocks][2][16 MT][D]
+  int64_t* prefix;                   // [B + 1] places in the list before each sequence
+  float2* part_ml;                   // [warps][2][16 MT]
+  float* part_o;                     // [warps][2][16 MT][D]
   int B, Hq, Hkv, G, D, HB;          // HB: groups of up to 16 MT query heads for a key-value head
-  int blocks, window;
+  int warps, window;
   float scale;                       // times log2 e
   FastDiv by_page;
-  bool q_f16;
+  bool q_f16, q_vec, same_places;    // 16-byte loads of q; keys and values lie alike
 };
 
 int launch_attend_bf16(const AttendParams& p, cudaStream_t st);
@@ -54,13 +56,13 @@ int launch_attend_fp8(const AttendParams& p, cudaStream_t st);
 // The instances: head dimensions up to DT, query heads of a group in MT fragments of 16.
 __host__ __device__ constexpr int attend_mt(int DT, int G) { return G > 16 && DT <= 128 ? 2 : 1; }
 __host__ __device__ constexpr int attend_dt(int64_t D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
-// blocks of a launch at most (their partial results have room for it)
-inline int attend_blocks(int DT) { return num_sms() * (DT <= 128 ? 2 : 1); }
+constexpr int kAttendWarps = 4;  // of a block
+inline int attend_warps(int DT) { return num_sms() * (DT <= 128 ? 2 : 1) * kAttendWarps; }  // of a launch
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kStages = 3;
+constexpr int kWarps = kAttendWarps;
+constexpr int kExtra = 1;
 constexpr float kLn2 = 0.69314718056f;
 
 __device__ unsigned int g_attend_error;
@@ -76,25 +78,21 @@ __device__ __forceinline__ void cp_async_wait() {
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
+               : "r"(a));
 }
 __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
+               : "r"(a));
 }
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (BF16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -119,16 +117,18 @@ struct AttendCfg {
   static constexpr int NT = kFp8 || DT == 64 ? 32 : 16;  // tokens of a tile
   static constexpr int kTile = NT * kRow;
   static constexpr int kStage = 2 * kTile;              // keys, values
+  static constexpr int kStages = MT == 2 && kStage == 8192 ? 2 : 3;
   static constexpr int kRows = 16 * MT;
   static constexpr float kShift = kBf16 ? 0.f : 15.f;   // weights are 2^kShift times the exponentials
-  static constexpr int kQRow = DT * 2 + 16;             // padded: 8 rows at one column lie in different banks
-  static constexpr int kOffQ = kWarps * kStages * kStage;
-  static constexpr int kOffRow = kOffQ + kRows * kQRow;       // fp32 [rows]: factor of a row's scores
-  static constexpr int kOffMl = kOffRow + kRows * 4;          // float2 [warps][rows]
-  static constexpr int kSmem = kOffMl + kWarps * kRows * 8;
+  static constexpr int kQRow = DT * 2;
+  static constexpr int kOffQ = kStages * kStage;        // of a warp
+  static constexpr int kOffScale = kOffQ + kRows * kQRow;  // fp32 [rows]: factor of a row's scores
+  static constexpr int kWarpBytes = kOffScale + 128;
+  static constexpr int kSmem = kWarps * kWarpBytes;
   static constexpr int kBlocks = DT <= 128 ? 2 : 1;     // of an SM
-  static_assert((kSmem + 2048) * kBlocks <= 228 * 1024, "shared memory");
-  static_assert(kStage >= 16 * DT * 4, "16 rows of fp32 sums in a ring slot");
+  static_assert((kSmem + 1024) * kBlocks <= 228 * 1024, "shared memory");
+  static_assert(kWarpBytes % 128 == 0 && kRows * 4 <= 128, "tiles on 128 bytes");
+  static_assert(kSmem >= (kWarps * 32 + 1) * 8, "room for the prefix");
   // place of 16-byte chunk c of row r: chunks are exchanged within 128 bytes so that 8 rows at one column lie in
   // different banks
   static __device__ __forceinline__ uint32_t at(int r, int c) {
@@ -137,112 +137,136 @@ struct AttendCfg {
     else
       return static_cast<uint32_t>(r * kRow + ((c ^ ((r >> 1) & 3)) << 4));
   }
+  static __device__ __forceinline__ uint32_t q_at(int r, int c) { return static_cast<uint32_t>(r * kQRow + ((c ^ (r & 7)) << 4)); }
 };
 
-// Sequence b's tokens and units.
+// Sequence b's tokens and tiles.
 struct SeqSpan {
-  int lo, hi, units;
+  int lo, hi, tiles;
 };
-template <int UNIT>
+template <int NT>
 __device__ __forceinline__ SeqSpan span_of(const AttendParams& p, int b) {
   SeqSpan s;
   const int64_t len = p.lens[b];
   if (len > p.max_len) atomicOr(&g_attend_error, 2u);
   s.hi = static_cast<int>(min(len, p.max_len));
   s.lo = p.window > 0 ? max(0, s.hi - p.window) : 0;
-  s.units = s.hi > s.lo ? (s.hi - s.lo + UNIT - 1) / UNIT : 0;
+  s.tiles = s.hi > s.lo ? (s.hi - s.lo + NT - 1) / NT : 0;
   return s;
 }
+// places of a sequence in the list
+__device__ __forceinline__ int64_t places_of(const SeqSpan& s, int HH) {
+  return s.tiles ? static_cast<int64_t>(s.tiles + kExtra) * HH : 0;
+}
+// Warps with work: each has a place at least.  The run of warp w is [w total / runs, (w + 1) total / runs), and the warp
+// that has place t is floor(((t + 1) runs - 1) / total).
+__device__ __forceinline__ int64_t runs_of(const AttendParams& p, int64_t total) {
+  return min(total, static_cast<int64_t>(p.warps));
+}
 
-// A place in the list of units.
+// A tile in the list, and how many places the run has from it on.
 struct Cursor {
-  int b, hh, u;  // sequence, head and group of query heads, unit
+  int b, hh, u;  // sequence, head and group of query heads, tile
   SeqSpan s;
+  int left;
 };
+
+// Two fp32 columns of a row of the output.
+__device__ __forceinline__ void store_out(void* out, int64_t at, float x, float y, bool bf16) {
+  uint16_t* o = static_cast<uint16_t*>(out) + at;
+  const uint32_t w = bf16 ? pack2<__nv_bfloat16>(x, y) : pack2<__half>(x, y);
+  o[0] = static_cast<uint16_t>(w);
+  o[1] = static_cast<uint16_t>(w >> 16);
+}
 
 template <int KIND, int DT, int MT>
 __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
     paged_attention_kernel(const __grid_constant__ AttendParams p) {
   using C = AttendCfg<KIND, DT, MT>;
-  constexpr int NT = C::NT, UNIT = kWarps * NT;
+  constexpr int NT = C::NT, kStages = C::kStages;
   constexpr bool kFp8 = C::kFp8;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t chunk_sum[kWarps * 32 + 1];  // units before the sequences of each thread
+  extern __shared__ __align__(128) uint8_t smem_all[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   pdl_wait();
 
-  // units before each run of sequences; the first block leaves those of every sequence for the second kernel
+  // places before each thread's sequences; the first block leaves those of every sequence for the second kernel
   const int HH = p.Hkv * p.HB, per = (p.B + kWarps * 32 - 1) / (kWarps * 32);
-  int64_t mine = 0;
-  for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) mine += static_cast<int64_t>(span_of<UNIT>(p, b).units) * HH;
+  int64_t* before = reinterpret_cast<int64_t*>(smem_all);  // [threads + 1], until the rings are filled
+  int64_t total, start, stop, at_seq;
+  Cursor here;  // of the tile that is computed next
   {
+    int64_t mine = 0;
+    for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) mine += places_of(span_of<NT>(p, b), HH);
     int64_t up = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t x = __shfl_up_sync(0xffffffffu, up, o);
       if (lane >= o) up += x;
     }
-    chunk_sum[tid + 1] = up;
-    if (tid == 0) chunk_sum[0] = 0;
+    if (lane == 31) before[warp] = up;
     __syncthreads();
-    int64_t before = 0;
-    for (int w = 0; w < warp; ++w) before += chunk_sum[(w + 1) * 32];
+    for (int w = 0; w < warp; ++w) up += before[w];
     __syncthreads();
-    chunk_sum[tid + 1] = up + before;
+    before[tid + 1] = up;
+    if (tid == 0) before[0] = 0;
+    __syncthreads();
     if (blockIdx.x == 0) {
-      int64_t at = up + before - mine;
+      int64_t at = up - mine;
       for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) {
         p.prefix[b] = at;
-        at += static_cast<int64_t>(span_of<UNIT>(p, b).units) * HH;
+        at += places_of(span_of<NT>(p, b), HH);
       }
-      if (tid == kWarps * 32 - 1) p.prefix[p.B] = up + before;
+      if (tid == kWarps * 32 - 1) p.prefix[p.B] = up;
     }
-    __syncthreads();
-  }
-  const int64_t total = chunk_sum[kWarps * 32];
-  const int64_t runs = min(total, static_cast<int64_t>(p.blocks));  // blocks with work: each has a unit at least
-  if (blockIdx.x >= runs) return;
-  const int64_t start = blockIdx.x * total / runs, stop = (blockIdx.x + 1) * total / runs;
-  const int count = static_cast<int>(stop - start);
-
-  Cursor here;  // of the unit that is computed next
-  {
+    total = before[kWarps * 32];
+    const int64_t runs = runs_of(p, total), run = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
+    const bool mine_too = run < runs;
+    start = mine_too ? run * total / runs : 0;
+    stop = mine_too ? (run + 1) * total / runs : 0;
     int c = 0;  // the last thread whose sequences begin at or before start
 #pragma unroll
     for (int step = kWarps * 16; step > 0; step >>= 1)
-      if (chunk_sum[c + step] <= start) c += step;
-    int64_t at = chunk_sum[c];
+      if (before[c + step] <= start) c += step;
+    at_seq = before[c];
     here.b = c * per;
-    here.s = span_of<UNIT>(p, here.b);
-    while (at + static_cast<int64_t>(here.s.units) * HH <= start) {
-      at += static_cast<int64_t>(here.s.units) * HH;
-      here.s = span_of<UNIT>(p, ++here.b);
-    }
-    const int64_t in = start - at;
-    here.hh = static_cast<int>(in / here.s.units);
-    here.u = static_cast<int>(in - static_cast<int64_t>(here.hh) * here.s.units);
+    __syncthreads();  // the rings may be filled
+  }
+  if (start >= stop) return;
+  here.s = span_of<NT>(p, here.b);
+  while (at_seq + places_of(here.s, HH) <= start) {
+    at_seq += places_of(here.s, HH);
+    here.s = span_of<NT>(p, ++here.b);
+  }
+  {
+    const int64_t in = start - at_seq, each = here.s.tiles + kExtra;
+    here.hh = static_cast<int>(in / each);
+    const int off = static_cast<int>(in - here.hh * each);
+    here.u = max(0, off - kExtra);
+    here.left = static_cast<int>(stop - start) - max(0, kExtra - off);
   }
   const auto advance = [&](Cursor& c) {
-    if (++c.u < c.s.units) return;
+    --c.left;
+    if (++c.u < c.s.tiles) return;
     c.u = 0;
-    if (++c.hh < HH) return;
+    c.left -= kExtra;
+    if (++c.hh < HH || c.left <= 0) return;
     c.hh = 0;
     do {
-      if (++c.b >= p.B) return;
-      c.s = span_of<UNIT>(p, c.b);
-    } while (c.s.units == 0);
+      c.s = span_of<NT>(p, ++c.b);  // the run has places left: there is another sequence with tiles
+    } while (c.s.tiles == 0);
   };
 
-  const uint32_t ring = smem_u32(smem) + warp * kStages * C::kStage;
-  constexpr int kChunks = C::kRow / 16, kRowsPer = 32 / kChunks > 0 ? 32 / kChunks : 1;  // rows of one copy by the warp
+  uint8_t* smem = smem_all + warp * C::kWarpBytes;
+  const uint32_t ring = smem_u32(smem);
+  constexpr int kChunks = C::kRow / 16, kRowsPer = 32 / kChunks;  // rows of one copy by the warp
   static_assert(kChunks <= 32, "a warp copies whole rows");
-  // The page of this lane's token of a unit (-1: none), one unit ahead of its copies.
+  // The page of this lane's token of a tile (-1: none), one tile ahead of its copies.
   const auto page_of = [&](const Cursor& c, int& slot) {
-    const int t = c.s.lo + c.u * UNIT + warp * NT + (lane & (NT - 1));
+    const int t = c.s.lo + c.u * NT + (lane & (NT - 1));
     int page = -1;
     slot = 0;
-    if (t < c.s.hi) {
+    if (c.left > 0 && t < c.s.hi) {
       const int n = p.by_page.div(t, slot);
       page = p.table[c.b * p.table_ld + n];
       if (page < 0 || page >= p.pages) {
@@ -252,8 +276,7 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
     }
     return page;
   };
-  const auto copy_unit = [&](int hh, int page, int slot, int stage) {
-    const int h = hh / p.HB;
+  const auto copy_tile = [&](int h, int page, int slot, int stage) {
     const int64_t k_at = page < 0 ? -1 : page * p.k_page + slot * p.k_slot + h * p.k_head;
     const int64_t v_at = page < 0 ? -1 : page * p.v_page + slot * p.v_slot + h * p.v_head;
     const int c = lane % kChunks, r0 = lane / kChunks;
@@ -262,7 +285,8 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
     const char *k = static_cast<const char*>(p.k) + c * 16, *v = static_cast<const char*>(p.v) + c * 16;
 #pragma unroll
     for (int r = 0; r < NT; r += kRowsPer) {
-      const int64_t ka = __shfl_sync(0xffffffffu, k_at, r + r0), va = __shfl_sync(0xffffffffu, v_at, r + r0);
+      const int64_t ka = __shfl_sync(0xffffffffu, k_at, r + r0);
+      const int64_t va = p.same_places ? ka : __shfl_sync(0xffffffffu, v_at, r + r0);
       const bool there = in_row && ka >= 0;
       const uint32_t to = C::at(r + r0, c);
       cp_async16(kt + to, there ? k + ka : static_cast<const char*>(p.k), there);
@@ -270,78 +294,95 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
     }
   };
 
-  // fill the ring: kStages - 1 units on their way, the next one's pages known
+  // fill the ring: kStages - 1 tiles on their way, the next one's pages known
   Cursor ahead = here;
-  int issued = 0, page, slot;
-  page = page_of(ahead, slot);
-  int ahead_hh = ahead.hh;
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    if (issued < count) {
-      copy_unit(ahead_hh, page, slot, i);
-      if (++issued < count) {
-        advance(ahead);
-        ahead_hh = ahead.hh;
-        page = page_of(ahead, slot);
-      }
+  int slot, page = page_of(ahead, slot), ahead_h = ahead.hh / p.HB;
+  const auto issue = [&](int stage) {
+    if (ahead.left > 0) {
+      copy_tile(ahead_h, page, slot, stage);
+      advance(ahead);
+      ahead_h = ahead.hh / p.HB;
+      page = page_of(ahead, slot);
     }
     cp_async_commit();
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue(i);
 
   constexpr int kNt = DT / 8;  // column fragments of O
   float o[MT][kNt][4], m[MT][2], l[MT][2];
   const int g = lane >> 2, j2 = (lane & 3) * 2;
-  const uint32_t q_s = smem_u32(smem) + C::kOffQ;
-  float* row_scale = reinterpret_cast<float*>(smem + C::kOffRow);
-  float2* join_ml = reinterpret_cast<float2*>(smem + C::kOffMl);
+  const uint32_t q_s = ring + C::kOffQ;
+  float* row_scale = reinterpret_cast<float*>(smem + C::kOffScale);
+  const bool bf16_out = C::kBf16 || (kFp8 && !p.q_f16);
 
-  int done = 0, stage = 0;
-  while (done < count) {
-    // --- a run of units of one sequence and head ---
-    const int run = min(here.s.units - here.u, count - done);
-    const bool whole = run == here.s.units;
+  int stage = 0;
+  bool first = true;
+  while (here.left > 0) {
+    // --- the tiles of one item ---
+    const int run = min(here.s.tiles - here.u, here.left);
+    const bool whole = run == here.s.tiles;
     const int h = here.hh / p.HB, head0 = h * p.G + (here.hh % p.HB) * C::kRows;
     const int live = min(C::kRows, (h + 1) * p.G - head0);  // query heads of this group
-    __syncthreads();  // nobody reads the last run's queries or rows any more
     {
       const float ks = kFp8 && p.k_scale ? p.k_scale[h] : 1.f;
-      for (int r = warp; r < C::kRows; r += kWarps) {
-        const uint16_t* src = static_cast<const uint16_t*>(p.q) + here.b * p.q_b + (head0 + r) * p.q_h;
-        uint16_t* dst = reinterpret_cast<uint16_t*>(smem + C::kOffQ + r * C::kQRow);
-        uint16_t e[DT / 32];
+      constexpr int kLanes = DT / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a turn
+      const int c = lane % kLanes, r0 = lane / kLanes;
+      const uint16_t* src = static_cast<const uint16_t*>(p.q) + here.b * p.q_b + (head0 + r0) * p.q_h + c * 8;
+      uint4 e[C::kRows / kPer];
 #pragma unroll
-        for (int i = 0; i < DT / 32; ++i) e[i] = r < live && lane + 32 * i < p.D ? src[lane + 32 * i] : 0;
+      for (int i = 0; i < C::kRows / kPer; ++i) {
+        e[i] = make_uint4(0, 0, 0, 0);
+        if (r0 + i * kPer < live && c * 8 < p.D) {
+          const uint16_t* at = src + i * kPer * p.q_h;
+          if (p.q_vec) {
+            e[i] = *reinterpret_cast<const uint4*>(at);
+          } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = at[2 * j] | static_cast<uint32_t>(at[2 * j + 1]) << 16;
+            e[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      __syncwarp();  // the last item's queries are read
+#pragma unroll
+      for (int i = 0; i < C::kRows / kPer; ++i) {
+        const int r = r0 + i * kPer;
+        uint32_t w[4] = {e[i].x, e[i].y, e[i].z, e[i].w};
         float factor = 1.f;
         if constexpr (kFp8) {
           // f16 operands: a bf16 row is scaled by a power of two so that its largest element lies in [2^14, 2^15), where
           // elements down to 2^-29 of it stay exact
           if (!p.q_f16) {
-            float top = 0.f;
+            float f[8], top = 0.f;
 #pragma unroll
-            for (int i = 0; i < DT / 32; ++i) top = fmaxf(top, fabsf(bf16_bits_to_float(e[i])));
-            top = warp_max(top);
+            for (int j = 0; j < 8; ++j) {
+              f[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+              top = fmaxf(top, fabsf(f[j]));
+            }
+#pragma unroll
+            for (int x = 1; x < kLanes; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
             const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
             // powers of two beyond fp32's range (tiny rows) are capped; infinities keep their place
             const int by = top > 0.f && ex < 128 ? min(14 - ex, 126) : 0;
             const float up = __uint_as_float(static_cast<uint32_t>(by + 127) << 23);
             factor = __uint_as_float(static_cast<uint32_t>(127 - by) << 23);
 #pragma unroll
-            for (int i = 0; i < DT / 32; ++i) e[i] = __half_as_ushort(__float2half_rn(bf16_bits_to_float(e[i]) * up));
+            for (int j = 0; j < 4; ++j) w[j] = pack2<__half>(f[2 * j] * up, f[2 * j + 1] * up);
           }
-#pragma unroll
-          for (int i = 0; i < DT / 32; ++i) {
-            // the order of d within 16 in which a key's codes come out of ldmatrix: four neighbours to a lane
-            const int d = lane + 32 * i, in = d & 15, to = (in >> 2) * 2 + (in & 1) + ((in & 2) << 2);
-            dst[(d & ~15) + to] = e[i];
-          }
+          // the order of d within 16 in which a key's codes come out of ldmatrix, four neighbours to a lane: pairs 0 2 4 6
+          // of the 16, then 1 3 5 7
+          const uint32_t to = (c & 1) * 8;
+          *reinterpret_cast<uint2*>(smem + C::kOffQ + C::q_at(r, c & ~1) + to) = make_uint2(w[0], w[2]);
+          *reinterpret_cast<uint2*>(smem + C::kOffQ + C::q_at(r, c | 1) + to) = make_uint2(w[1], w[3]);
         } else {
-#pragma unroll
-          for (int i = 0; i < DT / 32; ++i) dst[lane + 32 * i] = e[i];
+          *reinterpret_cast<uint4*>(smem + C::kOffQ + C::q_at(r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if (lane == 0) row_scale[r] = factor * p.scale * ks;
+        if (c == 0) row_scale[r] = factor * p.scale * ks;
       }
+      __syncwarp();
     }
-    __syncthreads();
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -352,172 +393,161 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
       l[mt][0] = l[mt][1] = 0.f;
     }
 
+#pragma unroll 1
     for (int i = 0; i < run; ++i) {
-      if (issued < count) {
-        int to = stage + kStages - 1;
-        if (to >= kStages) to -= kStages;
-        copy_unit(ahead_hh, page, slot, to);
-        if (++issued < count) {
-          advance(ahead);
-          ahead_hh = ahead.hh;
-          page = page_of(ahead, slot);
-        }
-      }
-      cp_async_commit();
+      issue(stage == 0 ? kStages - 1 : stage - 1);
       cp_async_wait<kStages - 1>();
       __syncwarp();
       const uint32_t kt = ring + stage * C::kStage, vt = kt + C::kTile;
       if (++stage == kStages) stage = 0;
-      const int left = here.s.hi - (here.s.lo + (here.u + i) * UNIT + warp * NT);  // tokens of this tile
-      if (left > 0) {
-        // scores
-        float s[MT][NT / 8][4];
+      const int left = here.s.hi - (here.s.lo + (here.u + i) * NT);  // tokens of this tile and behind it
+      // scores
+      float s[MT][NT / 8][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < NT / 8; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s[mt][n][x] = 0.f;
+      if constexpr (!kFp8) {
+#pragma unroll
+        for (int kk = 0; kk < DT / 16; ++kk) {
+          uint32_t a[MT][4];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            ldsm4(a[mt], q_s + C::q_at(mt * 16 + (lane & 15), 2 * kk + (lane >> 4)));
+#pragma unroll
+          for (int n = 0; n < NT / 16; ++n) {
+            uint32_t b[4];  // tokens 0-7 and 8-15, d 0-7 and 8-15 each
+            ldsm4(b, kt + C::at(n * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma16816<C::kBf16>(s[mt][2 * n], a[mt], b[0], b[1]);
+              mma16816<C::kBf16>(s[mt][2 * n + 1], a[mt], b[2], b[3]);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < DT / 32; ++kk) {
+          uint32_t a[2][MT][4];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              ldsm4(a[x][mt], q_s + C::q_at(mt * 16 + (lane & 15), 2 * (2 * kk + x) + (lane >> 4)));
+#pragma unroll
+          for (int n = 0; n < NT / 16; ++n) {
+            uint32_t b[4];  // tokens 0-7 and 8-15, d 0-15 and 16-31 each
+            ldsm4(b, kt + C::at(n * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t b0 = f16x2_of_e4m3x2(b[x]), b1 = f16x2_of_e4m3x2(b[x] >> 16);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) mma16816<false>(s[mt][2 * n + (x >> 1)], a[x & 1][mt], b0, b1);
+            }
+          }
+        }
+      }
+      // running maximum and sum, weights
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const float f0 = row_scale[mt * 16 + g], f1 = row_scale[mt * 16 + g + 8];
+        float top0 = m[mt][0], top1 = m[mt][1];
+#pragma unroll
+        for (int n = 0; n < NT / 8; ++n) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const bool in = n * 8 + j2 + x < left;
+            s[mt][n][x] = in ? s[mt][n][x] * f0 : -INFINITY;
+            s[mt][n][2 + x] = in ? s[mt][n][2 + x] * f1 : -INFINITY;
+            top0 = fmaxf(top0, s[mt][n][x]);
+            top1 = fmaxf(top1, s[mt][n][2 + x]);
+          }
+        }
+        top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 1));
+        top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
+        top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 2));
+        top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 2));
+        const float base0 = top0 == -INFINITY ? 0.f : top0, base1 = top1 == -INFINITY ? 0.f : top1;
+        if (__any_sync(0xffffffffu, top0 > m[mt][0] || top1 > m[mt][1])) {
+          const float c0 = exp2_fast(m[mt][0] - base0), c1 = exp2_fast(m[mt][1] - base1);
+          l[mt][0] *= c0;
+          l[mt][1] *= c1;
+#pragma unroll
+          for (int n = 0; n < kNt; ++n) {
+            o[mt][n][0] *= c0;
+            o[mt][n][1] *= c0;
+            o[mt][n][2] *= c1;
+            o[mt][n][3] *= c1;
+          }
+          m[mt][0] = top0;
+          m[mt][1] = top1;
+        }
+#pragma unroll
+        for (int n = 0; n < NT / 8; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            s[mt][n][x] = exp2_fast(s[mt][n][x] - base0 + C::kShift);
+            s[mt][n][2 + x] = exp2_fast(s[mt][n][2 + x] - base1 + C::kShift);
+            l[mt][0] += s[mt][n][x];
+            l[mt][1] += s[mt][n][2 + x];
+          }
+      }
+      // O += P V, 16 tokens at a time
+      const bool split = !kFp8 || p.q_f16;
+#pragma unroll
+      for (int n = 0; n < NT / 16; ++n) {
+        uint32_t hi[MT][4], lo[MT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int n = 0; n < NT / 8; ++n)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) s[mt][n][x] = 0.f;
+          for (int x = 0; x < 4; ++x) {
+            const float* w = &s[mt][2 * n + (x >> 1)][(x & 1) * 2];
+            if constexpr (C::kBf16) {
+              const uint32_t c0 = __float_as_uint(w[0] * (1.f - 0x1p-8f)), c1 = __float_as_uint(w[1] * (1.f - 0x1p-8f));
+              hi[mt][x] = prmt(c0, c1, 0x7632);
+              lo[mt][x] = pack2<__nv_bfloat16>(w[0] - __uint_as_float(c0 & 0xFFFF0000u),
+                                               w[1] - __uint_as_float(c1 & 0xFFFF0000u));
+            } else if (split) {
+              const __half2 c = __halves2half2(__float2half_rz(w[0] * (1.f - 0x1p-10f)),
+                                               __float2half_rz(w[1] * (1.f - 0x1p-10f)));
+              hi[mt][x] = *reinterpret_cast<const uint32_t*>(&c);
+              lo[mt][x] = pack2<__half>(w[0] - __low2float(c), w[1] - __high2float(c));
+            } else {
+              hi[mt][x] = pack2<__half>(w[0], w[1]);
+            }
+          }
         if constexpr (!kFp8) {
 #pragma unroll
-          for (int kk = 0; kk < DT / 16; ++kk) {
-            uint32_t a[MT][4];
+          for (int c = 0; c < DT / 16; ++c) {
+            uint32_t b[4];  // d 0-7: tokens 0-7 and 8-15; d 8-15 likewise
+            ldsm4_t(b, vt + C::at(n * 16 + (lane & 15), 2 * c + (lane >> 4)));
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              ldsm4(a[mt], q_s + (mt * 16 + (lane & 15)) * C::kQRow + kk * 32 + (lane >> 4) * 16);
-#pragma unroll
-            for (int n = 0; n < NT / 16; ++n) {
-              uint32_t b[4];  // tokens 0-7 and 8-15, d 0-7 and 8-15 each
-              ldsm4(b, kt + C::at(n * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                mma16816<C::kBf16>(s[mt][2 * n], a[mt], b[0], b[1]);
-                mma16816<C::kBf16>(s[mt][2 * n + 1], a[mt], b[2], b[3]);
-              }
+            for (int mt = 0; mt < MT; ++mt) {
+              mma16816<C::kBf16>(o[mt][2 * c], hi[mt], b[0], b[1]);
+              mma16816<C::kBf16>(o[mt][2 * c + 1], hi[mt], b[2], b[3]);
+              mma16816<C::kBf16>(o[mt][2 * c], lo[mt], b[0], b[1]);
+              mma16816<C::kBf16>(o[mt][2 * c + 1], lo[mt], b[2], b[3]);
             }
           }
         } else {
 #pragma unroll
-          for (int kk = 0; kk < DT / 32; ++kk) {
-            uint32_t a[2][MT][4];
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-                ldsm4(a[x][mt], q_s + (mt * 16 + (lane & 15)) * C::kQRow + (2 * kk + x) * 32 + (lane >> 4) * 16);
-#pragma unroll
-            for (int n = 0; n < NT / 16; ++n) {
-              uint32_t b[4];  // tokens 0-7 and 8-15, d 0-15 and 16-31 each
-              ldsm4(b, kt + C::at(n * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const uint32_t b0 = f16x2_of_e4m3x2(b[x]), b1 = f16x2_of_e4m3x2(b[x] >> 16);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) mma16816<false>(s[mt][2 * n + (x >> 1)], a[x & 1][mt], b0, b1);
-              }
-            }
-          }
-        }
-        // running maximum and sum, weights
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const float f0 = row_scale[mt * 16 + g], f1 = row_scale[mt * 16 + g + 8];
-          float top0 = m[mt][0], top1 = m[mt][1];
-#pragma unroll
-          for (int n = 0; n < NT / 8; ++n) {
+          for (int c = 0; c < DT / 32; ++c) {
+            uint32_t b[4];  // d 0-15: tokens 0-7 and 8-15; d 16-31 likewise; each word two tokens of two neighbours
+            ldsm4_t(b, vt + C::at(n * 16 + (lane & 15), 2 * c + (lane >> 4)));
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const bool in = n * 8 + j2 + x < left;
-              s[mt][n][x] = in ? s[mt][n][x] * f0 : -INFINITY;
-              s[mt][n][2 + x] = in ? s[mt][n][2 + x] * f1 : -INFINITY;
-              top0 = fmaxf(top0, s[mt][n][x]);
-              top1 = fmaxf(top1, s[mt][n][2 + x]);
-            }
-          }
-          top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 1));
-          top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
-          top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 2));
-          top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 2));
-          const float base0 = top0 == -INFINITY ? 0.f : top0, base1 = top1 == -INFINITY ? 0.f : top1;
-          if (__any_sync(0xffffffffu, top0 > m[mt][0] || top1 > m[mt][1])) {
-            const float c0 = exp2_fast(m[mt][0] - base0), c1 = exp2_fast(m[mt][1] - base1);
-            l[mt][0] *= c0;
-            l[mt][1] *= c1;
+              const uint32_t w0 = prmt(b[2 * x], 0, 0x3120), w1 = prmt(b[2 * x + 1], 0, 0x3120);
+              const uint32_t e0 = f16x2_of_e4m3x2(w0), e1 = f16x2_of_e4m3x2(w1);
+              const uint32_t d0 = f16x2_of_e4m3x2(w0 >> 16), d1 = f16x2_of_e4m3x2(w1 >> 16);
 #pragma unroll
-            for (int n = 0; n < kNt; ++n) {
-              o[mt][n][0] *= c0;
-              o[mt][n][1] *= c0;
-              o[mt][n][2] *= c1;
-              o[mt][n][3] *= c1;
-            }
-            m[mt][0] = top0;
-            m[mt][1] = top1;
-          }
-#pragma unroll
-          for (int n = 0; n < NT / 8; ++n)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              s[mt][n][x] = exp2_fast(s[mt][n][x] - base0 + C::kShift);
-              s[mt][n][2 + x] = exp2_fast(s[mt][n][2 + x] - base1 + C::kShift);
-              l[mt][0] += s[mt][n][x];
-              l[mt][1] += s[mt][n][2 + x];
-            }
-        }
-        // O += P V, 16 tokens at a time
-        const bool split = !kFp8 || p.q_f16;
-#pragma unroll
-        for (int n = 0; n < NT / 16; ++n) {
-          uint32_t hi[MT][4], lo[MT][4];
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float* w = &s[mt][2 * n + (x >> 1)][(x & 1) * 2];
-              if constexpr (C::kBf16) {
-                const uint32_t c0 = __float_as_uint(w[0] * (1.f - 0x1p-8f)), c1 = __float_as_uint(w[1] * (1.f - 0x1p-8f));
-                hi[mt][x] = prmt(c0, c1, 0x7632);
-                lo[mt][x] = pack2<__nv_bfloat16>(w[0] - __uint_as_float(c0 & 0xFFFF0000u),
-                                                 w[1] - __uint_as_float(c1 & 0xFFFF0000u));
-              } else if (split) {
-                const __half2 c = __halves2half2(__float2half_rz(w[0] * (1.f - 0x1p-10f)),
-                                                 __float2half_rz(w[1] * (1.f - 0x1p-10f)));
-                hi[mt][x] = *reinterpret_cast<const uint32_t*>(&c);
-                lo[mt][x] = pack2<__half>(w[0] - __low2float(c), w[1] - __high2float(c));
-              } else {
-                hi[mt][x] = pack2<__half>(w[0], w[1]);
-              }
-            }
-          if constexpr (!kFp8) {
-#pragma unroll
-            for (int c = 0; c < DT / 16; ++c) {
-              uint32_t b[4];  // d 0-7: tokens 0-7 and 8-15; d 8-15 likewise
-              ldsm4_t(b, vt + C::at(n * 16 + (lane & 15), 2 * c + (lane >> 4)));
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                mma16816<C::kBf16>(o[mt][2 * c], hi[mt], b[0], b[1]);
-                mma16816<C::kBf16>(o[mt][2 * c + 1], hi[mt], b[2], b[3]);
-                mma16816<C::kBf16>(o[mt][2 * c], lo[mt], b[0], b[1]);
-                mma16816<C::kBf16>(o[mt][2 * c + 1], lo[mt], b[2], b[3]);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < DT / 32; ++c) {
-              uint32_t b[4];  // d 0-15: tokens 0-7 and 8-15; d 16-31 likewise; each word two tokens of two neighbours
-              ldsm4_t(b, vt + C::at(n * 16 + (lane & 15), 2 * c + (lane >> 4)));
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const uint32_t w0 = prmt(b[2 * x], 0, 0x3120), w1 = prmt(b[2 * x + 1], 0, 0x3120);
-                const uint32_t e0 = f16x2_of_e4m3x2(w0), e1 = f16x2_of_e4m3x2(w1);
-                const uint32_t d0 = f16x2_of_e4m3x2(w0 >> 16), d1 = f16x2_of_e4m3x2(w1 >> 16);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {  // even and odd d
-                  mma16816<false>(o[mt][4 * c + 2 * x], hi[mt], e0, e1);
-                  mma16816<false>(o[mt][4 * c + 2 * x + 1], hi[mt], d0, d1);
-                  if (split) {
-                    mma16816<false>(o[mt][4 * c + 2 * x], lo[mt], e0, e1);
-                    mma16816<false>(o[mt][4 * c + 2 * x + 1], lo[mt], d0, d1);
-                  }
+              for (int mt = 0; mt < MT; ++mt) {  // even and odd d
+                mma16816<false>(o[mt][4 * c + 2 * x], hi[mt], e0, e1);
+                mma16816<false>(o[mt][4 * c + 2 * x + 1], hi[mt], d0, d1);
+                if (split) {
+                  mma16816<false>(o[mt][4 * c + 2 * x], lo[mt], e0, e1);
+                  mma16816<false>(o[mt][4 * c + 2 * x + 1], lo[mt], d0, d1);
                 }
               }
             }
@@ -527,173 +557,166 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
       __syncwarp();  // the tile's slot is free
     }
 
-    // --- join the warps: rows brought to the common maximum, added up in the order (0 + 2) + (1 + 3) ---
+    // --- the item's rows, or this warp's part of them ---
+    const int64_t part = ((static_cast<int64_t>(warp) * gridDim.x + blockIdx.x) * 2 + (first ? 0 : 1)) * C::kRows;
+    const float vs = kFp8 && p.v_scale ? p.v_scale[h] : 1.f;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 1);
-        l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 2);
-        if ((lane & 3) == 0) join_ml[warp * C::kRows + mt * 16 + g + 8 * x] = make_float2(m[mt][x], l[mt][x]);
-      }
-    __syncthreads();
-    float top[MT][2], sum[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float2 ml[kWarps];
-        float t = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          ml[w] = join_ml[w * C::kRows + mt * 16 + g + 8 * x];
-          t = fmaxf(t, ml[w].x);
+        float sum = l[mt][x];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const int r = mt * 16 + g + 8 * x;
+        if (r >= live) continue;
+        const float top = m[mt][x], inv = sum == 0.f ? 0.f : vs / sum;
+        if ((lane & 3) == 0) {
+          if (!whole)
+            p.part_ml[part + r] = make_float2(top, sum);
+          else if (p.lse)
+            p.lse[static_cast<int64_t>(here.b) * p.Hq + head0 + r] =
+                sum == 0.f ? -INFINITY : (top - C::kShift + log2f(sum)) * kLn2;
         }
-        const float base = t == -INFINITY ? 0.f : t;
-        float r = 0.f;
+        const int64_t out = here.b * p.o_b + (head0 + r) * p.o_h;
+        if constexpr (kFp8) {  // fragments n and n + 1 hold the even and odd ones of 16 columns: four neighbours to a lane
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) r += ml[w].y * exp2_fast(ml[w].x - base);
-        const float c = exp2_fast(m[mt][x] - base);
-#pragma unroll
-        for (int n = 0; n < kNt; ++n) {
-          o[mt][n][2 * x] *= c;
-          o[mt][n][2 * x + 1] *= c;
-        }
-        top[mt][x] = t;
-        sum[mt][x] = r;
-      }
-    // Through the slot that the sender read last: its next copy is issued behind the next run's first barrier.
-    const int last = stage == 0 ? kStages - 1 : stage - 1;
-    const auto exchange = [&](int from, int mt, bool take) {
-      float2* buf = reinterpret_cast<float2*>(smem + (from * kStages + last) * C::kStage) + lane;
-#pragma unroll
-      for (int n = 0; n < kNt; ++n)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float2* at = buf + (n * 2 + x) * 32;
-          if (take) {
-            const float2 v = *at;
-            o[mt][n][2 * x] += v.x;
-            o[mt][n][2 * x + 1] += v.y;
-          } else {
-            *at = make_float2(o[mt][n][2 * x], o[mt][n][2 * x + 1]);
-          }
-        }
-    };
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      if (mt > 0) __syncthreads();
-      if (warp >= 2) exchange(warp, mt, false);
-      __syncthreads();
-      if (warp < 2) exchange(warp + 2, mt, true);
-      if (warp == 1) exchange(1, mt, false);
-      __syncthreads();
-      if (warp == 0) exchange(1, mt, true);
-    }
-    if (warp == 0) {
-      const int slot_of = done == 0 ? 0 : 1;
-      const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot_of) * C::kRows;
-      const float vs = kFp8 && p.v_scale ? p.v_scale[h] : 1.f;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int r = mt * 16 + g + 8 * x;
-          if (r >= live) continue;
-          const float inv = sum[mt][x] == 0.f ? 0.f : vs / sum[mt][x];
-          if ((lane & 3) == 0) {
+          for (int n = 0; n < kNt; n += 2) {
+            const int d = n * 8 + 2 * j2;
+            const float v0 = o[mt][n][2 * x], v1 = o[mt][n + 1][2 * x], v2 = o[mt][n][2 * x + 1], v3 = o[mt][n + 1][2 * x + 1];
+            if (d >= p.D) continue;
             if (whole) {
-              if (p.lse)
-                p.lse[static_cast<int64_t>(here.b) * p.Hq + head0 + r] =
-                    sum[mt][x] == 0.f ? -INFINITY : (top[mt][x] - C::kShift + log2f(sum[mt][x])) * kLn2;
+              store_out(p.out, out + d, v0 * inv, v1 * inv, bf16_out);
+              store_out(p.out, out + d + 2, v2 * inv, v3 * inv, bf16_out);
             } else {
-              p.part_ml[part + r] = make_float2(top[mt][x], sum[mt][x]);
+              *reinterpret_cast<float4*>(p.part_o + (part + r) * p.D + d) = make_float4(v0, v1, v2, v3);
             }
           }
-          const int64_t out = here.b * p.o_b + (head0 + r) * p.o_h;
+        } else {
 #pragma unroll
-          for (int n = 0; n < kNt; ++n)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              // with E4M3 the fragments hold even and odd columns of 16
-              const int d = kFp8 ? (n >> 1) * 16 + 2 * (j2 + y) + (n & 1) : n * 8 + j2 + y;
-              const float val = o[mt][n][2 * x + y];
-              if (d >= p.D) continue;
-              if (!whole)
-                p.part_o[(part + r) * p.D + d] = val;
-              else if (C::kBf16 || (kFp8 && !p.q_f16))
-                static_cast<__nv_bfloat16*>(p.out)[out + d] = __float2bfloat16_rn(val * inv);
-              else
-                static_cast<__half*>(p.out)[out + d] = __float2half_rn(val * inv);
-            }
+          for (int n = 0; n < kNt; ++n) {
+            const int d = n * 8 + j2;
+            if (d >= p.D) continue;
+            if (whole)
+              store_out(p.out, out + d, o[mt][n][2 * x] * inv, o[mt][n][2 * x + 1] * inv, bf16_out);
+            else
+              *reinterpret_cast<float2*>(p.part_o + (part + r) * p.D + d) = make_float2(o[mt][n][2 * x], o[mt][n][2 * x + 1]);
+          }
         }
-    }
-    done += run;
+      }
+    first = false;
     here.u += run - 1;
-    if (done < count) advance(here);
+    here.left -= run - 1;
+    advance(here);
   }
 }
 
-// Joins the parts of what several blocks computed: a block for (sequence, head, group), its threads as [parts'
-// turns][rows][columns in fours].  Empty sequences get zeros here.
-constexpr int kJoinThreads = 256;
-template <int KIND, int DT, int MT>
-__global__ void __launch_bounds__(kJoinThreads) paged_attention_join_kernel(const __grid_constant__ AttendParams p) {
+// Joins the parts of the items that several warps shared, in the warps' order: WPR warps to a row (sequence, query head),
+// each a range of the parts.  Empty sequences get zeros here.
+constexpr int kJoinWarps = 8;
+template <int KIND, int DT, int MT, int WPR>
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_attention_join_kernel(const __grid_constant__ AttendParams p) {
   using C = AttendCfg<KIND, DT, MT>;
+  constexpr int kV = (DT + 127) / 128;  // float4 of a lane
   pdl_trigger();
   pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kJoinWarps / WPR) + warp / WPR;
+  if (row >= static_cast<int64_t>(p.B) * p.Hq) return;  // with WPR > 1 the whole block
+  const int b = static_cast<int>(row / p.Hq), head = static_cast<int>(row - static_cast<int64_t>(b) * p.Hq);
+  const int h = head / p.G, in = head - h * p.G, hh = h * p.HB + in / C::kRows, r = in % C::kRows;
   const int HH = p.Hkv * p.HB;
-  const int64_t item = blockIdx.x;
-  const int b = static_cast<int>(item / HH), hh = static_cast<int>(item - static_cast<int64_t>(b) * HH);
-  const int64_t first = p.prefix[b], units = (p.prefix[b + 1] - first) / HH, total = p.prefix[p.B];
-  const int h = hh / p.HB, head0 = h * p.G + (hh % p.HB) * C::kRows;
-  const int live = min(C::kRows, (h + 1) * p.G - head0);
+  const int64_t before = p.prefix[b], each = (p.prefix[b + 1] - before) / HH, total = p.prefix[p.B];
   const bool bf16 = C::kBf16 || (C::kFp8 && !p.q_f16);
-  const auto store = [&](int r, int d, float v) {
-    const int64_t at = b * p.o_b + (head0 + r) * p.o_h + d;
-    if (bf16)
-      static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
-    else
-      static_cast<__half*>(p.out)[at] = __float2half_rn(v);
-  };
-  if (units == 0) {
-    for (int i = threadIdx.x; i < live * p.D; i += kJoinThreads) store(i / p.D, i % p.D, 0.f);
-    if (p.lse)
-      for (int r = threadIdx.x; r < live; r += kJoinThreads) p.lse[static_cast<int64_t>(b) * p.Hq + head0 + r] = -INFINITY;
+  const int64_t out = b * p.o_b + head * p.o_h;
+  if (each == 0) {
+    if (warp % WPR) return;
+    for (int d = lane; d < p.D; d += 32) static_cast<uint16_t*>(p.out)[out + d] = 0;  // bf16's and f16's zero
+    if (p.lse && lane == 0) p.lse[row] = -INFINITY;
     return;
   }
-  const int64_t i0 = first + hh * units, i1 = i0 + units;
-  const int64_t runs = min(total, static_cast<int64_t>(p.blocks));
-  // the block that has unit t: start(c) = floor(c total / runs) <= t < start(c + 1)
-  const int c0 = static_cast<int>(((i0 + 1) * runs - 1) / total), c1 = static_cast<int>((i1 * runs - 1) / total);
-  if (c0 == c1) return;  // written by its only block
-  const bool starts = c0 * total / runs == i0;  // the first part is its block's first run
-  const float vs = C::kFp8 && p.v_scale ? p.v_scale[h] : 1.f;
-  for (int i = threadIdx.x; i < live * (p.D / 4); i += kJoinThreads) {
-    const int r = i / (p.D / 4), d = i % (p.D / 4) * 4;
-    float top = -INFINITY, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; ++c) {
-      const int64_t part = (static_cast<int64_t>(c) * 2 + (c == c0 && !starts ? 1 : 0)) * C::kRows + r;
-      const float2 ml = p.part_ml[part];
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + part * p.D + d);
-      const float t = fmaxf(top, ml.x), base = t == -INFINITY ? 0.f : t;
-      const float old = exp2_fast(top - base), now = exp2_fast(ml.x - base);
-      sum = sum * old + ml.y * now;
-      acc.x = acc.x * old + v.x * now;
-      acc.y = acc.y * old + v.y * now;
-      acc.z = acc.z * old + v.z * now;
-      acc.w = acc.w * old + v.w * now;
-      top = t;
+  const int64_t i0 = before + hh * each, runs = runs_of(p, total);
+  const int64_t c0 = ((i0 + kExtra + 1) * runs - 1) / total, c1 = ((i0 + each) * runs - 1) / total;
+  if (c0 == c1) return;  // written by its only warp
+  const int skip = c0 * total / runs >= i0 ? 0 : 1;  // whether the item is behind another one in its first warp's run
+  const int parts = static_cast<int>(c1 - c0) + 1, w = warp % WPR;
+  const int from = static_cast<int>(static_cast<int64_t>(w) * parts / WPR), to = static_cast<int>(static_cast<int64_t>(w + 1) * parts / WPR);
+  const auto at = [&](int i) { return ((c0 + i) * 2 + (i == 0 ? skip : 0)) * C::kRows + r; };
+  float top = -INFINITY, sum = 0.f;
+  float4 acc[kV];
+#pragma unroll
+  for (int x = 0; x < kV; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0_ = from; i0_ < to; i0_ += 32) {  // 32 parts at a time, one maximum and sum to a lane
+    const float2 ml = i0_ + lane < to ? p.part_ml[at(i0_ + lane)] : make_float2(-INFINITY, 0.f);
+    const float t = fmaxf(top, warp_max(ml.x)), base = t == -INFINITY ? 0.f : t;
+    const float old = exp2_fast(top - base), now = exp2_fast(ml.x - base);
+    sum = sum * old + warp_sum(ml.y * now);
+#pragma unroll
+    for (int x = 0; x < kV; ++x) acc[x].x *= old, acc[x].y *= old, acc[x].z *= old, acc[x].w *= old;
+    top = t;
+    const int n = min(32, to - i0_);
+    constexpr int kAhead = kV == 1 ? 8 : 4;
+#pragma unroll 1
+    for (int j = 0; j < n; j += kAhead) {
+      float4 v[kAhead][kV];
+#pragma unroll
+      for (int y = 0; y < kAhead; ++y)
+#pragma unroll
+        for (int x = 0; x < kV; ++x) {
+          const int d = (x * 32 + lane) * 4;
+          v[y][x] = j + y < n && d < p.D ? *reinterpret_cast<const float4*>(p.part_o + at(i0_ + j + y) * p.D + d)
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+      for (int y = 0; y < kAhead; ++y) {
+        const float f = __shfl_sync(0xffffffffu, now, (j + y) & 31);
+        if (j + y >= n) continue;
+#pragma unroll
+        for (int x = 0; x < kV; ++x) {
+          acc[x].x = fmaf(v[y][x].x, f, acc[x].x);
+          acc[x].y = fmaf(v[y][x].y, f, acc[x].y);
+          acc[x].z = fmaf(v[y][x].z, f, acc[x].z);
+          acc[x].w = fmaf(v[y][x].w, f, acc[x].w);
+        }
+      }
     }
-    const float inv = sum == 0.f ? 0.f : vs / sum;
-    store(r, d, acc.x * inv);
-    store(r, d + 1, acc.y * inv);
-    store(r, d + 2, acc.z * inv);
-    store(r, d + 3, acc.w * inv);
-    if (p.lse && d == 0)
-      p.lse[static_cast<int64_t>(b) * p.Hq + head0 + r] = sum == 0.f ? -INFINITY : (top - C::kShift + log2f(sum)) * kLn2;
   }
+  if constexpr (WPR > 1) {
+    static_assert(WPR == kJoinWarps, "a block to a row");
+    __shared__ float2 all_ml[WPR];
+    __shared__ float4 all_o[WPR][kV][32];
+    if (lane == 0) all_ml[w] = make_float2(top, sum);
+#pragma unroll
+    for (int x = 0; x < kV; ++x) all_o[w][x][lane] = acc[x];
+    __syncthreads();
+    if (w) return;
+    for (int y = 1; y < WPR; ++y) top = fmaxf(top, all_ml[y].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    sum = 0.f;
+#pragma unroll
+    for (int x = 0; x < kV; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int y = 0; y < WPR; ++y) {
+      const float f = exp2_fast(all_ml[y].x - base);
+      sum += all_ml[y].y * f;
+#pragma unroll
+      for (int x = 0; x < kV; ++x) {
+        const float4 v = all_o[y][x][lane];
+        acc[x].x = fmaf(v.x, f, acc[x].x);
+        acc[x].y = fmaf(v.y, f, acc[x].y);
+        acc[x].z = fmaf(v.z, f, acc[x].z);
+        acc[x].w = fmaf(v.w, f, acc[x].w);
+      }
+    }
+  }
+  const float vs = C::kFp8 && p.v_scale ? p.v_scale[h] : 1.f, inv = sum == 0.f ? 0.f : vs / sum;
+#pragma unroll
+  for (int x = 0; x < kV; ++x) {
+    const int d = (x * 32 + lane) * 4;
+    if (d >= p.D) continue;
+    store_out(p.out, out + d, acc[x].x * inv, acc[x].y * inv, bf16);
+    store_out(p.out, out + d + 2, acc[x].z * inv, acc[x].w * inv, bf16);
+  }
+  if (p.lse && lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top - C::kShift + log2f(sum)) * kLn2;
 }
 
 template <int KIND, int DT, int MT>
@@ -708,12 +731,17 @@ int launch_attend(AttendParams p, cudaStream_t st) {
       }))
     return rc;
   p.HB = static_cast<int>(ceil_div(p.G, C::kRows));
-  p.blocks = num_sms() * C::kBlocks;
-  if (int rc = launch_pdl("paged_attention_kernel", paged_attention_kernel<KIND, DT, MT>, dim3(p.blocks),
+  p.warps = attend_warps(DT);
+  if (int rc = launch_pdl("paged_attention_kernel", paged_attention_kernel<KIND, DT, MT>, dim3(p.warps / kWarps),
                           dim3(kWarps * 32), C::kSmem, st, p))
     return rc;
-  return launch_pdl("paged_attention_join_kernel", paged_attention_join_kernel<KIND, DT, MT>,
-                    dim3(static_cast<unsigned>(static_cast<int64_t>(p.B) * p.Hkv * p.HB)), dim3(kJoinThreads), 0, st, p);
+  // A row with more parts than a warp asks for at once is shared by a block's warps.
+  const int64_t rows = static_cast<int64_t>(p.B) * p.Hq;
+  if (static_cast<int64_t>(p.B) * p.Hkv * p.HB * 8 < p.warps)
+    return launch_pdl("paged_attention_join_kernel", paged_attention_join_kernel<KIND, DT, MT, kJoinWarps>,
+                      dim3(static_cast<unsigned>(rows)), dim3(kJoinWarps * 32), 0, st, p);
+  return launch_pdl("paged_attention_join_kernel", paged_attention_join_kernel<KIND, DT, MT, 1>,
+                    dim3(static_cast<unsigned>(ceil_div(rows, kJoinWarps))), dim3(kJoinWarps * 32), 0, st, p);
 }
 
 template <int KIND>
