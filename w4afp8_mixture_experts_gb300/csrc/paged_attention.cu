@@ -93,6 +93,7 @@ extern "C" int paged_attention_decode(const void* q, int64_t ldq_b, int64_t ldq_
   p.by_page = FastDiv(cache->page_size);
   p.q_f16 = dtype == W4A8_DTYPE_F16;
   p.q_vec = (bits_of(q) | static_cast<uint64_t>(ldq_b | ldq_h) * 2) % 16 == 0;
+  p.out_pair = (bits_of(out) | static_cast<uint64_t>(ldo_b | ldo_h) * 2) % 4 == 0;
   p.same_places = p.k_page == p.v_page && p.k_slot == p.v_slot && p.k_head == p.v_head;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (fp8) return launch_attend_fp8(p, st);

@@ -46,7 +46,7 @@ struct AttendParams {
   int warps, window;
   float scale;                       // times log2 e
   FastDiv by_page;
-  bool q_f16, q_vec, same_places;    // 16-byte loads of q; keys and values lie alike
+  bool q_f16, q_vec, out_pair, same_places;  // 16-byte loads of q, 4-byte stores; keys and values lie alike
 };
 
 int launch_attend_bf16(const AttendParams& p, cudaStream_t st);
@@ -128,7 +128,6 @@ struct AttendCfg {
   static constexpr int kBlocks = DT <= 128 ? 2 : 1;     // of an SM
   static_assert((kSmem + 1024) * kBlocks <= 228 * 1024, "shared memory");
   static_assert(kWarpBytes % 128 == 0 && kRows * 4 <= 128, "tiles on 128 bytes");
-  static_assert(kSmem >= (kWarps * 32 + 1) * 8, "room for the prefix");
   // place of 16-byte chunk c of row r: chunks are exchanged within 128 bytes so that 8 rows at one column lie in
   // different banks
   static __device__ __forceinline__ uint32_t at(int r, int c) {
@@ -171,10 +170,14 @@ struct Cursor {
   int left;
 };
 
-// Two fp32 columns of a row of the output.
-__device__ __forceinline__ void store_out(void* out, int64_t at, float x, float y, bool bf16) {
+// Two fp32 columns of a row of the output; `pair`: in one store.
+__device__ __forceinline__ void store_out(void* out, int64_t at, float x, float y, bool bf16, bool pair) {
   uint16_t* o = static_cast<uint16_t*>(out) + at;
   const uint32_t w = bf16 ? pack2<__nv_bfloat16>(x, y) : pack2<__half>(x, y);
+  if (pair) {
+    *reinterpret_cast<uint32_t*>(o) = w;
+    return;
+  }
   o[0] = static_cast<uint16_t>(w);
   o[1] = static_cast<uint16_t>(w >> 16);
 }
@@ -186,57 +189,57 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
   constexpr int NT = C::NT, kStages = C::kStages;
   constexpr bool kFp8 = C::kFp8;
   extern __shared__ __align__(128) uint8_t smem_all[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   pdl_wait();
 
-  // places before each thread's sequences; the first block leaves those of every sequence for the second kernel
-  const int HH = p.Hkv * p.HB, per = (p.B + kWarps * 32 - 1) / (kWarps * 32);
-  int64_t* before = reinterpret_cast<int64_t*>(smem_all);  // [threads + 1], until the rings are filled
-  int64_t total, start, stop, at_seq;
+  // Places before each lane's sequences: every warp adds them up for itself (no barrier; the lengths come from L1 after the
+  // first warp).  The first leaves those of every sequence for the second kernel.
+  const int HH = p.Hkv * p.HB, per = (p.B + 31) / 32;
+  const int64_t run_id = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
+  int64_t start, stop, at_seq;
   Cursor here;  // of the tile that is computed next
   {
+    const int b0 = lane * per, b1 = min(p.B, b0 + per);
     int64_t mine = 0;
-    for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) mine += places_of(span_of<NT>(p, b), HH);
+    SeqSpan s = {0, 0, 0};
+    for (int b = b0; b < b1; ++b) {
+      s = span_of<NT>(p, b);
+      mine += places_of(s, HH);
+    }
     int64_t up = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t x = __shfl_up_sync(0xffffffffu, up, o);
       if (lane >= o) up += x;
     }
-    if (lane == 31) before[warp] = up;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) up += before[w];
-    __syncthreads();
-    before[tid + 1] = up;
-    if (tid == 0) before[0] = 0;
-    __syncthreads();
-    if (blockIdx.x == 0) {
+    const int64_t total = __shfl_sync(0xffffffffu, up, 31);
+    if (run_id == 0) {
       int64_t at = up - mine;
-      for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) {
+      for (int b = b0; b < b1; ++b) {
         p.prefix[b] = at;
-        at += places_of(span_of<NT>(p, b), HH);
+        at += per == 1 ? mine : places_of(span_of<NT>(p, b), HH);
       }
-      if (tid == kWarps * 32 - 1) p.prefix[p.B] = up;
+      if (lane == 31) p.prefix[p.B] = up;
     }
-    total = before[kWarps * 32];
-    const int64_t runs = runs_of(p, total), run = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
-    const bool mine_too = run < runs;
-    start = mine_too ? run * total / runs : 0;
-    stop = mine_too ? (run + 1) * total / runs : 0;
-    int c = 0;  // the last thread whose sequences begin at or before start
-#pragma unroll
-    for (int step = kWarps * 16; step > 0; step >>= 1)
-      if (before[c + step] <= start) c += step;
-    at_seq = before[c];
+    const int64_t runs = runs_of(p, total);
+    if (run_id >= runs) return;
+    start = run_id * total / runs;
+    stop = (run_id + 1) * total / runs;
+    const int c = __popc(__ballot_sync(0xffffffffu, up <= start));  // the lane that has place `start`
+    at_seq = __shfl_sync(0xffffffffu, up - mine, c);
     here.b = c * per;
-    __syncthreads();  // the rings may be filled
-  }
-  if (start >= stop) return;
-  here.s = span_of<NT>(p, here.b);
-  while (at_seq + places_of(here.s, HH) <= start) {
-    at_seq += places_of(here.s, HH);
-    here.s = span_of<NT>(p, ++here.b);
+    if (per == 1) {
+      here.s.lo = __shfl_sync(0xffffffffu, s.lo, c);
+      here.s.hi = __shfl_sync(0xffffffffu, s.hi, c);
+      here.s.tiles = __shfl_sync(0xffffffffu, s.tiles, c);
+    } else {
+      here.s = span_of<NT>(p, here.b);
+      while (at_seq + places_of(here.s, HH) <= start) {
+        at_seq += places_of(here.s, HH);
+        here.s = span_of<NT>(p, ++here.b);
+      }
+    }
   }
   {
     const int64_t in = start - at_seq, each = here.s.tiles + kExtra;
@@ -558,7 +561,7 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
     }
 
     // --- the item's rows, or this warp's part of them ---
-    const int64_t part = ((static_cast<int64_t>(warp) * gridDim.x + blockIdx.x) * 2 + (first ? 0 : 1)) * C::kRows;
+    const int64_t part = (run_id * 2 + (first ? 0 : 1)) * C::kRows;
     const float vs = kFp8 && p.v_scale ? p.v_scale[h] : 1.f;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -585,8 +588,8 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
             const float v0 = o[mt][n][2 * x], v1 = o[mt][n + 1][2 * x], v2 = o[mt][n][2 * x + 1], v3 = o[mt][n + 1][2 * x + 1];
             if (d >= p.D) continue;
             if (whole) {
-              store_out(p.out, out + d, v0 * inv, v1 * inv, bf16_out);
-              store_out(p.out, out + d + 2, v2 * inv, v3 * inv, bf16_out);
+              store_out(p.out, out + d, v0 * inv, v1 * inv, bf16_out, p.out_pair);
+              store_out(p.out, out + d + 2, v2 * inv, v3 * inv, bf16_out, p.out_pair);
             } else {
               *reinterpret_cast<float4*>(p.part_o + (part + r) * p.D + d) = make_float4(v0, v1, v2, v3);
             }
@@ -597,7 +600,7 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
             const int d = n * 8 + j2;
             if (d >= p.D) continue;
             if (whole)
-              store_out(p.out, out + d, o[mt][n][2 * x] * inv, o[mt][n][2 * x + 1] * inv, bf16_out);
+              store_out(p.out, out + d, o[mt][n][2 * x] * inv, o[mt][n][2 * x + 1] * inv, bf16_out, p.out_pair);
             else
               *reinterpret_cast<float2*>(p.part_o + (part + r) * p.D + d) = make_float2(o[mt][n][2 * x], o[mt][n][2 * x + 1]);
           }
@@ -645,27 +648,31 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_attention_join_kernel(c
   float4 acc[kV];
 #pragma unroll
   for (int x = 0; x < kV; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0_ = from; i0_ < to; i0_ += 32) {  // 32 parts at a time, one maximum and sum to a lane
-    const float2 ml = i0_ + lane < to ? p.part_ml[at(i0_ + lane)] : make_float2(-INFINITY, 0.f);
+  constexpr int kAhead = kV == 1 ? 10 : 5;  // parts of O asked for at a time
+  float4 v[kAhead][kV];
+  const auto load = [&](int i) {
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y)
+#pragma unroll
+      for (int x = 0; x < kV; ++x) {
+        const int d = (x * 32 + lane) * 4;
+        v[y][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i + y < to && d < p.D) v[y][x] = *reinterpret_cast<const float4*>(p.part_o + at(i + y) * p.D + d);
+      }
+  };
+  for (int f0 = from; f0 < to; f0 += 32) {  // 32 parts at a time, one maximum and sum to a lane
+    load(f0);  // on its way together with the maxima
+    const float2 ml = f0 + lane < to ? p.part_ml[at(f0 + lane)] : make_float2(-INFINITY, 0.f);
     const float t = fmaxf(top, warp_max(ml.x)), base = t == -INFINITY ? 0.f : t;
     const float old = exp2_fast(top - base), now = exp2_fast(ml.x - base);
     sum = sum * old + warp_sum(ml.y * now);
 #pragma unroll
     for (int x = 0; x < kV; ++x) acc[x].x *= old, acc[x].y *= old, acc[x].z *= old, acc[x].w *= old;
     top = t;
-    const int n = min(32, to - i0_);
-    constexpr int kAhead = kV == 1 ? 8 : 4;
+    const int n = min(32, to - f0);
 #pragma unroll 1
     for (int j = 0; j < n; j += kAhead) {
-      float4 v[kAhead][kV];
-#pragma unroll
-      for (int y = 0; y < kAhead; ++y)
-#pragma unroll
-        for (int x = 0; x < kV; ++x) {
-          const int d = (x * 32 + lane) * 4;
-          v[y][x] = j + y < n && d < p.D ? *reinterpret_cast<const float4*>(p.part_o + at(i0_ + j + y) * p.D + d)
-                                         : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+      if (j > 0) load(f0 + j);
 #pragma unroll
       for (int y = 0; y < kAhead; ++y) {
         const float f = __shfl_sync(0xffffffffu, now, (j + y) & 31);
@@ -713,8 +720,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_attention_join_kernel(c
   for (int x = 0; x < kV; ++x) {
     const int d = (x * 32 + lane) * 4;
     if (d >= p.D) continue;
-    store_out(p.out, out + d, acc[x].x * inv, acc[x].y * inv, bf16);
-    store_out(p.out, out + d + 2, acc[x].z * inv, acc[x].w * inv, bf16);
+    store_out(p.out, out + d, acc[x].x * inv, acc[x].y * inv, bf16, p.out_pair);
+    store_out(p.out, out + d + 2, acc[x].z * inv, acc[x].w * inv, bf16, p.out_pair);
   }
   if (p.lse && lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top - C::kShift + log2f(sum)) * kLn2;
 }
