@@ -46,12 +46,12 @@ struct AttendParams {
   int warps, window;
   float scale;                       // times log2 e
   FastDiv by_page;
-  bool q_f16, q_vec, out_pair, same_places;  // 16-byte loads of q, 4-byte stores; keys and values lie alike
+  bool q_vec, out_pair, same_places;  // 16-byte loads of q, 4-byte stores; keys and values lie alike
 };
 
 int launch_attend_bf16(const AttendParams& p, cudaStream_t st);
 int launch_attend_f16(const AttendParams& p, cudaStream_t st);
-int launch_attend_fp8(const AttendParams& p, cudaStream_t st);
+int launch_attend_fp8(const AttendParams& p, bool q_f16, cudaStream_t st);
 
 // The instances: head dimensions up to DT, query heads of a group in MT fragments of 16.
 __host__ __device__ constexpr int attend_mt(int DT, int G) { return G > 16 && DT <= 128 ? 2 : 1; }
@@ -101,17 +101,18 @@ __device__ __forceinline__ float exp2_fast(float x) {  // 2 units in the last pl
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// two E4M3 codes (low half of a 32-bit word) -> f16 pair, exact
-__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t w) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(w)));
-  return r;
+// four E4M3 codes -> two f16 pairs, exact
+__device__ __forceinline__ void f16x4_of_e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
-// kind of a cache: 0 bf16, 1 f16, 2 E4M3 (its operands are f16)
+// kind of cache and queries: 0 bf16, 1 f16, 2 E4M3 and bf16, 3 E4M3 and f16 (products of E4M3 are taken in f16)
 template <int KIND, int DT, int MT>
 struct AttendCfg {
-  static constexpr bool kFp8 = KIND == 2, kBf16 = KIND == 0;
+  static constexpr bool kFp8 = KIND >= 2, kBf16 = KIND == 0;
+  static constexpr bool kBf16Out = KIND == 0 || KIND == 2, kSplit = KIND != 2;  // weights in two pieces
   static constexpr int kSize = kFp8 ? 1 : 2;
   static constexpr int kRow = DT * kSize;               // bytes of a token's row in a tile
   static constexpr int NT = kFp8 || DT == 64 ? 32 : 16;  // tokens of a tile
@@ -285,15 +286,28 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
     const int c = lane % kChunks, r0 = lane / kChunks;
     const bool in_row = c * 16 < p.D * C::kSize;
     const uint32_t kt = ring + stage * C::kStage, vt = kt + C::kTile;
-    const char *k = static_cast<const char*>(p.k) + c * 16, *v = static_cast<const char*>(p.v) + c * 16;
+    const int in = in_row ? c * 16 : 0;
+    const char *k = static_cast<const char*>(p.k) + in, *v = static_cast<const char*>(p.v) + in;
+    if (p.same_places) {
+      const int64_t apart = static_cast<const char*>(p.v) - static_cast<const char*>(p.k);
+#pragma unroll
+      for (int r = 0; r < NT; r += kRowsPer) {
+        const int64_t at = __shfl_sync(0xffffffffu, k_at, r + r0);
+        const bool there = in_row && at >= 0;
+        const uint32_t to = C::at(r + r0, c);
+        const char* from = k + (there ? at : 0);
+        cp_async16(kt + to, from, there);
+        cp_async16(vt + to, from + apart, there);
+      }
+      return;
+    }
 #pragma unroll
     for (int r = 0; r < NT; r += kRowsPer) {
-      const int64_t ka = __shfl_sync(0xffffffffu, k_at, r + r0);
-      const int64_t va = p.same_places ? ka : __shfl_sync(0xffffffffu, v_at, r + r0);
+      const int64_t ka = __shfl_sync(0xffffffffu, k_at, r + r0), va = __shfl_sync(0xffffffffu, v_at, r + r0);
       const bool there = in_row && ka >= 0;
       const uint32_t to = C::at(r + r0, c);
-      cp_async16(kt + to, there ? k + ka : static_cast<const char*>(p.k), there);
-      cp_async16(vt + to, there ? v + va : static_cast<const char*>(p.v), there);
+      cp_async16(kt + to, k + (there ? ka : 0), there);
+      cp_async16(vt + to, v + (there ? va : 0), there);
     }
   };
 
@@ -317,7 +331,7 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
   const int g = lane >> 2, j2 = (lane & 3) * 2;
   const uint32_t q_s = ring + C::kOffQ;
   float* row_scale = reinterpret_cast<float*>(smem + C::kOffScale);
-  const bool bf16_out = C::kBf16 || (kFp8 && !p.q_f16);
+  constexpr bool bf16_out = C::kBf16Out;
 
   int stage = 0;
   bool first = true;
@@ -357,7 +371,7 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
         if constexpr (kFp8) {
           // f16 operands: a bf16 row is scaled by a power of two so that its largest element lies in [2^14, 2^15), where
           // elements down to 2^-29 of it stay exact
-          if (!p.q_f16) {
+          if constexpr (C::kBf16Out) {
             float f[8], top = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -445,7 +459,8 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
             ldsm4(b, kt + C::at(n * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const uint32_t b0 = f16x2_of_e4m3x2(b[x]), b1 = f16x2_of_e4m3x2(b[x] >> 16);
+              uint32_t b0, b1;
+              f16x4_of_e4m3x4(b[x], b0, b1);
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) mma16816<false>(s[mt][2 * n + (x >> 1)], a[x & 1][mt], b0, b1);
             }
@@ -453,52 +468,59 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
         }
       }
       // running maximum and sum, weights
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const float f0 = row_scale[mt * 16 + g], f1 = row_scale[mt * 16 + g + 8];
-        float top0 = m[mt][0], top1 = m[mt][1];
+      const bool last = left < NT;
+      const auto weigh = [&](int mt, int x) {  // of the fragment's rows g + 8 x
+        const float f = row_scale[mt * 16 + g + 8 * x];
+        float top = m[mt][x];
 #pragma unroll
         for (int n = 0; n < NT / 8; ++n) {
+          s[mt][n][2 * x] *= f;
+          s[mt][n][2 * x + 1] *= f;
+        }
+        if (last) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const bool in = n * 8 + j2 + x < left;
-            s[mt][n][x] = in ? s[mt][n][x] * f0 : -INFINITY;
-            s[mt][n][2 + x] = in ? s[mt][n][2 + x] * f1 : -INFINITY;
-            top0 = fmaxf(top0, s[mt][n][x]);
-            top1 = fmaxf(top1, s[mt][n][2 + x]);
+          for (int n = 0; n < NT / 8; ++n) {
+            if (n * 8 + j2 >= left) s[mt][n][2 * x] = -INFINITY;
+            if (n * 8 + j2 + 1 >= left) s[mt][n][2 * x + 1] = -INFINITY;
           }
         }
-        top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 1));
-        top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
-        top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 2));
-        top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 2));
-        const float base0 = top0 == -INFINITY ? 0.f : top0, base1 = top1 == -INFINITY ? 0.f : top1;
-        if (__any_sync(0xffffffffu, top0 > m[mt][0] || top1 > m[mt][1])) {
-          const float c0 = exp2_fast(m[mt][0] - base0), c1 = exp2_fast(m[mt][1] - base1);
-          l[mt][0] *= c0;
-          l[mt][1] *= c1;
+#pragma unroll
+        for (int n = 0; n < NT / 8; ++n) top = fmaxf(top, fmaxf(s[mt][n][2 * x], s[mt][n][2 * x + 1]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float base = top == -INFINITY ? 0.f : top;
+        if (__any_sync(0xffffffffu, top > m[mt][x])) {
+          const float c = exp2_fast(m[mt][x] - base);
+          l[mt][x] *= c;
 #pragma unroll
           for (int n = 0; n < kNt; ++n) {
-            o[mt][n][0] *= c0;
-            o[mt][n][1] *= c0;
-            o[mt][n][2] *= c1;
-            o[mt][n][3] *= c1;
+            o[mt][n][2 * x] *= c;
+            o[mt][n][2 * x + 1] *= c;
           }
-          m[mt][0] = top0;
-          m[mt][1] = top1;
+          m[mt][x] = top;
         }
+        const float off = C::kShift - base;
+        float sum = 0.f;
 #pragma unroll
-        for (int n = 0; n < NT / 8; ++n)
+        for (int n = 0; n < NT / 8; ++n) {
+          s[mt][n][2 * x] = exp2_fast(s[mt][n][2 * x] + off);
+          s[mt][n][2 * x + 1] = exp2_fast(s[mt][n][2 * x + 1] + off);
+          sum += s[mt][n][2 * x] + s[mt][n][2 * x + 1];
+        }
+        l[mt][x] += sum;
+      };
+      const bool lower = live > 8;  // whether rows 8-15 of the first fragment are heads
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            s[mt][n][x] = exp2_fast(s[mt][n][x] - base0 + C::kShift);
-            s[mt][n][2 + x] = exp2_fast(s[mt][n][2 + x] - base1 + C::kShift);
-            l[mt][0] += s[mt][n][x];
-            l[mt][1] += s[mt][n][2 + x];
-          }
+      for (int mt = 0; mt < MT; ++mt) {
+        weigh(mt, 0);
+        if (mt > 0 || lower) {
+          weigh(mt, 1);
+        } else {
+#pragma unroll
+          for (int n = 0; n < NT / 8; ++n) s[mt][n][2] = s[mt][n][3] = 0.f;
+        }
       }
       // O += P V, 16 tokens at a time
-      const bool split = !kFp8 || p.q_f16;
 #pragma unroll
       for (int n = 0; n < NT / 16; ++n) {
         uint32_t hi[MT][4], lo[MT][4];
@@ -512,7 +534,7 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
               hi[mt][x] = prmt(c0, c1, 0x7632);
               lo[mt][x] = pack2<__nv_bfloat16>(w[0] - __uint_as_float(c0 & 0xFFFF0000u),
                                                w[1] - __uint_as_float(c1 & 0xFFFF0000u));
-            } else if (split) {
+            } else if constexpr (C::kSplit) {
               const __half2 c = __halves2half2(__float2half_rz(w[0] * (1.f - 0x1p-10f)),
                                                __float2half_rz(w[1] * (1.f - 0x1p-10f)));
               hi[mt][x] = *reinterpret_cast<const uint32_t*>(&c);
@@ -541,14 +563,14 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
             ldsm4_t(b, vt + C::at(n * 16 + (lane & 15), 2 * c + (lane >> 4)));
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const uint32_t w0 = prmt(b[2 * x], 0, 0x3120), w1 = prmt(b[2 * x + 1], 0, 0x3120);
-              const uint32_t e0 = f16x2_of_e4m3x2(w0), e1 = f16x2_of_e4m3x2(w1);
-              const uint32_t d0 = f16x2_of_e4m3x2(w0 >> 16), d1 = f16x2_of_e4m3x2(w1 >> 16);
+              uint32_t e0, e1, d0, d1;
+              f16x4_of_e4m3x4(prmt(b[2 * x], 0, 0x3120), e0, d0);
+              f16x4_of_e4m3x4(prmt(b[2 * x + 1], 0, 0x3120), e1, d1);
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {  // even and odd d
                 mma16816<false>(o[mt][4 * c + 2 * x], hi[mt], e0, e1);
                 mma16816<false>(o[mt][4 * c + 2 * x + 1], hi[mt], d0, d1);
-                if (split) {
+                if constexpr (C::kSplit) {
                   mma16816<false>(o[mt][4 * c + 2 * x], lo[mt], e0, e1);
                   mma16816<false>(o[mt][4 * c + 2 * x + 1], lo[mt], d0, d1);
                 }
@@ -629,7 +651,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_attention_join_kernel(c
   const int h = head / p.G, in = head - h * p.G, hh = h * p.HB + in / C::kRows, r = in % C::kRows;
   const int HH = p.Hkv * p.HB;
   const int64_t before = p.prefix[b], each = (p.prefix[b + 1] - before) / HH, total = p.prefix[p.B];
-  const bool bf16 = C::kBf16 || (C::kFp8 && !p.q_f16);
+  constexpr bool bf16 = C::kBf16Out;
   const int64_t out = b * p.o_b + head * p.o_h;
   if (each == 0) {
     if (warp % WPR) return;
