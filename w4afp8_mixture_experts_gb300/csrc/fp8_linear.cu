@@ -33,7 +33,7 @@ struct Fp8Params {
   int64_t lda_s, ldo;
   int M, N, groups;  // K / 128
   int out_dtype;
-  int vec_out;       // out rows take 16-byte stores (1) or 32-byte ones (2)
+  int vec_out;       // out's rows lie on 16-byte boundaries
 };
 
 // fp32 accumulator, E4M3 operands, K-major
@@ -71,8 +71,10 @@ constexpr int kPairEpiWarps = 8;
 constexpr int kPairThreads = 128 + kPairEpiWarps * 32;
 constexpr int kPairStageBytes = 2 * kTile;  // of one CTA: 128 rows of A, 128 rows of B
 constexpr int kStageRow = 17;               // fp32 row of a warp's 32 x 16 transposing block, padded
+constexpr int kStgBytes = 4096;             // of an epilogue warp: a box of 32 rows x 128 bytes on its way out
 constexpr int kPairOffStg = kPairStages * kPairStageBytes;
-constexpr int kPairOffBar = kPairOffStg + kPairEpiWarps * 32 * kStageRow * 4;
+constexpr int kPairOffBar = kPairOffStg + kPairEpiWarps * kStgBytes;
+static_assert(32 * kStageRow * 4 <= kStgBytes, "transposing block");
 constexpr int kPairSmem = kPairOffBar + (2 * kPairStages + 5) * 8 + 16 + 1024;
 static_assert(kPairSmem <= kMaxSmem, "shared memory");
 static_assert(kPairOffBar % 8 == 0, "barrier alignment");
@@ -94,32 +96,10 @@ __device__ __forceinline__ void pair_tile(const PairPlan& pl, int i, int& tm, in
   tm = band * kBand + in - tn * rows;
 }
 
-// 16 columns, from n on, of this thread's token m0 + lane.
+// 16 columns, from n on, of this thread's token m0 + lane, where out's rows are not aligned for copies: through shared memory,
+// so that the lanes of a warp touch neighbouring columns of two rows instead of 32 rows.
 __device__ __forceinline__ void store16(const Fp8Params& p, const float (&v)[16], int m0, int n, float* stg) {
   const int lane = threadIdx.x & 31;
-  if (p.vec_out && n + 16 <= p.N) {
-    const int64_t m = m0 + lane;
-    if (m >= p.M) return;
-    uint32_t w[8];
-    if (p.out_dtype == W4A8_DTYPE_F32) {
-      float* o = static_cast<float*>(p.out) + m * p.ldo + n;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * i + j]);
-        store32b(o + 8 * i, p.vec_out == 2, w);
-      }
-    } else {
-      const bool bf16 = p.out_dtype == W4A8_DTYPE_BF16;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        w[j] = bf16 ? pack2<__nv_bfloat16>(v[2 * j], v[2 * j + 1]) : pack2<__half>(v[2 * j], v[2 * j + 1]);
-      store32b(static_cast<uint16_t*>(p.out) + m * p.ldo + n, p.vec_out == 2, w);
-    }
-    return;
-  }
-  // rows without alignment, or a tile's last columns: through shared memory, so that the lanes of a warp touch
-  // neighbouring columns of two rows instead of 32 rows
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < 16; ++i) stg[lane * kStageRow + i] = v[i];
@@ -134,9 +114,54 @@ __device__ __forceinline__ void store16(const Fp8Params& p, const float (&v)[16]
   }
 }
 
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* src, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y), "r"(smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// A warp's 32 tokens x 128 columns as boxes of 128 bytes a row, written to shared memory (128-byte swizzle: no two of 8
+// lanes on one bank) and copied out by TMA, which leaves out what lies behind the last row or column.  The copies run
+// under the next tile's products.
+template <typename T>
+__device__ __forceinline__ void store_boxes(const Fp8Params& p, const CUtensorMap* to, const uint64_t (&sum)[64], int m0, int n,
+                                            uint8_t* stg) {
+  constexpr int kVec = 16 / sizeof(T), kBoxes = 128 * sizeof(T) / 128, kCols = 128 / sizeof(T);  // columns of a box
+  int lane;  // read here, so that no address of these stores is held during the products
+  asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));
+#pragma unroll
+  for (int b = 0; b < kBoxes; ++b) {
+    if (lane == 0) bulk_wait_read();  // the last box has left
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const int j = (b * kCols + c * kVec) / 2;
+      uint4 w;
+      if constexpr (sizeof(T) == 4) {
+        const float2 x = halves(sum[j]), y = halves(sum[j + 1]);
+        w = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+      } else {
+        const float2 x = halves(sum[j]), y = halves(sum[j + 1]), z = halves(sum[j + 2]), u = halves(sum[j + 3]);
+        w = make_uint4(pack2<T>(x.x, x.y), pack2<T>(y.x, y.y), pack2<T>(z.x, z.y), pack2<T>(u.x, u.y));
+      }
+      *reinterpret_cast<uint4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) = w;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (m0 < p.M && n + b * kCols < p.N) tma_store_2d(to, stg, n + b * kCols, m0);
+      bulk_commit();
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kPairThreads, 1)
-    fp8_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const Fp8Params p,
-                    const PairPlan pl) {
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                    const __grid_constant__ CUtensorMap to, const Fp8Params p, const PairPlan pl) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairOffBar);  // the pair's first CTA counts for both
@@ -252,7 +277,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
   // epilogue: warp e reads lane quarter e % 4 (its tokens) and, by e / 4, one half of the columns, which have one scale
   const int e = warp - 4, quarter = warp & 3, half = e >> 2;
-  float* stg = reinterpret_cast<float*>(smem + kPairOffStg) + e * 32 * kStageRow;
+  uint8_t* stg = smem + kPairOffStg + e * kStgBytes;
   const uint32_t lanes = (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
   const uint32_t tempty0 = map_to_cta(smem_u32(tempty), 0);
   const int nb_end = (p.N + 127) / 128;
@@ -299,6 +324,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     if (!ok) break;
     if (!cols) continue;
+    if (p.vec_out) {
+      if (p.out_dtype == W4A8_DTYPE_BF16)
+        store_boxes<__nv_bfloat16>(p, &to, sum, m0, nb * 128, stg);
+      else if (p.out_dtype == W4A8_DTYPE_F16)
+        store_boxes<__half>(p, &to, sum, m0, nb * 128, stg);
+      else
+        store_boxes<float>(p, &to, sum, m0, nb * 128, stg);
+      continue;
+    }
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       float f[16];
@@ -308,9 +342,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         f[2 * j] = t.x;
         f[2 * j + 1] = t.y;
       }
-      if (nb * 128 + 16 * q < p.N) store16(p, f, m0, nb * 128 + 16 * q, stg);
+      if (nb * 128 + 16 * q < p.N) store16(p, f, m0, nb * 128 + 16 * q, reinterpret_cast<float*>(stg));
     }
   }
+  if (lane == 0) bulk_wait();
   leave();
 }
 
@@ -470,27 +505,31 @@ __global__ void __launch_bounds__(SplitCfg<BN>::kThreads, SplitCfg<BN>::kBlocks)
     }
   }
   __syncwarp();
-  tc_fence_before();
-  const bool all_ok = __syncthreads_and(ok) != 0;  // also: every product and load of this CTA is done
-  if (warp == 2) {
-    tc_fence_after();
-    tmem_dealloc(tmem, C::kTmemCols);
-  }
+  // the tensor memory goes back when every warp has read it
+  const auto leave = [&] {
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+      tc_fence_after();
+      tmem_dealloc(tmem, C::kTmemCols);
+    }
+  };
   if (splits == 1) {
-    if (warp >= 4 && all_ok && n0 + f < p.N) {  // the lanes of a warp hold neighbouring columns of one token
+    if (warp >= 4 && ok && n0 + f < p.N) {  // the lanes of a warp hold neighbouring columns of one token
 #pragma unroll
       for (int j = 0; j < C::kCols; ++j) {
         const int m = m0 + half * C::kCols + j;
         if (m < p.M) store_any(p.out, m * p.ldo + n0 + f, sum[j], p.out_dtype);
       }
     }
+    leave();
     return;
   }
   cluster_arrive();
-  cluster_wait();  // every CTA of the tile is done with its ring
+  cluster_wait();  // every CTA of the tile is done with its ring: its loads and products
   // tokens [q BN / splits, (q + 1) BN / splits) belong to CTA q: red [source][token][128 W rows]
   const int most = (BN + splits - 1) / splits;
-  if (warp >= 4 && all_ok) {
+  if (warp >= 4 && ok) {
     const uint32_t red = smem_u32(smem);
     int q = (half * C::kCols + 1) * splits - 1;  // owner of the first token: the last CTA that starts at or before it
     q /= BN;
@@ -507,9 +546,11 @@ __global__ void __launch_bounds__(SplitCfg<BN>::kThreads, SplitCfg<BN>::kBlocks)
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(sum[j]) : "memory");
     }
   }
+  __syncwarp();
   cluster_arrive();
+  leave();
   cluster_wait();
-  if (!all_ok) return;
+  if (*abort_flag) return;
   const int begin = rank * BN / splits, own = (rank + 1) * BN / splits - begin;
   const float* red = reinterpret_cast<const float*>(smem);
   const int left = min(own, p.M - m0 - begin);  // tokens of mine that exist
@@ -583,6 +624,25 @@ int scale_map(CUtensorMap* m, const Fp8Params& p, int box) {
   return W4A8_OK;
 }
 
+// the output in boxes of 32 rows x 128 bytes, 128-byte swizzle
+int out_map(CUtensorMap* m, const Fp8Params& p) {
+  EncodeFn fn = encode_fn();
+  if (!fn) return set_error(W4A8_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint64_t size = dtype_size(p.out_dtype);
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.M)};
+  const cuuint64_t strides[1] = {p.M > 1 ? p.ldo * size : (p.N * size + 15) / 16 * 16};  // one row needs none
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), 32};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapDataType type = p.out_dtype == W4A8_DTYPE_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : p.out_dtype == W4A8_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  const CUresult r = fn(m, type, 2, p.out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return set_error(W4A8_ERR_INVALID_ARG, "tensor map for out rejected (CUresult %d)", static_cast<int>(r));
+  return W4A8_OK;
+}
+
 struct Call {
   const uint8_t *A, *B;
   Fp8Params p;
@@ -604,17 +664,18 @@ struct Pair {
     return launcher().prepare(dev, clusters, fp8_pair_kernel, kPairSmem, kPairThreads, 2, kRegsLaunch);
   }
   static int launch(const Call& c, int dev, cudaStream_t st) {
-    CUtensorMap ta, tb;
+    CUtensorMap ta, tb, to = {};
     int rc, clusters = 1;
     if ((rc = ready(dev, &clusters))) return rc;
     if ((rc = code_map(&ta, c.A, c.p.M, c.K, 128, "A"))) return rc;
     if ((rc = code_map(&tb, c.B, c.p.N, c.K, 128, "B"))) return rc;
+    if (c.p.vec_out && (rc = out_map(&to, c.p))) return rc;
     PairPlan pl;
     pl.tiles_m = static_cast<int>(ceil_div(c.p.M, 256));
     pl.tiles_n = static_cast<int>(ceil_div(c.p.N, 256));
     pl.tiles = pl.tiles_m * pl.tiles_n;  // at most 2^24
     return Launcher::launch("fp8_pair_kernel", fp8_pair_kernel, dim3(2 * std::min(pl.tiles, clusters)), kPairThreads,
-                            kPairSmem, 2, st, ta, tb, c.p, pl);
+                            kPairSmem, 2, st, ta, tb, to, c.p, pl);
   }
 };
 
@@ -716,7 +777,7 @@ extern "C" int fp8_block_linear(const uint8_t* A, const float* a_scales, int64_t
   c.p.groups = static_cast<int>(K / 128);
   c.p.out_dtype = out_dtype;
   const uint64_t bits = reinterpret_cast<uintptr_t>(out) | (M > 1 ? static_cast<uint64_t>(ldo) * dtype_size(out_dtype) : 0);
-  c.p.vec_out = bits % 32 == 0 ? 2 : bits % 16 == 0 ? 1 : 0;
+  c.p.vec_out = bits % 16 == 0;
   return launch_best(c, static_cast<cudaStream_t>(stream));
 }
 
