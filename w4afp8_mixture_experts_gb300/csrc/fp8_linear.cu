@@ -371,7 +371,10 @@ struct SplitCfg {
 
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&v)[N]) {
-  if constexpr (N == 32)
+  if constexpr (N == 64) {
+    tmem_ld32(at, v);
+    tmem_ld32(at + 32, v + 32);
+  } else if constexpr (N == 32)
     tmem_ld32(at, v);
   else if constexpr (N == 16)
     tmem_ld16(at, v);
@@ -476,12 +479,17 @@ __global__ void __launch_bounds__(SplitCfg<BN>::kThreads, SplitCfg<BN>::kBlocks)
       const float b = b0;
       b0 = b1;
       b1 = it + 2 < count ? bs[it + 2] : 0.f;
-      if (!(ok = warp_wait(&tfull[buf], (it / C::kBufs) & 1, abort_flag))) break;
-      // the scales were written by the copy that the products waited for; this warp waits for it too, to see them
+      // the scales come with the stage's copies, which this warp waits for as the products do
       if (!(ok = warp_wait(&full[s], (it / C::kStages) & 1, abort_flag))) break;
-      tc_fence_after();
       const float4* as = reinterpret_cast<const float4*>(smem + C::kOffScale + s * C::kScaleBytes) + half * (C::kCols / 4);
-      constexpr int kStep = BN == 128 ? 32 : BN == 16 ? 8 : 16;  // as many as fit the registers of two blocks
+      float4 scale[C::kCols / 4];
+      if constexpr (C::kCols <= 16) {  // read under the products; with more columns there are no registers for that
+#pragma unroll
+        for (int j = 0; j < C::kCols / 4; ++j) scale[j] = as[j];
+      }
+      if (!(ok = warp_wait(&tfull[buf], (it / C::kBufs) & 1, abort_flag))) break;
+      tc_fence_after();
+      constexpr int kStep = BN == 128 ? 64 : BN == 16 ? 8 : 16;  // columns on their way at a time
 #pragma unroll
       for (int c = 0; c < C::kCols; c += kStep) {
         uint32_t v[kStep];
@@ -489,7 +497,7 @@ __global__ void __launch_bounds__(SplitCfg<BN>::kThreads, SplitCfg<BN>::kBlocks)
         tmem_wait_ld_pin<kStep>(v);
 #pragma unroll
         for (int j = 0; j < kStep; j += 4) {
-          const float4 a = as[(c + j) / 4];
+          const float4 a = C::kCols <= 16 ? scale[(c + j) / 4] : as[(c + j) / 4];
           sum[c + j] = fmaf(__uint_as_float(v[j]), a.x * b, sum[c + j]);
           sum[c + j + 1] = fmaf(__uint_as_float(v[j + 1]), a.y * b, sum[c + j + 1]);
           sum[c + j + 2] = fmaf(__uint_as_float(v[j + 2]), a.z * b, sum[c + j + 2]);
@@ -649,10 +657,13 @@ struct Call {
   int64_t K;
 };
 
+// One configuration: how many clusters run at once, the launch, and what launch_best needs to know of it.
 struct Option {
   int (*ready)(int dev, int* clusters);
   int (*launch)(const Call& c, int dev, cudaStream_t st);
-  int rows, cols, parts;  // tokens and W rows of a tile, pieces of K
+  int rows, cols, parts;              // tokens and W rows of a tile, pieces of K
+  int stages, stage_bytes;            // of a CTA's ring
+  double fixed_us, stage_us, wave_us; // a launch without its stages, a stage, a further wave of tiles
 };
 
 struct Pair {
@@ -705,15 +716,25 @@ struct Split {
 
 template <int BN, int SPLITS>
 constexpr Option split_option() {
-  return {Split<BN, SPLITS>::ready, Split<BN, SPLITS>::launch, BN, 128, SPLITS};
+  using C = SplitCfg<BN>;
+  // the exchange of the pieces' sums: its barriers, and its bytes
+  constexpr double fixed = BN == 128 ? 4.2 : BN == 64 ? 3.4 : BN == 32 ? 3.0 : 2.6, exchange = SPLITS > 1 ? 1.4 + 0.7 * BN / 64 : 0;
+  return {Split<BN, SPLITS>::ready, Split<BN, SPLITS>::launch, BN, 128, SPLITS, C::kStages, C::kStageBytes, fixed + exchange,
+          BN == 128 ? 0.53 : BN == 64 ? 0.48 : BN == 32 ? 0.33 : 0.32, BN == 128 ? 5.4 : BN == 64 ? 4.1 : BN == 32 ? 3.9 : 3.6};
 }
 
 // Configuration asked for by a test (rows of a tile * 16 + pieces of K), 0: none.
 std::atomic<int> g_force{0};
 
+// The configuration with the smallest estimate
+//   fixed + max(waves * stages of a piece * stage, bytes of W / rate) + (waves - 1) * wave
+// stage: what a stage takes by itself, longer by half where two CTAs share every SM, or what L2 needs for the stages of all
+// CTAs (13.6 TB/s).  rate: 6.2 TB/s of memory, or what the bytes of W in flight give at 1.9 us of latency.  Fitted on a GB300
+// to 22 configurations of 75 shapes, drawn over 1 to 4096 rows, 64 to 24576 columns and K of 128 to 18432: its choice takes
+// 1.6 % more than the best on average and is within 10 % of it on 73 (777 x 1001 x 1536: 11.5 us, best 10.2).
 int launch_best(const Call& c, cudaStream_t st) {
   static const Option options[] = {
-      {Pair::ready, Pair::launch, 256, 256, 1},
+      {Pair::ready, Pair::launch, 256, 256, 1, kPairStages, kPairStageBytes, 4.9, 0.44, 1.9},
       split_option<128, 1>(), split_option<128, 2>(), split_option<128, 4>(),
       split_option<64, 1>(), split_option<64, 2>(), split_option<64, 3>(), split_option<64, 4>(), split_option<64, 5>(), split_option<64, 8>(),
       split_option<32, 1>(), split_option<32, 2>(), split_option<32, 3>(), split_option<32, 4>(), split_option<32, 5>(), split_option<32, 8>(),
@@ -722,6 +743,7 @@ int launch_best(const Call& c, cudaStream_t st) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return check_launch("cudaGetDevice");
   const int force = g_force.load(std::memory_order_relaxed);
+  const double sms = num_sms();
   const Option* best = nullptr;
   double best_us = 0.0;
   for (const Option& o : options) {
@@ -730,9 +752,13 @@ int launch_best(const Call& c, cudaStream_t st) {
     int clusters = 1;
     if (int rc = o.ready(dev, &clusters)) return rc;
     const int64_t tiles = ceil_div(c.p.M, o.rows) * ceil_div(c.p.N, o.cols), waves = ceil_div(tiles, clusters);
-    const double stage = o.rows == 256 ? 0.30 : o.rows == 128 ? 0.25 : 0.35;
-    const double us = (o.rows == 256 ? 6.0 : 4.0 + 0.1 * o.parts) +
-                      waves * (stage * static_cast<double>(ceil_div(c.p.groups, o.parts)) + (o.rows == 256 ? 1.0 : 2.0));
+    const double ctas = static_cast<double>(std::min<int64_t>(tiles, clusters)) * (o.rows == 256 ? 2 : o.parts);
+    const double stage = std::max(o.stage_us * (1.0 + 0.52 * std::max(0.0, ctas / sms - 1.0)), ctas * o.stage_bytes / 13.6e6);
+    const double rate = std::min(6.2e6, ctas * o.stages * kTile / 1.9);  // bytes of W per us
+    const double us = o.fixed_us +
+                      std::max(static_cast<double>(waves * ceil_div(c.p.groups, o.parts)) * stage,
+                               static_cast<double>(c.p.N) * static_cast<double>(c.K) / rate) +
+                      static_cast<double>(waves - 1) * o.wave_us;
     if (!best || us < best_us) {
       best = &o;
       best_us = us;
