@@ -600,9 +600,9 @@ typedef struct {
 /*
  * (12) Appends keys and values to a paged cache, keys rotated on the way.
  * Row t < indptr[B] is a token of the sequence b with indptr[b] <= t < indptr[b + 1]
- * (indptr int32 [B + 1], not decreasing, from 0; NULL: T = B and one token each), at
+ * (indptr int32 [B + 1], not decreasing, from 0; NULL: T >= B and one token each), at
  * position seq_lens[b] - (indptr[b + 1] - t): seq_lens counts the new tokens.  A row of a
- * negative position or behind indptr[B] is left out (a padded batch).
+ * negative position or behind the last sequence is left out (a padded batch).
  *   k, v [T][heads][D] of `dtype` (bf16 or f16; a 16-bit cache has the same type)
  *   rotary: positions NULL takes the cache position; rotary NULL, or freqs NULL: none.
  *   E4M3: code = e4m3(x / scale) in fp32, to nearest even, saturating.

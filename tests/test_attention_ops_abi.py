@@ -80,7 +80,7 @@ def _linear(L, A=P16, s=P16, lds=4, B=P16, bs=P16, M=4, N=32, K=128, out=P16, ld
     (lambda L: _append(L, strides=(2048, 128, 64, 2048, -128, 64)), b"strides"),
     (lambda L: _append(L, k_scale=16), b"scales"),
     (lambda L: _append(L, k_scale=18, dtype=E4M3), b"aligned"),
-    (lambda L: _append(L, T=4), b"T=4"),
+    (lambda L: _append(L, T=2), b"T=2"),
     (lambda L: _append(L, T=1 << 30, indptr=P16), b"below 2^31"),
     (lambda L: _append(L, indptr=P18), b"indptr"),
     (lambda L: _append(L, Hq=2), b"Hq=2"),

@@ -46,7 +46,7 @@ def _run(lib, past, new, H, D, page, dtype="bf16", cache="bf16", Hq=0, R=None, s
     ks = (0.01 + 0.02 * torch.rand(H, generator=g)).cuda() if scales else None
     vs = (0.01 + 0.02 * torch.rand(H, generator=g)).cuda() if scales else None
     lens_t = torch.tensor(lens, dtype=torch.int32, device="cuda")
-    one = all(n == 1 for n in new) and padding == 0 and seed % 2 == 0
+    one = all(n == 1 for n in new) and seed % 2 == 0
     indptr = None if one else torch.tensor(np.cumsum([0] + new), dtype=torch.int32, device="cuda")
     f = ref.inv_freq(R) if R else None
     pos_t = None if positions is None else torch.tensor(positions, device="cuda")
@@ -98,6 +98,7 @@ def _run(lib, past, new, H, D, page, dtype="bf16", cache="bf16", Hq=0, R=None, s
 CASES = [
     dict(past=[0], new=[1], H=1, D=8, page=16),
     dict(past=[5, 0, 31, 16], new=[1, 1, 1, 1], H=8, D=128, page=16, Hq=64, R=128),
+    dict(past=[7, 0, 32], new=[1, 1, 1], H=2, D=64, page=16, Hq=4, R=64, padding=5),
     dict(past=[5, 0, 31, 16], new=[1, 1, 1, 1], H=3, D=96, page=7, R=48, start=48, interleaved=True, seed=1),
     dict(past=[0, 700, 3], new=[300, 1, 77], H=5, D=64, page=64, Hq=5, R=32, padding=9, layout="heads first"),
     dict(past=[0, 0, 9, 0, 0, 2], new=[0, 40, 0, 0, 13, 0], H=2, D=72, page=1, R=24, start=8, padding=3),

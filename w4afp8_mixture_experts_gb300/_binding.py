@@ -604,7 +604,7 @@ def paged_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, indptr=None, *
     """Writes k, v [T, Hkv, D] (bf16 or f16) into the caches [pages, page_size, Hkv, D] (that type or float8_e4m3fn, any
     strides, D contiguous), keys rotated as in rotary_embedding when freqs is given, at the cache position or at
     positions [T].  Rows indptr[b] ... indptr[b + 1] are the last tokens of sequence b, whose length seq_lens[b] (int32
-    [B]) counts them; indptr None: one token each.  page_table int32 [B, n].  Rows behind indptr[B], or of a sequence of
+    [B]) counts them; indptr None: one token each.  page_table int32 [B, n].  Rows behind the last sequence, or of one of
     length 0, are left out.  k_scale, v_scale fp32 [Hkv]: an 8-bit cache holds x / scale.
     q [T, Hq, D] is rotated like the keys into q_out (made when None; may be q) and returned."""
     return (_ops or _load_ops()).append(k, v, k_cache, v_cache, page_table, seq_lens, indptr, freqs, positions,

@@ -94,7 +94,6 @@ extern "C" int paged_attention_decode(const void* q, int64_t ldq_b, int64_t ldq_
   const bool q_f16 = dtype == W4A8_DTYPE_F16;
   p.q_vec = (bits_of(q) | static_cast<uint64_t>(ldq_b | ldq_h) * 2) % 16 == 0;
   p.out_pair = (bits_of(out) | static_cast<uint64_t>(ldo_b | ldo_h) * 2) % 4 == 0;
-  p.same_places = p.k_page == p.v_page && p.k_slot == p.v_slot && p.k_head == p.v_head;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (fp8) return launch_attend_fp8(p, q_f16, st);
   return q_f16 ? launch_attend_f16(p, st) : launch_attend_bf16(p, st);

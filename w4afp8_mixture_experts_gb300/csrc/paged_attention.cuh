@@ -46,7 +46,7 @@ struct AttendParams {
   int warps, window;
   float scale;                       // times log2 e
   FastDiv by_page;
-  bool q_vec, out_pair, same_places;  // 16-byte loads of q, 4-byte stores; keys and values lie alike
+  bool q_vec, out_pair;  // 16-byte loads of q, 4-byte stores of out
 };
 
 int launch_attend_bf16(const AttendParams& p, cudaStream_t st);
@@ -268,42 +268,51 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
   const uint32_t ring = smem_u32(smem);
   constexpr int kChunks = C::kRow / 16, kRowsPer = 32 / kChunks;  // rows of one copy by the warp
   static_assert(kChunks <= 32, "a warp copies whole rows");
-  // The page of this lane's token of a tile (-1: none), one tile ahead of its copies.
-  const auto page_of = [&](const Cursor& c, int& slot) {
+  // Where a tile's tokens lie, looked up one tile ahead of its copies: the page and slot of this lane's token (-1: none).
+  struct Places {
+    int page, slot, valid;  // tokens of the tile
+    bool flat;              // all slots of the tile in one page
+  };
+  const auto places = [&](const Cursor& c) {
+    Places w;
     const int t = c.s.lo + c.u * NT + (lane & (NT - 1));
-    int page = -1;
-    slot = 0;
+    w.valid = c.s.hi - (c.s.lo + c.u * NT);
+    w.page = -1;
+    w.slot = 0;
     if (c.left > 0 && t < c.s.hi) {
-      const int n = p.by_page.div(t, slot);
-      page = p.table[c.b * p.table_ld + n];
-      if (page < 0 || page >= p.pages) {
+      const int n = p.by_page.div(t, w.slot);
+      w.page = p.table[c.b * p.table_ld + n];
+      if (w.page < 0 || w.page >= p.pages) {
         atomicOr(&g_attend_error, 2u);
-        page = -1;
+        w.page = -1;
       }
     }
-    return page;
+    w.flat = __shfl_sync(0xffffffffu, w.slot, 0) + NT <= static_cast<int>(p.by_page.d);
+    return w;
   };
-  const auto copy_tile = [&](int h, int page, int slot, int stage) {
-    const int64_t k_at = page < 0 ? -1 : page * p.k_page + slot * p.k_slot + h * p.k_head;
-    const int64_t v_at = page < 0 ? -1 : page * p.v_page + slot * p.v_slot + h * p.v_head;
+  const auto copy_tile = [&](int h, const Places& w, int stage) {
     const int c = lane % kChunks, r0 = lane / kChunks;
     const bool in_row = c * 16 < p.D * C::kSize;
     const uint32_t kt = ring + stage * C::kStage, vt = kt + C::kTile;
     const int in = in_row ? c * 16 : 0;
-    const char *k = static_cast<const char*>(p.k) + in, *v = static_cast<const char*>(p.v) + in;
-    if (p.same_places) {
-      const int64_t apart = static_cast<const char*>(p.v) - static_cast<const char*>(p.k);
+    const char *k = static_cast<const char*>(p.k) + in + h * p.k_head, *v = static_cast<const char*>(p.v) + in + h * p.v_head;
+    if (w.flat) {  // the same page and neighbouring slots, all of them the cache's own memory
+      const int page = __shfl_sync(0xffffffffu, w.page, 0), slot = __shfl_sync(0xffffffffu, w.slot, 0) + r0;
+      const int valid = page < 0 || !in_row ? 0 : w.valid - r0;
+      k += max(page, 0) * p.k_page + slot * p.k_slot;
+      v += max(page, 0) * p.v_page + slot * p.v_slot;
 #pragma unroll
       for (int r = 0; r < NT; r += kRowsPer) {
-        const int64_t at = __shfl_sync(0xffffffffu, k_at, r + r0);
-        const bool there = in_row && at >= 0;
         const uint32_t to = C::at(r + r0, c);
-        const char* from = k + (there ? at : 0);
-        cp_async16(kt + to, from, there);
-        cp_async16(vt + to, from + apart, there);
+        cp_async16(kt + to, k, r < valid);
+        cp_async16(vt + to, v, r < valid);
+        k += kRowsPer * p.k_slot;
+        v += kRowsPer * p.v_slot;
       }
       return;
     }
+    const int64_t k_at = w.page < 0 ? -1 : w.page * p.k_page + w.slot * p.k_slot;
+    const int64_t v_at = w.page < 0 ? -1 : w.page * p.v_page + w.slot * p.v_slot;
 #pragma unroll
     for (int r = 0; r < NT; r += kRowsPer) {
       const int64_t ka = __shfl_sync(0xffffffffu, k_at, r + r0), va = __shfl_sync(0xffffffffu, v_at, r + r0);
@@ -316,13 +325,14 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
 
   // fill the ring: kStages - 1 tiles on their way, the next one's pages known
   Cursor ahead = here;
-  int slot, page = page_of(ahead, slot), ahead_h = ahead.hh / p.HB;
+  Places where = places(ahead);
+  int ahead_h = ahead.hh / p.HB;
   const auto issue = [&](int stage) {
     if (ahead.left > 0) {
-      copy_tile(ahead_h, page, slot, stage);
+      copy_tile(ahead_h, where, stage);
       advance(ahead);
       ahead_h = ahead.hh / p.HB;
-      page = page_of(ahead, slot);
+      where = places(ahead);
     }
     cp_async_commit();
   };

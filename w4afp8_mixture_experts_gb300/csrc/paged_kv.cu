@@ -381,7 +381,7 @@ extern "C" int paged_kv_append(const void* k, int64_t ldk_t, int64_t ldk_h, cons
   W4A8_REQUIRE(Hq >= 0 && Hq < (1 << 16) && (q || Hq == 0), "Hq=%lld must be in [0, 2^16), and 0 without q", (long long)Hq);
   W4A8_REQUIRE(T >= 0 && T < (1ll << 31) && T * (Hq + 2 * H) < (1ll << 31), "T=%lld rows of %lld heads: below 2^31",
                (long long)T, (long long)(Hq + 2 * H));
-  W4A8_REQUIRE(indptr || T == cache->B, "T=%lld must be B=%lld without indptr", (long long)T, (long long)cache->B);
+  W4A8_REQUIRE(indptr || T >= cache->B, "T=%lld must be at least B=%lld without indptr", (long long)T, (long long)cache->B);
   W4A8_REQUIRE(bits_of(indptr) % 4 == 0, "indptr must be aligned to 4 bytes");
   W4A8_REQUIRE(ldk_t >= 0 && ldk_h >= 0 && ldv_t >= 0 && ldv_h >= 0 && ldq_t >= 0 && ldq_h >= 0 && ldqo_t >= 0 && ldqo_h >= 0,
                "strides must not be negative");

@@ -511,8 +511,8 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                   "), got (" + std::to_string(c.heads) + ", " + std::to_string(c.D) + ")");
     const int32_t* indptr =
         static_cast<const int32_t*>(vec(a[6], "indptr", dev, c.B + 1, at::kInt, at::kInt, nullptr));
-    if (!indptr && k.rows != c.B)
-      value_error("k must have " + std::to_string(c.B) + " rows without indptr, got " + std::to_string(k.rows));
+    if (!indptr && k.rows < c.B)
+      value_error("k must have at least " + std::to_string(c.B) + " rows without indptr, got " + std::to_string(k.rows));
     w4a8_rotary r;
     rotary_of(a[7], a[8], a[9], a[10], a[11], dev, k.rows, &r);
     const c10::cuda::CUDAGuard guard(dev);
