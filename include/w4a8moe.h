@@ -629,12 +629,14 @@ int paged_kv_append(const void* k, int64_t ldk_t, int64_t ldk_h, const void* v, 
  *   D: a multiple of 8 (of 16 with E4M3) up to 256; the cache's pointers and strides are
  *   multiples of 16 bytes.  Hq a multiple of heads, Hq / heads <= 256, B * heads < 2^24.
  *   ws: paged_attention_workspace_bytes() bytes, 16-byte aligned; its contents on entry do
- *   not matter.
+ *   not matter.  longest: the tokens that are looked at of a sequence at most, table_pages *
+ *   page_size or the window where that is less; few short sequences need no workspace (0
+ *   bytes, NULL will do).  longest < 0: enough for any.
  */
 int paged_attention_decode(const void* q, int64_t ldq_b, int64_t ldq_h, int dtype, int64_t Hq,
                            const w4a8_paged_cache* cache /* host pointer */, float scale, int64_t window, void* out,
                            int64_t ldo_b, int64_t ldo_h, float* lse, void* ws, size_t ws_bytes, void* stream);
-size_t paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t D);
+size_t paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t D, int cache_dtype, int64_t longest);
 
 /*
  * (14) FP8 Linear with a scale per block of 128:

@@ -129,7 +129,7 @@ def test_empty_calls_launch_nothing(clib):
     assert _append(clib, T=0, B=0, k=NULL) == 0
     assert _attend(clib, B=0, q=NULL, out=NULL) == 0
     assert _linear(clib, M=0, A=NULL, lds=0) == 0 and _linear(clib, N=0, ldo=0) == 0
-    assert clib.paged_attention_workspace_bytes(0, 4, 2, 64) == 0
+    assert clib.paged_attention_workspace_bytes(0, 4, 2, 64, 0, -1) == 0
 
 
 def test_sources_load_nothing_as_constant():

@@ -78,9 +78,10 @@ _SIGS = {
                                  _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp]),
     "paged_attention_decode": (_c_int, [_c_vp, _c_i64, _c_i64, _c_int, _c_i64, _c_vp, _c_f32, _c_i64, _c_vp, _c_i64,
                                         _c_i64, _c_vp, _c_vp, _c_sz, _c_vp]),
-    "paged_attention_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i64]),
+    "paged_attention_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i64, _c_int, _c_i64]),
     "fp8_block_linear": (_c_int, [_c_vp, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_int,
                                   _c_vp]),
+    "w4a8_test_paged_attention_way": (_c_int, [_c_int]),
     "w4a8_test_fp8_linear_config": (_c_int, [_c_int, _c_int]),
     "w4a8_test_linear_config": (_c_int, [_c_int, _c_int]),
     "w4a8_test_linear_wait": (_c_int, [_c_int, ctypes.c_uint64, _c_vp, _c_vp]),
@@ -623,8 +624,8 @@ def paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, *, scale=N
 
 
 def paged_attention_workspace_bytes(B: int, Hq: int, Hkv: int, D: int) -> int:
-    """Workspace of paged_attention_decode on the current device."""
-    return int(load().paged_attention_workspace_bytes(B, Hq, Hkv, D))
+    """Workspace of paged_attention_decode on the current device, enough for sequences of any length."""
+    return int(load().paged_attention_workspace_bytes(B, Hq, Hkv, D, 0, -1))
 
 
 def fp8_block_linear(A, a_scales, B, b_scales, *, out_dtype=None, out=None):

@@ -1,8 +1,12 @@
 // paged_attention_decode: argument checks, workspace, choice of the instance (paged_attention.cuh).
+#include <atomic>
+
 #include "paged_attention.cuh"
 
 namespace w4a8 {
 namespace {
+
+std::atomic<int> g_force{0};  // way asked for by a test
 
 // Workspace: places before each sequence, then (m, l) and O of two parts of every warp.
 struct AttendLayout {
@@ -17,6 +21,27 @@ AttendLayout attend_layout(int64_t B, int64_t G, int64_t D) {
   L.o = L.ml + up(rows * 8);
   L.total = L.o + up(rows * static_cast<size_t>(D) * 4);
   return L;
+}
+
+// Blocks of the cluster that shares an item of up to `longest` tokens, 0 where the list's warps take all items: the smaller
+// estimate.  A cluster needs one launch and no joining kernel but has few warps; as many blocks as stay resident are used.
+// Per warp's tile of 8 KB 0.8 us alone and 1.15 with every SM busy, 1.05 from the list (where sequences are half as long as
+// the table on average); fitted to 1 to 256 sequences of up to 16 to 4096 tokens (16 x 512, 8 heads: 10 us, 16 by the list; 16
+// x 1024 14 and 20; 1 x 4096 13.6 both; 64 x 1024 39 and 37).
+int attend_cluster(int64_t B, int64_t Hq, int64_t heads, int64_t D, bool fp8, int64_t longest) {
+  const int force = g_force.load(std::memory_order_relaxed);
+  if (force) return force & 15;
+  const int DT = attend_dt(D), G = static_cast<int>(Hq / heads), NT = attend_tile(fp8, DT), warps = attend_warps(DT);
+  const int64_t items = B * heads * ceil_div(G, 16 * attend_mt(DT, G)), tiles = ceil_div(longest, NT), resident = warps / kAttendWarps;
+  for (int c = 8; c >= 1; c /= 2) {
+    if (items * c > resident || (c > 1 && (c - 1) * kAttendWarps >= tiles)) continue;
+    const double tile = 2.0 * NT * DT * (fp8 ? 1 : 2) / 8192;
+    const double here = 5.5 + tile * static_cast<double>(ceil_div(tiles, c * kAttendWarps)) *
+                                  (0.8 + 0.35 * static_cast<double>(items * c) / static_cast<double>(resident));
+    const double list = 11.0 + tile * 1.05 * static_cast<double>(ceil_div(items * tiles, warps));
+    return here <= list ? c : 0;
+  }
+  return 0;
 }
 
 uint64_t bits_of(const void* q) { return static_cast<uint64_t>(reinterpret_cast<uintptr_t>(q)); }
@@ -55,7 +80,8 @@ extern "C" int paged_attention_decode(const void* q, int64_t ldq_b, int64_t ldq_
   W4A8_REQUIRE((bits_of(cache->k) | bits_of(cache->v) | strides) % 16 == 0,
                "the cache's pointers and strides must be multiples of 16 bytes");
   const AttendLayout L = attend_layout(B, G, D);
-  W4A8_REQUIRE(ws && ws_bytes >= L.total && aligned16(ws), "%zu bytes of 16-byte aligned workspace are needed", L.total);
+  const int cluster = attend_cluster(B, Hq, H, D, fp8, window > 0 && window < max_len ? window : max_len);
+  W4A8_REQUIRE(cluster || (ws && ws_bytes >= L.total && aligned16(ws)), "%zu bytes of 16-byte aligned workspace are needed", L.total);
   AttendParams p = {};
   p.q = q;
   p.k = cache->k;
@@ -89,6 +115,7 @@ extern "C" int paged_attention_decode(const void* q, int64_t ldq_b, int64_t ldq_
   p.G = G;
   p.D = static_cast<int>(D);
   p.window = static_cast<int>(window < max_len ? window : 0);  // a window beyond the table leaves nothing out
+  p.cluster = cluster;
   p.scale = scale * 1.44269504089f;
   p.by_page = FastDiv(cache->page_size);
   const bool q_f16 = dtype == W4A8_DTYPE_F16;
@@ -99,7 +126,15 @@ extern "C" int paged_attention_decode(const void* q, int64_t ldq_b, int64_t ldq_
   return q_f16 ? launch_attend_f16(p, st) : launch_attend_bf16(p, st);
 }
 
-extern "C" size_t paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t D) {
+extern "C" int w4a8_test_paged_attention_way(int way) {
+  W4A8_REQUIRE(way == 0 || way == 16 || way == 1 || way == 2 || way == 4 || way == 8, "way=%d must be 0, 1, 2, 4, 8 or 16", way);
+  w4a8::g_force.store(way);
+  return W4A8_OK;
+}
+
+extern "C" size_t paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t D, int cache_dtype,
+                                                  int64_t longest) {
   if (B <= 0 || heads <= 0 || Hq < heads || D < 8 || D > 256) return 0;
+  if (longest >= 0 && w4a8::attend_cluster(B, Hq, heads, D, cache_dtype == W4A8_DTYPE_E4M3, longest)) return 0;
   return w4a8::attend_layout(B, Hq / heads, D).total;
 }

@@ -44,6 +44,7 @@ struct AttendParams {
   float* part_o;                     // [warps][2][16 MT][D]
   int B, Hq, Hkv, G, D, HB;          // HB: groups of up to 16 MT query heads for a key-value head
   int warps, window;
+  int cluster;                       // blocks of a cluster that shares an item (0: the list)
   float scale;                       // times log2 e
   FastDiv by_page;
   bool q_vec, out_pair;  // 16-byte loads of q, 4-byte stores of out
@@ -56,6 +57,7 @@ int launch_attend_fp8(const AttendParams& p, bool q_f16, cudaStream_t st);
 // The instances: head dimensions up to DT, query heads of a group in MT fragments of 16.
 __host__ __device__ constexpr int attend_mt(int DT, int G) { return G > 16 && DT <= 128 ? 2 : 1; }
 __host__ __device__ constexpr int attend_dt(int64_t D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+__host__ __device__ constexpr int attend_tile(bool fp8, int DT) { return fp8 || DT == 64 ? 32 : 16; }  // tokens of a tile
 constexpr int kAttendWarps = 4;  // of a block
 inline int attend_warps(int DT) { return num_sms() * (DT <= 128 ? 2 : 1) * kAttendWarps; }  // of a launch
 
@@ -115,7 +117,7 @@ struct AttendCfg {
   static constexpr bool kBf16Out = KIND == 0 || KIND == 2, kSplit = KIND != 2;  // weights in two pieces
   static constexpr int kSize = kFp8 ? 1 : 2;
   static constexpr int kRow = DT * kSize;               // bytes of a token's row in a tile
-  static constexpr int NT = kFp8 || DT == 64 ? 32 : 16;  // tokens of a tile (E4M3, 16 and 6 slots: 102 -> 128 us)
+  static constexpr int NT = attend_tile(kFp8, DT);      // (E4M3, 16 tokens and 6 slots: 102 -> 128 us)
   static constexpr int kTile = NT * kRow;
   static constexpr int kStage = 2 * kTile;              // keys, values
   static constexpr int kStages = MT == 2 && kStage == 8192 ? 2 : 3;
@@ -128,6 +130,10 @@ struct AttendCfg {
   static constexpr int kOffQ = kStages * kStage;        // of a warp
   static constexpr int kOffScale = kOffQ + kRows * kQRow;  // fp32 [rows]: factor of a row's scores
   static constexpr int kWarpBytes = kOffScale + 128;
+  // a warp's part for its cluster: fp32 rows, padded so that 8 of them lie in different banks, over the ring (and the
+  // queries); maxima and sums at the queries' end
+  static constexpr int kJoinRow = DT + 8, kOffMl = kOffScale - kRows * 8;
+  static_assert(kRows * kJoinRow * 4 <= kOffMl, "room for the part");
   static constexpr int kSmem = kWarps * kWarpBytes;
   static constexpr int kBlocks = DT <= 128 ? 2 : 1;     // of an SM
   static_assert((kSmem + 1024) * kBlocks <= 228 * 1024, "shared memory");
@@ -186,7 +192,9 @@ __device__ __forceinline__ void store_out(void* out, int64_t at, float x, float 
   o[1] = static_cast<uint16_t>(w >> 16);
 }
 
-template <int KIND, int DT, int MT>
+// CLUSTER: an item to a cluster of blocks instead, whose warps share its tiles and join their rows through distributed
+// shared memory: one launch, no list, no workspace.  For few short sequences.
+template <int KIND, int DT, int MT, bool CLUSTER>
 __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
     paged_attention_kernel(const __grid_constant__ AttendParams p) {
   using C = AttendCfg<KIND, DT, MT>;
@@ -201,9 +209,17 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
   // first warp).  The first leaves those of every sequence for the second kernel.
   const int HH = p.Hkv * p.HB, per = (p.B + 31) / 32;
   const int64_t run_id = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
-  int64_t start, stop, at_seq;
   Cursor here;  // of the tile that is computed next
-  {
+  if constexpr (CLUSTER) {
+    const int item = blockIdx.x / p.cluster, worker = (blockIdx.x - item * p.cluster) * kWarps + warp;
+    here.b = item / HH;
+    here.hh = item - here.b * HH;
+    here.s = span_of<NT>(p, here.b);
+    const int workers = p.cluster * kWarps;
+    here.u = static_cast<int>(static_cast<int64_t>(worker) * here.s.tiles / workers);
+    here.left = static_cast<int>(static_cast<int64_t>(worker + 1) * here.s.tiles / workers) - here.u;
+  } else {
+    int64_t start, stop, at_seq;
     const int b0 = lane * per, b1 = min(p.B, b0 + per);
     int64_t mine = 0;
     SeqSpan s = {0, 0, 0};
@@ -244,8 +260,6 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
         here.s = span_of<NT>(p, ++here.b);
       }
     }
-  }
-  {
     const int64_t in = start - at_seq, each = here.s.tiles + kExtra;
     here.hh = static_cast<int>(in / each);
     const int off = static_cast<int>(in - here.hh * each);
@@ -348,6 +362,12 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
 
   int stage = 0;
   bool first = true;
+  if constexpr (CLUSTER) {
+    if (here.left <= 0) {  // an item of fewer tiles than warps: rows of no weight
+      float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
+      for (int r = lane; r < C::kRows; r += 32) ml[r] = make_float2(-INFINITY, 0.f);
+    }
+  }
   while (here.left > 0) {
     // --- the tiles of one item ---
     const int run = min(here.s.tiles - here.u, here.left);
@@ -615,6 +635,34 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
       __syncwarp();  // the tile's slot is free
     }
 
+    if constexpr (CLUSTER) {  // this warp's rows into its ring, which nothing uses any more
+      cp_async_wait<0>();
+      __syncwarp();
+      float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
+      float* rows = reinterpret_cast<float*>(smem);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float sum = l[mt][x];
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          const int r = mt * 16 + g + 8 * x;
+          if ((lane & 3) == 0) ml[r] = make_float2(m[mt][x], sum);
+          float* row = rows + r * C::kJoinRow;
+          if constexpr (kFp8) {
+#pragma unroll
+            for (int n = 0; n < kNt; n += 2)
+              *reinterpret_cast<float4*>(row + n * 8 + 2 * j2) =
+                  make_float4(o[mt][n][2 * x], o[mt][n + 1][2 * x], o[mt][n][2 * x + 1], o[mt][n + 1][2 * x + 1]);
+          } else {
+#pragma unroll
+            for (int n = 0; n < kNt; ++n)
+              *reinterpret_cast<float2*>(row + n * 8 + j2) = make_float2(o[mt][n][2 * x], o[mt][n][2 * x + 1]);
+          }
+        }
+      break;
+    }
     // --- the item's rows, or this warp's part of them ---
     const int64_t part = (run_id * 2 + (first ? 0 : 1)) * C::kRows;
     const float vs = kFp8 && p.v_scale ? p.v_scale[h] : 1.f;
@@ -665,6 +713,62 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
     here.u += run - 1;
     here.left -= run - 1;
     advance(here);
+  }
+  if constexpr (CLUSTER) {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // the cluster's threads share the rows' columns in fours, and add up the warps' parts in their order
+    const int h = here.hh / p.HB, head0 = h * p.G + (here.hh % p.HB) * C::kRows, live = min(C::kRows, (h + 1) * p.G - head0);
+    const int rank = blockIdx.x % p.cluster, fours = p.D / 4;
+    const float vs = kFp8 && p.v_scale ? p.v_scale[h] : 1.f;
+    const uint32_t base = smem_u32(smem_all);
+    const auto part_of = [&](int w, uint32_t at) {  // an address in the part of warp w of the cluster
+      uint32_t a;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(base + (w & (kWarps - 1)) * C::kWarpBytes + at), "r"(w / kWarps));
+      return a;
+    };
+    for (int i = rank * kWarps * 32 + threadIdx.x; i < live * fours; i += p.cluster * kWarps * 32) {
+      const int r = i / fours, d = (i - r * fours) * 4;
+      float top = -INFINITY, sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w0 = 0; w0 < p.cluster * kWarps; w0 += kWarps) {  // a block's parts on their way together
+        float2 ml[kWarps];
+        float4 v[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(ml[w].x), "=f"(ml[w].y) : "r"(part_of(w0 + w, C::kOffMl + r * 8)));
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(v[w].x), "=f"(v[w].y), "=f"(v[w].z), "=f"(v[w].w)
+                       : "r"(part_of(w0 + w, (r * C::kJoinRow + d) * 4)));
+        }
+        float t = top;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) t = fmaxf(t, ml[w].x);
+        const float to = t == -INFINITY ? 0.f : t, old = exp2_fast(top - to);
+        sum *= old, acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
+        top = t;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          if (ml[w].y == 0.f) continue;  // no weight: its rows may hold anything
+          const float f = exp2_fast(ml[w].x - to);
+          sum = fmaf(ml[w].y, f, sum);
+          acc.x = fmaf(v[w].x, f, acc.x);
+          acc.y = fmaf(v[w].y, f, acc.y);
+          acc.z = fmaf(v[w].z, f, acc.z);
+          acc.w = fmaf(v[w].w, f, acc.w);
+        }
+      }
+      const float inv = sum == 0.f ? 0.f : vs / sum;
+      const int64_t out = here.b * p.o_b + (head0 + r) * p.o_h + d;
+      store_out(p.out, out, acc.x * inv, acc.y * inv, bf16_out, p.out_pair);
+      store_out(p.out, out + 2, acc.z * inv, acc.w * inv, bf16_out, p.out_pair);
+      if (p.lse && d == 0)
+        p.lse[static_cast<int64_t>(here.b) * p.Hq + head0 + r] = sum == 0.f ? -INFINITY : (top - C::kShift + log2f(sum)) * kLn2;
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // no block leaves while another reads its rows
   }
 }
 
@@ -786,15 +890,36 @@ int launch_attend(AttendParams p, cudaStream_t st) {
   using C = AttendCfg<KIND, DT, MT>;
   static DeviceOnce once;
   if (int rc = once.run([] {
-        return cudaFuncSetAttribute(paged_attention_kernel<KIND, DT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    C::kSmem) == cudaSuccess
+        return cudaFuncSetAttribute(paged_attention_kernel<KIND, DT, MT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    C::kSmem) == cudaSuccess &&
+                       cudaFuncSetAttribute(paged_attention_kernel<KIND, DT, MT, true>,
+                                            cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) == cudaSuccess
                    ? static_cast<int>(W4A8_OK)
                    : check_launch("cudaFuncSetAttribute(paged_attention)");
       }))
     return rc;
   p.HB = static_cast<int>(ceil_div(p.G, C::kRows));
   p.warps = attend_warps(DT);
-  if (int rc = launch_pdl("paged_attention_kernel", paged_attention_kernel<KIND, DT, MT>, dim3(p.warps / kWarps),
+  if (p.cluster) {
+    const int64_t items = static_cast<int64_t>(p.B) * p.Hkv * p.HB;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(static_cast<unsigned>(items * p.cluster));
+    lc.blockDim = dim3(kWarps * 32);
+    lc.dynamicSmemBytes = C::kSmem;
+    lc.stream = st;
+    lc.attrs = attr;
+    lc.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&lc, paged_attention_kernel<KIND, DT, MT, true>, p);
+    if (e != cudaSuccess) return set_error(W4A8_ERR_CUDA, "paged_attention_kernel: %s", cudaGetErrorString(e));
+    return check_launch("paged_attention_kernel");
+  }
+  if (int rc = launch_pdl("paged_attention_kernel", paged_attention_kernel<KIND, DT, MT, false>, dim3(p.warps / kWarps),
                           dim3(kWarps * 32), C::kSmem, st, p))
     return rc;
   // A row with more parts than a warp asks for at once is shared by a block's warps.

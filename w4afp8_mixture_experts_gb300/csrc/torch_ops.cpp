@@ -578,7 +578,9 @@ PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ws = t.data_ptr();
       ws_bytes = t.numel();
     } else {
-      ws_bytes = static_cast<int64_t>(paged_attention_workspace_bytes(c.B, q.heads, c.heads, c.D));
+      const int64_t window = as_int(a[6]), reach = c.table_pages * c.page_size;
+      ws_bytes = static_cast<int64_t>(paged_attention_workspace_bytes(c.B, q.heads, c.heads, c.D, c.dtype,
+                                                                      window > 0 && window < reach ? window : reach));
       if (ws_bytes) {
         room = empty(1, ws_bytes, at::kByte, dev);
         ws = room.data_ptr();
