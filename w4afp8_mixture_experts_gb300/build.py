@@ -52,7 +52,7 @@ def build_shared(srcs, out, deps, extra=(), jobs=None) -> str:
     nvcc = nvcc_path()
     os.makedirs(os.path.dirname(out), exist_ok=True)
     objs = [os.path.join(os.path.dirname(out), os.path.basename(s)[:-3] + ".o") for s in srcs]
-    with cf.ThreadPoolExecutor(max_workers=jobs or min(8, os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=jobs or min(16, os.cpu_count() or 4)) as ex:
         list(ex.map(lambda so: _compile(nvcc, so[0], so[1], deps, list(extra)), zip(srcs, objs)))
     if not (os.path.exists(out) and os.path.getmtime(out) >= _newest(objs)):
         cmd = [nvcc] + ARCH + ["-shared", "-o", out] + objs
@@ -122,7 +122,7 @@ def build() -> str:
     deps = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
     if not _torch_ops_headers():
         warnings.warn("torch's or Python's headers are missing: block_norm, dense_linear and moe_route_grouped_topk are "
-                      "built for the C ABI only, not for Python")
+                      "built for the C ABI only, not for Python, and so are the operators of the attention half")
         for stale in (EXT, EXT + ".cmd"):
             if os.path.exists(stale):
                 os.remove(stale)
