@@ -75,6 +75,7 @@ class Case:
         q = _np(self.q)
         for b, n in enumerate(self.lens):
             lo = max(0, n - window) if window else 0
+            n = max(n, 0)
             want, bound, l, lb = ref.attend(q[b], self.k[b][lo:], self.v[b][lo:], scale, self.dtype, piece)
             err = np.abs(_np(out[b]) - want)
             assert (err <= bound).all(), (b, n, (err - bound).max())
@@ -95,7 +96,7 @@ def way(lib, request):
     clib.w4a8_test_paged_attention_way(0)
 
 
-LENS = [[1], [0], [17, 0, 1, 64, 65, 333, 15, 16], [5000], [130, 2000, 0, 0, 700]]
+LENS = [[1], [0], [17, -3, 1, 64, 65, 333, 15, 16], [5000], [130, 2000, 0, 0, 700]]
 
 
 @pytest.mark.parametrize("lens", LENS, ids=["one", "none", "ragged", "long", "mixed"])
@@ -293,6 +294,12 @@ def test_parts_join_to_the_whole(lib):
     size = (a.float().abs() * wa[..., None] + b.float().abs() * wb[..., None]) / (wa + wb)[..., None] + whole.float().abs()
     assert torch.all((both - whole.float()).abs() <= 2.0 ** -11 * size * 1.1 + 1e-6)
     assert torch.all((top + (wa + wb).log() - lse).abs() <= 1e-5)
+
+
+def test_a_table_without_pages(lib, way):
+    c = Case([5, 0], 4, 2, 64, 16)
+    out, lse = lib.paged_attention_decode(c.q, c.kc, c.vc, c.table[:, :0], c.lens_t, return_lse=True)
+    assert lib.device_error() == 2 and torch.all(out == 0) and torch.all(lse == -math.inf)
 
 
 def test_empty_batch(lib):

@@ -137,6 +137,18 @@ def test_saturates_and_keeps_nan(lib):
         assert got[:3] == [448.0, -448.0, 448.0] and got[3] != got[3] and got[4:] == [448.0, 448.0, 0.0, 0.0]
 
 
+@pytest.mark.parametrize("scale", [1e-41, 1e-30, 0.75, 3e4, 1e30, -0.5])
+def test_scales_of_any_size(lib, scale):
+    x = torch.tensor([0.0, 1.0, -3.5, 2.0 ** -20, 3e38, -1e-38, 100.0, float("inf")], device="cuda").to(torch.bfloat16)
+    kc, vc = (torch.zeros((1, 1, 1, 8), device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+    one = torch.ones(1, dtype=torch.int32, device="cuda")
+    s = torch.full((1,), scale, device="cuda")
+    lib.paged_kv_append(x.view(1, 1, 8), x.view(1, 1, 8), kc, vc, one.view(1, 1) - 1, one, k_scale=s, v_scale=s)
+    # the quotient rounded to fp32 once, then to E4M3, beyond 448 saturating
+    q = (x.double().cpu() / s.double().cpu()).float().clamp(-448, 448)
+    assert torch.equal(kc.flatten().cpu().float(), q.to(torch.float8_e4m3fn).float()) and torch.equal(kc.view(torch.uint8), vc.view(torch.uint8))
+
+
 def test_padded_decode_batch(lib):
     # sequences of length 0 in a batch of one token each: nothing is stored for them
     B, H, D = 6, 2, 64

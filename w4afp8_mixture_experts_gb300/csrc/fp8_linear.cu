@@ -258,13 +258,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           __syncwarp();
         }
       }
-      if (!ok) {
-        if (elect_one())
-          asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(mdrain))
-                       : "memory");
-        __syncwarp();
-        drain_bar(mdrain, 0);
-      }
+      // no product is in flight when the tensor memory goes back, also where the epilogue has given up
+      if (elect_one())
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(mdrain))
+                     : "memory");
+      __syncwarp();
+      drain_bar(mdrain, 0);
     }
     leave();
     if (warp == 2) {
@@ -464,11 +463,10 @@ __global__ void __launch_bounds__(SplitCfg<BN>::kThreads, SplitCfg<BN>::kBlocks)
       }
       __syncwarp();
     }
-    if (!ok) {
-      if (elect_one()) mma_commit(mdrain);
-      __syncwarp();
-      drain_bar(mdrain, 0);
-    }
+    // no product is in flight when the ring and the tensor memory go on, also where the sums' warps have given up
+    if (elect_one()) mma_commit(mdrain);
+    __syncwarp();
+    drain_bar(mdrain, 0);
   } else if (warp >= 4) {
     const float* bs = p.b_s + static_cast<int64_t>(nb) * p.groups + g0;
     float b0 = count > 0 ? bs[0] : 0.f, b1 = count > 1 ? bs[1] : 0.f;  // loaded two groups ahead

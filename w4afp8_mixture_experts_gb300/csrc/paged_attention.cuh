@@ -149,15 +149,16 @@ struct AttendCfg {
   static __device__ __forceinline__ uint32_t q_at(int r, int c) { return static_cast<uint32_t>(r * kQRow + ((c ^ (r & 7)) << 4)); }
 };
 
-// Sequence b's tokens and tiles.
+// Sequence b's tokens and tiles.  CHECK: a length behind the table's last page is reported (not where lengths are only added
+// up: loads wait for such a branch).
 struct SeqSpan {
   int lo, hi, tiles;
 };
-template <int NT>
+template <int NT, bool CHECK = true>
 __device__ __forceinline__ SeqSpan span_of(const AttendParams& p, int b) {
   SeqSpan s;
   const int64_t len = p.lens[b];
-  if (len > p.max_len) atomicOr(&g_attend_error, 2u);
+  if (CHECK && len > p.max_len) atomicOr(&g_attend_error, 2u);
   s.hi = static_cast<int>(min(len, p.max_len));
   s.lo = p.window > 0 ? max(0, s.hi - p.window) : 0;
   s.tiles = s.hi > s.lo ? (s.hi - s.lo + NT - 1) / NT : 0;
@@ -223,8 +224,9 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
     const int b0 = lane * per, b1 = min(p.B, b0 + per);
     int64_t mine = 0;
     SeqSpan s = {0, 0, 0};
+#pragma unroll 4
     for (int b = b0; b < b1; ++b) {
-      s = span_of<NT>(p, b);
+      s = span_of<NT, false>(p, b);
       mine += places_of(s, HH);
     }
     int64_t up = mine;
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
       int64_t at = up - mine;
       for (int b = b0; b < b1; ++b) {
         p.prefix[b] = at;
-        at += per == 1 ? mine : places_of(span_of<NT>(p, b), HH);
+        at += per == 1 ? mine : places_of(span_of<NT, false>(p, b), HH);
       }
       if (lane == 31) p.prefix[p.B] = up;
     }
@@ -254,10 +256,10 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
       here.s.hi = __shfl_sync(0xffffffffu, s.hi, c);
       here.s.tiles = __shfl_sync(0xffffffffu, s.tiles, c);
     } else {
-      here.s = span_of<NT>(p, here.b);
+      here.s = span_of<NT, false>(p, here.b);
       while (at_seq + places_of(here.s, HH) <= start) {
         at_seq += places_of(here.s, HH);
-        here.s = span_of<NT>(p, ++here.b);
+        here.s = span_of<NT, false>(p, ++here.b);
       }
     }
     const int64_t in = start - at_seq, each = here.s.tiles + kExtra;
@@ -787,6 +789,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_attention_join_kernel(c
   const int b = static_cast<int>(row / p.Hq), head = static_cast<int>(row - static_cast<int64_t>(b) * p.Hq);
   const int h = head / p.G, in = head - h * p.G, hh = h * p.HB + in / C::kRows, r = in % C::kRows;
   const int HH = p.Hkv * p.HB;
+  if (lane == 0 && head == 0 && p.lens[b] > p.max_len) atomicOr(&g_attend_error, 2u);
   const int64_t before = p.prefix[b], each = (p.prefix[b + 1] - before) / HH, total = p.prefix[p.B];
   constexpr bool bf16 = C::kBf16Out;
   const int64_t out = b * p.o_b + head * p.o_h;

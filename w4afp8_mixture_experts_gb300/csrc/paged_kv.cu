@@ -49,9 +49,10 @@ struct alignas(sizeof(T) * V) Vec {
   T e[V];
 };
 
-// the correctly rounded quotient; where it is past what E4M3 holds its last bits do not matter
+// the correctly rounded quotient, r = 1 / scale; where it is past what E4M3 holds its last bits do not matter
 __device__ __forceinline__ float over(float v, float scale, float r) {
-  return fabsf(v * r) < 512.f ? div_by_scale(v, scale, r) : v * r;
+  const float q = v * r;
+  return fabsf(q) >= 512.f && fabsf(r) < INFINITY ? q : div_by_scale(v, scale, r);
 }
 
 // Where the two vectors of an item lie in its row; the second may be missing (-1).
