@@ -132,9 +132,9 @@ def test_window(lib, way, window, cache):
     c.check(lib, *c.call(lib, return_lse=True, window=window), window=window)
 
 
-@pytest.mark.parametrize("B", [2, 37, 130, 700])
+@pytest.mark.parametrize("B", [2, 32, 33, 37, 130, 700, 1024, 1025, 2600])
 def test_many_sequences(lib, way, B):
-    c = Case([(37 * b) % 101 for b in range(B)], 4, 2, 64, 16, seed=B)
+    c = Case([(37 * b) % 101 if B < 1000 else (37 * b) % 11 for b in range(B)], 4, 2, 64, 16, seed=B)
     c.check(lib, *c.call(lib, return_lse=True))
 
 

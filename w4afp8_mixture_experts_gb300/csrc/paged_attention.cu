@@ -8,16 +8,17 @@ namespace {
 
 std::atomic<int> g_force{0};  // way asked for by a test
 
-// Workspace: places before each sequence, then (m, l) and O of two parts of every warp.
+// Workspace: places before each sequence, the runs' starts, then (m, l) and O of two parts of every warp.
 struct AttendLayout {
-  size_t ml, o, total;
+  size_t starts, ml, o, total;
 };
 AttendLayout attend_layout(int64_t B, int64_t G, int64_t D) {
   const auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
   const int DT = attend_dt(D);
   const size_t rows = static_cast<size_t>(attend_warps(DT)) * 2 * 16 * attend_mt(DT, static_cast<int>(G));
   AttendLayout L;
-  L.ml = up(static_cast<size_t>(B + 1) * 8);
+  L.starts = up(static_cast<size_t>(B + 1) * 8);
+  L.ml = L.starts + up(static_cast<size_t>(attend_warps(DT)) * sizeof(RunStart));
   L.o = L.ml + up(rows * 8);
   L.total = L.o + up(rows * static_cast<size_t>(D) * 4);
   return L;
@@ -107,6 +108,7 @@ extern "C" int paged_attention_decode(const void* q, int64_t ldq_b, int64_t ldq_
   p.max_len = max_len;
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.prefix = reinterpret_cast<int64_t*>(w);
+  p.starts = reinterpret_cast<RunStart*>(w + L.starts);
   p.part_ml = reinterpret_cast<float2*>(w + L.ml);
   p.part_o = reinterpret_cast<float*>(w + L.o);
   p.B = static_cast<int>(B);

@@ -29,6 +29,12 @@
 
 namespace w4a8 {
 
+// An item of the list: its sequence, head and group, its first place and its places.
+struct RunStart {
+  int64_t first, each;
+  int b, hh;
+};
+
 struct AttendParams {
   const void* q;
   const void *k, *v;
@@ -39,12 +45,14 @@ struct AttendParams {
   int64_t q_b, q_h, o_b, o_h;
   int64_t k_page, k_slot, k_head, v_page, v_slot, v_head;  // bytes
   int64_t table_ld, pages, max_len;  // max_len: positions that the table reaches
-  int64_t* prefix;                   // [B + 1] places in the list before each sequence
+  int64_t* prefix;                   // [B + 1] places in the list before each sequence (the last: all of them)
+  RunStart* starts;                  // [warps] the item in which each run starts
   float2* part_ml;                   // [warps][2][16 MT]
   float* part_o;                     // [warps][2][16 MT][D]
   int B, Hq, Hkv, G, D, HB;          // HB: groups of up to 16 MT query heads for a key-value head
   int warps, window;
   int cluster;                       // blocks of a cluster that shares an item (0: the list)
+  bool by_rows;                      // the second kernel goes by rows, through `prefix`; else by the runs' starts
   float scale;                       // times log2 e
   FastDiv by_page;
   bool q_vec, out_pair;  // 16-byte loads of q, 4-byte stores of out
@@ -206,10 +214,18 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
   pdl_trigger();
   pdl_wait();
 
-  // Places before each lane's sequences: every warp adds them up for itself (no barrier; the lengths come from L1 after the
-  // first warp).  The first leaves those of every sequence for the second kernel.
-  const int HH = p.Hkv * p.HB, per = (p.B + 31) / 32;
+  const int HH = p.Hkv * p.HB;
   const int64_t run_id = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
+  // zeros for the sequences without a tile, each of them a warp's
+  const auto zero_empty = [&] {
+    for (int b = static_cast<int>(run_id); b < p.B; b += p.warps) {
+      if (span_of<NT>(p, b).tiles) continue;
+      for (int i = lane; i < p.Hq * p.D; i += 32)
+        static_cast<uint16_t*>(p.out)[b * p.o_b + i / p.D * p.o_h + i % p.D] = 0;  // bf16's and f16's zero
+      if (p.lse)
+        for (int i = lane; i < p.Hq; i += 32) p.lse[static_cast<int64_t>(b) * p.Hq + i] = -INFINITY;
+    }
+  };
   Cursor here;  // of the tile that is computed next
   if constexpr (CLUSTER) {
     const int item = blockIdx.x / p.cluster, worker = (blockIdx.x - item * p.cluster) * kWarps + warp;
@@ -220,53 +236,79 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
     here.u = static_cast<int>(static_cast<int64_t>(worker) * here.s.tiles / workers);
     here.left = static_cast<int>(static_cast<int64_t>(worker + 1) * here.s.tiles / workers) - here.u;
   } else {
-    int64_t start, stop, at_seq;
-    const int b0 = lane * per, b1 = min(p.B, b0 + per);
-    int64_t mine = 0;
-    SeqSpan s = {0, 0, 0};
-#pragma unroll 4
-    for (int b = b0; b < b1; ++b) {
-      s = span_of<NT, false>(p, b);
-      mine += places_of(s, HH);
-    }
-    int64_t up = mine;
+    // Every warp adds up the places of all sequences for itself (no barrier; the lengths come from L1 after the first warp),
+    // in up to 32 chunks of 32 `turns` neighbours, lane k holding the sum of chunk k.
+    const auto scan = [&](int64_t v) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, up, o);
-      if (lane >= o) up += x;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+      }
+      return v;
+    };
+    const auto places_at = [&](int b) { return b < p.B ? places_of(span_of<NT, false>(p, b), HH) : 0; };
+    const int turns = (p.B + 1023) / 1024, chunk = 32 * turns;
+    int64_t mine = 0, v = 0;
+    int k = 0, turn = 0;
+    const auto close = [&] {  // chunk k: the warp's sum in two pieces, each below 2^32 (a list has fewer than 2^38 places)
+      const int64_t all = static_cast<int64_t>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> 24))) * (1 << 24) +
+                          __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v & 0xFFFFFF));
+      if (lane == k) mine = all;
+      ++k;
+      v = turn = 0;
+    };
+    for (int t = 0; t * 32 < p.B; t += 8) {
+      int64_t x[8];  // on their way together
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = places_at((t + j) * 32 + lane);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v += x[j];
+        if (++turn == turns) close();
+      }
     }
+    if (turn > 0) close();
+    int64_t up = scan(mine);
     const int64_t total = __shfl_sync(0xffffffffu, up, 31);
     if (run_id == 0) {
-      int64_t at = up - mine;
-      for (int b = b0; b < b1; ++b) {
-        p.prefix[b] = at;
-        at += per == 1 ? mine : places_of(span_of<NT, false>(p, b), HH);
+      if (lane == 0) p.prefix[p.B] = total;
+      if (p.by_rows) {
+        int64_t at = 0;
+        for (int b = lane; b < p.B + lane; b += 32) {
+          const int64_t v = places_at(b), to = scan(v);
+          if (b < p.B) p.prefix[b] = at + to - v;
+          at += __shfl_sync(0xffffffffu, to, 31);
+        }
       }
-      if (lane == 31) p.prefix[p.B] = up;
     }
     const int64_t runs = runs_of(p, total);
-    if (run_id >= runs) return;
-    start = run_id * total / runs;
-    stop = (run_id + 1) * total / runs;
-    const int c = __popc(__ballot_sync(0xffffffffu, up <= start));  // the lane that has place `start`
-    at_seq = __shfl_sync(0xffffffffu, up - mine, c);
-    here.b = c * per;
-    if (per == 1) {
-      here.s.lo = __shfl_sync(0xffffffffu, s.lo, c);
-      here.s.hi = __shfl_sync(0xffffffffu, s.hi, c);
-      here.s.tiles = __shfl_sync(0xffffffffu, s.tiles, c);
-    } else {
-      here.s = span_of<NT, false>(p, here.b);
-      while (at_seq + places_of(here.s, HH) <= start) {
-        at_seq += places_of(here.s, HH);
-        here.s = span_of<NT, false>(p, ++here.b);
-      }
+    if (run_id >= runs) {
+      zero_empty();
+      return;
     }
+    const int64_t start = run_id * total / runs, stop = (run_id + 1) * total / runs;
+    // the chunk that has place `start`, then the sequence
+    const int c = __popc(__ballot_sync(0xffffffffu, up <= start));
+    int64_t at_seq = __shfl_sync(0xffffffffu, up - mine, c);
+    for (int i = 0; i < turns; ++i) {
+      const int b = c * chunk + i * 32 + lane;
+      const int64_t v = places_at(b);
+      up = at_seq + scan(v);
+      const int l = __popc(__ballot_sync(0xffffffffu, up <= start));
+      if (l < 32) {
+        here.b = c * chunk + i * 32 + l;
+        at_seq = __shfl_sync(0xffffffffu, up - v, l);
+        break;
+      }
+      at_seq = __shfl_sync(0xffffffffu, up, 31);
+    }
+    here.s = span_of<NT, false>(p, here.b);
     const int64_t in = start - at_seq, each = here.s.tiles + kExtra;
     here.hh = static_cast<int>(in / each);
     const int off = static_cast<int>(in - here.hh * each);
     here.u = max(0, off - kExtra);
     here.left = static_cast<int>(stop - start) - max(0, kExtra - off);
+    if (lane == 0 && !p.by_rows) p.starts[run_id] = {at_seq + here.hh * each, each, here.b, here.hh};
   }
   const auto advance = [&](Cursor& c) {
     --c.left;
@@ -354,6 +396,7 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) issue(i);
+  if constexpr (!CLUSTER) zero_empty();  // while the first tiles are on their way
 
   constexpr int kNt = DT / 8;  // column fragments of O
   float o[MT][kNt][4], m[MT][2], l[MT][2];
@@ -672,45 +715,60 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        float sum = l[mt][x];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        const int r = mt * 16 + g + 8 * x;
-        if (r >= live) continue;
-        const float top = m[mt][x], inv = sum == 0.f ? 0.f : vs / sum;
-        if ((lane & 3) == 0) {
-          if (!whole)
-            p.part_ml[part + r] = make_float2(top, sum);
-          else if (p.lse)
-            p.lse[static_cast<int64_t>(here.b) * p.Hq + head0 + r] =
-                sum == 0.f ? -INFINITY : (top - C::kShift + log2f(sum)) * kLn2;
-        }
-        const int64_t out = here.b * p.o_b + (head0 + r) * p.o_h;
-        if constexpr (kFp8) {  // fragments n and n + 1 hold the even and odd ones of 16 columns: four neighbours to a lane
+        l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 1);
+        l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 2);
+      }
+    // WHOLE, PAIR: chosen once for all stores (chosen at each of them, they took 0.8 us)
+    const auto write = [&](auto whole_, auto pair_) {
+      constexpr bool WHOLE = decltype(whole_)::value, PAIR = decltype(pair_)::value;
 #pragma unroll
-          for (int n = 0; n < kNt; n += 2) {
-            const int d = n * 8 + 2 * j2;
-            const float v0 = o[mt][n][2 * x], v1 = o[mt][n + 1][2 * x], v2 = o[mt][n][2 * x + 1], v3 = o[mt][n + 1][2 * x + 1];
-            if (d >= p.D) continue;
-            if (whole) {
-              store_out(p.out, out + d, v0 * inv, v1 * inv, bf16_out, p.out_pair);
-              store_out(p.out, out + d + 2, v2 * inv, v3 * inv, bf16_out, p.out_pair);
-            } else {
-              *reinterpret_cast<float4*>(p.part_o + (part + r) * p.D + d) = make_float4(v0, v1, v2, v3);
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int r = mt * 16 + g + 8 * x;
+          if (r >= live) continue;
+          const float top = m[mt][x], sum = l[mt][x], inv = sum == 0.f ? 0.f : vs / sum;
+          if ((lane & 3) == 0) {
+            if (!WHOLE)
+              p.part_ml[part + r] = make_float2(top, sum);
+            else if (p.lse)
+              p.lse[static_cast<int64_t>(here.b) * p.Hq + head0 + r] =
+                  sum == 0.f ? -INFINITY : (top - C::kShift + log2f(sum)) * kLn2;
+          }
+          const int64_t out = here.b * p.o_b + (head0 + r) * p.o_h;
+          float* row = p.part_o + (part + r) * p.D;
+          if constexpr (kFp8) {  // fragments n and n + 1 hold the even and odd ones of 16 columns: four neighbours to a lane
+#pragma unroll
+            for (int n = 0; n < kNt; n += 2) {
+              const int d = n * 8 + 2 * j2;
+              const float v0 = o[mt][n][2 * x], v1 = o[mt][n + 1][2 * x], v2 = o[mt][n][2 * x + 1], v3 = o[mt][n + 1][2 * x + 1];
+              if (d >= p.D) continue;
+              if (WHOLE) {
+                store_out(p.out, out + d, v0 * inv, v1 * inv, bf16_out, PAIR);
+                store_out(p.out, out + d + 2, v2 * inv, v3 * inv, bf16_out, PAIR);
+              } else {
+                *reinterpret_cast<float4*>(row + d) = make_float4(v0, v1, v2, v3);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < kNt; ++n) {
+              const int d = n * 8 + j2;
+              if (d >= p.D) continue;
+              if (WHOLE)
+                store_out(p.out, out + d, o[mt][n][2 * x] * inv, o[mt][n][2 * x + 1] * inv, bf16_out, PAIR);
+              else
+                *reinterpret_cast<float2*>(row + d) = make_float2(o[mt][n][2 * x], o[mt][n][2 * x + 1]);
             }
           }
-        } else {
-#pragma unroll
-          for (int n = 0; n < kNt; ++n) {
-            const int d = n * 8 + j2;
-            if (d >= p.D) continue;
-            if (whole)
-              store_out(p.out, out + d, o[mt][n][2 * x] * inv, o[mt][n][2 * x + 1] * inv, bf16_out, p.out_pair);
-            else
-              *reinterpret_cast<float2*>(p.part_o + (part + r) * p.D + d) = make_float2(o[mt][n][2 * x], o[mt][n][2 * x + 1]);
-          }
         }
-      }
+    };
+    if (!whole)
+      write(std::false_type{}, std::false_type{});
+    else if (p.out_pair)
+      write(std::true_type{}, std::true_type{});
+    else
+      write(std::true_type{}, std::false_type{});
     first = false;
     here.u += run - 1;
     here.left -= run - 1;
@@ -774,118 +832,136 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
   }
 }
 
-// Joins the parts of the items that several warps shared, in the warps' order: WPR warps to a row (sequence, query head),
-// each a range of the parts.  Empty sequences get zeros here.
+// Joins the parts of the items that several warps shared, in the warps' order.
+//   ROWS: a block to a row (sequence, query head), its warps each a range of the parts: few items, many parts.
+//   else: a block to a run's start; where it is the first one inside an item, the block's warps take the item's rows.  (Looking
+//   at all rows instead, of which few need it, took 14 us for 512 sequences of 64 heads.)
 constexpr int kJoinWarps = 8;
-template <int KIND, int DT, int MT, int WPR>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_attention_join_kernel(const __grid_constant__ AttendParams p) {
+template <int KIND, int DT, int MT, bool ROWS>
+__global__ void __launch_bounds__(kJoinWarps * 32, ROWS || DT > 128 ? 1 : 4)
+    paged_attention_join_kernel(const __grid_constant__ AttendParams p) {
   using C = AttendCfg<KIND, DT, MT>;
   constexpr int kV = (DT + 127) / 128;  // float4 of a lane
+  constexpr int WPR = ROWS ? kJoinWarps : 1;
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kJoinWarps / WPR) + warp / WPR;
-  if (row >= static_cast<int64_t>(p.B) * p.Hq) return;  // with WPR > 1 the whole block
-  const int b = static_cast<int>(row / p.Hq), head = static_cast<int>(row - static_cast<int64_t>(b) * p.Hq);
-  const int h = head / p.G, in = head - h * p.G, hh = h * p.HB + in / C::kRows, r = in % C::kRows;
-  const int HH = p.Hkv * p.HB;
-  if (lane == 0 && head == 0 && p.lens[b] > p.max_len) atomicOr(&g_attend_error, 2u);
-  const int64_t before = p.prefix[b], each = (p.prefix[b + 1] - before) / HH, total = p.prefix[p.B];
   constexpr bool bf16 = C::kBf16Out;
-  const int64_t out = b * p.o_b + head * p.o_h;
-  if (each == 0) {
-    if (warp % WPR) return;
-    for (int d = lane; d < p.D; d += 32) static_cast<uint16_t*>(p.out)[out + d] = 0;  // bf16's and f16's zero
-    if (p.lse && lane == 0) p.lse[row] = -INFINITY;
-    return;
+  const int64_t total = p.prefix[p.B];
+  int b, hh, r0;
+  int64_t i0, each, runs;
+  if constexpr (ROWS) {
+    b = static_cast<int>(blockIdx.x / p.Hq);
+    const int head = blockIdx.x - b * p.Hq, h = head / p.G, in = head - h * p.G;
+    hh = h * p.HB + in / C::kRows;
+    r0 = in % C::kRows;
+    const int64_t before = p.prefix[b];
+    each = (p.prefix[b + 1] - before) / (p.Hkv * p.HB);
+    if (each == 0) return;  // an empty sequence
+    i0 = before + hh * each;
+    runs = runs_of(p, total);
+  } else {
+    const int64_t c = blockIdx.x + 1;
+    const RunStart s = p.starts[c];
+    runs = runs_of(p, total);
+    if (c >= runs) return;
+    b = s.b;
+    hh = s.hh;
+    i0 = s.first;
+    each = s.each;
+    r0 = warp;
+    // its place is behind the item's first tile, which the run before it has
+    if (c * total / runs <= i0 + kExtra || (c - 1) * total / runs > i0 + kExtra) return;
   }
-  const int64_t i0 = before + hh * each, runs = runs_of(p, total);
   const int64_t c0 = ((i0 + kExtra + 1) * runs - 1) / total, c1 = ((i0 + each) * runs - 1) / total;
   if (c0 == c1) return;  // written by its only warp
   const int skip = c0 * total / runs >= i0 ? 0 : 1;  // whether the item is behind another one in its first warp's run
+  const int h = hh / p.HB, head0 = h * p.G + (hh % p.HB) * C::kRows, live = min(C::kRows, (h + 1) * p.G - head0);
   const int parts = static_cast<int>(c1 - c0) + 1, w = warp % WPR;
   const int from = static_cast<int>(static_cast<int64_t>(w) * parts / WPR), to = static_cast<int>(static_cast<int64_t>(w + 1) * parts / WPR);
-  const auto at = [&](int i) { return ((c0 + i) * 2 + (i == 0 ? skip : 0)) * C::kRows + r; };
-  float top = -INFINITY, sum = 0.f;
-  float4 acc[kV];
+  for (int r = r0; r < live; r += ROWS ? live : kJoinWarps) {
+    const int64_t row = static_cast<int64_t>(b) * p.Hq + head0 + r, out = b * p.o_b + (head0 + r) * p.o_h;
+    const auto at = [&](int i) { return ((c0 + i) * 2 + (i == 0 ? skip : 0)) * C::kRows + r; };
+    float top = -INFINITY, sum = 0.f;
+    float4 acc[kV];
 #pragma unroll
-  for (int x = 0; x < kV; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kAhead = kV == 1 ? 10 : 5;  // parts of O asked for at a time
-  float4 v[kAhead][kV];
-  const auto load = [&](int i) {
+    for (int x = 0; x < kV; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kAhead = ROWS ? (kV == 1 ? 10 : 5) : 3;  // parts of O asked for at a time
+    float4 v[kAhead][kV];
+    const auto load = [&](int i) {
 #pragma unroll
-    for (int y = 0; y < kAhead; ++y)
-#pragma unroll
-      for (int x = 0; x < kV; ++x) {
-        const int d = (x * 32 + lane) * 4;
-        v[y][x] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i + y < to && d < p.D) v[y][x] = *reinterpret_cast<const float4*>(p.part_o + at(i + y) * p.D + d);
-      }
-  };
-  for (int f0 = from; f0 < to; f0 += 32) {  // 32 parts at a time, one maximum and sum to a lane
-    load(f0);  // on its way together with the maxima
-    const float2 ml = f0 + lane < to ? p.part_ml[at(f0 + lane)] : make_float2(-INFINITY, 0.f);
-    const float t = fmaxf(top, warp_max(ml.x)), base = t == -INFINITY ? 0.f : t;
-    const float old = exp2_fast(top - base), now = exp2_fast(ml.x - base);
-    sum = sum * old + warp_sum(ml.y * now);
-#pragma unroll
-    for (int x = 0; x < kV; ++x) acc[x].x *= old, acc[x].y *= old, acc[x].z *= old, acc[x].w *= old;
-    top = t;
-    const int n = min(32, to - f0);
-#pragma unroll 1
-    for (int j = 0; j < n; j += kAhead) {
-      if (j > 0) load(f0 + j);
-#pragma unroll
-      for (int y = 0; y < kAhead; ++y) {
-        const float f = __shfl_sync(0xffffffffu, now, (j + y) & 31);
-        if (j + y >= n) continue;
+      for (int y = 0; y < kAhead; ++y)
 #pragma unroll
         for (int x = 0; x < kV; ++x) {
-          acc[x].x = fmaf(v[y][x].x, f, acc[x].x);
-          acc[x].y = fmaf(v[y][x].y, f, acc[x].y);
-          acc[x].z = fmaf(v[y][x].z, f, acc[x].z);
-          acc[x].w = fmaf(v[y][x].w, f, acc[x].w);
+          const int d = (x * 32 + lane) * 4;
+          v[y][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i + y < to && d < p.D) v[y][x] = *reinterpret_cast<const float4*>(p.part_o + at(i + y) * p.D + d);
+        }
+    };
+    for (int f0 = from; f0 < to; f0 += 32) {  // 32 parts at a time, one maximum and sum to a lane
+      load(f0);  // on its way together with the maxima
+      const float2 ml = f0 + lane < to ? p.part_ml[at(f0 + lane)] : make_float2(-INFINITY, 0.f);
+      const float t = fmaxf(top, warp_max(ml.x)), base = t == -INFINITY ? 0.f : t;
+      const float old = exp2_fast(top - base), now = exp2_fast(ml.x - base);
+      sum = sum * old + warp_sum(ml.y * now);
+#pragma unroll
+      for (int x = 0; x < kV; ++x) acc[x].x *= old, acc[x].y *= old, acc[x].z *= old, acc[x].w *= old;
+      top = t;
+      const int n = min(32, to - f0);
+#pragma unroll 1
+      for (int j = 0; j < n; j += kAhead) {
+        if (j > 0) load(f0 + j);
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+          const float f = __shfl_sync(0xffffffffu, now, (j + y) & 31);
+          if (j + y >= n) continue;
+#pragma unroll
+          for (int x = 0; x < kV; ++x) {
+            acc[x].x = fmaf(v[y][x].x, f, acc[x].x);
+            acc[x].y = fmaf(v[y][x].y, f, acc[x].y);
+            acc[x].z = fmaf(v[y][x].z, f, acc[x].z);
+            acc[x].w = fmaf(v[y][x].w, f, acc[x].w);
+          }
         }
       }
     }
-  }
-  if constexpr (WPR > 1) {
-    static_assert(WPR == kJoinWarps, "a block to a row");
-    __shared__ float2 all_ml[WPR];
-    __shared__ float4 all_o[WPR][kV][32];
-    if (lane == 0) all_ml[w] = make_float2(top, sum);
+    if constexpr (ROWS) {
+      __shared__ float2 all_ml[WPR];
+      __shared__ float4 all_o[WPR][kV][32];
+      if (lane == 0) all_ml[w] = make_float2(top, sum);
 #pragma unroll
-    for (int x = 0; x < kV; ++x) all_o[w][x][lane] = acc[x];
-    __syncthreads();
-    if (w) return;
-    for (int y = 1; y < WPR; ++y) top = fmaxf(top, all_ml[y].x);
-    const float base = top == -INFINITY ? 0.f : top;
-    sum = 0.f;
+      for (int x = 0; x < kV; ++x) all_o[w][x][lane] = acc[x];
+      __syncthreads();
+      if (w) return;
+      for (int y = 1; y < WPR; ++y) top = fmaxf(top, all_ml[y].x);
+      const float base = top == -INFINITY ? 0.f : top;
+      sum = 0.f;
 #pragma unroll
-    for (int x = 0; x < kV; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int x = 0; x < kV; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int y = 0; y < WPR; ++y) {
-      const float f = exp2_fast(all_ml[y].x - base);
-      sum += all_ml[y].y * f;
+      for (int y = 0; y < WPR; ++y) {
+        const float f = exp2_fast(all_ml[y].x - base);
+        sum += all_ml[y].y * f;
 #pragma unroll
-      for (int x = 0; x < kV; ++x) {
-        const float4 v = all_o[y][x][lane];
-        acc[x].x = fmaf(v.x, f, acc[x].x);
-        acc[x].y = fmaf(v.y, f, acc[x].y);
-        acc[x].z = fmaf(v.z, f, acc[x].z);
-        acc[x].w = fmaf(v.w, f, acc[x].w);
+        for (int x = 0; x < kV; ++x) {
+          const float4 v = all_o[y][x][lane];
+          acc[x].x = fmaf(v.x, f, acc[x].x);
+          acc[x].y = fmaf(v.y, f, acc[x].y);
+          acc[x].z = fmaf(v.z, f, acc[x].z);
+          acc[x].w = fmaf(v.w, f, acc[x].w);
+        }
       }
     }
-  }
-  const float vs = C::kFp8 && p.v_scale ? p.v_scale[h] : 1.f, inv = sum == 0.f ? 0.f : vs / sum;
+    const float vs = C::kFp8 && p.v_scale ? p.v_scale[h] : 1.f, inv = sum == 0.f ? 0.f : vs / sum;
 #pragma unroll
-  for (int x = 0; x < kV; ++x) {
-    const int d = (x * 32 + lane) * 4;
-    if (d >= p.D) continue;
-    store_out(p.out, out + d, acc[x].x * inv, acc[x].y * inv, bf16, p.out_pair);
-    store_out(p.out, out + d + 2, acc[x].z * inv, acc[x].w * inv, bf16, p.out_pair);
+    for (int x = 0; x < kV; ++x) {
+      const int d = (x * 32 + lane) * 4;
+      if (d >= p.D) continue;
+      store_out(p.out, out + d, acc[x].x * inv, acc[x].y * inv, bf16, p.out_pair);
+      store_out(p.out, out + d + 2, acc[x].z * inv, acc[x].w * inv, bf16, p.out_pair);
+    }
+    if (p.lse && lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top - C::kShift + log2f(sum)) * kLn2;
   }
-  if (p.lse && lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top - C::kShift + log2f(sum)) * kLn2;
 }
 
 template <int KIND, int DT, int MT>
@@ -922,16 +998,16 @@ int launch_attend(AttendParams p, cudaStream_t st) {
     if (e != cudaSuccess) return set_error(W4A8_ERR_CUDA, "paged_attention_kernel: %s", cudaGetErrorString(e));
     return check_launch("paged_attention_kernel");
   }
+  // few items have many parts each
+  p.by_rows = static_cast<int64_t>(p.B) * p.Hkv * p.HB * 8 < p.warps;
   if (int rc = launch_pdl("paged_attention_kernel", paged_attention_kernel<KIND, DT, MT, false>, dim3(p.warps / kWarps),
                           dim3(kWarps * 32), C::kSmem, st, p))
     return rc;
-  // A row with more parts than a warp asks for at once is shared by a block's warps.
-  const int64_t rows = static_cast<int64_t>(p.B) * p.Hq;
-  if (static_cast<int64_t>(p.B) * p.Hkv * p.HB * 8 < p.warps)
-    return launch_pdl("paged_attention_join_kernel", paged_attention_join_kernel<KIND, DT, MT, kJoinWarps>,
-                      dim3(static_cast<unsigned>(rows)), dim3(kJoinWarps * 32), 0, st, p);
-  return launch_pdl("paged_attention_join_kernel", paged_attention_join_kernel<KIND, DT, MT, 1>,
-                    dim3(static_cast<unsigned>(ceil_div(rows, kJoinWarps))), dim3(kJoinWarps * 32), 0, st, p);
+  if (p.by_rows)
+    return launch_pdl("paged_attention_join_kernel", paged_attention_join_kernel<KIND, DT, MT, true>,
+                      dim3(static_cast<unsigned>(p.B * p.Hq)), dim3(kJoinWarps * 32), 0, st, p);
+  return launch_pdl("paged_attention_join_kernel", paged_attention_join_kernel<KIND, DT, MT, false>,
+                    dim3(static_cast<unsigned>(p.warps - 1)), dim3(kJoinWarps * 32), 0, st, p);
 }
 
 template <int KIND>
