@@ -53,6 +53,11 @@ __device__ __forceinline__ void fma2(uint64_t& sum, uint32_t v0, uint32_t v1, ui
       : "+l"(sum)
       : "r"(v0), "r"(v1), "l"(scale2));
 }
+__device__ __forceinline__ uint64_t mul2(float x, float y, uint64_t scale2) {
+  uint64_t r;
+  asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tmul.rn.f32x2 %0, v, %3;\n\t}" : "=l"(r) : "f"(x), "f"(y), "l"(scale2));
+  return r;
+}
 __device__ __forceinline__ uint64_t twice(float v) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
@@ -428,7 +433,7 @@ __global__ void __launch_bounds__(SplitCfg<BN>::kThreads, SplitCfg<BN>::kBlocks)
   const int g0 = static_cast<int>(static_cast<int64_t>(rank) * p.groups / splits);
   const int count = static_cast<int>(static_cast<int64_t>(rank + 1) * p.groups / splits) - g0;
   bool ok = true;
-  float sum[C::kCols];
+  uint64_t sum[C::kCols / 2];  // two tokens each
   const int quarter = warp & 3, half = (warp >> 2) - 1, f = quarter * 32 + lane;
   if (warp == 0) {
     int it = 0;
@@ -471,10 +476,10 @@ __global__ void __launch_bounds__(SplitCfg<BN>::kThreads, SplitCfg<BN>::kBlocks)
     const float* bs = p.b_s + static_cast<int64_t>(nb) * p.groups + g0;
     float b0 = count > 0 ? bs[0] : 0.f, b1 = count > 1 ? bs[1] : 0.f;  // loaded two groups ahead
 #pragma unroll
-    for (int j = 0; j < C::kCols; ++j) sum[j] = 0.f;
+    for (int j = 0; j < C::kCols / 2; ++j) sum[j] = 0;
     for (int it = 0; it < count; ++it) {
       const int s = it % C::kStages, buf = it % C::kBufs;
-      const float b = b0;
+      const uint64_t b = twice(b0);
       b0 = b1;
       b1 = it + 2 < count ? bs[it + 2] : 0.f;
       // the scales come with the stage's copies, which this warp waits for as the products do
@@ -496,10 +501,8 @@ __global__ void __launch_bounds__(SplitCfg<BN>::kThreads, SplitCfg<BN>::kBlocks)
 #pragma unroll
         for (int j = 0; j < kStep; j += 4) {
           const float4 a = C::kCols <= 16 ? scale[(c + j) / 4] : as[(c + j) / 4];
-          sum[c + j] = fmaf(__uint_as_float(v[j]), a.x * b, sum[c + j]);
-          sum[c + j + 1] = fmaf(__uint_as_float(v[j + 1]), a.y * b, sum[c + j + 1]);
-          sum[c + j + 2] = fmaf(__uint_as_float(v[j + 2]), a.z * b, sum[c + j + 2]);
-          sum[c + j + 3] = fmaf(__uint_as_float(v[j + 3]), a.w * b, sum[c + j + 3]);
+          fma2(sum[(c + j) / 2], v[j], v[j + 1], mul2(a.x, a.y, b));
+          fma2(sum[(c + j) / 2 + 1], v[j + 2], v[j + 3], mul2(a.z, a.w, b));
         }
       }
       tc_fence_before();
@@ -525,7 +528,8 @@ __global__ void __launch_bounds__(SplitCfg<BN>::kThreads, SplitCfg<BN>::kBlocks)
 #pragma unroll
       for (int j = 0; j < C::kCols; ++j) {
         const int m = m0 + half * C::kCols + j;
-        if (m < p.M) store_any(p.out, m * p.ldo + n0 + f, sum[j], p.out_dtype);
+        const float2 v = halves(sum[j / 2]);
+        if (m < p.M) store_any(p.out, m * p.ldo + n0 + f, j % 2 ? v.y : v.x, p.out_dtype);
       }
     }
     leave();
@@ -549,7 +553,8 @@ __global__ void __launch_bounds__(SplitCfg<BN>::kThreads, SplitCfg<BN>::kBlocks)
         end = (q + 1) * BN / splits;
       }
       const uint32_t to = map_to_cta(red + ((rank * most + tok - begin) * 128 + f) * 4, q);
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(sum[j]) : "memory");
+      const float2 v = halves(sum[j / 2]);
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(j % 2 ? v.y : v.x) : "memory");
     }
   }
   __syncwarp();
@@ -716,9 +721,9 @@ template <int BN, int SPLITS>
 constexpr Option split_option() {
   using C = SplitCfg<BN>;
   // the exchange of the pieces' sums: its barriers, and its bytes
-  constexpr double fixed = BN == 128 ? 4.2 : BN == 64 ? 3.4 : BN == 32 ? 3.0 : 2.6, exchange = SPLITS > 1 ? 1.4 + 0.7 * BN / 64 : 0;
+  constexpr double fixed = BN == 128 ? 4.4 : BN == 64 ? 3.6 : BN == 32 ? 3.0 : 2.7, exchange = SPLITS > 1 ? 1.35 + 0.82 * BN / 64 : 0;
   return {Split<BN, SPLITS>::ready, Split<BN, SPLITS>::launch, BN, 128, SPLITS, C::kStages, C::kStageBytes, fixed + exchange,
-          BN == 128 ? 0.53 : BN == 64 ? 0.48 : BN == 32 ? 0.33 : 0.32, BN == 128 ? 5.4 : BN == 64 ? 4.1 : BN == 32 ? 3.9 : 3.6};
+          BN == 128 ? 0.48 : BN == 64 ? 0.44 : BN == 32 ? 0.33 : 0.30, BN == 128 ? 5.7 : BN == 64 ? 4.4 : BN == 32 ? 4.0 : 3.3};
 }
 
 // Configuration asked for by a test (rows of a tile * 16 + pieces of K), 0: none.
@@ -727,12 +732,12 @@ std::atomic<int> g_force{0};
 // The configuration with the smallest estimate
 //   fixed + max(waves * stages of a piece * stage, bytes of W / rate) + (waves - 1) * wave
 // stage: what a stage takes by itself, longer by half where two CTAs share every SM, or what L2 needs for the stages of all
-// CTAs (13.6 TB/s).  rate: 6.2 TB/s of memory, or what the bytes of W in flight give at 1.9 us of latency.  Fitted on a GB300
-// to 22 configurations of 75 shapes, drawn over 1 to 4096 rows, 64 to 24576 columns and K of 128 to 18432: its choice takes
-// 1.6 % more than the best on average and is within 10 % of it on 73 (777 x 1001 x 1536: 11.5 us, best 10.2).
+// CTAs (13.9 TB/s).  rate: 6.2 TB/s of memory, or what the bytes of W in flight give at 1.95 us of latency.  Fitted on a GB300
+// to 22 configurations of 110 shapes, drawn over 1 to 4096 rows, 64 to 24576 columns and K of 128 to 18432: its choice takes
+// 1.9 % more than the best on average and is within 10 % of it on 103 (659 x 1984 x 3456: 19.9 us, best 17.0).
 int launch_best(const Call& c, cudaStream_t st) {
   static const Option options[] = {
-      {Pair::ready, Pair::launch, 256, 256, 1, kPairStages, kPairStageBytes, 4.9, 0.44, 1.9},
+      {Pair::ready, Pair::launch, 256, 256, 1, kPairStages, kPairStageBytes, 5.1, 0.43, 1.8},
       split_option<128, 1>(), split_option<128, 2>(), split_option<128, 4>(),
       split_option<64, 1>(), split_option<64, 2>(), split_option<64, 3>(), split_option<64, 4>(), split_option<64, 5>(), split_option<64, 8>(),
       split_option<32, 1>(), split_option<32, 2>(), split_option<32, 3>(), split_option<32, 4>(), split_option<32, 5>(), split_option<32, 8>(),
@@ -751,8 +756,8 @@ int launch_best(const Call& c, cudaStream_t st) {
     if (int rc = o.ready(dev, &clusters)) return rc;
     const int64_t tiles = ceil_div(c.p.M, o.rows) * ceil_div(c.p.N, o.cols), waves = ceil_div(tiles, clusters);
     const double ctas = static_cast<double>(std::min<int64_t>(tiles, clusters)) * (o.rows == 256 ? 2 : o.parts);
-    const double stage = std::max(o.stage_us * (1.0 + 0.52 * std::max(0.0, ctas / sms - 1.0)), ctas * o.stage_bytes / 13.6e6);
-    const double rate = std::min(6.2e6, ctas * o.stages * kTile / 1.9);  // bytes of W per us
+    const double stage = std::max(o.stage_us * (1.0 + 0.45 * std::max(0.0, ctas / sms - 1.0)), ctas * o.stage_bytes / 13.9e6);
+    const double rate = std::min(6.2e6, ctas * o.stages * kTile / 1.95);  // bytes of W per us
     const double us = o.fixed_us +
                       std::max(static_cast<double>(waves * ceil_div(c.p.groups, o.parts)) * stage,
                                static_cast<double>(c.p.N) * static_cast<double>(c.K) / rate) +
