@@ -122,6 +122,14 @@ def test_append_to_8_bits(lib, case, scales):
     _run(lib, **{**case, "cache": "fp8"}, scales=scales)
 
 
+@pytest.mark.parametrize("D,R,start,H,Hq", [(90, 44, 46, 3, 5), (90, 44, 0, 2, 0), (1022, 1020, 2, 2, 1), (1023, 2, 1021, 1, 1),
+                                              (6, 2, 2, 4, 8), (100, 0, 0, 2, 0), (1, 0, 0, 3, 0)])
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("f16", "fp8"), ("bf16", "fp8")])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_narrow_vectors(lib, D, R, start, H, Hq, dtype, cache, interleaved):
+    _run(lib, [3, 0, 40], [20, 1, 30], H, D, 7, R=R, start=start, Hq=Hq, dtype=dtype, cache=cache, interleaved=interleaved)
+
+
 def test_positions_of_their_own(lib):
     _run(lib, [4, 0], [3, 6], 2, 64, 16, R=64, Hq=2, positions=[9, 8, 7, 100000, 5, 4, 3, 2, 1])
 

@@ -41,6 +41,16 @@ def test_sizes(lib, T, H, D, R, start, dtype, interleaved):
     assert torch.equal(again, got)
 
 
+@pytest.mark.parametrize("T,H,D,R,start", [
+    (3, 2, 1024, 1022, 1), (9, 3, 1022, 1020, 2), (9, 3, 1020, 508, 4), (41, 5, 90, 44, 46),
+    (41, 5, 90, 44, 0), (7, 1, 6, 2, 2), (200, 3, 101, 50, 51)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_narrow_vectors(lib, T, H, D, R, start, dtype, interleaved):
+    # rows that fall into vectors of 2, 4 or 8 bytes, several of them to a thread, the last thread's not all there
+    test_sizes(lib, T, H, D, R, start, dtype, interleaved)
+
+
 @pytest.mark.parametrize("pos", [0, 1, -1, 4095, 163839, 1 << 20, (1 << 31) - 1, -(1 << 31)])
 def test_far_positions_keep_their_angle(lib, pos):
     # a float32 product of position and frequency would be off by up to 64 radians here

@@ -1,8 +1,8 @@
 // rotary_embedding and paged_kv_append: rows of heads moved, and rotated by position on the way.
 //
 // Both are one kernel over rows (token, head): the heads of a token are its queries, then (append) its keys and its
-// values.  A block takes a run of neighbouring rows.  A thread has the same place in each of its rows (an item: two vectors
-// whose elements are turned with one another, or that stay), asks for the first of them, the block works out where its
+// values.  A block takes a run of neighbouring rows.  A thread has the same places in each of its rows (items: two vectors
+// whose elements are turned with one another, or that stay), asks for its first row's, the block works out where its
 // tokens go and the cosines and sines of their angles once for all heads, and then the vectors are turned and stored.
 // Bound by memory; the angles of a token cost R / 2 sincospif and are shared by its heads.
 //
@@ -16,6 +16,7 @@
 namespace w4a8 {
 namespace {
 
+constexpr int kMaxDim = 1024;  // of a head
 constexpr int kThreads = 128;
 constexpr int kBlocks = 8;   // of an SM
 constexpr int kRounds = 16;  // rows of a thread, at most
@@ -38,11 +39,16 @@ struct RowParams {
   int T, B, Hq, Hkv, D, R, start, table_pages;
   int rot_items, items;  // of a row: those with pairs to turn, all of them
   int rows_per_block;
-  int row_threads;       // threads of a row: its items, or all where there are more
+  int row_threads;       // threads of a row, each with kItems of its items
   FastDiv by_row, by_heads, by_page, by_half;
   float cos_scale, sin_scale;
   bool interleaved, positions64;
 };
+
+// Items of a thread in a row: more where they are narrow, as a row costs a thread as much (8192 x 40 x 101 f16, single
+// elements: 81 us with one item, 45 with 4; 8192 x 40 x 80 in 8 bytes: 26 with one, 19 with 2).
+template <typename T, int V>
+constexpr int kItems = V * sizeof(T) <= 4 ? 4 : V * sizeof(T) == 8 ? 2 : 1;
 
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
@@ -109,86 +115,104 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rotary_rows_kernel(const __
   if (APPEND && tid == 0) first_seq = 0;
   pdl_wait();
 
+  constexpr int K = kItems<T, V>;
+  static_assert(K * kThreads * 2 * V >= kMaxDim, "a block holds every item of a row");
   struct Row {
-    Vec<T, V> a, b;
+    Vec<T, V> a[K], b[K];
     int tok, head;  // token in the block
   };
-  auto load = [&](Row& r, int row, int e0, int e1, int v0, int v1) {
+  int e0[K], e1[K], v0[K], v1[K];  // places of this thread's items, in turned rows and in rows of values
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    e0[i] = e1[i] = v0[i] = v1[i] = -1;
+    if (item + i * p.row_threads >= p.items) continue;
+    places<V>(p, item + i * p.row_threads, false, e0[i], e1[i]);
+    if (APPEND) places<V>(p, item + i * p.row_threads, true, v0[i], v1[i]);
+  }
+  const auto load = [&](Row& r, int row) {
     if (row >= rows) return;
     r.tok = p.by_heads.div(in0 + row, r.head);
     const int64_t t = tok0 + r.tok;
     const T* src;
+    bool value = false;
     if (!APPEND || r.head < p.Hq) {
       src = static_cast<const T*>(p.q) + t * p.q_t + r.head * p.q_h;
     } else if (r.head < p.Hq + p.Hkv) {
       src = static_cast<const T*>(p.k) + t * p.k_t + (r.head - p.Hq) * p.k_h;
     } else {
       src = static_cast<const T*>(p.v) + t * p.v_t + (r.head - p.Hq - p.Hkv) * p.v_h;
-      e0 = v0, e1 = v1;
+      value = true;
     }
-    if (e0 >= 0) r.a = *reinterpret_cast<const Vec<T, V>*>(src + e0);
-    if (e1 >= 0) r.b = *reinterpret_cast<const Vec<T, V>*>(src + e1);
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const int x = value ? v0[i] : e0[i], y = value ? v1[i] : e1[i];
+      if (x >= 0) r.a[i] = *reinterpret_cast<const Vec<T, V>*>(src + x);
+      if (y >= 0) r.b[i] = *reinterpret_cast<const Vec<T, V>*>(src + y);
+    }
   };
-  auto finish = [&](Row& w, int row, int e0, int e1, int v0, int v1) {
+  const auto finish = [&](Row& w, int row) {
     if (row >= rows) return;
-    const bool value = APPEND && w.head >= p.Hq + p.Hkv;
-    float x[V], y[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) x[j] = to_f32(w.a.e[j]), y[j] = to_f32(w.b.e[j]);
-    if (value) {
-      e0 = v0, e1 = v1;
-    } else if (item < p.rot_items) {
-      const float2* t = cs + w.tok * half + item * V;
-      if (p.interleaved) {
-        float z[2 * V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) z[j] = x[j], z[V + j] = y[j];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float2 f = t[j];
-          const float re = z[2 * j] * f.x - z[2 * j + 1] * f.y, im = z[2 * j + 1] * f.x + z[2 * j] * f.y;
-          z[2 * j] = re;
-          z[2 * j + 1] = im;
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) x[j] = z[j], y[j] = z[V + j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float2 f = t[j];
-          const float re = x[j] * f.x - y[j] * f.y, im = y[j] * f.x + x[j] * f.y;
-          x[j] = re;
-          y[j] = im;
-        }
+    const bool value = APPEND && w.head >= p.Hq + p.Hkv, query = !APPEND || w.head < p.Hq;
+    if (APPEND && (query ? at_pos[w.tok] < 0 : at_k[w.tok] < 0)) return;  // a row that belongs to no sequence, or has no place
+    const int64_t t = tok0 + w.tok;
+    const int h = w.head - p.Hq - (value ? p.Hkv : 0);
+    T* out = static_cast<T*>(p.qo) + t * p.o_t + w.head * p.o_h;
+    TC* to = nullptr;
+    float scale = 1.f, r = 1.f;
+    if (APPEND && !query) {
+      to = value ? static_cast<TC*>(p.vc) + at_v[w.tok] + h * p.v_head : static_cast<TC*>(p.kc) + at_k[w.tok] + h * p.k_head;
+      const float* scales = value ? p.v_scale : p.k_scale;
+      if (sizeof(TC) == 1 && scales) {
+        scale = scales[h];
+        r = __frcp_rn(scale);
       }
     }
-    const int64_t t = tok0 + w.tok;
-    if (!APPEND || w.head < p.Hq) {
-      if (APPEND && at_pos[w.tok] < 0) return;  // a row that belongs to no sequence
-      T* to = static_cast<T*>(p.qo) + t * p.o_t + w.head * p.o_h;
-      if (e0 >= 0) store_vec<T, V>(to + e0, x, 1.f, 1.f);
-      if (e1 >= 0) store_vec<T, V>(to + e1, y, 1.f, 1.f);
-      return;
-    }
-    if constexpr (APPEND) {
-      if (at_k[w.tok] < 0) return;
-      const int h = w.head - p.Hq - (value ? p.Hkv : 0);
-      TC* to = value ? static_cast<TC*>(p.vc) + at_v[w.tok] + h * p.v_head
-                     : static_cast<TC*>(p.kc) + at_k[w.tok] + h * p.k_head;
-      const float* scales = value ? p.v_scale : p.k_scale;
-      const float scale = sizeof(TC) == 1 && scales ? scales[h] : 1.f, r = sizeof(TC) == 1 ? __frcp_rn(scale) : 1.f;
-      if (e0 >= 0) store_vec<TC, V>(to + e0, x, scale, r);
-      if (e1 >= 0) store_vec<TC, V>(to + e1, y, scale, r);
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      float x[V], y[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[j] = to_f32(w.a[i].e[j]), y[j] = to_f32(w.b[i].e[j]);
+      const int at = item + i * p.row_threads;
+      if (!value && at < p.rot_items) {
+        const float2* f = cs + w.tok * half + at * V;
+        if (p.interleaved) {
+          float z[2 * V];
+#pragma unroll
+          for (int j = 0; j < V; ++j) z[j] = x[j], z[V + j] = y[j];
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const float2 c = f[j];
+            const float re = z[2 * j] * c.x - z[2 * j + 1] * c.y, im = z[2 * j + 1] * c.x + z[2 * j] * c.y;
+            z[2 * j] = re;
+            z[2 * j + 1] = im;
+          }
+#pragma unroll
+          for (int j = 0; j < V; ++j) x[j] = z[j], y[j] = z[V + j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const float2 c = f[j];
+            const float re = x[j] * c.x - y[j] * c.y, im = y[j] * c.x + x[j] * c.y;
+            x[j] = re;
+            y[j] = im;
+          }
+        }
+      }
+      const int p0 = value ? v0[i] : e0[i], p1 = value ? v1[i] : e1[i];
+      if (!APPEND || query) {
+        if (p0 >= 0) store_vec<T, V>(out + p0, x, 1.f, 1.f);
+        if (p1 >= 0) store_vec<T, V>(out + p1, y, 1.f, 1.f);
+      } else {
+        if (p0 >= 0) store_vec<TC, V>(to + p0, x, scale, r);
+        if (p1 >= 0) store_vec<TC, V>(to + p1, y, scale, r);
+      }
     }
   };
 
-  int e0, e1, v0, v1;
-  places<V>(p, item, false, e0, e1);
-  places<V>(p, item, true, v0, v1);
   Row w;
   const bool mine = lane_row < step;  // the last threads may be no whole row
   const int first = mine ? lane_row : rows;
-  load(w, first, e0, e1, v0, v1);
+  load(w, first);
 
   if constexpr (APPEND) {
     if (p.indptr) {  // the sequence of the block's first token: how many end before it
@@ -246,17 +270,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rotary_rows_kernel(const __
   // from other warps (64 us), as do 4 blocks of 256 threads with as many rounds (59).
 #pragma unroll 1
   for (int row = first; row < rows; row += step) {
-    finish(w, row, e0, e1, v0, v1);
-    load(w, row + step, e0, e1, v0, v1);
-  }
-  // rows of more items than threads: the items behind the first kThreads
-  for (item += kThreads; item < p.items; item += kThreads) {
-    places<V>(p, item, false, e0, e1);
-    places<V>(p, item, true, v0, v1);
-    for (int row = 0; row < rows; ++row) {
-      load(w, row, e0, e1, v0, v1);
-      finish(w, row, e0, e1, v0, v1);
-    }
+    finish(w, row);
+    load(w, row + step);
   }
 }
 
@@ -265,7 +280,7 @@ int launch_rows(RowParams p, cudaStream_t st) {
   const int heads = p.Hq + 2 * p.Hkv, half = p.R / 2;
   p.rot_items = half / V;
   p.items = p.rot_items + static_cast<int>(ceil_div(p.D - p.R, 2 * V));
-  p.row_threads = std::min(p.items, kThreads);
+  p.row_threads = static_cast<int>(ceil_div(p.items, kItems<T, V>));
   p.by_row = FastDiv(p.row_threads);
   p.by_heads = FastDiv(heads);
   p.by_half = FastDiv(half > 0 ? half : 1);
@@ -281,15 +296,16 @@ int launch_rows(RowParams p, cudaStream_t st) {
                     dim3(static_cast<unsigned>(ceil_div(p.rows, p.rows_per_block))), dim3(kThreads), 0, st, p);
 }
 
-// Rows in vectors of 16 bytes, 8 bytes or single elements: the widest that every start, stride and part of a head allows.
+// Rows in vectors of 16, 8 or 4 bytes or single elements: the widest that every start, stride and part of a head allows.
 template <typename T, typename TC, bool APPEND>
 int launch_vec(const RowParams& p, uint64_t starts_t, uint64_t starts_c, uint64_t elems, cudaStream_t st) {
-  constexpr int kFull = 16 / sizeof(T), kHalf = 8 / sizeof(T);
+  constexpr int kFull = 16 / sizeof(T), kHalf = 8 / sizeof(T), kFourth = 4 / sizeof(T);
   const auto fits = [&](int v) {
     return starts_t % (v * sizeof(T)) == 0 && starts_c % (v * sizeof(TC)) == 0 && elems % v == 0;
   };
   if (fits(kFull)) return launch_rows<T, TC, kFull, APPEND>(p, st);
   if (fits(kHalf)) return launch_rows<T, TC, kHalf, APPEND>(p, st);
+  if (kFourth > 1 && fits(kFourth)) return launch_rows<T, TC, kFourth, APPEND>(p, st);
   return launch_rows<T, TC, 1, APPEND>(p, st);
 }
 
@@ -340,7 +356,7 @@ extern "C" int rotary_embedding(const void* x, int64_t ldx_t, int64_t ldx_h, int
                                 const w4a8_rotary* rotary, void* out, int64_t ldo_t, int64_t ldo_h, void* stream) {
   using namespace w4a8;
   W4A8_REQUIRE(dtype >= W4A8_DTYPE_BF16 && dtype <= W4A8_DTYPE_F32, "dtype=%d must be bf16, f16 or fp32", dtype);
-  W4A8_REQUIRE(D >= 1 && D <= 1024, "D=%lld must be in [1, 1024]", (long long)D);
+  W4A8_REQUIRE(D >= 1 && D <= kMaxDim, "D=%lld must be in [1, %d]", (long long)D, kMaxDim);
   W4A8_REQUIRE(T >= 0 && H >= 0 && T < (1ll << 31) && H < (1ll << 31) && T * H < (1ll << 31),
                "T=%lld times H=%lld must be below 2^31", (long long)T, (long long)H);
   W4A8_REQUIRE(ldx_t >= 0 && ldx_h >= 0 && ldo_t >= 0 && ldo_h >= 0, "strides must not be negative");
@@ -378,7 +394,7 @@ extern "C" int paged_kv_append(const void* k, int64_t ldk_t, int64_t ldk_h, cons
   using namespace w4a8;
   if (int rc = check_cache(cache, dtype)) return rc;
   const int64_t D = cache->D, H = cache->heads;
-  W4A8_REQUIRE(D >= 1 && D <= 1024, "D=%lld must be in [1, 1024]", (long long)D);
+  W4A8_REQUIRE(D >= 1 && D <= kMaxDim, "D=%lld must be in [1, %d]", (long long)D, kMaxDim);
   W4A8_REQUIRE(Hq >= 0 && Hq < (1 << 16) && (q || Hq == 0), "Hq=%lld must be in [0, 2^16), and 0 without q", (long long)Hq);
   W4A8_REQUIRE(T >= 0 && T < (1ll << 31) && T * (Hq + 2 * H) < (1ll << 31), "T=%lld rows of %lld heads: below 2^31",
                (long long)T, (long long)(Hq + 2 * H));
