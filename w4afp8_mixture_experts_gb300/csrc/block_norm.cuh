@@ -149,20 +149,6 @@ __device__ __forceinline__ void normalise(float (&u)[VPT][V], int kind, int H, f
     for (int i = 0; i < V; ++i) u[j][i] *= inv;
 }
 
-template <int N>
-__device__ __forceinline__ void copy_async(void* dst, const void* src) {
-  static_assert(N == 4 || N == 8 || N == 16);
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(N) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {  // all but the N newest groups have landed
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Threads of a row where the kernel's code fixes them (0: blockDim.x): with many single elements to a thread, columns
 // that are known offsets from the first leave registers for the elements.
 __host__ __device__ constexpr int row_threads(int V, int VPT) { return V == 1 && VPT > 8 ? 1024 : 0; }

@@ -2,7 +2,7 @@
 //
 // Both are one kernel over rows (token, head): the heads of a token are its queries, then (append) its keys and its
 // values.  A block takes a run of neighbouring rows.  A thread has the same places in each of its rows (items: two vectors
-// whose elements are turned with one another, or that stay), asks for its first row's, the block works out where its
+// whose elements are turned with one another, or that stay), asks for its first two rows', the block works out where its
 // tokens go and the cosines and sines of their angles once for all heads, and then the vectors are turned and stored.
 // Bound by memory; the angles of a token cost R / 2 sincospif and are shared by its heads.
 //
@@ -18,8 +18,9 @@ namespace {
 
 constexpr int kMaxDim = 1024;  // of a head
 constexpr int kThreads = 128;
-constexpr int kBlocks = 8;   // of an SM
-constexpr int kRounds = 16;  // rows of a thread, at most
+constexpr int kBlocks = 8;    // of an SM
+constexpr int kRounds = 12;   // rows of a thread, at most
+constexpr int kAhead = 2;     // rows of a thread on their way
 constexpr int kMaxCs = 2048;  // cosine and sine pairs of a block's tokens
 constexpr int kMaxTok = 64;   // tokens of a block
 
@@ -61,25 +62,28 @@ __device__ __forceinline__ float over(float v, float scale, float r) {
   return fabsf(q) >= 512.f && fabsf(r) < INFINITY ? q : div_by_scale(v, scale, r);
 }
 
-// Where the two vectors of an item lie in its row; the second may be missing (-1).
-// Turned items: V elements of the first halves of the pairs and V of the second ones, or V pairs of neighbours.
-// Others: two neighbouring vectors of the elements that stay.
+// Where the two vectors of an item lie in its row; the second may be missing (-1).  Neighbouring items have neighbouring
+// vectors, so that a warp's copies are whole lines (8192 x 72 x 128 neighbours: 64 to 70 us with both vectors of an item
+// side by side, 47 so).  Turned items: a vector of the turned part's first half and one of its second, which hold pairs
+// between them, or pairs of neighbours each (single elements: a pair of neighbours).  Others: one of the first and one of
+// the second half of what stays.
 template <int V>
 __device__ __forceinline__ void places(const RowParams& p, int item, bool value, int& e0, int& e1) {
   if (value) {
-    e0 = 2 * V * item;
-    e1 = e0 + V < p.D ? e0 + V : -1;
-    if (e0 >= p.D) e0 = -1;
+    e0 = V * item;
+    e1 = V * (item + p.items);
   } else if (item < p.rot_items) {
-    e0 = p.start + (p.interleaved ? 2 : 1) * V * item;
-    e1 = e0 + (p.interleaved ? V : p.R / 2);
+    const bool side = V == 1 && p.interleaved;
+    e0 = p.start + (side ? 2 : V) * item;
+    e1 = e0 + (side ? 1 : p.R / 2);
   } else {
-    const int at = 2 * V * (item - p.rot_items);
-    e0 = at < p.start ? at : at + p.R;
-    e1 = at + V < p.start ? at + V : at + V + p.R;
-    if (e1 >= p.D) e1 = -1;
-    if (e0 >= p.D) e0 = -1;
+    e0 = V * (item - p.rot_items);
+    e1 = e0 + V * (p.items - p.rot_items);
+    if (e0 >= p.start) e0 += p.R;
+    if (e1 >= p.start) e1 += p.R;
   }
+  if (e0 >= p.D) e0 = -1;
+  if (e1 >= p.D) e1 = -1;
 }
 
 template <typename TC, int V>
@@ -95,6 +99,33 @@ __device__ __forceinline__ void store_vec(TC* to, const float (&f)[V], float sca
       reinterpret_cast<uint16_t*>(o.e)[j / 2] = e4m3x2(over(f[j], scale, r), over(f[j + 1], scale, r));
   }
   *reinterpret_cast<Vec<TC, V>*>(to) = o;
+}
+
+__device__ __forceinline__ void turn(float& x, float& y, float2 c) {
+  const float re = x * c.x - y * c.y;
+  y = y * c.x + x * c.y;
+  x = re;
+}
+
+// The cosines and sines of a token: its P neighbouring pairs in n vectors, kept two at a time vector by vector, so that the
+// threads of a row read side by side (8192 x 72 x 128: 46.6 us, 48.9 in the order of the pairs; 2000 x 40 x 128: 7.8, 10.5).
+template <int P>
+__device__ __forceinline__ int angle_place(int pair, int n) {
+  return P == 1 ? pair : (pair % P / 2 * n + pair / P) * 2 + pair % 2;
+}
+
+template <int P>
+__device__ __forceinline__ void angles(const float2* cs, int n, int vec, float2 (&c)[P]) {
+  if constexpr (P == 1) {
+    c[0] = cs[vec];
+  } else {
+#pragma unroll
+    for (int j = 0; j < P; j += 2) {
+      const float4 two = *reinterpret_cast<const float4*>(cs + (j / 2 * n + vec) * 2);
+      c[j] = make_float2(two.x, two.y);
+      c[j + 1] = make_float2(two.z, two.w);
+    }
+  }
 }
 
 template <typename T, typename TC, int V, bool APPEND>
@@ -117,10 +148,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rotary_rows_kernel(const __
 
   constexpr int K = kItems<T, V>;
   static_assert(K * kThreads * 2 * V >= kMaxDim, "a block holds every item of a row");
-  struct Row {
-    Vec<T, V> a[K], b[K];
-    int tok, head;  // token in the block
-  };
+  constexpr bool kAsync = sizeof(Vec<T, V>) == 16;  // rows wait in shared memory; narrow ones in registers
+  constexpr int kSlots = kAsync ? kAhead : 1;
+  __shared__ Vec<T, V> ring[kAsync ? kAhead : 1][kAsync ? 2 * K : 1][kAsync ? kThreads : 1];
+  Vec<T, V> wa[K], wb[K];
   int e0[K], e1[K], v0[K], v1[K];  // places of this thread's items, in turned rows and in rows of values
 #pragma unroll
   for (int i = 0; i < K; ++i) {
@@ -129,38 +160,46 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rotary_rows_kernel(const __
     places<V>(p, item + i * p.row_threads, false, e0[i], e1[i]);
     if (APPEND) places<V>(p, item + i * p.row_threads, true, v0[i], v1[i]);
   }
-  const auto load = [&](Row& r, int row) {
-    if (row >= rows) return;
-    r.tok = p.by_heads.div(in0 + row, r.head);
-    const int64_t t = tok0 + r.tok;
-    const T* src;
-    bool value = false;
-    if (!APPEND || r.head < p.Hq) {
-      src = static_cast<const T*>(p.q) + t * p.q_t + r.head * p.q_h;
-    } else if (r.head < p.Hq + p.Hkv) {
-      src = static_cast<const T*>(p.k) + t * p.k_t + (r.head - p.Hq) * p.k_h;
-    } else {
-      src = static_cast<const T*>(p.v) + t * p.v_t + (r.head - p.Hq - p.Hkv) * p.v_h;
-      value = true;
-    }
+  const auto load = [&](int row, int slot) {
+    if (row < rows) {
+      int head;
+      const int64_t t = tok0 + p.by_heads.div(in0 + row, head);
+      const T* src;
+      bool value = false;
+      if (!APPEND || head < p.Hq) {
+        src = static_cast<const T*>(p.q) + t * p.q_t + head * p.q_h;
+      } else if (head < p.Hq + p.Hkv) {
+        src = static_cast<const T*>(p.k) + t * p.k_t + (head - p.Hq) * p.k_h;
+      } else {
+        src = static_cast<const T*>(p.v) + t * p.v_t + (head - p.Hq - p.Hkv) * p.v_h;
+        value = true;
+      }
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
-      const int x = value ? v0[i] : e0[i], y = value ? v1[i] : e1[i];
-      if (x >= 0) r.a[i] = *reinterpret_cast<const Vec<T, V>*>(src + x);
-      if (y >= 0) r.b[i] = *reinterpret_cast<const Vec<T, V>*>(src + y);
+      for (int i = 0; i < K; ++i) {
+        const int x = value ? v0[i] : e0[i], y = value ? v1[i] : e1[i];
+        if constexpr (kAsync) {
+          if (x >= 0) copy_async<16>(&ring[slot][2 * i][tid], src + x);
+          if (y >= 0) copy_async<16>(&ring[slot][2 * i + 1][tid], src + y);
+        } else {
+          if (x >= 0) wa[i] = *reinterpret_cast<const Vec<T, V>*>(src + x);
+          if (y >= 0) wb[i] = *reinterpret_cast<const Vec<T, V>*>(src + y);
+        }
+      }
     }
+    if constexpr (kAsync) copy_commit();
   };
-  const auto finish = [&](Row& w, int row) {
-    if (row >= rows) return;
-    const bool value = APPEND && w.head >= p.Hq + p.Hkv, query = !APPEND || w.head < p.Hq;
-    if (APPEND && (query ? at_pos[w.tok] < 0 : at_k[w.tok] < 0)) return;  // a row that belongs to no sequence, or has no place
-    const int64_t t = tok0 + w.tok;
-    const int h = w.head - p.Hq - (value ? p.Hkv : 0);
-    T* out = static_cast<T*>(p.qo) + t * p.o_t + w.head * p.o_h;
+  const auto finish = [&](int row) {
+    int head;
+    const int tok = p.by_heads.div(in0 + row, head);  // in the block
+    const bool value = APPEND && head >= p.Hq + p.Hkv, query = !APPEND || head < p.Hq;
+    if (APPEND && (query ? at_pos[tok] < 0 : at_k[tok] < 0)) return;  // a row that belongs to no sequence, or has no place
+    const int64_t t = tok0 + tok;
+    const int h = head - p.Hq - (value ? p.Hkv : 0);
+    T* out = static_cast<T*>(p.qo) + t * p.o_t + head * p.o_h;
     TC* to = nullptr;
     float scale = 1.f, r = 1.f;
     if (APPEND && !query) {
-      to = value ? static_cast<TC*>(p.vc) + at_v[w.tok] + h * p.v_head : static_cast<TC*>(p.kc) + at_k[w.tok] + h * p.k_head;
+      to = value ? static_cast<TC*>(p.vc) + at_v[tok] + h * p.v_head : static_cast<TC*>(p.kc) + at_k[tok] + h * p.k_head;
       const float* scales = value ? p.v_scale : p.k_scale;
       if (sizeof(TC) == 1 && scales) {
         scale = scales[h];
@@ -171,31 +210,25 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rotary_rows_kernel(const __
     for (int i = 0; i < K; ++i) {
       float x[V], y[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) x[j] = to_f32(w.a[i].e[j]), y[j] = to_f32(w.b[i].e[j]);
+      for (int j = 0; j < V; ++j) x[j] = to_f32(wa[i].e[j]), y[j] = to_f32(wb[i].e[j]);
       const int at = item + i * p.row_threads;
       if (!value && at < p.rot_items) {
-        const float2* f = cs + w.tok * half + at * V;
-        if (p.interleaved) {
-          float z[2 * V];
+        const float2* f = cs + tok * half;
+        if (p.interleaved && V > 1) {
+          constexpr int P = V > 1 ? V / 2 : 1;
+          float2 c[P], d[P];
+          angles<P>(f, half / P, at, c);
+          angles<P>(f, half / P, at + p.rot_items, d);
 #pragma unroll
-          for (int j = 0; j < V; ++j) z[j] = x[j], z[V + j] = y[j];
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const float2 c = f[j];
-            const float re = z[2 * j] * c.x - z[2 * j + 1] * c.y, im = z[2 * j + 1] * c.x + z[2 * j] * c.y;
-            z[2 * j] = re;
-            z[2 * j + 1] = im;
+          for (int j = 0; j < P; ++j) {
+            turn(x[2 * j], x[(2 * j + 1) % V], c[j]);
+            turn(y[2 * j], y[(2 * j + 1) % V], d[j]);
           }
-#pragma unroll
-          for (int j = 0; j < V; ++j) x[j] = z[j], y[j] = z[V + j];
         } else {
+          float2 c[V];
+          angles<V>(f, half / V, at, c);
 #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const float2 c = f[j];
-            const float re = x[j] * c.x - y[j] * c.y, im = y[j] * c.x + x[j] * c.y;
-            x[j] = re;
-            y[j] = im;
-          }
+          for (int j = 0; j < V; ++j) turn(x[j], y[j], c[j]);
         }
       }
       const int p0 = value ? v0[i] : e0[i], p1 = value ? v1[i] : e1[i];
@@ -209,10 +242,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rotary_rows_kernel(const __
     }
   };
 
-  Row w;
   const bool mine = lane_row < step;  // the last threads may be no whole row
   const int first = mine ? lane_row : rows;
-  load(w, first);
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) load(first + i * step, i);
 
   if constexpr (APPEND) {
     if (p.indptr) {  // the sequence of the block's first token: how many end before it
@@ -262,16 +295,26 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rotary_rows_kernel(const __
     const uint64_t turns = static_cast<uint64_t>(pos) * static_cast<uint64_t>(p.freqs[f]);
     float s, c;
     sincospif(static_cast<float>(static_cast<int32_t>(turns >> 32)) * 4.656612873e-10f, &s, &c);  // 2^-31
-    cs[i] = make_float2(c * p.cos_scale, s * p.sin_scale);
+    constexpr int P = V > 1 ? V / 2 : 1;
+    const int place = p.interleaved ? angle_place<P>(f, half / P) : angle_place<V>(f, half / V);
+    cs[tok * half + place] = make_float2(c * p.cos_scale, s * p.sin_scale);
   }
   __syncthreads();
 
-  // 32 warps of an SM hide one another's loads.  8192 x 72 x 128: 54 us; two rows of a thread on their way take registers
-  // from other warps (64 us), as do 4 blocks of 256 threads with as many rounds (59).
+  // Two rows of a thread on their way through shared memory (8192 x 72 x 128: 46.6 us; about 2 more with one row; 55 with
+  // one in registers, where two take room from other warps: 64).  A third finds no room beside the angles.
+  int slot = 0;
 #pragma unroll 1
   for (int row = first; row < rows; row += step) {
-    finish(w, row);
-    load(w, row + step);
+    if constexpr (kAsync) {
+      copy_wait<kSlots - 1>();
+#pragma unroll
+      for (int i = 0; i < K; ++i) wa[i] = ring[slot][2 * i][tid], wb[i] = ring[slot][2 * i + 1][tid];
+      load(row + kSlots * step, slot);
+      slot = slot + 1 == kSlots ? 0 : slot + 1;
+    }
+    finish(row);
+    if constexpr (!kAsync) load(row + step, 0);
   }
 }
 
@@ -285,7 +328,8 @@ int launch_rows(RowParams p, cudaStream_t st) {
   p.by_heads = FastDiv(heads);
   p.by_half = FastDiv(half > 0 ? half : 1);
   // Rows of a block: as many rounds for each thread as make whole waves of blocks, up to kRounds (a block's start, with its
-  // angles, costs about two rounds; 8192 x 72 x 128 takes 55 us with 8 rounds, 59 with 4), and no more tokens than have room.
+  // angles, costs about two rounds; 8192 x 72 x 128 takes 46.6 us, 47.3 with up to 16; an append of 16384 x 80 76.3 and 77.5,
+  // and 4 more with up to 8), and no more tokens than have room.
   const int tokens = std::min(kMaxTok, half > 0 ? kMaxCs / half : kMaxTok);
   const int64_t step = kThreads / p.row_threads, slots = kBlocks * num_sms();
   const int64_t rounds = ceil_div(ceil_div(p.rows, step), slots), waves = ceil_div(rounds, kRounds);
