@@ -329,3 +329,44 @@ def test_refusals(lib):
         with pytest.raises(err, match=msg):
             lib.paged_attention_decode(**{**base, **change})
     assert lib.device_error() == 0
+
+
+def _one_page(length, D=8, page=458766, pages=4681):
+    # a table of 2^31 - 2 places, all in one page of a cache of 7 MB
+    c = Case([1], 2, 1, D, 16)
+    c.kc, c.vc = (torch.zeros((1, page, 1, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    c.table = torch.zeros((1, pages), dtype=torch.int32, device="cuda")
+    c.lens_t.fill_(length)
+    return c
+
+
+@pytest.mark.parametrize("length", [2 ** 31 - 2, 2 ** 31 - 3, 2 ** 31 - 18, 2 ** 31 - 34])
+@pytest.mark.parametrize("window", [1, 7, 40, 5000])
+def test_a_window_at_the_end_of_the_longest_table(lib, way, length, window):
+    # the last tile ends behind 2^31
+    c = _one_page(length)
+    g = torch.Generator("cuda").manual_seed(window)
+    at = torch.arange(length - window, length, device="cuda") % 458766
+    for t in (c.kc, c.vc):
+        t.fill_(math.nan)
+        t[0, at] = torch.randn((window, 1, 8), device="cuda", generator=g).to(torch.bfloat16)
+    out, lse = c.call(lib, return_lse=True, window=window)
+    k, v = (_np(t)[0, at.cpu().numpy()] for t in (c.kc, c.vc))
+    want, bound, l, lb = ref.attend(_np(c.q)[0], k, v, 8 ** -0.5, "bf16", 2.0 ** -14)
+    assert (np.abs(_np(out)[0] - want) <= bound).all() and (np.abs(_np(lse)[0] - l) <= lb).all()
+    assert lib.device_error() == 0
+
+
+@pytest.mark.parametrize("length", [2 ** 31 - 2, 2 ** 31 - 20])
+def test_a_sequence_as_long_as_the_longest_table(lib, length):
+    # scores of 0: the sum of the weights is the length.  Each of up to 8 * 152 warps adds up whole numbers below 2^24, exact;
+    # their sums are joined with a rounding each, and the logarithm is within a few units of 21.5
+    c = _one_page(length)
+    c.vc.fill_(1.0)
+    out, lse = c.call(lib, return_lse=True)
+    runs = 8 * torch.cuda.get_device_properties(0).multi_processor_count
+    assert 2 ** 31 / runs < 2 ** 24
+    assert (np.abs(_np(lse) - math.log(length)) <= (runs + 64) * ref.U + 4 * 22 * ref.U).all()
+    # a warp's sum of values is cut off by up to a unit (2 u) at each of two additions of 16 weights' pieces
+    assert (np.abs(_np(out) - 1.0) <= 2 * (2 ** 31 / runs / 16 + 64) * 2 * ref.U + 2.0 ** -8).all()
+    assert lib.device_error() == 0

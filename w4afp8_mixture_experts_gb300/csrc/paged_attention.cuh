@@ -169,7 +169,8 @@ __device__ __forceinline__ SeqSpan span_of(const AttendParams& p, int b) {
   if (CHECK && len > p.max_len) atomicOr(&g_attend_error, 2u);
   s.hi = static_cast<int>(min(len, p.max_len));
   s.lo = p.window > 0 ? max(0, s.hi - p.window) : 0;
-  s.tiles = s.hi > s.lo ? (s.hi - s.lo + NT - 1) / NT : 0;
+  // the last tile of a sequence may end behind 2^31: unsigned
+  s.tiles = s.hi > s.lo ? static_cast<int>((static_cast<uint32_t>(s.hi - s.lo) + (NT - 1)) / NT) : 0;
   return s;
 }
 // places of a sequence in the list
@@ -333,12 +334,12 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
   };
   const auto places = [&](const Cursor& c) {
     Places w;
-    const int t = c.s.lo + c.u * NT + (lane & (NT - 1));
-    w.valid = c.s.hi - (c.s.lo + c.u * NT);
+    const int from = c.s.lo + c.u * NT, in = lane & (NT - 1);
+    w.valid = c.s.hi - from;
     w.page = -1;
     w.slot = 0;
-    if (c.left > 0 && t < c.s.hi) {
-      const int n = p.by_page.div(t, w.slot);
+    if (c.left > 0 && in < w.valid) {  // (from + in may lie behind 2^31 where the tile ends behind the last token)
+      const int n = p.by_page.div(from + in, w.slot);
       w.page = p.table[c.b * p.table_ld + n];
       if (w.page < 0 || w.page >= p.pages) {
         atomicOr(&g_attend_error, 2u);
