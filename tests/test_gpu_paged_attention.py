@@ -370,3 +370,14 @@ def test_a_sequence_as_long_as_the_longest_table(lib, length):
     # a warp's sum of values is cut off by up to a unit (2 u) at each of two additions of 16 weights' pieces
     assert (np.abs(_np(out) - 1.0) <= 2 * (2 ** 31 / runs / 16 + 64) * 2 * ref.U + 2.0 ** -8).all()
     assert lib.device_error() == 0
+
+
+def test_empty_rows_of_more_than_31_bits_of_outputs(lib):
+    # 2^23 heads of 256 for one sequence, all of them zeros
+    Hq, Hkv, D = 1 << 23, 1 << 15, 256
+    q = torch.zeros((1, 1, D), dtype=torch.bfloat16, device="cuda").expand(1, Hq, D)
+    cache = torch.zeros((1, 1, Hkv, D), dtype=torch.bfloat16, device="cuda")
+    table, lens = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((1, 1), (1,)))
+    out = torch.full((1, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    _, lse = lib.paged_attention_decode(q, cache, cache, table, lens, return_lse=True, out=out)
+    assert int(torch.count_nonzero(out)) == 0 and torch.all(lse == -math.inf) and lib.device_error() == 0

@@ -219,10 +219,11 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
   const int64_t run_id = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
   // zeros for the sequences without a tile, each of them a warp's
   const auto zero_empty = [&] {
+    const uint32_t D = p.D, all = p.Hq * D;  // below 256 * 2^16 heads of up to 256: past 2^31, within 2^32 - 2^16
     for (int b = static_cast<int>(run_id); b < p.B; b += p.warps) {
       if (span_of<NT>(p, b).tiles) continue;
-      for (int i = lane; i < p.Hq * p.D; i += 32)
-        static_cast<uint16_t*>(p.out)[b * p.o_b + i / p.D * p.o_h + i % p.D] = 0;  // bf16's and f16's zero
+      for (uint32_t i = lane; i < all; i += 32)
+        static_cast<uint16_t*>(p.out)[b * p.o_b + i / D * p.o_h + i % D] = 0;  // bf16's and f16's zero
       if (p.lse)
         for (int i = lane; i < p.Hq; i += 32) p.lse[static_cast<int64_t>(b) * p.Hq + i] = -INFINITY;
     }
