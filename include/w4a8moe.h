@@ -580,8 +580,8 @@ int rotary_embedding(const void* x, int64_t ldx_t, int64_t ldx_h, int dtype, int
  * k_scale[h], a value its code times v_scale[h] (NULL: 1).
  * Entries of the page table that no position of seq_lens[b] reaches are not read.
  * A page id outside [0, pages), or a position behind the table's last page, sets
- * the device error word (code 2): nothing is stored there, and such a key and value
- * read as zeros.
+ * the device error word (code 2).  Nothing is stored there.  Read, a key and value of
+ * such a page are zeros; positions behind the table are left out.
  */
 typedef struct {
   void* k;
@@ -621,9 +621,10 @@ int paged_kv_append(const void* k, int64_t ldk_t, int64_t ldk_h, const void* v, 
  *   s_p = scale * q[b][h] . K[b][p][h / (Hq / heads)],  p in [lo, seq_lens[b])
  *   lo = max(0, seq_lens[b] - window), or 0 when window = 0
  *   out[b][h] = sum_p softmax(s)_p V[b][p][..],  lse[b][h] = log sum_p exp(s_p)
- * A sequence without positions (seq_lens[b] <= 0) gives zeros and -inf.  Nothing outside
- * the positions named is read.  Scores, softmax and sums are fp32; the weights are taken
- * to the values' product in two pieces of 16 bits (16-bit caches) or in f16 (E4M3).
+ * A sequence without positions (seq_lens[b] <= 0, or lo behind the table's last page) gives
+ * zeros and -inf.  Nothing outside the positions named is read.  Scores, softmax and sums are
+ * fp32; the weights are taken to the values' product in two pieces of 16 bits (16-bit caches,
+ * f16 outputs) or in one f16 (E4M3 with bf16 outputs).
  *   q [B][Hq][D] of `dtype` (bf16 or f16; a 16-bit cache has the same type), element d of
  *   head h of sequence b at b * ldq_b + h * ldq_h + d; out likewise; lse fp32 [B][Hq] or NULL
  *   D: a multiple of 8 (of 16 with E4M3) up to 256; the cache's pointers and strides are

@@ -381,3 +381,24 @@ def test_empty_rows_of_more_than_31_bits_of_outputs(lib):
     out = torch.full((1, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
     _, lse = lib.paged_attention_decode(q, cache, cache, table, lens, return_lse=True, out=out)
     assert int(torch.count_nonzero(out)) == 0 and torch.all(lse == -math.inf) and lib.device_error() == 0
+
+
+@pytest.mark.parametrize("window", [0, 1, 30, 57, 60, 96, 200, 2 ** 31 - 1, 2 ** 40])
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+def test_positions_behind_the_table_are_left_out(lib, way, window, cache):
+    # lengths of up to 40 more than the tables have places for: what is there counts, in a window before the length
+    places = 96
+    c = Case([places, places, 40, places, 0], 6, 2, 64, 16, "bf16", cache, seed=5)
+    over = [places + 1, places + 40, 40, places, 0]
+    c.lens_t.copy_(torch.tensor(over, dtype=torch.int32))
+    table = c.table[:, :places // 16].contiguous()
+    out, lse = lib.paged_attention_decode(c.q, c.kc, c.vc, table, c.lens_t, k_scale=c.ks, v_scale=c.vs, window=window,
+                                          return_lse=True)
+    assert lib.device_error() == 2 and lib.device_error() == 0
+    q, piece = _np(c.q), 2.0 ** -11 if cache == "fp8" else 2.0 ** -14
+    for b, n in enumerate(over):
+        lo = max(0, n - window) if window else 0
+        want, bound, l, lb = ref.attend(q[b], c.k[b][lo:], c.v[b][lo:], 0.125, "bf16", piece)
+        assert (np.abs(_np(out[b]) - want) <= bound).all(), b
+        got, fine = _np(lse[b]), np.isfinite(l)
+        assert np.array_equal(np.isneginf(got), np.isneginf(l)) and (np.abs(got[fine] - l[fine]) <= lb[fine]).all(), b

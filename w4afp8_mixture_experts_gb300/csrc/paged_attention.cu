@@ -116,7 +116,7 @@ extern "C" int paged_attention_decode(const void* q, int64_t ldq_b, int64_t ldq_
   p.Hkv = static_cast<int>(H);
   p.G = G;
   p.D = static_cast<int>(D);
-  p.window = static_cast<int>(window < max_len ? window : 0);  // a window beyond the table leaves nothing out
+  p.window = static_cast<int>(window < INT32_MAX ? window : 0);  // no length is above that: nothing is left out
   p.cluster = cluster;
   p.scale = scale * 1.44269504089f;
   p.by_page = FastDiv(cache->page_size);

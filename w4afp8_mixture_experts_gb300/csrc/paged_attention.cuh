@@ -157,8 +157,9 @@ struct AttendCfg {
   static __device__ __forceinline__ uint32_t q_at(int r, int c) { return static_cast<uint32_t>(r * kQRow + ((c ^ (r & 7)) << 4)); }
 };
 
-// Sequence b's tokens and tiles.  CHECK: a length behind the table's last page is reported (not where lengths are only added
-// up: loads wait for such a branch).
+// Sequence b's tokens and tiles.  Of a sequence longer than its table the positions behind it are left out; a window lies
+// before the length all the same.  CHECK: such a length is reported (not where lengths are only added up: loads wait for
+// such a branch).
 struct SeqSpan {
   int lo, hi, tiles;
 };
@@ -168,7 +169,7 @@ __device__ __forceinline__ SeqSpan span_of(const AttendParams& p, int b) {
   const int64_t len = p.lens[b];
   if (CHECK && len > p.max_len) atomicOr(&g_attend_error, 2u);
   s.hi = static_cast<int>(min(len, p.max_len));
-  s.lo = p.window > 0 ? max(0, s.hi - p.window) : 0;
+  s.lo = p.window > 0 ? static_cast<int>(max(static_cast<int64_t>(0), len - p.window)) : 0;
   // the last tile of a sequence may end behind 2^31: unsigned
   s.tiles = s.hi > s.lo ? static_cast<int>((static_cast<uint32_t>(s.hi - s.lo) + (NT - 1)) / NT) : 0;
   return s;
