@@ -59,3 +59,19 @@ def test_given_frequencies_keep_whole_turns_out():
 def test_refusals(kw):
     with pytest.raises(ValueError):
         rotary_frequencies(device="cpu", **kw)
+
+
+@pytest.mark.parametrize("dim,base,factor", [(64, 10000.0, 8.0), (128, 5e5, 4.0), (4, 100.0, 2.0)])
+def test_given_frequencies_are_scaled_like_those_of_a_base(dim, base, factor):
+    f = [base ** (-2 * i / dim) for i in range(dim // 2)]
+    for scaling in ("none", "linear", "ntk"):
+        want = _radians(rotary_frequencies(dim, base, scaling=scaling, factor=factor, device="cpu"))
+        assert _close(_radians(rotary_frequencies(dim, base, scaling=scaling, factor=factor, inv_freq=f, device="cpu")), want)
+
+
+def test_ntk_of_given_frequencies():
+    # the first pair keeps its frequency, the last is divided by factor, whatever the frequencies are
+    got = _radians(rotary_frequencies(8, scaling="ntk", factor=8.0, inv_freq=[1.0, 0.3, 0.2, 0.1], device="cpu"))
+    assert _close(got, [1.0, 0.3 * 8.0 ** (-1 / 3), 0.2 * 8.0 ** (-2 / 3), 0.1 / 8.0])
+    with pytest.raises(ValueError, match="ntk"):
+        rotary_frequencies(2, scaling="ntk", inv_freq=[1.0], device="cpu")

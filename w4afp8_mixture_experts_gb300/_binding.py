@@ -553,8 +553,9 @@ def rotary_frequencies(dim: int, base: float = 10000.0, *, scaling: str = "none"
 
     f_i = base^(-2 i / dim) radians per position (or inv_freq, a sequence of dim / 2 numbers), scaled for contexts
     `factor` times longer than the `length` that a model was trained on: "linear" divides all by factor, "ntk" takes
-    base * factor^(dim / (dim - 2)), "yarn" divides those with fewer than beta_slow turns over `length`, keeps those
-    with more than beta_fast, and blends in between (its factor on the rotated values is rotary_yarn_scale)."""
+    base * factor^(dim / (dim - 2)), that is f_i * factor^(-2 i / (dim - 2)), "yarn" divides those with fewer than
+    beta_slow turns over `length`, keeps those with more than beta_fast, and blends in between (its factor on the
+    rotated values is rotary_yarn_scale)."""
     if dim < 2 or dim % 2:
         raise ValueError(f"dim must be even and positive, got {dim}")
     if scaling not in _SCALINGS:
@@ -566,12 +567,14 @@ def rotary_frequencies(dim: int, base: float = 10000.0, *, scaling: str = "none"
         f = [float(v) for v in inv_freq]
         if len(f) != half or not all(math.isfinite(v) for v in f):
             raise ValueError(f"inv_freq must have {half} finite numbers")
-    else:
+    if scaling == "ntk" and dim == 2:
+        raise ValueError("ntk scaling needs dim above 2")
+    if inv_freq is None:
         if scaling == "ntk":
-            if dim == 2:
-                raise ValueError("ntk scaling needs dim above 2")
             base = base * factor ** (dim / (dim - 2))
         f = [base ** (-2.0 * i / dim) for i in range(half)]
+    elif scaling == "ntk":  # the same change of the base, a power for each pair
+        f = [v * factor ** (-2.0 * i / (dim - 2)) for i, v in enumerate(f)]
     if scaling == "linear":
         f = [v / factor for v in f]
     elif scaling == "yarn":
