@@ -75,3 +75,27 @@ def test_ntk_of_given_frequencies():
     assert _close(got, [1.0, 0.3 * 8.0 ** (-1 / 3), 0.2 * 8.0 ** (-2 / 3), 0.1 / 8.0])
     with pytest.raises(ValueError, match="ntk"):
         rotary_frequencies(2, scaling="ntk", inv_freq=[1.0], device="cpu")
+
+
+@pytest.mark.parametrize("dim,base", [(64, 10000.0), (128, 5e5)])
+def test_yarn_of_given_frequencies_of_the_same_base(dim, base):
+    # their places among the base's pairs are logarithms, off by 1e-13 at most: as much of the blend's width of 10 pairs
+    f = [base ** (-2 * i / dim) for i in range(dim // 2)]
+    want = _radians(rotary_frequencies(dim, base, scaling="yarn", factor=40.0, device="cpu"))
+    got = _radians(rotary_frequencies(dim, base, scaling="yarn", factor=40.0, inv_freq=f, device="cpu"))
+    assert all(abs(x - y) <= 1e-12 * y for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("f", [[500000.0 ** (-2 * i / 64) for i in range(32)], [0.9 ** i for i in range(32)],
+                               [1e-5 * (i + 1) for i in range(32)], [0.0] + [-0.8 ** i for i in range(31)]])
+def test_yarn_of_given_frequencies_goes_by_their_own_turns(f):
+    # the default base's pairs lie 10000^(2 / 64) = 1.334 apart, so that the blend ends within 42.7 and 0.75 turns
+    got = _radians(rotary_frequencies(64, scaling="yarn", factor=40.0, length=4096, inv_freq=f, device="cpu"))
+    for g, p in zip(got, f):
+        turns = abs(p) * 4096 / (2 * math.pi)
+        if turns > 42.7:
+            assert _close([g], [p])
+        elif turns < 0.74:
+            assert _close([g], [p / 40])
+        else:
+            assert abs(p) / 40 * (1 - 1e-12) <= abs(g) <= abs(p) * (1 + 1e-12)

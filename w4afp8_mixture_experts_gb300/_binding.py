@@ -555,7 +555,8 @@ def rotary_frequencies(dim: int, base: float = 10000.0, *, scaling: str = "none"
     `factor` times longer than the `length` that a model was trained on: "linear" divides all by factor, "ntk" takes
     base * factor^(dim / (dim - 2)), that is f_i * factor^(-2 i / (dim - 2)), "yarn" divides those with fewer than
     beta_slow turns over `length`, keeps those with more than beta_fast, and blends in between (its factor on the
-    rotated values is rotary_yarn_scale)."""
+    rotated values is rotary_yarn_scale).  The blend is linear in a frequency's place among those of `base`, from and to a
+    whole place; a given frequency's place follows from its own turns."""
     if dim < 2 or dim % 2:
         raise ValueError(f"dim must be even and positive, got {dim}")
     if scaling not in _SCALINGS:
@@ -581,7 +582,10 @@ def rotary_frequencies(dim: int, base: float = 10000.0, *, scaling: str = "none"
         def pair_of(turns):  # the pair that makes this many turns over `length`
             return dim * math.log(length / (turns * 2 * math.pi)) / (2 * math.log(base))
         lo, hi = max(math.floor(pair_of(beta_fast)), 0), min(math.ceil(pair_of(beta_slow)), dim - 1)
-        keep = [1.0 - min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0) for i in range(half)]
+        at = range(half)
+        if inv_freq is not None:  # which pair of `base` each would be, by its own turns over `length`
+            at = [pair_of(abs(v) * length / (2 * math.pi)) if v else math.inf for v in f]
+        keep = [1.0 - min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0) for i in at]
         f = [v / factor * (1.0 - k) + v * k for v, k in zip(f, keep)]
     turns = [int(math.fmod(v / (2 * math.pi), 1.0) * 2.0 ** 64) for v in f]
     turns = [(t + 2 ** 63) % 2 ** 64 - 2 ** 63 for t in turns]
