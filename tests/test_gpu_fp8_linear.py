@@ -166,3 +166,25 @@ def test_refusals(lib):
         with pytest.raises(err, match=msg):
             lib.fp8_block_linear(a, a_s, b, b_s, **kw)
     assert lib.device_error() == 0
+
+
+@pytest.fixture
+def without(lib, request):
+    clib = lib.load()
+    assert clib.w4a8_test_fp8_linear_without(request.param) == 0
+    yield request.param
+    clib.w4a8_test_fp8_linear_without(0)
+
+
+@pytest.mark.parametrize("without", [256, 128, 64, 32, 16], indirect=True)
+@pytest.mark.parametrize("M,N,K", [(1, 256, 128), (90, 300, 512), (700, 2600, 256)])
+def test_a_configuration_that_is_not_there_leaves_the_others(lib, without, M, N, K):
+    # as where a kernel was built with other registers than it needs: the rest serves the call, an error only without any
+    _check(lib, M, N, K, "bf16", seed=N)
+    clib = lib.load()
+    assert clib.w4a8_test_fp8_linear_config(without, 1) == 0
+    try:
+        with pytest.raises(lib.W4A8Error, match=f"{without} rows"):
+            _check(lib, M, N, K)
+    finally:
+        clib.w4a8_test_fp8_linear_config(0, 0)

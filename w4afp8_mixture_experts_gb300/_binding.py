@@ -83,6 +83,7 @@ _SIGS = {
                                   _c_vp]),
     "w4a8_test_paged_attention_way": (_c_int, [_c_int]),
     "w4a8_test_fp8_linear_config": (_c_int, [_c_int, _c_int]),
+    "w4a8_test_fp8_linear_without": (_c_int, [_c_int]),
     "w4a8_test_linear_config": (_c_int, [_c_int, _c_int]),
     "w4a8_test_linear_wait": (_c_int, [_c_int, ctypes.c_uint64, _c_vp, _c_vp]),
 }

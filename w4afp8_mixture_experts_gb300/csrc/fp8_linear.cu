@@ -726,8 +726,9 @@ constexpr Option split_option() {
           BN == 128 ? 0.48 : BN == 64 ? 0.44 : BN == 32 ? 0.33 : 0.30, BN == 128 ? 5.7 : BN == 64 ? 4.4 : BN == 32 ? 4.0 : 3.3};
 }
 
-// Configuration asked for by a test (rows of a tile * 16 + pieces of K), 0: none.
-std::atomic<int> g_force{0};
+// Configuration asked for by a test (rows of a tile * 16 + pieces of K), 0: none; and rows of a tile whose configurations a
+// test takes for not available, 0: none.
+std::atomic<int> g_force{0}, g_without{0};
 
 // The configuration with the smallest estimate
 //   fixed + max(waves * stages of a piece * stage, bytes of W / rate) + (waves - 1) * wave
@@ -749,11 +750,20 @@ int launch_best(const Call& c, cudaStream_t st) {
   const double sms = num_sms();
   const Option* best = nullptr;
   double best_us = 0.0;
+  int missing = W4A8_OK;  // status of configurations that this build or device does not have
   for (const Option& o : options) {
     if (o.parts > c.p.groups || ceil_div(c.p.M, o.rows) > 65535) continue;
     if (force && force % 16 <= c.p.groups && force != o.rows * 16 + o.parts) continue;
-    int clusters = 1;
-    if (int rc = o.ready(dev, &clusters)) return rc;
+    int clusters = 1, rc = W4A8_OK;
+    if (o.rows == g_without.load(std::memory_order_relaxed))
+      rc = set_error(W4A8_ERR_UNSUPPORTED, "configurations of %d rows are left out", o.rows);
+    else
+      rc = o.ready(dev, &clusters);
+    if (rc == W4A8_ERR_UNSUPPORTED) {
+      missing = rc;
+      continue;
+    }
+    if (rc) return rc;
     const int64_t tiles = ceil_div(c.p.M, o.rows) * ceil_div(c.p.N, o.cols), waves = ceil_div(tiles, clusters);
     const double ctas = static_cast<double>(std::min<int64_t>(tiles, clusters)) * (o.rows == 256 ? 2 : o.parts);
     const double stage = std::max(o.stage_us * (1.0 + 0.45 * std::max(0.0, ctas / sms - 1.0)), ctas * o.stage_bytes / 13.9e6);
@@ -767,7 +777,7 @@ int launch_best(const Call& c, cudaStream_t st) {
       best_us = us;
     }
   }
-  if (!best) return set_error(W4A8_ERR_UNSUPPORTED, "no configuration for M=%d, N=%d", c.p.M, c.p.N);
+  if (!best) return missing ? missing : set_error(W4A8_ERR_UNSUPPORTED, "no configuration for M=%d, N=%d", c.p.M, c.p.N);
   return best->launch(c, dev, st);
 }
 
@@ -812,5 +822,10 @@ extern "C" int fp8_block_linear(const uint8_t* A, const float* a_scales, int64_t
 
 extern "C" int w4a8_test_fp8_linear_config(int rows, int pieces) {
   w4a8::g_force.store(rows > 0 ? rows * 16 + pieces : 0);
+  return W4A8_OK;
+}
+
+extern "C" int w4a8_test_fp8_linear_without(int rows) {
+  w4a8::g_without.store(rows);
   return W4A8_OK;
 }
