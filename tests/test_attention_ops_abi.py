@@ -143,3 +143,29 @@ def test_sources_load_nothing_as_constant():
     for f in files:
         code = re.sub(r"//[^\n]*", "", open(f).read())
         assert not re.findall(r"__ldg|\.nc\b|__restrict__|__builtin_nontemporal_load", code), os.path.basename(f)
+
+
+def _whole(L, B=3, T=3, k=P16, q=P16, Hq=2, qo=P16, **kw):
+    c = _cache(B=B, **kw)
+    return L.paged_kv_append_whole(k, 128, 64, P16, 128, 64, BF16, T, NULL, ctypes.byref(c), NULL, q, 64, 64, Hq, qo, 64, 64,
+                                   NULL)
+
+
+@pytest.mark.parametrize("call,msg", [
+    (lambda L: _whole(L, T=2), b"T=2"),
+    (lambda L: _whole(L, qo=NULL), b"null"),
+    (lambda L: _whole(L, B=0, qo=NULL), b"null"),
+    (lambda L: _whole(L, B=0, k=NULL), b"null"),
+    (lambda L: _whole(L, lens=0), b"null"),
+    (lambda L: _whole(L, table=0), b"page_table"),
+    (lambda L: _whole(L, q=NULL), b"Hq=2"),
+    (lambda L: _whole(L, D=0), b"D=0"),
+])
+def test_append_of_whole_outputs_refused_before_launch(clib, call, msg):
+    assert call(clib) == 1
+    assert msg in clib.w4a8_last_error(), clib.w4a8_last_error()
+
+
+def test_append_of_whole_outputs_without_rows_launches_nothing(clib):
+    assert _whole(clib, B=0, T=0, k=NULL, qo=NULL) == 0
+    assert _whole(clib, B=0, Hq=0, q=NULL, qo=NULL) == 0

@@ -249,3 +249,50 @@ def test_refusals(lib):
         with pytest.raises(err, match=msg):
             lib.paged_kv_append(**{**base, **change})
     assert lib.paged_kv_append(**base) is None and lib.device_error() == 0
+
+
+@pytest.mark.parametrize("indptr", [False, True])
+@pytest.mark.parametrize("dtype,cache,D", [("bf16", "bf16", 64), ("f16", "fp8", 64), ("bf16", "bf16", 90), ("f16", "f16", 33)])
+@pytest.mark.parametrize("turned", [False, True])
+def test_queries_left_out_are_zeros_in_fresh_memory(lib, indptr, dtype, cache, D, turned):
+    # an empty sequence, one of negative length, rows behind the last: a tensor made by the call holds zeros there, a given
+    # one what it held
+    H, Hq, rows = 2, 6, 9
+    lens = torch.tensor([3, 0, 1, -4, 17], dtype=torch.int32, device="cuda")
+    table = torch.arange(10, dtype=torch.int32, device="cuda").view(5, 2)
+    k, v = (torch.randn((rows, H, D), device="cuda").to(DT[dtype]) for _ in range(2))
+    q = torch.randn((rows, Hq, D), device="cuda").to(DT[dtype])
+    ends = torch.tensor([0, 2, 3, 4, 4, 6], dtype=torch.int32, device="cuda") if indptr else None
+    left = [2, 6, 7, 8] if indptr else [1, 3, 5, 6, 7, 8]
+    rest = [i for i in range(rows) if i not in left]
+    kw = dict(freqs=lib.rotary_frequencies(D // 2 * 2)) if turned else {}
+    kc, vc = (torch.full((10, 16, H, D), 3.0, device="cuda").to(DT[cache]) for _ in range(2))
+    given = torch.full_like(q, 7.0)
+    lib.paged_kv_append(k, v, kc, vc, table, lens, ends, q=q, q_out=given, **kw)
+    assert torch.all(given[left] == 7.0)
+    for _ in range(3):
+        keep = kc.clone(), vc.clone()
+        poison = torch.full_like(q, float("nan"))  # the memory that the call is given next, most likely
+        del poison
+        made = lib.paged_kv_append(k, v, kc, vc, table, lens, ends, q=q, **kw)
+        assert torch.all(made[left] == 0) and torch.equal(made[rest], given[rest])
+        assert torch.equal(kc.view(torch.uint8), keep[0].view(torch.uint8))
+        assert torch.equal(vc.view(torch.uint8), keep[1].view(torch.uint8))
+    assert lib.device_error() == 0
+
+
+def test_queries_of_a_batch_without_sequences(lib):
+    q = torch.randn((5, 4, 64), device="cuda").to(torch.bfloat16)
+    k, c = q[:, :2], torch.full((3, 16, 2, 64), 3.0, device="cuda").to(torch.bfloat16)
+    none, table = torch.zeros(0, dtype=torch.int32, device="cuda"), torch.zeros((0, 2), dtype=torch.int32, device="cuda")
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for indptr in (None, zero):
+        poison = torch.full_like(q, float("nan"))
+        del poison
+        made = lib.paged_kv_append(k, k, c, c.clone(), table, none, indptr, q=q)
+        assert torch.all(made == 0) and torch.all(c == 3.0)
+        given = torch.full_like(q, 7.0)
+        lib.paged_kv_append(k, k, c, c.clone(), table, none, indptr, q=q, q_out=given)
+        assert torch.all(given == 7.0)
+    assert lib.paged_kv_append(k, k, c, c.clone(), table, none, None, q=q[:, :0]).shape == (5, 0, 64)
+    assert lib.device_error() == 0

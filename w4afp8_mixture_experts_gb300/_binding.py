@@ -76,6 +76,8 @@ _SIGS = {
                                   _c_vp]),
     "paged_kv_append": (_c_int, [_c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64, _c_int, _c_i64, _c_vp, _c_vp, _c_vp,
                                  _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp]),
+    "paged_kv_append_whole": (_c_int, [_c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64, _c_int, _c_i64, _c_vp, _c_vp, _c_vp,
+                                       _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp]),
     "paged_attention_decode": (_c_int, [_c_vp, _c_i64, _c_i64, _c_int, _c_i64, _c_vp, _c_f32, _c_i64, _c_vp, _c_i64,
                                         _c_i64, _c_vp, _c_vp, _c_sz, _c_vp]),
     "paged_attention_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i64, _c_int, _c_i64]),
@@ -615,7 +617,8 @@ def paged_kv_append(k, v, k_cache, v_cache, page_table, seq_lens, indptr=None, *
     positions [T].  Rows indptr[b] ... indptr[b + 1] are the last tokens of sequence b, whose length seq_lens[b] (int32
     [B]) counts them; indptr None: one token each.  page_table int32 [B, n].  Rows behind the last sequence, or of one of
     length 0, are left out.  k_scale, v_scale fp32 [Hkv]: an 8-bit cache holds x / scale.
-    q [T, Hq, D] is rotated like the keys into q_out (made when None; may be q) and returned."""
+    q [T, Hq, D] is rotated like the keys into q_out (made when None; may be q) and returned; rows that are left out are
+    zeros in a q_out made here and stay as they were in a given one."""
     return (_ops or _load_ops()).append(k, v, k_cache, v_cache, page_table, seq_lens, indptr, freqs, positions,
                                         interleaved, start, scale, k_scale, v_scale, q, q_out)
 

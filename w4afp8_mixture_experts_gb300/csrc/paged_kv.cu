@@ -44,6 +44,7 @@ struct RowParams {
   FastDiv by_row, by_heads, by_page, by_half;
   float cos_scale, sin_scale;
   bool interleaved, positions64;
+  bool zero_left;  // queries of rows that are left out become zeros (else they stay as they are)
 };
 
 // Items of a thread in a row: more where they are narrow, as a row costs a thread as much (8192 x 40 x 101 f16, single
@@ -192,10 +193,20 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rotary_rows_kernel(const __
     int head;
     const int tok = p.by_heads.div(in0 + row, head);  // in the block
     const bool value = APPEND && head >= p.Hq + p.Hkv, query = !APPEND || head < p.Hq;
-    if (APPEND && (query ? at_pos[tok] < 0 : at_k[tok] < 0)) return;  // a row that belongs to no sequence, or has no place
     const int64_t t = tok0 + tok;
     const int h = head - p.Hq - (value ? p.Hkv : 0);
     T* out = static_cast<T*>(p.qo) + t * p.o_t + head * p.o_h;
+    if (APPEND && (query ? at_pos[tok] < 0 : at_k[tok] < 0)) {  // a row that belongs to no sequence, or has no place
+      if (query && p.zero_left) {
+        const Vec<T, V> zeros = {};
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+          if (e0[i] >= 0) *reinterpret_cast<Vec<T, V>*>(out + e0[i]) = zeros;
+          if (e1[i] >= 0) *reinterpret_cast<Vec<T, V>*>(out + e1[i]) = zeros;
+        }
+      }
+      return;
+    }
     TC* to = nullptr;
     float scale = 1.f, r = 1.f;
     if (APPEND && !query) {
@@ -431,11 +442,12 @@ extern "C" int rotary_embedding(const void* x, int64_t ldx_t, int64_t ldx_h, int
   return launch_vec<__nv_bfloat16, __nv_bfloat16, false>(p, starts, starts, elems, st);
 }
 
-extern "C" int paged_kv_append(const void* k, int64_t ldk_t, int64_t ldk_h, const void* v, int64_t ldv_t, int64_t ldv_h,
-                               int dtype, int64_t T, const int32_t* indptr, const w4a8_paged_cache* cache,
-                               const w4a8_rotary* rotary, const void* q, int64_t ldq_t, int64_t ldq_h, int64_t Hq,
-                               void* q_out, int64_t ldqo_t, int64_t ldqo_h, void* stream) {
-  using namespace w4a8;
+namespace w4a8 {
+namespace {
+
+int append(const void* k, int64_t ldk_t, int64_t ldk_h, const void* v, int64_t ldv_t, int64_t ldv_h, int dtype, int64_t T,
+           const int32_t* indptr, const w4a8_paged_cache* cache, const w4a8_rotary* rotary, const void* q, int64_t ldq_t,
+           int64_t ldq_h, int64_t Hq, void* q_out, int64_t ldqo_t, int64_t ldqo_h, bool zero_left, void* stream) {
   if (int rc = check_cache(cache, dtype)) return rc;
   const int64_t D = cache->D, H = cache->heads;
   W4A8_REQUIRE(D >= 1 && D <= kMaxDim, "D=%lld must be in [1, %d]", (long long)D, kMaxDim);
@@ -447,9 +459,10 @@ extern "C" int paged_kv_append(const void* k, int64_t ldk_t, int64_t ldk_h, cons
   W4A8_REQUIRE(ldk_t >= 0 && ldk_h >= 0 && ldv_t >= 0 && ldv_h >= 0 && ldq_t >= 0 && ldq_h >= 0 && ldqo_t >= 0 && ldqo_h >= 0,
                "strides must not be negative");
   if (int rc = check_rotary(rotary, D, false)) return rc;
-  if (T == 0 || cache->B == 0) return W4A8_OK;
-  W4A8_REQUIRE(k && v && cache->seq_lens && (!q || Hq == 0 || q_out), "null pointer");
-  W4A8_REQUIRE(cache->table_pages == 0 || cache->page_table, "null pointer: page_table");
+  zero_left = zero_left && q && Hq > 0;
+  if (T == 0 || (cache->B == 0 && !zero_left)) return W4A8_OK;
+  W4A8_REQUIRE(k && v && (cache->B == 0 || cache->seq_lens) && (!q || Hq == 0 || q_out), "null pointer");
+  W4A8_REQUIRE(cache->B == 0 || cache->table_pages == 0 || cache->page_table, "null pointer: page_table");
   W4A8_REQUIRE(cache->pages == 0 || (cache->k && cache->v), "null pointer: k and v of the cache");
   const bool fp8 = cache->dtype == W4A8_DTYPE_E4M3;
   const uint64_t size = 2, csize = fp8 ? 1 : 2;
@@ -458,6 +471,7 @@ extern "C" int paged_kv_append(const void* k, int64_t ldk_t, int64_t ldk_h, cons
                "k, v, q, q_out and the cache must be aligned to their element size");
   RowParams p = {};
   p.cos_scale = p.sin_scale = 1.f;
+  p.zero_left = zero_left;
   set_rotary(p, rotary);
   p.q = q;
   p.qo = q_out;
@@ -505,4 +519,23 @@ extern "C" int paged_kv_append(const void* k, int64_t ldk_t, int64_t ldk_h, cons
                : launch_vec<__half, __half, true>(p, starts, places, elems, st);
   return fp8 ? launch_vec<__nv_bfloat16, uint8_t, true>(p, starts, places, elems, st)
              : launch_vec<__nv_bfloat16, __nv_bfloat16, true>(p, starts, places, elems, st);
+}
+
+}  // namespace
+}  // namespace w4a8
+
+extern "C" int paged_kv_append(const void* k, int64_t ldk_t, int64_t ldk_h, const void* v, int64_t ldv_t, int64_t ldv_h,
+                               int dtype, int64_t T, const int32_t* indptr, const w4a8_paged_cache* cache,
+                               const w4a8_rotary* rotary, const void* q, int64_t ldq_t, int64_t ldq_h, int64_t Hq,
+                               void* q_out, int64_t ldqo_t, int64_t ldqo_h, void* stream) {
+  return w4a8::append(k, ldk_t, ldk_h, v, ldv_t, ldv_h, dtype, T, indptr, cache, rotary, q, ldq_t, ldq_h, Hq, q_out, ldqo_t,
+                      ldqo_h, false, stream);
+}
+
+extern "C" int paged_kv_append_whole(const void* k, int64_t ldk_t, int64_t ldk_h, const void* v, int64_t ldv_t, int64_t ldv_h,
+                                     int dtype, int64_t T, const int32_t* indptr, const w4a8_paged_cache* cache,
+                                     const w4a8_rotary* rotary, const void* q, int64_t ldq_t, int64_t ldq_h, int64_t Hq,
+                                     void* q_out, int64_t ldqo_t, int64_t ldqo_h, void* stream) {
+  return w4a8::append(k, ldk_t, ldk_h, v, ldv_t, ldv_h, dtype, T, indptr, cache, rotary, q, ldq_t, ldq_h, Hq, q_out, ldqo_t,
+                      ldqo_h, true, stream);
 }

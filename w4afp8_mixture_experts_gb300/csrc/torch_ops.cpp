@@ -535,9 +535,9 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else if (a[15] != Py_None) {
       value_error("q_out given without q");
     }
-    check(paged_kv_append(k.p, k.ld_t, k.ld_h, v.p, v.ld_t, v.ld_h, dtype_id(k.dtype), k.rows, indptr, &c, &r, q.p, q.ld_t,
-                          q.ld_h, q.heads, const_cast<void*>(o.p), o.ld_t, o.ld_h,
-                          c10::cuda::getCurrentCUDAStream(dev.index()).stream()));
+    const auto append = made.defined() ? paged_kv_append_whole : paged_kv_append;
+    check(append(k.p, k.ld_t, k.ld_h, v.p, v.ld_t, v.ld_h, dtype_id(k.dtype), k.rows, indptr, &c, &r, q.p, q.ld_t, q.ld_h,
+                 q.heads, const_cast<void*>(o.p), o.ld_t, o.ld_h, c10::cuda::getCurrentCUDAStream(dev.index()).stream()));
     return made.defined() ? THPVariable_Wrap(std::move(made)) : Py_NewRef(a[15]);
   });
 }
