@@ -296,3 +296,17 @@ def test_queries_of_a_batch_without_sequences(lib):
         assert torch.all(given == 7.0)
     assert lib.paged_kv_append(k, k, c, c.clone(), table, none, None, q=q[:, :0]).shape == (5, 0, 64)
     assert lib.device_error() == 0
+
+
+@pytest.mark.parametrize("length", [-(2 ** 31), -(2 ** 31) + 1, -(2 ** 31) + 2, -1])
+@pytest.mark.parametrize("indptr", [False, True])
+def test_the_smallest_lengths_are_left_out(lib, length, indptr):
+    k = torch.randn((3, 1, 16), device="cuda").to(torch.bfloat16)
+    kc, vc = (torch.full((3, 4, 1, 16), 3.0, device="cuda").to(torch.bfloat16) for _ in range(2))
+    table = torch.zeros((1, 2), dtype=torch.int32, device="cuda")
+    lens = torch.tensor([length], dtype=torch.int32, device="cuda")
+    ends = torch.tensor([0, 3], dtype=torch.int32, device="cuda") if indptr else None
+    q = torch.full_like(k, 7.0)
+    lib.paged_kv_append(k, k, kc, vc, table, lens, ends, q=k, q_out=q)
+    assert lib.device_error() == 0
+    assert torch.all(kc == 3.0) and torch.all(vc == 3.0) and torch.all(q == 7.0)

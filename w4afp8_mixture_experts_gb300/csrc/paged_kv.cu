@@ -277,7 +277,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rotary_rows_kernel(const __
         in = seq < p.B && p.indptr[seq] <= t;
         if (in) end = p.indptr[seq + 1];
       }
-      const int pos = in ? p.lens[seq] - (end - t) : -1;
+      const int len = in ? p.lens[seq] : 0;
+      const int pos = len > 0 ? len - (end - t) : -1;  // (of a negative length the difference may lie below -2^31)
       int64_t place = -1;
       int slot = 0;
       if (pos >= 0) {
