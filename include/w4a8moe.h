@@ -631,7 +631,8 @@ int paged_kv_append_whole(const void* k, int64_t ldk_t, int64_t ldk_h, const voi
  * fp32; the weights are taken to the values' product in two pieces of 16 bits (16-bit caches,
  * f16 outputs) or in one f16 (E4M3 with bf16 outputs).
  *   q [B][Hq][D] of `dtype` (bf16 or f16; a 16-bit cache has the same type), element d of
- *   head h of sequence b at b * ldq_b + h * ldq_h + d; out likewise; lse fp32 [B][Hq] or NULL
+ *   head h of sequence b at b * ldq_b + h * ldq_h + d; out likewise (it may be q, with the same
+ *   strides; no other overlap); lse fp32 [B][Hq] or NULL
  *   D: a multiple of 8 (of 16 with E4M3) up to 256; the cache's pointers and strides are
  *   multiples of 16 bytes.  Hq a multiple of heads, Hq / heads <= 256, B * heads < 2^24.
  *   ws: paged_attention_workspace_bytes() bytes, 16-byte aligned; its contents on entry do

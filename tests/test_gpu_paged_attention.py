@@ -402,3 +402,45 @@ def test_positions_behind_the_table_are_left_out(lib, way, window, cache):
         assert (np.abs(_np(out[b]) - want) <= bound).all(), b
         got, fine = _np(lse[b]), np.isfinite(l)
         assert np.array_equal(np.isneginf(got), np.isneginf(l)) and (np.abs(got[fine] - l[fine]) <= lb[fine]).all(), b
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(65, 1, 64), (100, 1, 128), (256, 1, 128), (512, 2, 64), (130, 1, 256), (256, 1, 256)])
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "fp8"), ("f16", "fp8")])
+def test_up_to_256_heads_to_a_key_value_head(lib, way, Hq, Hkv, D, dtype, cache):
+    c = Case([1, 700, 0, 33, 129], Hq, Hkv, D, 16, dtype, cache, seed=Hq + D)
+    c.check(lib, *c.call(lib, return_lse=True))
+
+
+@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 63, 64, 65, 500, 1998, 2000])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_window_over_bf16(lib, way, window, D):
+    c = Case([1, 64, 333, 0, 1999], 6, 2, D, 16, "bf16", seed=window)
+    c.check(lib, *c.call(lib, return_lse=True, window=window), window=window)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [33, 400])
+def test_values_of_infinity_each_way(lib, way, dtype, n):
+    # one of each sign in columns of their own: infinite there, the other columns as without them
+    c = Case([n, 7], 20, 1, 64, 16, dtype)
+    want = c.call(lib)
+    c.vc[c.table[0, 1].long(), 3, 0, 5] = math.inf
+    c.vc[c.table[0, 0].long(), 9, 0, 60] = -math.inf
+    out = c.call(lib)
+    assert torch.all(out[0, :, 5] == math.inf) and torch.all(out[0, :, 60] == -math.inf)
+    keep = [i for i in range(64) if i not in (5, 60)]
+    assert torch.equal(out[0][:, keep], want[0][:, keep]) and torch.equal(out[1], want[1])
+
+
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "fp8"), ("f16", "fp8")])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 64), (40, 1, 128), (40, 1, 256)])
+def test_outputs_over_the_queries(lib, way, dtype, cache, Hq, Hkv, D):
+    c = Case([2000, 0, 1, 90, 300], Hq, Hkv, D, 16, dtype, cache, seed=D)
+    want, lse = c.call(lib, return_lse=True)
+    c.check(lib, want, lse)
+    rows = torch.randn((5, Hq + 3, D + 8), device="cuda").to(DT[dtype])
+    for q in (c.q.clone(), rows[:, 1:1 + Hq, 8:]):  # by themselves, and part of other rows
+        q.copy_(c.q)
+        got = lib.paged_attention_decode(q, c.kc, c.vc, c.table, c.lens_t, k_scale=c.ks, v_scale=c.vs, out=q)
+        assert got is q and torch.equal(q, want)
+    assert lib.device_error() == 0

@@ -629,7 +629,7 @@ def paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, *, scale=N
     (see paged_kv_append; Hq a multiple of Hkv, D a multiple of 8 up to 256, of 16 with 8-bit caches).  scale defaults
     to D^-0.5; window > 0 sees the last `window` tokens only; tokens that page_table has no place for are left out, and
     reported (device_error).  Returns out [B, Hq, D] of q's type, with return_lse (out, fp32 [B, Hq] log-sums of the
-    exponentials); an empty sequence gives zeros and -inf.  ws is a uint8 workspace of
+    exponentials); an empty sequence gives zeros and -inf.  out may be q.  ws is a uint8 workspace of
     paged_attention_workspace_bytes(B, Hq, Hkv, D) bytes (made when None)."""
     return (_ops or _load_ops()).attend(q, k_cache, v_cache, page_table, seq_lens, scale, window, k_scale, v_scale,
                                         return_lse, out, ws)
