@@ -180,3 +180,18 @@ def test_refusals(lib):
     with pytest.raises(lib.W4A8Error, match="D=1025"):
         lib.rotary_embedding(torch.zeros((1, 1, 1025), device="cuda"), pos[:1], f)
     assert lib.device_error() == 0
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("shift", [0, 1, 4])
+def test_one_head_from_shared_rows(lib, interleaved, shift):
+    # views whose strides say little: one head expanded from a row each, tokens that overlap, a token shared by all
+    T, D = 37, 64
+    src = torch.randn(T * D + 16, device="cuda", generator=torch.Generator("cuda").manual_seed(shift)).to(torch.bfloat16)
+    pos = torch.arange(T, device="cuda") * 1000
+    freqs = lib.rotary_frequencies(D)
+    for x in (src[shift:shift + T * D].view(T, 1, D).expand(T, 1, D), src[shift:].as_strided((T, 1, D), (8, 0, 1), shift),
+              src[shift:shift + D].view(1, 1, D).expand(T, 1, D)):
+        got = lib.rotary_embedding(x, pos, freqs, interleaved=interleaved)
+        want, slack = ref.rotate(_np(x), _np(pos), ref.inv_freq(D), interleaved)
+        _check(got, want, slack, "bf16")
