@@ -643,7 +643,7 @@ def paged_attention_workspace_bytes(B: int, Hq: int, Hkv: int, D: int) -> int:
 def fp8_block_linear(A, a_scales, B, b_scales, *, out_dtype=None, out=None):
     """A [M, K] times B [N, K]^T in E4M3 (uint8 codes or float8_e4m3fn), K a multiple of 128: a_scales fp32 [K/128, ld]
     per token and 128 columns, as fp8_quant_per_token_group writes them, b_scales fp32 [ceil(N/128), K/128] per 128 x
-    128 weights -> [M, N] of out_dtype (bf16 by default, f16 or fp32)."""
+    128 weights -> [M, N] of out_dtype (bf16 by default, f16 or fp32), which a given out has too."""
     return (_ops or _load_ops()).fp8_linear(A, a_scales, B, b_scales, out_dtype, out)
 
 

@@ -27,7 +27,7 @@ struct FastDiv {
   }
 };
 
-// Checks of a cache that its operators share; `size`: bytes of an element.
+// Checks of a cache that its operators share.
 inline int check_cache(const w4a8_paged_cache* c, int dtype) {
   W4A8_REQUIRE(c, "null pointer: cache");
   W4A8_REQUIRE(dtype == W4A8_DTYPE_BF16 || dtype == W4A8_DTYPE_F16, "dtype=%d must be bf16 or f16", dtype);
