@@ -79,18 +79,6 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ uint32_t map_to_cta(uint32_t saddr, uint32_t cta) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(cta));
-  return r;
-}
 // An arrival on a barrier of another CTA that hands over tensor memory only (ordered by the tcgen05 fences): with a
 // release at cluster scope each arrival waited for the warp's outstanding global stores as well.
 __device__ __forceinline__ void remote_arrive(uint32_t cluster_addr) {

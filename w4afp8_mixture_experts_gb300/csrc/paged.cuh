@@ -27,6 +27,8 @@ struct FastDiv {
   }
 };
 
+inline uint64_t bits_of(const void* q) { return static_cast<uint64_t>(reinterpret_cast<uintptr_t>(q)); }
+
 // Checks of a cache that its operators share.
 inline int check_cache(const w4a8_paged_cache* c, int dtype) {
   W4A8_REQUIRE(c, "null pointer: cache");

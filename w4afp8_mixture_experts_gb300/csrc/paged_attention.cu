@@ -45,8 +45,6 @@ int attend_cluster(int64_t B, int64_t Hq, int64_t heads, int64_t D, bool fp8, in
   return 0;
 }
 
-uint64_t bits_of(const void* q) { return static_cast<uint64_t>(reinterpret_cast<uintptr_t>(q)); }
-
 }  // namespace
 }  // namespace w4a8
 

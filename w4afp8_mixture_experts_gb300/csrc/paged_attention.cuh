@@ -80,11 +80,6 @@ __device__ unsigned int g_attend_error;
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -395,7 +390,7 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
       ahead_h = ahead.hh / p.HB;
       where = places(ahead);
     }
-    cp_async_commit();
+    copy_commit();
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) issue(i);
@@ -543,7 +538,7 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
     };
     const auto tile_at = [&](int st) { return ring + st * C::kStage; };
     if constexpr (C::kPipe) {
-      cp_async_wait<kStages - 2>();
+      copy_wait<kStages - 2>();
       __syncwarp();
       scores(tile_at(stage));
     }
@@ -551,7 +546,7 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
     for (int i = 0; i < run; ++i) {
       issue(stage == 0 ? kStages - 1 : stage - 1);
       if constexpr (!C::kPipe) {
-        cp_async_wait<kStages - 1>();
+        copy_wait<kStages - 1>();
         __syncwarp();
         scores(tile_at(stage));
       }
@@ -638,7 +633,7 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
       // The next tile's scores beside O += P V: two independent rows of products.  Behind the item's last tile they are of no
       // use and left.
       if constexpr (C::kPipe) {
-        cp_async_wait<kStages - 2>();
+        copy_wait<kStages - 2>();
         __syncwarp();
         scores(tile_at(stage));
       }
@@ -684,7 +679,7 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
     }
 
     if constexpr (CLUSTER) {  // this warp's rows into its ring, which nothing uses any more
-      cp_async_wait<0>();
+      copy_wait<0>();
       __syncwarp();
       float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
       float* rows = reinterpret_cast<float*>(smem);
@@ -779,17 +774,15 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
   }
   if constexpr (CLUSTER) {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
     // the cluster's threads share the rows' columns in fours, and add up the warps' parts in their order
     const int h = here.hh / p.HB, head0 = h * p.G + (here.hh % p.HB) * C::kRows, live = min(C::kRows, (h + 1) * p.G - head0);
     const int rank = blockIdx.x % p.cluster, fours = p.D / 4;
     const float vs = kFp8 && p.v_scale ? p.v_scale[h] : 1.f;
     const uint32_t base = smem_u32(smem_all);
     const auto part_of = [&](int w, uint32_t at) {  // an address in the part of warp w of the cluster
-      uint32_t a;
-      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(base + (w & (kWarps - 1)) * C::kWarpBytes + at), "r"(w / kWarps));
-      return a;
+      return map_to_cta(base + (w & (kWarps - 1)) * C::kWarpBytes + at, w / kWarps);
     };
     for (int i = rank * kWarps * 32 + threadIdx.x; i < live * fours; i += p.cluster * kWarps * 32) {
       const int r = i / fours, d = (i - r * fours) * 4;
@@ -830,8 +823,8 @@ __global__ void __launch_bounds__(kWarps * 32, AttendCfg<KIND, DT, MT>::kBlocks)
         p.lse[static_cast<int64_t>(here.b) * p.Hq + head0 + r] = sum == 0.f ? -INFINITY : (top - C::kShift + log2f(sum)) * kLn2;
     }
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // no block leaves while another reads its rows
+    cluster_arrive();
+    cluster_wait();  // no block leaves while another reads its rows
   }
 }
 

@@ -365,8 +365,6 @@ int launch_vec(const RowParams& p, uint64_t starts_t, uint64_t starts_c, uint64_
   return launch_rows<T, TC, 1, APPEND>(p, st);
 }
 
-uint64_t bits_of(const void* q) { return static_cast<uint64_t>(reinterpret_cast<uintptr_t>(q)); }
-
 // A gcd by powers of two of everything that a vector's width has to divide: the lowest set bit of the union of the bits.
 uint64_t lowest(uint64_t bits) { return bits ? bits & (~bits + 1) : 1ull << 32; }
 
