@@ -194,19 +194,19 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rotary_rows_kernel(const __
     const int tok = p.by_heads.div(in0 + row, head);  // in the block
     const bool value = APPEND && head >= p.Hq + p.Hkv, query = !APPEND || head < p.Hq;
     const int64_t t = tok0 + tok;
-    const int h = head - p.Hq - (value ? p.Hkv : 0);
-    T* out = static_cast<T*>(p.qo) + t * p.o_t + head * p.o_h;
     if (APPEND && (query ? at_pos[tok] < 0 : at_k[tok] < 0)) {  // a row that belongs to no sequence, or has no place
-      if (query && p.zero_left) {
-        const Vec<T, V> zeros = {};
+      if (!query || !p.zero_left) return;
+      T* out = static_cast<T*>(p.qo) + t * p.o_t + head * p.o_h;
+      const Vec<T, V> zeros = {};
 #pragma unroll
-        for (int i = 0; i < K; ++i) {
-          if (e0[i] >= 0) *reinterpret_cast<Vec<T, V>*>(out + e0[i]) = zeros;
-          if (e1[i] >= 0) *reinterpret_cast<Vec<T, V>*>(out + e1[i]) = zeros;
-        }
+      for (int i = 0; i < K; ++i) {
+        if (e0[i] >= 0) *reinterpret_cast<Vec<T, V>*>(out + e0[i]) = zeros;
+        if (e1[i] >= 0) *reinterpret_cast<Vec<T, V>*>(out + e1[i]) = zeros;
       }
       return;
     }
+    const int h = head - p.Hq - (value ? p.Hkv : 0);
+    T* out = static_cast<T*>(p.qo) + t * p.o_t + head * p.o_h;
     TC* to = nullptr;
     float scale = 1.f, r = 1.f;
     if (APPEND && !query) {
@@ -277,8 +277,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rotary_rows_kernel(const __
         in = seq < p.B && p.indptr[seq] <= t;
         if (in) end = p.indptr[seq + 1];
       }
-      const int len = in ? p.lens[seq] : 0;
-      const int pos = len > 0 ? len - (end - t) : -1;  // (of a negative length the difference may lie below -2^31)
+      const int pos = in ? max(p.lens[seq], 0) - (end - t) : -1;  // (from a negative length it may pass -2^31)
       int64_t place = -1;
       int slot = 0;
       if (pos >= 0) {
