@@ -58,7 +58,8 @@ class AttentionHalf:
 
     def prefill(self, x, cache, indptr):
         """Keys and values of the prompts x bf16 [T, H], rows indptr[b] ... indptr[b + 1] the last tokens of sequence b, into
-        the cache; returns the rotated queries for an attention over the prompts themselves."""
+        the cache; returns the rotated queries (attention of prompts is not among the operators; rows of padding come back as
+        they are)."""
         q, k, v = self.project_qkv(x)
         return m.paged_kv_append(k, v, cache.k, cache.v, cache.page_table, cache.seq_lens, indptr, q=q, q_out=q,
                                  **self.rotary, **cache.scales)
