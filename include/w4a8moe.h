@@ -616,10 +616,10 @@ int paged_kv_append(const void* k, int64_t ldk_t, int64_t ldk_h, const void* v, 
                     const w4a8_rotary* rotary /* host pointer */, const void* q, int64_t ldq_t, int64_t ldq_h,
                     int64_t Hq, void* q_out, int64_t ldqo_t, int64_t ldqo_h, void* stream);
 /* The same, but all of q_out is written (fresh memory): queries of rows that are left out become zeros. */
-int paged_kv_append_whole(const void* k, int64_t ldk_t, int64_t ldk_h, const void* v, int64_t ldv_t, int64_t ldv_h, int dtype,
-                    int64_t T, const int32_t* indptr, const w4a8_paged_cache* cache /* host pointer */,
-                    const w4a8_rotary* rotary /* host pointer */, const void* q, int64_t ldq_t, int64_t ldq_h,
-                    int64_t Hq, void* q_out, int64_t ldqo_t, int64_t ldqo_h, void* stream);
+int paged_kv_append_whole(const void* k, int64_t ldk_t, int64_t ldk_h, const void* v, int64_t ldv_t, int64_t ldv_h,
+                          int dtype, int64_t T, const int32_t* indptr, const w4a8_paged_cache* cache /* host pointer */,
+                          const w4a8_rotary* rotary /* host pointer */, const void* q, int64_t ldq_t, int64_t ldq_h,
+                          int64_t Hq, void* q_out, int64_t ldqo_t, int64_t ldqo_h, void* stream);
 
 /*
  * (13) Attention of one new token per sequence over a paged cache:
